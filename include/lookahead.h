@@ -399,6 +399,144 @@ LA_API int la_pool_size(la_pool* pool, int* n_keys);
 /* No counterpart on the pages: frees the pool. */
 LA_API void la_pool_destroy(la_pool* pool);
 
+/* ---- paged KV cache held in 4 bits, and the step attention over it ----
+ * For serving many or long sequences: a cached key or value costs
+ * head_dim / 2 + 4 bytes instead of 2 head_dim.  The calls stand on their own
+ * (a caller's own layer loop), like la_attention; one layer's pages are one
+ * la_kv4_desc, and all layers share the block table and the slots.
+ *
+ * A step of a batch: la_kv4_attention of every layer over the lengths so far;
+ * after verification, la_kv4_plan turns the lengths and the accepted counts
+ * into pages and slots, and la_kv4_append of every layer writes the accepted
+ * rows' K and V there.  Nothing needs the host in between: all lengths,
+ * tables and counts are device memory, every call is asynchronous on `stream`
+ * and can be captured into a CUDA graph.
+ *
+ * Format.  A vector x of one token and KV head is held as codes c in 0..15, a
+ * bf16 scale s and a zero point z, and stands for (c - z) s: with
+ * hi = max(0, max x) and lo = min(0, min x), s is the smallest bf16 number
+ * with 15 s >= hi - lo, z the nearest integer to -lo / s and c the nearest
+ * integer to x / s (ties to even) plus z, clamped to 0..15.  hi = lo gives
+ * zeros.  A vector that holds a NaN or an infinity reads back as NaN.  The
+ * decisions are those of exact arithmetic.  Pages: [n_pages][n_kv_heads]
+ * [page / 16] blocks of 16 head_dim + 128 bytes for 16 tokens: K codes
+ * [head_dim / 64][16 tokens][32 bytes], V codes likewise, 16 K parameter
+ * words, 16 V parameter words.  8 codes of channels 8w..8w+7 are one 32-bit
+ * word, channel 2i at bits 4i, channel 2i + 1 at bits 16 + 4i; a parameter
+ * word is the scale's bf16 bits above 0x4300 | z.  Slot = page index * page +
+ * offset in the page.
+ *
+ * Errors that depend on device memory (a slot, page or row index outside its
+ * range, a length over its bound, too few pages) cannot be returned: the
+ * offending part is skipped as each call says, and the first code stays in
+ * *status.  Nothing outside the buffers given is read or written for such
+ * values. */
+typedef struct la_kv4_desc {
+    int n_kv_heads, head_dim; /* head_dim 64 or 128, n_kv_heads <= 1024             */
+    int page;                 /* tokens per page: 16, 32, 64 or 128                 */
+    int n_pages;              /* pages; n_pages * page < 2^31                       */
+    int max_pages;            /* block-table entries of one sequence                */
+    void* pages;              /* DEVICE, n_pages * la_kv4_page_bytes(), 16-byte aligned */
+    int32_t* status;          /* DEVICE int32, 0 at first, or NULL: the first error */
+} la_kv4_desc;
+
+/* No counterpart on the pages: sizing of this library's device memory.
+ * Bytes of one page (needs no GPU); 0 for unsupported shapes. */
+LA_API size_t la_kv4_page_bytes(const la_kv4_desc* c);
+
+/* No counterpart on the pages: cache book-keeping of a batch.
+ * Pages and slots for n_new[b] further tokens of each sequence.
+ *   lens        DEVICE int32[batch]: tokens held (< 0: not a sequence; it is
+ *               left alone and its n_new is not read as a count)
+ *   n_new       DEVICE int32[batch] >= 0
+ *   free_pages  DEVICE int32[]: a stack of free page indexes, *n_free of them
+ *   n_free      DEVICE int32
+ *   table       DEVICE int32[batch][max_pages]: entries of new pages are
+ *               written, taken from the stack's top, b ascending and each
+ *               sequence's pages in order; the others are left
+ *   slots       DEVICE int32[n_slots]: with slot_stride = 0 the new tokens'
+ *               slots one sequence after the other (n_slots at least the sum
+ *               of n_new; the rest is set to -1); with slot_stride > 0
+ *               sequence b's at b * slot_stride, unused ones -1 (n_slots =
+ *               batch * slot_stride)
+ *   new_lens    DEVICE int32[batch]: lens + n_new (may be lens itself)
+ *   pages_left  DEVICE int32: *n_free less the pages taken (may be n_free)
+ * All or nothing: if the pages, a table row, n_slots or slot_stride do not
+ * suffice (LA_ERR_CAPACITY in *status) or a count is negative (LA_ERR_ARG),
+ * every slot is -1 and the table, lengths and page count stay.  desc.pages is
+ * not used.  batch <= 8192.  LA_ERR_ARG also for output buffers that overlap
+ * others than said. */
+LA_API int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int32_t* n_new, int batch,
+                       const int32_t* free_pages, const int32_t* n_free, int32_t* table, int32_t* slots, int n_slots,
+                       int slot_stride, int32_t* new_lens, int32_t* pages_left, void* stream);
+
+/* No counterpart on the pages: cache book-keeping of a batch.
+ * Give back the pages of the sequences with done[b] != 0 (DEVICE
+ * int32[batch]): pushed onto the stack (room for n_pages entries), b
+ * ascending, each sequence's pages in order; their lens become 0 and *n_free
+ * grows.  Sequences with lens[b] < 0 hold no pages.  Nothing is given back
+ * (LA_ERR_ARG in *status) when a sequence would hold more than max_pages
+ * pages or the stack more than n_pages.  batch <= 8192. */
+LA_API int la_kv4_release(const la_kv4_desc* c, const int32_t* done, int batch, int32_t* lens, const int32_t* table,
+                          int32_t* free_pages, int32_t* n_free, void* stream);
+
+/* No counterpart on the pages (their KV commit, into this cache's format).
+ * Quantise K and V of n tokens into their slots.
+ *   k, v    DEVICE dtype (LA_BF16 or LA_FP32) [n_rows][n_kv_heads][head_dim],
+ *           rows ld elements apart, 16-byte aligned rows
+ *   rows    DEVICE int32[n]: the row of each token, or NULL: row i
+ *   slots   DEVICE int32[n]: < 0: skipped; a slot may appear once.  A slot or
+ *           row outside its range is skipped (LA_ERR_ARG in *status). */
+LA_API int la_kv4_append(const la_kv4_desc* c, const void* k, const void* v, int dtype, int ld, int n_rows,
+                         const int32_t* rows, const int32_t* slots, int n, void* stream);
+
+/* No counterpart on the pages: reads the cache back.
+ * The values (c - z) s of n slots' K and V into rows 0..n-1 of k and v
+ * (layout as in la_kv4_append; fp32 is exact, bf16 rounds once).  Rows of
+ * slots < 0, or outside the pages (LA_ERR_ARG in *status), are left as they
+ * were. */
+LA_API int la_kv4_read(const la_kv4_desc* c, const int32_t* slots, int n, void* k, void* v, int dtype, int ld,
+                       void* stream);
+
+/* A step's rows and where they are.  Sequence b's T = 1 + (W+G)(N-1) rows
+ * (as in la_attention: the current token, W x (N-1) lookahead rows, G
+ * candidates x (N-1) verification rows) are rows b*T .. b*T+T-1.  W = G = 0 is
+ * a single token, W = 0 and G = 1 a chain of N rows (a block of a prompt). */
+typedef struct la_kv4_attn {
+    const void* q;        /* DEVICE bf16 [batch * T][n_heads][head_dim], rows q_ld apart  */
+    const void* k_step;   /* DEVICE bf16 [batch * T][n_kv_heads][head_dim], kv_ld apart   */
+    const void* v_step;   /* likewise                                                     */
+    void* out;            /* DEVICE bf16 [batch * T][n_heads * head_dim]                  */
+    const int32_t* lens;  /* DEVICE int32[batch]: cached tokens; < 0: rows left alone     */
+    const int32_t* table; /* DEVICE int32[batch][max_pages]                               */
+    int batch, n_heads;   /* batch <= 65535, n_heads a multiple of n_kv_heads             */
+    int W, N, G;          /* T <= 128, 2 <= N <= 128                                      */
+    int q_ld, kv_ld;      /* multiples of 8                                               */
+    int max_len;          /* no length is above it (0: max_pages * page); a tight bound
+                             lets short batches use fewer, fuller workers                 */
+    void* workspace;      /* DEVICE, la_kv4_attention_bytes(), 16-byte aligned            */
+    size_t ws_bytes;
+} la_kv4_attn;
+
+/* No counterpart on the pages: sizing of this library's device memory.
+ * Workspace of la_kv4_attention for these shapes (needs no GPU; pointers are
+ * not looked at); 0 when none is needed or the shape is unsupported. */
+LA_API size_t la_kv4_attention_bytes(const la_kv4_desc* c, const la_kv4_attn* a);
+
+/* Pages: "Summary" (both branches share one forward pass under one mask).
+ * la_attention for a batch over a paged 4-bit cache: row i of sequence b
+ * attends to the values of the lens[b] cached tokens and to the step rows the
+ * 2D-window + verification mask lets it see (never none: each row sees row
+ * 0), scaled by 1 / sqrt(head_dim).  Positions past a length are never used,
+ * whatever bytes they hold, and a NaN or infinity in a step row reaches only
+ * rows that see it.  A length above its bound leaves that sequence's rows
+ * alone, a page index outside the pool counts as no keys (LA_ERR_ARG in
+ * *status).  Asynchronous on `stream`; the order of sums depends on the
+ * shapes and lengths alone, so equal calls give equal bits.  Two calls that
+ * may run at the same time (two streams, two captured graphs) need a
+ * workspace each. */
+LA_API int la_kv4_attention(const la_kv4_desc* c, const la_kv4_attn* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
