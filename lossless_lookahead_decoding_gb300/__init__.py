@@ -513,39 +513,14 @@ class KV4Cache:
         self.desc = la_kv4_desc(heads, self.head_dim, page, n, max_pages, pages.data_ptr(), self.status.data_ptr())
         if not la_kv4_page_bytes(self.desc):
             raise ValueError("unsupported cache shape")
-        self._lib, self._desc = lib(), C.byref(self.desc)
-        self._attn = la_kv4_attn()
-        self._dtypes = {torch.bfloat16: LA_BF16, torch.float32: LA_FP32}
-        self._bf16, self._i32 = torch.bfloat16, torch.int32
-        self._dev, self._cur = torch.cuda.current_device, torch.cuda.current_stream
+        lib()
+        from . import _kv4
+        self._kv4, self._handle = _kv4, _kv4.handle(pages, self.status, C.addressof(self.desc))
 
     @staticmethod
     def empty_pages(n_pages: int, n_kv_heads: int, head_dim: int, page: int, device="cuda"):
         import torch
         return torch.zeros((n_pages, n_kv_heads, page // 16, 16 * head_dim + 128), dtype=torch.uint8, device=device)
-
-    def _stream(self):
-        if self._dev() != self.device.index:
-            raise ValueError("the cache's device is not the current one")
-        return self._cur().cuda_stream or None
-
-    def _ints(self, *tensors):
-        for t in tensors:
-            if t.dtype is not self._i32 or t.device != self.device or not t.is_contiguous():
-                raise ValueError("expected contiguous int32 tensors on the cache's device")
-
-    def _vectors(self, x, heads, what):
-        """Row stride (in elements) of [rows, heads * head_dim] or [rows, heads, head_dim]."""
-        D = self.head_dim
-        if x.device != self.device:
-            raise ValueError(what + ": not on the cache's device")
-        if x.dim() == 2:
-            ok = x.shape[1] == heads * D and x.stride(1) == 1
-        else:
-            ok = x.dim() == 3 and x.shape[1] == heads and x.shape[2] == D and x.stride(2) == 1 and x.stride(1) == D
-        if not ok:
-            raise ValueError(what + ": expected rows of heads x head_dim with unit stride inside a row")
-        return max(x.stride(0), heads * D) if x.shape[0] < 2 else x.stride(0)
 
     @staticmethod
     def _done(rc, what):
@@ -561,80 +536,38 @@ class KV4Cache:
 
     def plan(self, lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left, stride: int = 0):
         """Pages and slots of ``n_new`` further tokens of each sequence (``la_kv4_plan``)."""
-        self._ints(lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left)
-        B = lens.shape[0]
-        if n_new.shape[0] != B or new_lens.shape[0] != B or table.dim() != 2 or table.shape[0] != B or table.shape[1] != self.max_pages:
-            raise ValueError("plan: lens, n_new and new_lens of one length, table [batch, max_pages]")
-        self._done(self._lib.la_kv4_plan(self._desc, lens.data_ptr(), n_new.data_ptr(), B, free_pages.data_ptr(),
-                                         n_free.data_ptr(), table.data_ptr(), slots.data_ptr(), slots.numel(), stride,
-                                         new_lens.data_ptr(), pages_left.data_ptr(), self._stream()), "la_kv4_plan")
+        rc = self._kv4.plan(self._handle, lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left, stride)
+        if rc:
+            self._done(rc, "la_kv4_plan")
 
     def release(self, done, lens, table, free_pages, n_free):
         """Give back the pages of the sequences with ``done`` != 0 (``la_kv4_release``)."""
-        self._ints(done, lens, table, free_pages, n_free)
-        B = lens.shape[0]
-        if done.shape[0] != B or table.dim() != 2 or table.shape[0] != B or table.shape[1] != self.max_pages:
-            raise ValueError("release: done and lens of one length, table [batch, max_pages]")
-        if free_pages.numel() < self.pages.shape[0]:
-            raise ValueError("release: free_pages needs room for every page")
-        self._done(self._lib.la_kv4_release(self._desc, done.data_ptr(), B, lens.data_ptr(), table.data_ptr(),
-                                            free_pages.data_ptr(), n_free.data_ptr(), self._stream()), "la_kv4_release")
+        rc = self._kv4.release(self._handle, done, lens, table, free_pages, n_free)
+        if rc:
+            self._done(rc, "la_kv4_release")
 
     def append(self, k, v, slots, rows=None):
         """Quantise tokens' K and V (bf16 or fp32) into their slots; ``rows``:
         the row of k and v each slot takes (``la_kv4_append``)."""
-        ld, n = self._vectors(k, self.n_kv_heads, "k"), slots.numel()
-        if self._vectors(v, self.n_kv_heads, "v") != ld or v.dtype is not k.dtype or v.shape[0] != k.shape[0] or k.dtype not in self._dtypes:
-            raise ValueError("append: k and v of one type (bf16 or fp32) and layout")
-        self._ints(slots, *(() if rows is None else (rows,)))
-        if rows is not None and rows.numel() != n:
-            raise ValueError("append: one row for each slot")
-        self._done(self._lib.la_kv4_append(self._desc, k.data_ptr(), v.data_ptr(), self._dtypes[k.dtype], ld, k.shape[0],
-                                           None if rows is None else rows.data_ptr(), slots.data_ptr(), n,
-                                           self._stream()), "la_kv4_append")
+        rc = self._kv4.append(self._handle, k, v, slots, rows)
+        if rc:
+            self._done(rc, "la_kv4_append")
 
     def read(self, slots, k, v):
         """The values held in ``slots`` into rows 0.. of k and v (``la_kv4_read``)."""
-        ld, n = self._vectors(k, self.n_kv_heads, "k"), slots.numel()
-        if self._vectors(v, self.n_kv_heads, "v") != ld or v.dtype is not k.dtype or k.dtype not in self._dtypes:
-            raise ValueError("read: k and v of one type (bf16 or fp32) and layout")
-        if k.shape[0] < n or v.shape[0] < n:
-            raise ValueError("read: fewer rows than slots")
-        self._ints(slots)
-        self._done(self._lib.la_kv4_read(self._desc, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                         self._dtypes[k.dtype], ld, self._stream()), "la_kv4_read")
+        rc = self._kv4.read(self._handle, slots, k, v)
+        if rc:
+            self._done(rc, "la_kv4_read")
 
     def attention_bytes(self, batch: int, n_heads: int, W: int, N: int, G: int, max_len: int = 0) -> int:
         """Bytes of workspace ``attention`` needs for these shapes."""
-        a = la_kv4_attn(batch=batch, n_heads=n_heads, W=W, N=N, G=G, max_len=max_len)
-        return int(self._lib.la_kv4_attention_bytes(self._desc, C.byref(a)))
+        return la_kv4_attention_bytes(self.desc, la_kv4_attn(batch=batch, n_heads=n_heads, W=W, N=N, G=G, max_len=max_len))
 
     def attention(self, q, k_step, v_step, lens, table, W: int, N: int, G: int, out, workspace, max_len: int = 0):
         """Masked attention of a step's rows over the cache (``la_kv4_attention``).
         ``q``: bf16 ``[batch * T, n_heads * head_dim]``, ``k_step`` and
         ``v_step`` likewise for the KV heads (views into a fused projection
         do), ``out``: contiguous ``[batch * T, n_heads * head_dim]``."""
-        D, B = self.head_dim, lens.shape[0]
-        rows, H = out.shape[0], out.shape[1] // D
-        if out.dim() != 2 or not out.is_contiguous() or rows != B * (1 + (W + G) * (N - 1)) or out.shape[1] != H * D:
-            raise ValueError("attention: out is contiguous [batch * T, n_heads * head_dim]")
-        if q.shape[0] != rows or k_step.shape[0] != rows or v_step.shape[0] != rows:
-            raise ValueError("attention: q, k_step and v_step have out's rows")
-        bf = self._bf16
-        if q.dtype is not bf or k_step.dtype is not bf or v_step.dtype is not bf or out.dtype is not bf:
-            raise ValueError("attention: bf16 only")
-        if out.device != self.device:
-            raise ValueError("out: not on the cache's device")
-        self._ints(lens, table)
-        if table.dim() != 2 or table.shape[0] != B or table.shape[1] != self.max_pages:
-            raise ValueError("attention: table is [batch, max_pages]")
-        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
-            raise ValueError("attention: workspace is contiguous, on the cache's device")
-        a = self._attn
-        a.q, a.k_step, a.v_step, a.out = q.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), out.data_ptr()
-        a.lens, a.table, a.batch, a.n_heads, a.W, a.N, a.G = lens.data_ptr(), table.data_ptr(), B, H, W, N, G
-        a.q_ld, a.kv_ld, a.max_len = self._vectors(q, H, "q"), self._vectors(k_step, self.n_kv_heads, "k_step"), max_len
-        if self._vectors(v_step, self.n_kv_heads, "v_step") != a.kv_ld:
-            raise ValueError("attention: k_step and v_step of one layout")
-        a.workspace, a.ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-        self._done(self._lib.la_kv4_attention(self._desc, C.byref(a), self._stream()), "la_kv4_attention")
+        rc = self._kv4.attention(self._handle, q, k_step, v_step, lens, table, W, N, G, out, workspace, max_len)
+        if rc:
+            self._done(rc, "la_kv4_attention")

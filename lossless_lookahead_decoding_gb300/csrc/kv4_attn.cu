@@ -5,15 +5,21 @@
 // For one sequence and KV head ("item") the rows are the T step rows times the
 // query heads that share the KV head, in tiles of 8 NB rows.  With a key's
 // parameters s, z and codes c:
-//   S = q . (c - z) s = s (q . (128 + c) - (128 + z) sum q)
+//   S = q . (c - z) s = s (q . c - z sum q)
 //   O = sum_keys p (c - z) s = sum_keys (p s) (c - z)
 // so scales multiply the few scores and probabilities and not the many codes.
-// K's codes go to the tensor core as 128 + c, the form the unpacking gives
-// for free; the sum over q is subtracted in fp32, where 128 |q| costs 2^-16 of
-// a code step.  V's would lose more (O shrinks as the context grows, 128 sum p
-// does not), so 128 + z is subtracted from each pair of codes: exact.
-// Rounding: p s to bf16 (relative 2^-9 a key, unbiased), then the output;
-// scores, sums and outputs stay in fp32.
+// A code masked out of its word is an fp16 subnormal as it stands: bits 0-3 of
+// a half are c 2^-24, bits 4-7 are c 2^-20.  So unpacking is one AND a pair
+// and one shift per two pairs, and both products run in fp16 with fp32 sums:
+//  * q is scaled by a power of two per row (largest magnitude in [2^11, 2^12))
+//    and, for the channels at bits 4-7, by 1/16: exact for every element
+//    within 2^-18 of the row's largest, and off by 2^-36 of it below;
+//  * p s goes to fp16: relative 2^-11, or 2^-25 absolute where the running
+//    reference keeps the largest between 1 and 2^8 (bf16 would cost 2^-8);
+//  * z sum(p s) is subtracted by the tensor core too, by a second product
+//    with -z in place of the codes: the outputs' sums return near zero in
+//    every tile (they shrink as the context grows, z sum(p s) does not) and
+//    no instruction per code is spent.
 //
 // Both products have the keys (K: 16 keys x 16 channels) or the channels (V:
 // 16 channels x 16 keys) as the 16-row side of m16n8k16 and the query rows as
@@ -22,20 +28,21 @@
 // by an 8 x 8 transpose in registers.  Channels and keys are permuted so that
 // each lane's fragments are contiguous bytes (kv4_key).
 //
-// HBM bound: 2 D / 2 + 8 bytes a key and KV head.  Each warp streams blocks of
-// 16 keys (one contiguous bulk copy each) into a ring of its own, so no warp
-// waits for another inside an item.  The running maximum moves only when a
-// score exceeds it by more than 8 (a vote, no reduction per tile): the sums
-// then hold terms up to 2^8.
+// HBM bound: D + 8 bytes a key and KV head.  One warp of a CTA streams blocks
+// of 16 keys (one contiguous bulk copy each) into a ring for each of the
+// others, so no warp waits for another inside an item.  The running reference
+// M moves only when a p s exceeds 2^8 (a vote, no reduction per tile).
 //
-// Items are cut into equal runs of blocks over the teams (a warp, or a CTA of
-// 8 warps whose partial results meet in shared memory), whatever the
+// Items are cut into equal runs of blocks over the teams (a warp, or a CTA
+// whose warps' partial results meet in shared memory), whatever the
 // sequences' lengths; an item that falls to several teams leaves partial
 // outputs, which k_kv4_merge joins in a fixed order.
 #include <algorithm>
 #include <climits>
 #include <cmath>
 #include <mutex>
+
+#include <cuda_fp16.h>
 
 #include "kv4.cuh"
 
@@ -45,7 +52,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 7;  // and one that fills their rings: 8 warps leave 128 registers each at two CTAs per SM
 constexpr int kSMs = 152;
 
 // The key of a tile held in row i of a score fragment (and in slot i of the
@@ -67,14 +74,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+#define LA_MMA16816(name, type)                                                                                        \
+    __device__ __forceinline__ void name(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,    \
+                                         uint32_t b1)                                                                  \
+    {                                                                                                                  \
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." type "." type                                            \
+                     ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                                      \
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                  \
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                          \
+    }
+LA_MMA16816(mma_f16, "f16")
+LA_MMA16816(mma_b16, "bf16")
+#undef LA_MMA16816
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
@@ -89,10 +100,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
-    __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 
 // bf16 pair with its NaNs and infinities replaced by 0; whether there were any
@@ -104,8 +122,8 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& u)
     return lo || hi;
 }
 
-// two codes at bits 4i and 16 + 4i as bf16 128 + c
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;  // a pair of codes: c 2^-24, c 2^-20
+constexpr float kMinScale = 0x1p-92f;  // V scales below it count as it (values under 2^-88)
 
 // ------------------------------------------------------------ the schedule ---
 
@@ -215,28 +233,96 @@ struct RowsSmem {
     static constexpr int kStages = NB == 1 && TW > 1 ? 4 : 6;
     static constexpr int kBlk = kv4_block_bytes(D);
     static constexpr int kRing = kWarps * kStages * kBlk;
-    static constexpr int kBar = kRing;
-    static constexpr int kMisc = kBar + kWarps * kStages * 8;                   // starts and scan scratch
-    static constexpr int kMerge = kMisc + kWarps * (int)(sizeof(Start) + 8);
-    static constexpr int kMergeBytes = TW == 1 ? 0 : kWarps * kR * (D + 4) * 4;  // [warp][row][D | max, sum]
+    static constexpr int kBar = kRing;                                          // full, empty
+    static constexpr int kLive = kBar + kWarps * kStages * 16;                  // keys of each stage's block
+    static constexpr int kMisc = kLive + (kWarps * kStages * 4 + 15) / 16 * 16;  // starts and scan scratch
+    static constexpr int kMerge = kMisc + (kWarps * (int)sizeof(Start) + (kWarps + 2) * 8 + 15) / 16 * 16;
+    static constexpr int kMergeBytes = TW == 1 ? 0 : kWarps * kR * (D + 4) * 4;  // [warp][row][D | M, sum]
     static constexpr int kBytes = kMerge + kMergeBytes;
+    static_assert(kMisc % 8 == 0 && kMerge % 16 == 0, "alignment");
 };
 
+constexpr int kThreads = (kWarps + 1) * 32;
+
+// Warp kWarps: lane w fills the ring of warp w, block by block in the order in
+// which that warp takes them.  The lanes poll their rings' empty barriers in
+// turn; the page of the next block is looked up a round ahead.
+template <int D, int TW, int S, int BLK>
+__device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                        int* live, int wi)
+{
+    const uint64_t pol = policy_evict_first();
+    Run r;
+    r.left = 0;
+    r.t0 = r.t1 = 0;
+    bool more = st.count > 0;
+    if (more) r.begin(a, st);
+    int t = r.t0 + wi, page = 0, head = 0, left = 0, blk = 0, n = 0;
+    bool pend = false;
+    auto find = [&]() {
+        pend = false;
+        while (more) {
+            if (t < r.t1 && t * 16 < r.len) {
+                page = __ldg(a.table + (size_t)r.b * a.max_pages + (t >> a.blk_log2));
+                head = r.item / a.mtiles;
+                blk = t & ((1 << a.blk_log2) - 1);
+                left = r.len - t * 16;
+                pend = true;
+                t += TW;
+                return;
+            }
+            more = r.next(a);
+            t = r.t0 + wi;
+        }
+    };
+    find();
+    unsigned long long since = 0;
+    int s = 0, phase = 1;  // the first pass over the ring does not wait
+    while (__any_sync(0xffffffffu, pend)) {
+        bool moved = false;
+        if (pend && (n < S || mbar_try_wait(empty + s, phase))) {
+            const bool ok = (unsigned)page < (unsigned)a.n_pages;
+            if (!ok) kv4_raise(a.status, LA_ERR_ARG);
+            live[s] = ok ? left : 0;
+            mbar_expect_tx(full + s, BLK);
+            bulk_load(ring + s * BLK, a.pages + kv4_block_at(ok ? page : 0, head, blk, a.Hkv, a.blk_log2, D), BLK, full + s, pol);
+            n++;
+            if (++s == S) s = 0, phase ^= 1;
+            find();
+            moved = true;
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+            since = 0;
+        } else {
+            __nanosleep(40);
+            const unsigned long long now = globaltimer();
+            if (!since) since = now;
+            if (now - since > 2 * kWaitNs) {  // the consumers gave up: they have reported it
+                pend = false;
+            }
+        }
+    }
+    // no copy may still be on its way when the CTA ends: the last S of this
+    // lane's, whichever of them were issued
+    for (int i = 0; i < S && i < n; i++) {
+        const int k = n - 1 - i;
+        mbar_drain(full + k % S, (k / S) & 1);
+    }
+}
+
 template <int D, int NB, int TW>
-__global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn a)
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn a)
 {
     using L = RowsSmem<D, NB, TW>;
     constexpr int S = L::kStages, R = L::kR, PAN = D / 64, MB = D / 16, DV = D / 8;
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wi = TW == 1 ? 0 : warp;  // this warp's place in its team
-    uint8_t* ring = sm + warp * S * L::kBlk;
-    uint64_t* bar = (uint64_t*)(sm + L::kBar) + warp * S;
+    uint64_t *full = (uint64_t*)(sm + L::kBar), *empty = full + kWarps * S;
+    int* live_of = (int*)(sm + L::kLive);
     Start* starts = (Start*)(sm + L::kMisc);
-    long long* scratch = (long long*)(starts + kWarps);
-    const int team = TW == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
-    if (lane == 0) {
-        for (int s = 0; s < S; s++) mbar_init(bar + s, 1);
+    if (threadIdx.x < kWarps * S) {
+        mbar_init(full + threadIdx.x, 1);
+        mbar_init(empty + threadIdx.x, 1);
         mbar_fence_init();
     }
     pdl_wait();
@@ -244,93 +330,36 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < a.B; b += blockDim.x)
             if (a.lens[b] > a.max_len) kv4_raise(a.status, LA_ERR_ARG);
-    find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, scratch);
+    // (its barriers also publish the mbarriers)
+    find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, (long long*)(starts + kWarps));
+    if (warp == kWarps) {
+        const int w = min(lane, kWarps - 1);
+        Start st = starts[TW == 1 ? w : 0];
+        if (lane >= kWarps) st.count = 0;
+        produce<D, TW, S, L::kBlk>(a, st, sm + w * S * L::kBlk, full + w * S, empty + w * S, live_of + w * S, TW == 1 ? 0 : w);
+        return;
+    }
+    const int wi = TW == 1 ? 0 : warp;  // this warp's place in its team
+    const int team = TW == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
     const Start st = starts[TW == 1 ? warp : 0];
+    const uint8_t* ring = sm + warp * S * L::kBlk;
+    full += warp * S, empty += warp * S, live_of += warp * S;
     MergeRec rec{0, 0, 0};
-    MergeRec* recs = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
-
-    const uint64_t pol = policy_evict_first();
     const int group = a.H / a.Hkv;
-    // ---- the producing side: which of this warp's tiles comes next
-    Run pr;
-    pr.left = 0;
-    pr.t0 = pr.t1 = 0;
-    pr.begin(a, st);
-    int pt = st.count > 0 ? pr.t0 + wi : 0;
-    bool more = st.count > 0;
-    int pend_page = 0, pend_head = 0, pend_blk = 0, issued = 0, taken = 0;
-    bool pend = false;
-    uint32_t bad_mask = 0;  // stages whose page index is outside the pool
-    auto find_next = [&]() {
-        pend = false;
-        while (more) {
-            if (pt < pr.t1 && pt * 16 < pr.len) {
-                const int pg = (pt * 16) >> (4 + a.blk_log2);
-                pend_page = a.table[(size_t)pr.b * a.max_pages + pg];
-                pend_head = pr.item / a.mtiles;
-                pend_blk = pt & ((1 << a.blk_log2) - 1);
-                pend = true;
-                pt += TW;
-                return;
-            }
-            more = pr.next(a);
-            if (more) pt = pr.t0 + wi;
-        }
-    };
-    auto issue = [&]() {
-        if (!pend) return;
-        const int s = issued % S;
-        const bool ok = (unsigned)pend_page < (unsigned)a.n_pages;
-        bad_mask = (bad_mask & ~(1u << s)) | (ok ? 0u : 1u << s);
-        if (lane == 0) {
-            if (!ok) kv4_raise(a.status, LA_ERR_ARG);
-            mbar_expect_tx(bar + s, L::kBlk);
-            bulk_load(ring + s * L::kBlk,
-                      a.pages + kv4_block_at(ok ? pend_page : 0, pend_head, pend_blk, a.Hkv, a.blk_log2, D), L::kBlk,
-                      bar + s, pol);
-        }
-        issued++;
-        find_next();
-    };
-    __syncwarp();
-    find_next();
-    for (int i = 0; i < S - 1; i++) issue();
-
     bool alive = true;  // no wait has given up
+    int s = 0, phase = 0;
     Run run;
     run.left = 0;
-    run.begin(a, st);
     if (st.count > 0) {
+        run.begin(a, st);
         bool first = true;
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
-            // ---- this lane's part of the query rows: row 8 nb + g, channels 64 p + 16 t ..
-            uint32_t q[NB][PAN][8];
-            float qs[NB][2];  // sum over the channels of rows 2t, 2t + 1
-#pragma unroll
-            for (int nb = 0; nb < NB; nb++) {
+            const int ntc = (run.len + 15) / 16;
+            auto q_row = [&](int nb) {
                 const int r = mt * R + nb * 8 + g;
-                float sum = 0.f;
-                const __nv_bfloat16* src =
-                    a.q + (size_t)(run.b * (long long)a.T + r / group) * a.q_ld + (size_t)(head * group + r % group) * D + 16 * t;
-#pragma unroll
-                for (int p = 0; p < PAN; p++) {
-                    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-                    if (r < a.rows) {
-                        u0 = *(const uint4*)(src + 64 * p);
-                        u1 = *(const uint4*)(src + 64 * p + 8);
-                    }
-                    q[nb][p][0] = u0.x, q[nb][p][1] = u0.y, q[nb][p][2] = u0.z, q[nb][p][3] = u0.w;
-                    q[nb][p][4] = u1.x, q[nb][p][5] = u1.y, q[nb][p][6] = u1.z, q[nb][p][7] = u1.w;
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        sum += __uint_as_float(q[nb][p][i] << 16) + __uint_as_float(q[nb][p][i] & 0xffff0000u);
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                qs[nb][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-                qs[nb][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-            }
+                return a.q + (size_t)(run.b * (long long)a.T + r / group) * a.q_ld + (size_t)(head * group + r % group) * D + 16 * t;
+            };
             float o[NB][MB][4], m[NB][2], l[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; nb++) {
@@ -341,50 +370,78 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
 #pragma unroll
                     for (int j = 0; j < 4; j++) o[nb][i][j] = 0.f;
             }
-            // scores x[nb][i]: key kv4_key(g + 8 (i >> 1)) of the tile, row 2t + (i & 1);
-            // turned into probabilities; the running maximum follows when it must
-            auto softmax = [&](float (&x)[NB][4]) {
-                bool up = false;
-#pragma unroll
-                for (int nb = 0; nb < NB; nb++)
-                    up |= fmaxf(x[nb][0], x[nb][2]) > m[nb][0] + 8.f || fmaxf(x[nb][1], x[nb][3]) > m[nb][1] + 8.f;
-                if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                        for (int r = 0; r < 2; r++) {
-                            float mx = fmaxf(x[nb][r], x[nb][r + 2]);
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                            mx = fmaxf(mx, m[nb][r]);
-                            const float c = mx == m[nb][r] ? 1.f : ex2(m[nb][r] - mx);
-                            m[nb][r] = mx;
-                            l[nb][r] *= c;
-#pragma unroll
-                            for (int i = 0; i < MB; i++) o[nb][i][r] *= c, o[nb][i][r + 2] *= c;
-                        }
-                }
+            // Move the reference of row 2t + r to the largest y = log2(p s) seen (x: log2 p before it).
+            auto raise_ref = [&](float (&y)[NB][4]) {
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float mu = m[nb][i & 1] == -INFINITY ? 0.f : m[nb][i & 1];
-                        x[nb][i] = ex2(x[nb][i] - mu);
-                        l[nb][i & 1] += x[nb][i];
+                    for (int r = 0; r < 2; r++) {
+                        float mx = fmaxf(y[nb][r], y[nb][r + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mx, m[nb][r]);
+                        const float c = mx == m[nb][r] ? 1.f : ex2(m[nb][r] - mx);
+                        m[nb][r] = mx;
+                        l[nb][r] *= c;
+#pragma unroll
+                        for (int i = 0; i < MB; i++) o[nb][i][r] *= c, o[nb][i][r + 2] *= c;
                     }
             };
-            for (int tile = run.t0 + wi; tile < run.t1; tile += TW) {
-                float x[NB][4];
+            if (run.t0 + wi < min(run.t1, ntc)) {
+                // ---------------------------------------------- cached keys
+                // this lane's part of the query rows: row 8 nb + g, channels 64 p + 16 t ..
+                uint32_t q[NB][PAN][8];
+                float qs[NB][2], qf[NB][2];  // rows 2t, 2t + 1: sum of q, what undoes q's and the codes' powers of two
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++) x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.f;
-                if (tile * 16 < run.len) {
-                    // ------------------------------------------ cached keys
-                    issue();
-                    const int s = taken % S;
-                    if (alive) {
+                for (int nb = 0; nb < NB; nb++) {
+                    const bool valid = mt * R + nb * 8 + g < a.rows;
+                    const __nv_bfloat16* src = q_row(nb);
+                    uint32_t raw[PAN][8];
+                    float sum = 0.f, top = 0.f;
+#pragma unroll
+                    for (int p = 0; p < PAN; p++) {
+                        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+                        if (valid) {
+                            u0 = *(const uint4*)(src + 64 * p);
+                            u1 = *(const uint4*)(src + 64 * p + 8);
+                        }
+                        raw[p][0] = u0.x, raw[p][1] = u0.y, raw[p][2] = u0.z, raw[p][3] = u0.w;
+                        raw[p][4] = u1.x, raw[p][5] = u1.y, raw[p][6] = u1.z, raw[p][7] = u1.w;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const float lo = __uint_as_float(raw[p][i] << 16), hi = __uint_as_float(raw[p][i] & 0xffff0000u);
+                            sum += lo + hi;
+                            top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+                        }
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // exponent of the row's largest, kept where both powers of two are normal numbers
+                    const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 236);
+                    const float down = __uint_as_float((uint32_t)(127 + 11 + 127 - e) << 23);    // 2^(11 - (e - 127))
+                    const float up = __uint_as_float((uint32_t)(e - 11 + 24 - 8) << 23) * 256.f;  // 2^(24 - 11 + e - 127)
+#pragma unroll
+                    for (int p = 0; p < PAN; p++)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const float f = i & 1 ? down * 0.0625f : down;
+                            q[nb][p][i] = pack_f16(__uint_as_float(raw[p][i] << 16) * f,
+                                                   __uint_as_float(raw[p][i] & 0xffff0000u) * f);
+                        }
+                    qs[nb][0] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t);
+                    qs[nb][1] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t + 4);
+                    qf[nb][0] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t);
+                    qf[nb][1] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t + 4);
+                }
+                const int k0 = kv4_key(g), k1 = k0 + 8;
+                const int kA = t, kB = 4 + (t ^ 3);  // V's keys: probability slots 2t, 2t + 1; + 8: slots 2t + 8, 2t + 9
+                for (int tile = run.t0 + wi; tile < min(run.t1, ntc); tile += TW) {
+                    if (alive && !mbar_try_wait(full + s, phase)) {
                         const unsigned long long since = globaltimer();
-                        while (!mbar_try_wait(bar + s, (taken / S) & 1))
+                        while (!mbar_try_wait(full + s, phase))
                             if (globaltimer() - since > kWaitNs) {
                                 alive = false;
                                 kv4_raise(a.status, LA_ERR_TIMEOUT);
@@ -392,172 +449,238 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                             }
                     }
                     const uint8_t* blk = ring + s * L::kBlk;
-                    const int live = (bad_mask >> s) & 1 ? 0 : run.len - tile * 16;  // keys below it count
-                    taken++;
-                    const int k0 = kv4_key(g), k1 = kv4_key(g + 8);
+                    const int live = live_of[s];
+                    float x[NB][4], x2[NB][4];  // two sums each, to halve the chain of dependent products
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) x[nb][i] = x2[nb][i] = 0.f;
 #pragma unroll
                     for (int p = 0; p < PAN; p++) {
                         const uint2 w0 = *(const uint2*)(blk + p * 512 + k0 * 32 + t * 8);
                         const uint2 w1 = *(const uint2*)(blk + p * 512 + k1 * 32 + t * 8);
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const uint32_t u0 = i < 2 ? w0.x : w0.y, u1 = i < 2 ? w1.x : w1.y;
-                            const int j = (i & 1) * 2;
-                            const uint32_t a0 = codes(u0, j), a1 = codes(u1, j), a2 = codes(u0, j + 1), a3 = codes(u1, j + 1);
+                            uint32_t u0 = i < 2 ? w0.x : w0.y, u1 = i < 2 ? w1.x : w1.y;
+                            if (i & 1) u0 >>= 8, u1 >>= 8;
 #pragma unroll
                             for (int nb = 0; nb < NB; nb++)
-                                mma16816(x[nb], a0, a1, a2, a3, q[nb][p][2 * i], q[nb][p][2 * i + 1]);
+                                mma_f16(i < 2 ? x[nb] : x2[nb], u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, q[nb][p][2 * i],
+                                        q[nb][p][2 * i + 1]);
                         }
                     }
-                    const uint32_t* kp = (const uint32_t*)(blk + 16 * D);
-                    const uint32_t p0 = kp[k0], p1 = kp[k1];
-                    const float s0 = __uint_as_float(p0 & 0xffff0000u) * a.sl2, s1 = __uint_as_float(p1 & 0xffff0000u) * a.sl2;
-                    const float z0 = __uint_as_float(p0 << 16), z1 = __uint_as_float(p1 << 16);
+                    const uint32_t* par = (const uint32_t*)(blk + 16 * D);  // K, then V
+                    const uint32_t p0 = par[k0], p1 = par[k1];
+                    uint32_t v0 = par[16 + k0], v1 = par[16 + k1];
+                    uint32_t vA = par[16 + kA], vB = par[16 + kB], vC = par[24 + kA], vE = par[24 + kB];
+                    const float s0 = __uint_as_float(p0 & 0xffff0000u), s1 = __uint_as_float(p1 & 0xffff0000u);
+                    const float z0 = 128.f - __uint_as_float(p0 << 16), z1 = 128.f - __uint_as_float(p1 << 16);  // -z
 #pragma unroll
                     for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            x[nb][r] = k0 < live ? s0 * fmaf(-z0, qs[nb][r], x[nb][r]) : -INFINITY;
-                            x[nb][r + 2] = k1 < live ? s1 * fmaf(-z1, qs[nb][r], x[nb][r + 2]) : -INFINITY;
+                            x[nb][r] = s0 * fmaf(x[nb][r] + x2[nb][r], qf[nb][r], z0 * qs[nb][r]);
+                            x[nb][r + 2] = s1 * fmaf(x[nb][r + 2] + x2[nb][r + 2], qf[nb][r], z1 * qs[nb][r]);
                         }
-                    softmax(x);
-                    const uint32_t* vp = kp + 16;
-                    const float v0 = k0 < live ? __uint_as_float(vp[k0] & 0xffff0000u) : 0.f;
-                    const float v1 = k1 < live ? __uint_as_float(vp[k1] & 0xffff0000u) : 0.f;
+                    if (live < 16) {
+                        // the last block of a sequence (or a bad page): the rest of it may hold anything
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) {
+                                if (k0 >= live) x[nb][r] = -INFINITY;
+                                if (k1 >= live) x[nb][r + 2] = -INFINITY;
+                            }
+                        if (k0 >= live) v0 = 0;
+                        if (k1 >= live) v1 = 0;
+                    }
+                    const float sv0 = max_nan(__uint_as_float(v0 & 0xffff0000u), kMinScale);
+                    const float sv1 = max_nan(__uint_as_float(v1 & 0xffff0000u), kMinScale);
+                    float e[NB][4];
+                    auto weigh = [&]() {  // e: probabilities; returns the largest p s of this lane
+                        float top = 0.f;
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) {
+                                const float mu = fmaxf(m[nb][r], -3e38f);
+                                e[nb][r] = ex2(x[nb][r] - mu);
+                                e[nb][r + 2] = ex2(x[nb][r + 2] - mu);
+                                top = fmaxf(top, fmaxf(e[nb][r] * sv0, e[nb][r + 2] * sv1));
+                            }
+                        return top;
+                    };
+                    if (__any_sync(0xffffffffu, weigh() > 256.f)) {
+                        const float l0 = __log2f(sv0), l1 = __log2f(sv1);
+                        float y[NB][4];
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) y[nb][r] = x[nb][r] + l0, y[nb][r + 2] = x[nb][r + 2] + l1;
+                        raise_ref(y);
+                        weigh();
+                    }
                     uint32_t b0[NB], b1[NB];
 #pragma unroll
                     for (int nb = 0; nb < NB; nb++) {
-                        b0[nb] = transpose8(pack_bf16(x[nb][0] * v0, x[nb][1] * v0));
-                        b1[nb] = transpose8(pack_bf16(x[nb][2] * v1, x[nb][3] * v1));
+                        l[nb][0] += e[nb][0] + e[nb][2];
+                        l[nb][1] += e[nb][1] + e[nb][3];
+                        b0[nb] = transpose8(pack_f16(e[nb][0] * sv0, e[nb][1] * sv0));
+                        b1[nb] = transpose8(pack_f16(e[nb][2] * sv1, e[nb][3] * sv1));
                     }
-                    // V of keys A, B (probability slots 2t, 2t + 1) and C, E (8 + 2t, 9 + 2t)
-                    const int kA = t, kB = 4 + (t ^ 3), kC = 8 + kA, kE = 8 + kB;
-                    const uint32_t zAB = __byte_perm(kA < live ? vp[kA] : 0x4300u, kB < live ? vp[kB] : 0x4300u, 0x5410);
-                    const uint32_t zCE = __byte_perm(kC < live ? vp[kC] : 0x4300u, kE < live ? vp[kE] : 0x4300u, 0x5410);
+                    // -z of the same keys as fp16 2^-24 z and 2^-20 z
+                    const uint32_t zAB = __byte_perm(vA, vB, 0x5410) & kLo, zCE = __byte_perm(vC, vE, 0x5410) & kLo;
+                    const uint32_t zl0 = zAB | 0x80008000u, zl1 = zCE | 0x80008000u;
+                    const uint32_t zh0 = (zAB << 4) | 0x80008000u, zh1 = (zCE << 4) | 0x80008000u;
                     const uint8_t* vc = blk + 8 * D;
                     if (D == 128) {
                         const uint8_t* vb = vc + (g >> 2) * 512 + (g & 3) * 8;
                         const uint2 wA = *(const uint2*)(vb + kA * 32), wB = *(const uint2*)(vb + kB * 32);
-                        const uint2 wC = *(const uint2*)(vb + kC * 32), wE = *(const uint2*)(vb + kE * 32);
+                        const uint2 wC = *(const uint2*)(vb + kA * 32 + 256), wE = *(const uint2*)(vb + kB * 32 + 256);
 #pragma unroll
                         for (int hf = 0; hf < 2; hf++) {
                             const uint32_t sel = hf ? 0x7632 : 0x5410;
-                            const uint32_t ab0 = __byte_perm(wA.x, wB.x, sel), ab1 = __byte_perm(wA.y, wB.y, sel);
-                            const uint32_t ce0 = __byte_perm(wC.x, wE.x, sel), ce1 = __byte_perm(wC.y, wE.y, sel);
+                            uint32_t ab0 = __byte_perm(wA.x, wB.x, sel), ab1 = __byte_perm(wA.y, wB.y, sel);
+                            uint32_t ce0 = __byte_perm(wC.x, wE.x, sel), ce1 = __byte_perm(wC.y, wE.y, sel);
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
-                                const uint32_t a0 = sub_bf16x2(codes(ab0, j), zAB), a1 = sub_bf16x2(codes(ab1, j), zAB);
-                                const uint32_t a2 = sub_bf16x2(codes(ce0, j), zCE), a3 = sub_bf16x2(codes(ce1, j), zCE);
+                                const uint32_t mk = j & 1 ? kHi : kLo;
+                                if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
 #pragma unroll
                                 for (int nb = 0; nb < NB; nb++)
-                                    mma16816(o[nb][(hf * 4 + j) % MB], a0, a1, a2, a3, b0[nb], b1[nb]);
+                                    mma_f16(o[nb][(hf * 4 + j) % MB], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[nb], b1[nb]);
                             }
                         }
                     } else {
                         const uint32_t wA = *(const uint32_t*)(vc + kA * 32 + g * 4), wB = *(const uint32_t*)(vc + kB * 32 + g * 4);
-                        const uint32_t wC = *(const uint32_t*)(vc + kC * 32 + g * 4), wE = *(const uint32_t*)(vc + kE * 32 + g * 4);
-                        const uint32_t ab0 = __byte_perm(wA, wB, 0x5410), ab1 = __byte_perm(wA, wB, 0x7632);
-                        const uint32_t ce0 = __byte_perm(wC, wE, 0x5410), ce1 = __byte_perm(wC, wE, 0x7632);
+                        const uint32_t wC = *(const uint32_t*)(vc + kA * 32 + 256 + g * 4), wE = *(const uint32_t*)(vc + kB * 32 + 256 + g * 4);
+                        uint32_t ab0 = __byte_perm(wA, wB, 0x5410), ab1 = __byte_perm(wA, wB, 0x7632);
+                        uint32_t ce0 = __byte_perm(wC, wE, 0x5410), ce1 = __byte_perm(wC, wE, 0x7632);
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const uint32_t a0 = sub_bf16x2(codes(ab0, j), zAB), a1 = sub_bf16x2(codes(ab1, j), zAB);
-                            const uint32_t a2 = sub_bf16x2(codes(ce0, j), zCE), a3 = sub_bf16x2(codes(ce1, j), zCE);
+                            const uint32_t mk = j & 1 ? kHi : kLo;
+                            if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma16816(o[nb][j], a0, a1, a2, a3, b0[nb], b1[nb]);
+                            for (int nb = 0; nb < NB; nb++) mma_f16(o[nb][j], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[nb], b1[nb]);
                         }
                     }
-                    __syncwarp();  // every lane has read the stage: issue() may fill it again
-                } else {
-                    // ------------------------------------- the step's own rows
-                    const int j0 = (tile - (run.len + 15) / 16) * 16;
-                    const size_t col = (size_t)head * D;
-                    auto row = [&](const __nv_bfloat16* base, int j) {
-                        return base + (size_t)(run.b * (long long)a.T + j) * a.kv_ld + col;
-                    };
-                    const int k0 = j0 + kv4_key(g), k1 = j0 + kv4_key(g + 8);
 #pragma unroll
-                    for (int p = 0; p < PAN; p++)
+                    for (int j = 0; j < MB; j++)
 #pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-                            if (k0 < a.T) u0 = *(const uint4*)(row(a.ks, k0) + 64 * p + 16 * t + 8 * i);
-                            if (k1 < a.T) u1 = *(const uint4*)(row(a.ks, k1) + 64 * p + 16 * t + 8 * i);
+                        for (int nb = 0; nb < NB; nb++)
+                            mma_f16(o[nb][j], j & 1 ? zh0 : zl0, j & 1 ? zh0 : zl0, j & 1 ? zh1 : zl1, j & 1 ? zh1 : zl1, b0[nb], b1[nb]);
+                    __syncwarp();  // every lane has read the stage
+                    if (lane == 0) mbar_arrive(empty + s);
+                    if (++s == S) s = 0, phase ^= 1;
+                }
+            }
+            // ------------------------------------------ the step's own rows
+            // (in bf16, with their values brought to the codes' powers of two)
+            int tile = run.t0 + wi;
+            if (tile < ntc) tile += (ntc - tile + TW - 1) / TW * TW;
+            for (; tile < run.t1; tile += TW) {
+                const int j0 = (tile - ntc) * 16;
+                const size_t col = (size_t)head * D;
+                auto row = [&](const __nv_bfloat16* base, int j) {
+                    return base + (size_t)(run.b * (long long)a.T + j) * a.kv_ld + col;
+                };
+                const int k0 = j0 + kv4_key(g), k1 = k0 + 8;
+                float x[NB][4];
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++) {
-                                mma16816(x[nb], u0.x, u1.x, u0.y, u1.y, q[nb][p][4 * i], q[nb][p][4 * i + 1]);
-                                mma16816(x[nb], u0.z, u1.z, u0.w, u1.w, q[nb][p][4 * i + 2], q[nb][p][4 * i + 3]);
-                            }
-                        }
+                for (int nb = 0; nb < NB; nb++) x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.f;
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
+                for (int p = 0; p < PAN; p++)
 #pragma unroll
-                        for (int r = 0; r < 2; r++) {
-                            const int i = (mt * R + nb * 8 + 2 * t + r) / group;  // the step row
-                            x[nb][r] = k0 < a.T && kv4_sees(i, k0, a.W, a.n1) ? x[nb][r] * a.sl2 : -INFINITY;
-                            x[nb][r + 2] = k1 < a.T && kv4_sees(i, k1, a.W, a.n1) ? x[nb][r + 2] * a.sl2 : -INFINITY;
-                        }
-                    softmax(x);
-                    uint32_t b0[NB], b1[NB];
+                    for (int i = 0; i < 2; i++) {
+                        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+                        if (k0 < a.T) u0 = *(const uint4*)(row(a.ks, k0) + 64 * p + 16 * t + 8 * i);
+                        if (k1 < a.T) u1 = *(const uint4*)(row(a.ks, k1) + 64 * p + 16 * t + 8 * i);
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++) {
-                        b0[nb] = transpose8(pack_bf16(x[nb][0], x[nb][1]));
-                        b1[nb] = transpose8(pack_bf16(x[nb][2], x[nb][3]));
-                    }
-                    // A NaN or an infinity among the values must reach the rows that see its key
-                    // and no others, and zero times it is NaN: the product runs without it
-                    bool odd = false;
-                    const int key[4] = {j0 + t, j0 + 4 + (t ^ 3), j0 + 8 + t, j0 + 12 + (t ^ 3)};
-#pragma unroll
-                    for (int half = 0; half < DV / 8; half++) {
-                        // channels DV g + 8 half ..
-                        uint4 v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            v[e] = make_uint4(0, 0, 0, 0);
-                            if (key[e] < a.T) v[e] = *(const uint4*)(row(a.vs, key[e]) + DV * g + 8 * half);
-                            odd |= drop_nonfinite(v[e].x) | drop_nonfinite(v[e].y) | drop_nonfinite(v[e].z) | drop_nonfinite(v[e].w);
-                        }
-                        const uint32_t* vA = (const uint32_t*)&v[0];
-                        const uint32_t* vB = (const uint32_t*)&v[1];
-                        const uint32_t* vC = (const uint32_t*)&v[2];
-                        const uint32_t* vE = (const uint32_t*)&v[3];
-                        if (D == 128) {
-                            // fragment rows g and g + 8 hold channels 16 g + 2j (+ 1) and 16 g + 8 + 2j (+ 1):
-                            // half the fragment at a time, the other half zero
-#pragma unroll
-                            for (int j = 0; j < 8; j++) {
-                                const uint32_t sel = j < 4 ? 0x5410 : 0x7632;
-                                const uint32_t ab = __byte_perm(vA[j & 3], vB[j & 3], sel);
-                                const uint32_t ce = __byte_perm(vC[j & 3], vE[j & 3], sel);
-#pragma unroll
-                                for (int nb = 0; nb < NB; nb++)
-                                    mma16816(o[nb][j % MB], half ? 0u : ab, half ? ab : 0u, half ? 0u : ce, half ? ce : 0u,
-                                             b0[nb], b1[nb]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                const uint32_t a0 = __byte_perm(vA[j], vB[j], 0x5410), a1 = __byte_perm(vA[j], vB[j], 0x7632);
-                                const uint32_t a2 = __byte_perm(vC[j], vE[j], 0x5410), a3 = __byte_perm(vC[j], vE[j], 0x7632);
-#pragma unroll
-                                for (int nb = 0; nb < NB; nb++) mma16816(o[nb][j], a0, a1, a2, a3, b0[nb], b1[nb]);
-                            }
+                        for (int nb = 0; nb < NB; nb++) {
+                            uint4 u = make_uint4(0, 0, 0, 0);
+                            if (mt * R + nb * 8 + g < a.rows) u = *(const uint4*)(q_row(nb) + 64 * p + 8 * i);
+                            mma_b16(x[nb], u0.x, u1.x, u0.y, u1.y, u.x, u.y);
+                            mma_b16(x[nb], u0.z, u1.z, u0.w, u1.w, u.z, u.w);
                         }
                     }
-                    if (__any_sync(0xffffffffu, odd)) {
-                        for (int j = j0; j < min(j0 + 16, a.T); j++) {
 #pragma unroll
-                            for (int c = 0; c < DV; c++) {
-                                const float v = __bfloat162float(row(a.vs, j)[DV * g + c]);
-                                if (fabsf(v) < INFINITY) continue;
-                                const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
+                for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                                for (int nb = 0; nb < NB; nb++)
+                    for (int r = 0; r < 2; r++) {
+                        const int i = (mt * R + nb * 8 + 2 * t + r) / group;  // the step row
+                        x[nb][r] = k0 < a.T && kv4_sees(i, k0, a.W, a.n1) ? x[nb][r] * a.sl2 : -INFINITY;
+                        x[nb][r + 2] = k1 < a.T && kv4_sees(i, k1, a.W, a.n1) ? x[nb][r + 2] * a.sl2 : -INFINITY;
+                    }
+                raise_ref(x);
+                uint32_t b0[NB][2], b1[NB][2];
 #pragma unroll
-                                    for (int r = 0; r < 2; r++)
-                                        if (kv4_sees((mt * R + nb * 8 + 2 * t + r) / group, j, a.W, a.n1))
-                                            o[nb][mb % MB][r + 2 * hi] += v;
-                            }
+                for (int nb = 0; nb < NB; nb++) {
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) e[i] = ex2(x[nb][i] - fmaxf(m[nb][i & 1], -3e38f));
+                    l[nb][0] += e[0] + e[2];
+                    l[nb][1] += e[1] + e[3];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float f = h ? 0x1p-20f : 0x1p-24f;
+                        b0[nb][h] = transpose8(pack_bf16(e[0] * f, e[1] * f));
+                        b1[nb][h] = transpose8(pack_bf16(e[2] * f, e[3] * f));
+                    }
+                }
+                // A NaN or an infinity among the values must reach the rows that see its key
+                // and no others, and zero times it is NaN: the product runs without it
+                bool odd = false;
+                const int key[4] = {j0 + t, j0 + 4 + (t ^ 3), j0 + 8 + t, j0 + 12 + (t ^ 3)};
+#pragma unroll
+                for (int half = 0; half < DV / 8; half++) {
+                    // channels DV g + 8 half ..
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (key[i] < a.T) v[i] = *(const uint4*)(row(a.vs, key[i]) + DV * g + 8 * half);
+                        odd |= drop_nonfinite(v[i].x) | drop_nonfinite(v[i].y) | drop_nonfinite(v[i].z) | drop_nonfinite(v[i].w);
+                    }
+                    const uint32_t* vA = (const uint32_t*)&v[0];
+                    const uint32_t* vB = (const uint32_t*)&v[1];
+                    const uint32_t* vC = (const uint32_t*)&v[2];
+                    const uint32_t* vE = (const uint32_t*)&v[3];
+                    if (D == 128) {
+                        // fragment rows g and g + 8 hold channels 16 g + 2j (+ 1) and 16 g + 8 + 2j (+ 1):
+                        // half the fragment at a time, the other half zero
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const uint32_t sel = j < 4 ? 0x5410 : 0x7632;
+                            const uint32_t ab = __byte_perm(vA[j & 3], vB[j & 3], sel);
+                            const uint32_t ce = __byte_perm(vC[j & 3], vE[j & 3], sel);
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++)
+                                mma_b16(o[nb][j % MB], half ? 0u : ab, half ? ab : 0u, half ? 0u : ce, half ? ce : 0u, b0[nb][j & 1],
+                                        b1[nb][j & 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t a0 = __byte_perm(vA[j], vB[j], 0x5410), a1 = __byte_perm(vA[j], vB[j], 0x7632);
+                            const uint32_t a2 = __byte_perm(vC[j], vE[j], 0x5410), a3 = __byte_perm(vC[j], vE[j], 0x7632);
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) mma_b16(o[nb][j], a0, a1, a2, a3, b0[nb][j & 1], b1[nb][j & 1]);
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    for (int j = j0; j < min(j0 + 16, a.T); j++) {
+#pragma unroll
+                        for (int c = 0; c < DV; c++) {
+                            const float v = __bfloat162float(row(a.vs, j)[DV * g + c]);
+                            if (fabsf(v) < INFINITY) continue;
+                            const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                                for (int r = 0; r < 2; r++)
+                                    if (kv4_sees((mt * R + nb * 8 + 2 * t + r) / group, j, a.W, a.n1))
+                                        o[nb][mb % MB][r + 2 * hi] += v;
                         }
                     }
                 }
@@ -573,16 +696,14 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                 }
             const bool whole = run.t0 == 0 && run.t1 == run.nt;
             float* part = a.part + ((size_t)team * 2 + (run.t0 == 0 ? 1 : 0)) * part_floats(R, D);
-            if (run.t0 == 0 && !whole) {
-                rec = MergeRec{run.b, run.item, run.nt - run.t1};
-            }
+            if (run.t0 == 0 && !whole) rec = MergeRec{run.b, run.item, run.nt - run.t1};
             // channel c (of DV, from DV g) of row 2t + r
             auto chan = [&](int nb, int r, int c) -> float {
-                if (D == 128) {
-                    const int mb = ((c & 7) >> 1) + 4 * (c & 1);
-                    return o[nb][mb % MB][r + (c >= 8 ? 2 : 0)];
-                }
-                return o[nb][c >> 1][r + 2 * (c & 1)];
+                const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
+                return o[nb][mb % MB][r + 2 * hi] * (mb & 1 ? 0x1p20f : 0x1p24f);
+            };
+            auto out_row = [&](int gr) {
+                return a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
             };
             if (TW == 1) {
 #pragma unroll
@@ -597,7 +718,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
 #pragma unroll
                             for (int c = 0; c < DV; c += 2)
                                 y[c / 2] = pack_bf16(chan(nb, r, c) * inv, chan(nb, r, c + 1) * inv);
-                            __nv_bfloat16* dst = a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + DV * g;
+                            __nv_bfloat16* dst = out_row(gr) + DV * g;
 #pragma unroll
                             for (int c = 0; c < DV / 2; c += 4) *(uint4*)(dst + 2 * c) = make_uint4(y[c], y[c + 1], y[c + 2], y[c + 3]);
                         } else {
@@ -610,7 +731,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                     }
             } else {
                 float* mg = (float*)(sm + L::kMerge);
-                if (!first) __syncthreads();  // the last item's results have been read
+                if (!first) named_sync(1, kWarps * 32);  // the last item's results have been read
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
@@ -621,9 +742,9 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                             *(float4*)(dst + DV * g + c) = make_float4(chan(nb, r, c), chan(nb, r, c + 1), chan(nb, r, c + 2), chan(nb, r, c + 3));
                         if (g == 0) *(float2*)(dst + D) = make_float2(m[nb][r], l[nb][r]);
                     }
-                __syncthreads();
-                for (int e = threadIdx.x; e < R * D / 4; e += kWarps * 32) {
-                    const int lr = e / (D / 4), c = (e % (D / 4)) * 4, gr = mt * R + lr;
+                named_sync(1, kWarps * 32);
+                for (int i = threadIdx.x; i < R * D / 4; i += kWarps * 32) {
+                    const int lr = i / (D / 4), c = (i % (D / 4)) * 4, gr = mt * R + lr;
                     if (gr >= a.rows) continue;
                     float2 ml[kWarps];
                     float mx = -INFINITY;
@@ -632,7 +753,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                         ml[w] = *(const float2*)(mg + ((size_t)w * R + lr) * (D + 4) + D);
                         mx = fmaxf(mx, ml[w].x);
                     }
-                    const float mu = mx == -INFINITY ? 0.f : mx;
+                    const float mu = fmaxf(mx, -3e38f);
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
 #pragma unroll
@@ -644,8 +765,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
                     }
                     if (whole) {
                         const float inv = 1.f / sum;
-                        *(uint2*)(a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
-                            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                        *(uint2*)(out_row(gr) + c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
                     } else {
                         *(float4*)(part + (size_t)lr * D + c) = acc;
                         if (c == 0) *(float2*)(part + (size_t)R * D + 2 * lr) = make_float2(mx, sum);
@@ -655,8 +775,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 2 : 1) k_kv4_rows(Kv4At
             }
         } while (run.next(a));
     }
-    if (!alive)  // no copy may still be on its way when the CTA ends
-        for (; taken < issued; taken++) mbar_drain(bar + taken % S, (taken / S) & 1);
+    MergeRec* recs = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
     if (a.part && (TW == 1 ? lane == 0 : threadIdx.x == 0) && team < a.nteams) recs[team] = rec;
 }
 
@@ -699,7 +818,7 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
             const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
             mx = fmaxf(mx, part[(size_t)R * D + 2 * lr]);
         }
-        const float mu = mx == -INFINITY ? 0.f : mx;
+        const float mu = fmaxf(mx, -3e38f);
         for (int i = i0; i <= last; i++) {
             if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;
             const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
@@ -767,8 +886,8 @@ int attn_ready()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return LA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
-        if (!(set_smem<128, 1, 1>() && set_smem<128, 1, 8>() && set_smem<128, 2, 1>() && set_smem<128, 2, 8>() &&
-              set_smem<64, 1, 1>() && set_smem<64, 1, 8>() && set_smem<64, 2, 1>() && set_smem<64, 2, 8>()))
+        if (!(set_smem<128, 1, 1>() && set_smem<128, 1, kWarps>() && set_smem<128, 2, 1>() && set_smem<128, 2, kWarps>() &&
+              set_smem<64, 1, 1>() && set_smem<64, 1, kWarps>() && set_smem<64, 2, 1>() && set_smem<64, 2, kWarps>()))
             return LA_ERR_CUDA;
         g_ready[dev] = 1;
     }
@@ -778,8 +897,8 @@ int attn_ready()
 template <int D, int NB>
 cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
-    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, NB, 1>, dim3(p.grid), dim3(kWarps * 32), RowsSmem<D, NB, 1>::kBytes, s, k)
-                              : launch_pdl(k_kv4_rows<D, NB, 8>, dim3(p.grid), dim3(kWarps * 32), RowsSmem<D, NB, 8>::kBytes, s, k);
+    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, NB, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, 1>::kBytes, s, k)
+                              : launch_pdl(k_kv4_rows<D, NB, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, kWarps>::kBytes, s, k);
     if (e == cudaSuccess && p.merge) e = launch_pdl(k_kv4_merge<D, 8 * NB>, dim3(p.nteams), dim3(256), 0, s, k);
     return e;
 }
