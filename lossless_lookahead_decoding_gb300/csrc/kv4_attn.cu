@@ -54,6 +54,8 @@ using namespace ptx;
 
 constexpr int kWarps = 7;  // and one that fills their rings: 8 warps leave 128 registers each at two CTAs per SM
 constexpr int kSMs = 152;
+constexpr int kKeys = 32;  // a tile: two blocks, for independent instructions and one vote per 32 keys
+constexpr float kNoRef = -3e38f;  // below every score: exp2(-inf - kNoRef) = 0
 
 // The key of a tile held in row i of a score fragment (and in slot i of the
 // probabilities): with these, the four keys whose V a lane reads at once lie
@@ -106,6 +108,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float y;
@@ -133,24 +137,27 @@ __device__ __forceinline__ int seq_len(const Kv4Attn& a, int b)
     return len > a.max_len ? -1 : len;  // too long: raised by k_kv4_rows, left alone everywhere
 }
 
-__device__ __forceinline__ int item_tiles(const Kv4Attn& a, int len)
+// An item's work in units of a tile: `extra` units for its queries and its
+// result, its cached tiles, its step rows' tiles.
+__device__ __forceinline__ int item_units(const Kv4Attn& a, int len)
 {
-    return len < 0 ? 0 : (len + 15) / 16 + (a.T + 15) / 16;
+    return len < 0 ? 0 : a.extra + (len + kKeys - 1) / kKeys + (a.T + 15) / 16;
 }
 
 struct Start {
     int b;
-    long long off, count;  // offset in the tiles of sequence b's items; tiles of the team
+    long long off, count;  // offset in the units of sequence b's items; units of the team
+    long long total;       // units of all items
 };
 
 // Where each of the CTA's teams begins: teams t0 .. t0 + n - 1 of a.nteams
-// take equal runs of all items' tiles in (sequence, item) order.
+// take equal runs of all items' units in (sequence, item) order.
 __device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long long* scratch)
 {
     const int items = a.Hkv * a.mtiles, per = ceil_div(a.B, (int)blockDim.x), b0 = threadIdx.x * per;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     long long mine = 0;
-    for (int b = b0; b < min(b0 + per, a.B); b++) mine += (long long)items * item_tiles(a, seq_len(a, b));
+    for (int b = b0; b < min(b0 + per, a.B); b++) mine += (long long)items * item_units(a, seq_len(a, b));
     if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
     long long x = mine;
 #pragma unroll
@@ -171,9 +178,9 @@ __device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long
             if (u0 >= u1 || u0 < before || u0 >= before + mine) continue;
             long long at = before;
             for (int b = b0; b < min(b0 + per, a.B); b++) {
-                const long long c = (long long)items * item_tiles(a, seq_len(a, b));
+                const long long c = (long long)items * item_units(a, seq_len(a, b));
                 if (u0 < at + c) {
-                    starts[i] = Start{b, u0 - at, u1 - u0};
+                    starts[i] = Start{b, u0 - at, u1 - u0, total};
                     break;
                 }
                 at += c;
@@ -183,21 +190,26 @@ __device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long
     __syncthreads();
 }
 
-// The run of tiles of one item that a team works on.
+// The run of units of one item that a team works on, and its tiles t0 .. t1 - 1.
 struct Run {
-    int b, item, len, nt, t0, t1;
+    int b, item, len, nu, u0, u1, t0, t1;
     long long left;
+    __device__ __forceinline__ void cut(const Kv4Attn& a, int from)
+    {
+        u0 = from;
+        u1 = (int)min((long long)nu, u0 + left);
+        left -= u1 - u0;
+        t0 = max(u0 - a.extra, 0);
+        t1 = max(u1 - a.extra, 0);
+    }
     __device__ __forceinline__ void begin(const Kv4Attn& a, const Start& s)
     {
         left = s.count;
-        if (left <= 0) return;
         b = s.b;
         len = seq_len(a, b);
-        nt = item_tiles(a, len);
-        item = (int)(s.off / nt);
-        t0 = (int)(s.off - (long long)item * nt);
-        t1 = (int)min((long long)nt, t0 + left);
-        left -= t1 - t0;
+        nu = item_units(a, len);
+        item = (int)(s.off / nu);
+        cut(a, (int)(s.off - (long long)item * nu));
     }
     __device__ __forceinline__ bool next(const Kv4Attn& a)
     {
@@ -207,12 +219,10 @@ struct Run {
             do {
                 if (++b >= a.B) return false;  // only if the lengths change under the call
                 len = seq_len(a, b);
-                nt = item_tiles(a, len);
-            } while (nt == 0);
+                nu = item_units(a, len);
+            } while (nu == 0);
         }
-        t0 = 0;
-        t1 = (int)min((long long)nt, left);
-        left -= t1;
+        cut(a, 0);
         return true;
     }
 };
@@ -220,7 +230,8 @@ struct Run {
 // Items that several teams hold, one record per team, filled by the team that
 // holds the item's first tile.
 struct MergeRec {
-    int b, item, rest;  // rest: the item's tiles that other teams hold (0: none begins here)
+    int b, item, rest, pad;  // rest: the item's units that other teams hold (0: none begins here)
+    long long total;         // units of all items
 };
 
 __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
@@ -230,8 +241,8 @@ __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)
 template <int D, int NB, int TW>
 struct RowsSmem {
     static constexpr int kR = 8 * NB;
-    static constexpr int kStages = NB == 1 && TW > 1 ? 4 : 6;
-    static constexpr int kBlk = kv4_block_bytes(D);
+    static constexpr int kStages = NB == 1 && TW > 1 ? 2 : 3;
+    static constexpr int kBlk = 2 * kv4_block_bytes(D);
     static constexpr int kRing = kWarps * kStages * kBlk;
     static constexpr int kBar = kRing;                                          // full, empty
     static constexpr int kLive = kBar + kWarps * kStages * 16;                  // keys of each stage's block
@@ -247,7 +258,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 // Warp kWarps: lane w fills the ring of warp w, block by block in the order in
 // which that warp takes them.  The lanes poll their rings' empty barriers in
 // turn; the page of the next block is looked up a round ahead.
-template <int D, int TW, int S, int BLK>
+template <int D, int TW, int S>
 __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8_t* ring, uint64_t* full, uint64_t* empty,
                                         int* live, int wi)
 {
@@ -257,16 +268,21 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
     r.t0 = r.t1 = 0;
     bool more = st.count > 0;
     if (more) r.begin(a, st);
-    int t = r.t0 + wi, page = 0, head = 0, left = 0, blk = 0, n = 0;
+    constexpr int BLK = kv4_block_bytes(D);
+    int t = r.t0 + wi, page = 0, page1 = 0, head = 0, left = 0, blk = 0, n = 0;
     bool pend = false;
     auto find = [&]() {
         pend = false;
         while (more) {
-            if (t < r.t1 && t * 16 < r.len) {
-                page = __ldg(a.table + (size_t)r.b * a.max_pages + (t >> a.blk_log2));
+            if (t < r.t1 && t * kKeys < r.len) {
+                // block 2t of the sequence and, when it has one, 2t + 1: in the same
+                // page unless pages hold a single block
+                const int* entry = a.table + (size_t)r.b * a.max_pages + ((2 * t) >> a.blk_log2);
+                page = __ldg(entry);
+                left = r.len - t * kKeys;
+                page1 = left > 16 ? (a.blk_log2 ? page : __ldg(entry + 1)) : -2;
                 head = r.item / a.mtiles;
-                blk = t & ((1 << a.blk_log2) - 1);
-                left = r.len - t * 16;
+                blk = (2 * t) & ((1 << a.blk_log2) - 1);
                 pend = true;
                 t += TW;
                 return;
@@ -281,11 +297,23 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
     while (__any_sync(0xffffffffu, pend)) {
         bool moved = false;
         if (pend && (n < S || mbar_try_wait(empty + s, phase))) {
-            const bool ok = (unsigned)page < (unsigned)a.n_pages;
-            if (!ok) kv4_raise(a.status, LA_ERR_ARG);
-            live[s] = ok ? left : 0;
-            mbar_expect_tx(full + s, BLK);
-            bulk_load(ring + s * BLK, a.pages + kv4_block_at(ok ? page : 0, head, blk, a.Hkv, a.blk_log2, D), BLK, full + s, pol);
+            // two numbers of keys: the first block's and the second's
+            const bool ok0 = (unsigned)page < (unsigned)a.n_pages, ok1 = (unsigned)page1 < (unsigned)a.n_pages;
+            if (!ok0 || (!ok1 && page1 != -2)) kv4_raise(a.status, LA_ERR_ARG);
+            live[s] = (ok0 ? min(left, 16) : 0) | (ok1 ? left - 16 < 16 ? left - 16 : 16 : 0) << 8;
+            uint8_t* dst = ring + s * 2 * BLK;
+            const uint8_t* src = a.pages + kv4_block_at(ok0 ? page : 0, head, blk, a.Hkv, a.blk_log2, D);
+            if (page1 == -2) {
+                mbar_expect_tx(full + s, BLK);
+                bulk_load(dst, src, BLK, full + s, pol);
+            } else if (a.blk_log2) {
+                mbar_expect_tx(full + s, 2 * BLK);
+                bulk_load(dst, src, 2 * BLK, full + s, pol);
+            } else {
+                mbar_expect_tx(full + s, 2 * BLK);
+                bulk_load(dst, src, BLK, full + s, pol);
+                bulk_load(dst + BLK, a.pages + kv4_block_at(ok1 ? page1 : 0, head, 0, a.Hkv, 0, D), BLK, full + s, pol);
+            }
             n++;
             if (++s == S) s = 0, phase ^= 1;
             find();
@@ -314,7 +342,7 @@ template <int D, int NB, int TW>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn a)
 {
     using L = RowsSmem<D, NB, TW>;
-    constexpr int S = L::kStages, R = L::kR, PAN = D / 64, MB = D / 16, DV = D / 8;
+    constexpr int S = L::kStages, R = L::kR, PAN = D / 64, MB = D / 16, DV = D / 8, BLK = kv4_block_bytes(D);
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint64_t *full = (uint64_t*)(sm + L::kBar), *empty = full + kWarps * S;
@@ -336,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
         const int w = min(lane, kWarps - 1);
         Start st = starts[TW == 1 ? w : 0];
         if (lane >= kWarps) st.count = 0;
-        produce<D, TW, S, L::kBlk>(a, st, sm + w * S * L::kBlk, full + w * S, empty + w * S, live_of + w * S, TW == 1 ? 0 : w);
+        produce<D, TW, S>(a, st, sm + w * S * L::kBlk, full + w * S, empty + w * S, live_of + w * S, TW == 1 ? 0 : w);
         return;
     }
     const int wi = TW == 1 ? 0 : warp;  // this warp's place in its team
@@ -344,7 +372,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
     const Start st = starts[TW == 1 ? warp : 0];
     const uint8_t* ring = sm + warp * S * L::kBlk;
     full += warp * S, empty += warp * S, live_of += warp * S;
-    MergeRec rec{0, 0, 0};
+    MergeRec* rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D)) + team;
+    const bool writes_rec = a.part && team < a.nteams && lane == 0 && wi == 0;
+    if (writes_rec) rec->rest = 0;
     const int group = a.H / a.Hkv;
     bool alive = true;  // no wait has given up
     int s = 0, phase = 0;
@@ -355,7 +385,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
         bool first = true;
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
-            const int ntc = (run.len + 15) / 16;
+            const int ntc = (run.len + kKeys - 1) / kKeys;
+            // the step's rows of this KV head are needed last: have them near by then
+            if (run.t1 > ntc && lane < min(a.T, 16)) {
+                const size_t at = (size_t)(run.b * (long long)a.T + lane) * a.kv_ld + (size_t)head * D;
+                prefetch_l1(a.ks + at), prefetch_l1(a.vs + at);
+                if (D == 128) prefetch_l1(a.ks + at + 64), prefetch_l1(a.vs + at + 64);
+            }
             auto q_row = [&](int nb) {
                 const int r = mt * R + nb * 8 + g;
                 return a.q + (size_t)(run.b * (long long)a.T + r / group) * a.q_ld + (size_t)(head * group + r % group) * D + 16 * t;
@@ -363,25 +399,26 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
             float o[NB][MB][4], m[NB][2], l[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; nb++) {
-                m[nb][0] = m[nb][1] = -INFINITY;
+                m[nb][0] = m[nb][1] = kNoRef;
                 l[nb][0] = l[nb][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MB; i++)
 #pragma unroll
                     for (int j = 0; j < 4; j++) o[nb][i][j] = 0.f;
             }
-            // Move the reference of row 2t + r to the largest y = log2(p s) seen (x: log2 p before it).
-            auto raise_ref = [&](float (&y)[NB][4]) {
+            // Move the reference of row 2t + r to the largest y = log2(p s) of the tile; y(i) is
+            // the largest of this lane's for row 2t + (i & 1) of row block i >> 1.
+            auto raise_ref = [&](auto&& y) {
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
-                        float mx = fmaxf(y[nb][r], y[nb][r + 2]);
+                        float mx = y(nb, r);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         mx = fmaxf(mx, m[nb][r]);
-                        const float c = mx == m[nb][r] ? 1.f : ex2(m[nb][r] - mx);
+                        const float c = ex2(m[nb][r] - mx);
                         m[nb][r] = mx;
                         l[nb][r] *= c;
 #pragma unroll
@@ -448,127 +485,140 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                                 break;
                             }
                     }
-                    const uint8_t* blk = ring + s * L::kBlk;
+                    const uint8_t* stage = ring + s * L::kBlk;
                     const int live = live_of[s];
-                    float x[NB][4], x2[NB][4];  // two sums each, to halve the chain of dependent products
+                    float x[2][NB][4], sv[2][2];  // per block: scores; V scales of the keys k0, k1
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
+                    for (int u = 0; u < 2; u++) {
+                        const uint8_t* blk = stage + u * BLK;
 #pragma unroll
-                        for (int i = 0; i < 4; i++) x[nb][i] = x2[nb][i] = 0.f;
+                        for (int nb = 0; nb < NB; nb++) x[u][nb][0] = x[u][nb][1] = x[u][nb][2] = x[u][nb][3] = 0.f;
 #pragma unroll
-                    for (int p = 0; p < PAN; p++) {
-                        const uint2 w0 = *(const uint2*)(blk + p * 512 + k0 * 32 + t * 8);
-                        const uint2 w1 = *(const uint2*)(blk + p * 512 + k1 * 32 + t * 8);
+                        for (int p = 0; p < PAN; p++) {
+                            const uint2 w0 = *(const uint2*)(blk + p * 512 + k0 * 32 + t * 8);
+                            const uint2 w1 = *(const uint2*)(blk + p * 512 + k1 * 32 + t * 8);
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            uint32_t u0 = i < 2 ? w0.x : w0.y, u1 = i < 2 ? w1.x : w1.y;
-                            if (i & 1) u0 >>= 8, u1 >>= 8;
+                            for (int i = 0; i < 4; i++) {
+                                uint32_t u0 = i < 2 ? w0.x : w0.y, u1 = i < 2 ? w1.x : w1.y;
+                                if (i & 1) u0 >>= 8, u1 >>= 8;
+#pragma unroll
+                                for (int nb = 0; nb < NB; nb++)
+                                    mma_f16(x[u][nb], u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, q[nb][p][2 * i], q[nb][p][2 * i + 1]);
+                            }
+                        }
+                        const uint32_t* par = (const uint32_t*)(blk + 16 * D);  // K, then V
+                        const uint32_t p0 = par[k0], p1 = par[k1];
+                        const float s0 = __uint_as_float(p0 & 0xffff0000u), s1 = __uint_as_float(p1 & 0xffff0000u);
+                        const float z0 = 128.f - __uint_as_float(p0 << 16), z1 = 128.f - __uint_as_float(p1 << 16);  // -z
+                        sv[u][0] = max_nan(__uint_as_float(par[16 + k0] & 0xffff0000u), kMinScale);
+                        sv[u][1] = max_nan(__uint_as_float(par[16 + k1] & 0xffff0000u), kMinScale);
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) {
+                                x[u][nb][r] = s0 * fmaf(x[u][nb][r], qf[nb][r], z0 * qs[nb][r]);
+                                x[u][nb][r + 2] = s1 * fmaf(x[u][nb][r + 2], qf[nb][r], z1 * qs[nb][r]);
+                            }
+                    }
+                    if (live != 0x1010) {
+                        // the last blocks of a sequence (or a bad page): the rest may hold anything
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            const int n = (live >> (8 * u)) & 255;
 #pragma unroll
                             for (int nb = 0; nb < NB; nb++)
-                                mma_f16(i < 2 ? x[nb] : x2[nb], u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, q[nb][p][2 * i],
-                                        q[nb][p][2 * i + 1]);
+#pragma unroll
+                                for (int r = 0; r < 2; r++) {
+                                    if (k0 >= n) x[u][nb][r] = -INFINITY;
+                                    if (k1 >= n) x[u][nb][r + 2] = -INFINITY;
+                                }
+                            if (k0 >= n) sv[u][0] = kMinScale;
+                            if (k1 >= n) sv[u][1] = kMinScale;
                         }
                     }
-                    const uint32_t* par = (const uint32_t*)(blk + 16 * D);  // K, then V
-                    const uint32_t p0 = par[k0], p1 = par[k1];
-                    uint32_t v0 = par[16 + k0], v1 = par[16 + k1];
-                    uint32_t vA = par[16 + kA], vB = par[16 + kB], vC = par[24 + kA], vE = par[24 + kB];
-                    const float s0 = __uint_as_float(p0 & 0xffff0000u), s1 = __uint_as_float(p1 & 0xffff0000u);
-                    const float z0 = 128.f - __uint_as_float(p0 << 16), z1 = 128.f - __uint_as_float(p1 << 16);  // -z
+                    float e[2][NB][4];              // probabilities
+                    uint32_t b0[2][NB], b1[2][NB];  // p s of the keys k0 and k1, rows 2t and 2t + 1
+                    auto weigh = [&]() {            // whether some p s is above 2^8
+                        __half2 top = __float2half2_rn(0.f);
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
+                        for (int u = 0; u < 2; u++)
 #pragma unroll
-                        for (int r = 0; r < 2; r++) {
-                            x[nb][r] = s0 * fmaf(x[nb][r] + x2[nb][r], qf[nb][r], z0 * qs[nb][r]);
-                            x[nb][r + 2] = s1 * fmaf(x[nb][r + 2] + x2[nb][r + 2], qf[nb][r], z1 * qs[nb][r]);
-                        }
-                    if (live < 16) {
-                        // the last block of a sequence (or a bad page): the rest of it may hold anything
+                            for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                            for (int r = 0; r < 2; r++) {
-                                if (k0 >= live) x[nb][r] = -INFINITY;
-                                if (k1 >= live) x[nb][r + 2] = -INFINITY;
+                                for (int i = 0; i < 4; i++) e[u][nb][i] = ex2(x[u][nb][i] - m[nb][i & 1]);
+                                b0[u][nb] = pack_f16(e[u][nb][0] * sv[u][0], e[u][nb][1] * sv[u][0]);
+                                b1[u][nb] = pack_f16(e[u][nb][2] * sv[u][1], e[u][nb][3] * sv[u][1]);
+                                top = __hmax2(top, __hmax2(*(__half2*)&b0[u][nb], *(__half2*)&b1[u][nb]));
                             }
-                        if (k0 >= live) v0 = 0;
-                        if (k1 >= live) v1 = 0;
-                    }
-                    const float sv0 = max_nan(__uint_as_float(v0 & 0xffff0000u), kMinScale);
-                    const float sv1 = max_nan(__uint_as_float(v1 & 0xffff0000u), kMinScale);
-                    float e[NB][4];
-                    auto weigh = [&]() {  // e: probabilities; returns the largest p s of this lane
-                        float top = 0.f;
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                            for (int r = 0; r < 2; r++) {
-                                const float mu = fmaxf(m[nb][r], -3e38f);
-                                e[nb][r] = ex2(x[nb][r] - mu);
-                                e[nb][r + 2] = ex2(x[nb][r + 2] - mu);
-                                top = fmaxf(top, fmaxf(e[nb][r] * sv0, e[nb][r + 2] * sv1));
-                            }
-                        return top;
+                        return !__hble2(top, __float2half2_rn(256.f));
                     };
-                    if (__any_sync(0xffffffffu, weigh() > 256.f)) {
-                        const float l0 = __log2f(sv0), l1 = __log2f(sv1);
-                        float y[NB][4];
+                    if (__any_sync(0xffffffffu, weigh())) {
+                        raise_ref([&](int nb, int r) {
+                            float y = kNoRef;
 #pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                            for (int r = 0; r < 2; r++) y[nb][r] = x[nb][r] + l0, y[nb][r + 2] = x[nb][r + 2] + l1;
-                        raise_ref(y);
+                            for (int u = 0; u < 2; u++)
+                                y = fmaxf(y, fmaxf(x[u][nb][r] + __log2f(sv[u][0]), x[u][nb][r + 2] + __log2f(sv[u][1])));
+                            return y;
+                        });
                         weigh();
                     }
-                    uint32_t b0[NB], b1[NB];
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++) {
-                        l[nb][0] += e[nb][0] + e[nb][2];
-                        l[nb][1] += e[nb][1] + e[nb][3];
-                        b0[nb] = transpose8(pack_f16(e[nb][0] * sv0, e[nb][1] * sv0));
-                        b1[nb] = transpose8(pack_f16(e[nb][2] * sv1, e[nb][3] * sv1));
-                    }
-                    // -z of the same keys as fp16 2^-24 z and 2^-20 z
-                    const uint32_t zAB = __byte_perm(vA, vB, 0x5410) & kLo, zCE = __byte_perm(vC, vE, 0x5410) & kLo;
-                    const uint32_t zl0 = zAB | 0x80008000u, zl1 = zCE | 0x80008000u;
-                    const uint32_t zh0 = (zAB << 4) | 0x80008000u, zh1 = (zCE << 4) | 0x80008000u;
-                    const uint8_t* vc = blk + 8 * D;
-                    if (D == 128) {
-                        const uint8_t* vb = vc + (g >> 2) * 512 + (g & 3) * 8;
-                        const uint2 wA = *(const uint2*)(vb + kA * 32), wB = *(const uint2*)(vb + kB * 32);
-                        const uint2 wC = *(const uint2*)(vb + kA * 32 + 256), wE = *(const uint2*)(vb + kB * 32 + 256);
+                    for (int u = 0; u < 2; u++) {
+                        const uint8_t* blk = stage + u * BLK;
+                        const uint32_t* vpar = (const uint32_t*)(blk + 16 * D + 64);
+                        const uint32_t vA = vpar[kA], vB = vpar[kB], vC = vpar[8 + kA], vE = vpar[8 + kB];
 #pragma unroll
-                        for (int hf = 0; hf < 2; hf++) {
-                            const uint32_t sel = hf ? 0x7632 : 0x5410;
-                            uint32_t ab0 = __byte_perm(wA.x, wB.x, sel), ab1 = __byte_perm(wA.y, wB.y, sel);
-                            uint32_t ce0 = __byte_perm(wC.x, wE.x, sel), ce1 = __byte_perm(wC.y, wE.y, sel);
+                        for (int nb = 0; nb < NB; nb++) {
+                            l[nb][0] += e[u][nb][0] + e[u][nb][2];
+                            l[nb][1] += e[u][nb][1] + e[u][nb][3];
+                            b0[u][nb] = transpose8(b0[u][nb]);
+                            b1[u][nb] = transpose8(b1[u][nb]);
+                        }
+                        // -z of the same keys as fp16 2^-24 z and 2^-20 z
+                        const uint32_t zAB = __byte_perm(vA, vB, 0x5410) & kLo, zCE = __byte_perm(vC, vE, 0x5410) & kLo;
+                        const uint32_t zl0 = zAB | 0x80008000u, zl1 = zCE | 0x80008000u;
+                        const uint32_t zh0 = (zAB * 16) | 0x80008000u, zh1 = (zCE * 16) | 0x80008000u;
+                        const uint8_t* vc = blk + 8 * D;
+                        if (D == 128) {
+                            const uint8_t* vb = vc + (g >> 2) * 512 + (g & 3) * 8;
+                            const uint2 wA = *(const uint2*)(vb + kA * 32), wB = *(const uint2*)(vb + kB * 32);
+                            const uint2 wC = *(const uint2*)(vb + kA * 32 + 256), wE = *(const uint2*)(vb + kB * 32 + 256);
+#pragma unroll
+                            for (int hf = 0; hf < 2; hf++) {
+                                const uint32_t sel = hf ? 0x7632 : 0x5410;
+                                uint32_t ab0 = __byte_perm(wA.x, wB.x, sel), ab1 = __byte_perm(wA.y, wB.y, sel);
+                                uint32_t ce0 = __byte_perm(wC.x, wE.x, sel), ce1 = __byte_perm(wC.y, wE.y, sel);
+#pragma unroll
+                                for (int j = 0; j < 4; j++) {
+                                    const uint32_t mk = j & 1 ? kHi : kLo;
+                                    if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
+#pragma unroll
+                                    for (int nb = 0; nb < NB; nb++)
+                                        mma_f16(o[nb][(hf * 4 + j) % MB], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u][nb], b1[u][nb]);
+                                }
+                            }
+                        } else {
+                            const uint8_t* vb = vc + g * 4;
+                            const uint32_t wA = *(const uint32_t*)(vb + kA * 32), wB = *(const uint32_t*)(vb + kB * 32);
+                            const uint32_t wC = *(const uint32_t*)(vb + kA * 32 + 256), wE = *(const uint32_t*)(vb + kB * 32 + 256);
+                            uint32_t ab0 = __byte_perm(wA, wB, 0x5410), ab1 = __byte_perm(wA, wB, 0x7632);
+                            uint32_t ce0 = __byte_perm(wC, wE, 0x5410), ce1 = __byte_perm(wC, wE, 0x7632);
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
                                 const uint32_t mk = j & 1 ? kHi : kLo;
                                 if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
 #pragma unroll
                                 for (int nb = 0; nb < NB; nb++)
-                                    mma_f16(o[nb][(hf * 4 + j) % MB], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[nb], b1[nb]);
+                                    mma_f16(o[nb][j], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u][nb], b1[u][nb]);
                             }
                         }
-                    } else {
-                        const uint32_t wA = *(const uint32_t*)(vc + kA * 32 + g * 4), wB = *(const uint32_t*)(vc + kB * 32 + g * 4);
-                        const uint32_t wC = *(const uint32_t*)(vc + kA * 32 + 256 + g * 4), wE = *(const uint32_t*)(vc + kB * 32 + 256 + g * 4);
-                        uint32_t ab0 = __byte_perm(wA, wB, 0x5410), ab1 = __byte_perm(wA, wB, 0x7632);
-                        uint32_t ce0 = __byte_perm(wC, wE, 0x5410), ce1 = __byte_perm(wC, wE, 0x7632);
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t mk = j & 1 ? kHi : kLo;
-                            if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
+                        for (int j = 0; j < MB; j++)
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma_f16(o[nb][j], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[nb], b1[nb]);
-                        }
+                            for (int nb = 0; nb < NB; nb++)
+                                mma_f16(o[nb][j], j & 1 ? zh0 : zl0, j & 1 ? zh0 : zl0, j & 1 ? zh1 : zl1, j & 1 ? zh1 : zl1, b0[u][nb],
+                                        b1[u][nb]);
                     }
-#pragma unroll
-                    for (int j = 0; j < MB; j++)
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-                            mma_f16(o[nb][j], j & 1 ? zh0 : zl0, j & 1 ? zh0 : zl0, j & 1 ? zh1 : zl1, j & 1 ? zh1 : zl1, b0[nb], b1[nb]);
                     __syncwarp();  // every lane has read the stage
                     if (lane == 0) mbar_arrive(empty + s);
                     if (++s == S) s = 0, phase ^= 1;
@@ -611,13 +661,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                         x[nb][r] = k0 < a.T && kv4_sees(i, k0, a.W, a.n1) ? x[nb][r] * a.sl2 : -INFINITY;
                         x[nb][r + 2] = k1 < a.T && kv4_sees(i, k1, a.W, a.n1) ? x[nb][r + 2] * a.sl2 : -INFINITY;
                     }
-                raise_ref(x);
+                raise_ref([&](int nb, int r) { return fmaxf(x[nb][r], x[nb][r + 2]); });
                 uint32_t b0[NB][2], b1[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++) {
                     float e[4];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) e[i] = ex2(x[nb][i] - fmaxf(m[nb][i & 1], -3e38f));
+                    for (int i = 0; i < 4; i++) e[i] = ex2(x[nb][i] - m[nb][i & 1]);
                     l[nb][0] += e[0] + e[2];
                     l[nb][1] += e[1] + e[3];
 #pragma unroll
@@ -694,9 +744,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                     l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], 8);
                     l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], 16);
                 }
-            const bool whole = run.t0 == 0 && run.t1 == run.nt;
-            float* part = a.part + ((size_t)team * 2 + (run.t0 == 0 ? 1 : 0)) * part_floats(R, D);
-            if (run.t0 == 0 && !whole) rec = MergeRec{run.b, run.item, run.nt - run.t1};
+            const bool whole = run.u0 == 0 && run.u1 == run.nu;
+            float* part = a.part + ((size_t)team * 2 + (run.u0 == 0 ? 1 : 0)) * part_floats(R, D);
+            if (run.u0 == 0 && !whole && writes_rec) *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, starts[TW == 1 ? warp : 0].total};
             // channel c (of DV, from DV g) of row 2t + r
             auto chan = [&](int nb, int r, int c) -> float {
                 const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
@@ -753,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                         ml[w] = *(const float2*)(mg + ((size_t)w * R + lr) * (D + 4) + D);
                         mx = fmaxf(mx, ml[w].x);
                     }
-                    const float mu = fmaxf(mx, -3e38f);
+                    const float mu = fmaxf(mx, kNoRef);
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
 #pragma unroll
@@ -775,8 +825,6 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
             }
         } while (run.next(a));
     }
-    MergeRec* recs = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
-    if (a.part && (TW == 1 ? lane == 0 : threadIdx.x == 0) && team < a.nteams) recs[team] = rec;
 }
 
 // ------------------------------------------------------------------- merge ---
@@ -790,54 +838,42 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
 {
     pdl_wait();
     pdl_trigger();
+    // one warp per team and 128 floats of the item's rows
+    const int chunks = ceil_div(min(R, a.rows) * D, 128), w = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int i0 = w / chunks;
+    if (i0 >= a.nteams) return;
     const MergeRec* recs = (const MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
-    const MergeRec rec = recs[blockIdx.x];
+    const MergeRec rec = recs[i0];
     if (rec.rest == 0) return;
-    __shared__ long long red[8];
-    const int items = a.Hkv * a.mtiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long mine = 0;
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) mine += (long long)items * item_tiles(a, seq_len(a, b));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) red[warp] = mine;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < 8; w++) total += red[w];
-    const int i0 = blockIdx.x;
+    const long long total = rec.total;
     const long long end = total * (i0 + 1) / a.nteams + rec.rest;  // where the item ends
     int last = i0 + 1;  // teams i0 .. last hold a part
     while (total * (last + 1) / a.nteams < end) last++;
     const int head = rec.item / a.mtiles, mt = rec.item % a.mtiles, group = a.H / a.Hkv;
-    for (int e = threadIdx.x; e < R * D / 4; e += blockDim.x) {
-        const int lr = e / (D / 4), c = (e % (D / 4)) * 4, gr = mt * R + lr;
-        if (gr >= a.rows) continue;
-        float mx = -INFINITY, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = i0; i <= last; i++) {
-            if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;  // a team without tiles
-            const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
-            mx = fmaxf(mx, part[(size_t)R * D + 2 * lr]);
-        }
-        const float mu = fmaxf(mx, -3e38f);
-        for (int i = i0; i <= last; i++) {
-            if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;
-            const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
-            const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
-            const float4 v = *(const float4*)(part + (size_t)lr * D + c);
-            const float f = ex2(ml.x - mu);
-            sum += f * ml.y;
-            acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-        }
-        const float inv = 1.f / sum;
-        *(uint2*)(a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    const int at = (w % chunks) * 128 + (threadIdx.x & 31) * 4, lr = at / D, c = at % D, gr = mt * R + lr;
+    if (lr >= R || gr >= a.rows) return;
+    // running join in team order
+    float mx = kNoRef, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = i0; i <= last; i++) {
+        if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;  // a team without units
+        const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
+        const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
+        const float4 v = *(const float4*)(part + (size_t)lr * D + c);
+        const float top = fmaxf(mx, ml.x), f = ex2(mx - top), h = ex2(ml.x - top);
+        mx = top;
+        sum = sum * f + ml.y * h;
+        acc.x = acc.x * f + v.x * h, acc.y = acc.y * f + v.y * h, acc.z = acc.z * f + v.z * h, acc.w = acc.w * f + v.w * h;
     }
+    const float inv = 1.f / sum;
+    *(uint2*)(a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // ---------------------------------------------------------------- launches ---
 
 struct Plan {
-    int nb, tw, grid, nteams, mtiles;
+    int nb, tw, grid, nteams, mtiles, extra;
     bool merge;
     size_t bytes;
 };
@@ -855,12 +891,15 @@ Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
     p.nb = rows <= 8 ? 1 : 2;
     p.mtiles = ceil_div(rows, 8 * p.nb);
     const long long items = (long long)a.batch * c.n_kv_heads * p.mtiles;
-    const long long tiles = items * ((max_len_of(c, a) + 15) / 16 + (T + 15) / 16);
+    const long long tiles = items * ((max_len_of(c, a) + kKeys - 1) / kKeys + (T + 15) / 16);  // at most
     const int ctas = p.nb == 1 ? 2 * kSMs : kSMs;  // resident at once
     p.tw = items >= (long long)ctas * kWarps ? 1 : kWarps;
+    // an item's queries and result take as long as so many tiles (32 keys); without them the teams
+    // that get many short sequences finish last.  128 greedy 7B sequences: 86 us at 0, 66 at 4, 71 at 8;
+    // CTA teams on 16 long 34B sequences of 1 to 64 K: 124 us at 0, 117 at 21, 118 at 42
+    p.extra = p.tw == 1 ? 4 : 18;
     const long long teams = (long long)ctas * (p.tw == 1 ? kWarps : 1);
     p.nteams = (int)std::max(1LL, std::min(teams, std::max(items, tiles / kWarps)));
-    if (p.nteams > items && p.nteams < 2 * items) p.nteams = (int)items;
     p.grid = p.tw == 1 ? ceil_div(p.nteams, kWarps) : p.nteams;
     // one sequence: every item has the same tiles, so whole items a team stay whole
     p.merge = !(a.batch == 1 && items % p.nteams == 0);
@@ -899,7 +938,10 @@ cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
     cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, NB, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, 1>::kBytes, s, k)
                               : launch_pdl(k_kv4_rows<D, NB, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, kWarps>::kBytes, s, k);
-    if (e == cudaSuccess && p.merge) e = launch_pdl(k_kv4_merge<D, 8 * NB>, dim3(p.nteams), dim3(256), 0, s, k);
+    if (e == cudaSuccess && p.merge) {
+        const int chunks = ceil_div(std::min(8 * NB, k.rows) * D, 128);
+        e = launch_pdl(k_kv4_merge<D, 8 * NB>, dim3(ceil_div(p.nteams * chunks, 8)), dim3(256), 0, s, k);
+    }
     return e;
 }
 
@@ -922,7 +964,7 @@ int launch_kv4_attn(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a)
     k.q_ld = a.q_ld, k.kv_ld = a.kv_ld;
     k.n_pages = c.n_pages, k.max_pages = c.max_pages, k.max_len = max_len_of(c, a);
     k.blk_log2 = c.page == 16 ? 0 : c.page == 32 ? 1 : c.page == 64 ? 2 : 3;
-    k.rows = k.T * (a.n_heads / c.n_kv_heads), k.mtiles = p.mtiles, k.nteams = p.nteams;
+    k.rows = k.T * (a.n_heads / c.n_kv_heads), k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = p.extra;
     k.sl2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     const cudaError_t e = c.head_dim == 128 ? (p.nb == 1 ? go<128, 1>(s, p, k) : go<128, 2>(s, p, k))
                                             : (p.nb == 1 ? go<64, 1>(s, p, k) : go<64, 2>(s, p, k));
