@@ -42,20 +42,14 @@
 #include <cmath>
 #include <mutex>
 
-#include <cuda_fp16.h>
-
-#include "kv4.cuh"
+#include "kv4_sched.cuh"
 
 namespace la {
 
 namespace {
 
-using namespace ptx;
-
 constexpr int kWarps = 7;  // and one that fills their rings: 8 warps leave 128 registers each at two CTAs per SM
-constexpr int kSMs = 152;
-constexpr int kKeys = 32;  // a tile: two blocks, for independent instructions and one vote per 32 keys
-constexpr float kNoRef = -3e38f;  // below every score: exp2(-inf - kNoRef) = 0
+constexpr int kKeysLog2 = 5, kKeys = 1 << kKeysLog2;  // a tile: two blocks, for independent instructions and one vote per 32 keys
 
 // The key of a tile held in row i of a score fragment (and in slot i of the
 // probabilities): with these, the four keys whose V a lane reads at once lie
@@ -65,15 +59,6 @@ __device__ __forceinline__ int kv4_key(int i)
 {
     const int h = (i >> 1) & 3;
     return (i & 8) + ((i & 1) ? 4 + (h ^ 3) : h);
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
-        : "memory");
 }
 
 #define LA_MMA16816(name, type)                                                                                        \
@@ -96,18 +81,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -126,115 +99,7 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& u)
     return lo || hi;
 }
 
-constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;  // a pair of codes: c 2^-24, c 2^-20
 constexpr float kMinScale = 0x1p-92f;  // V scales below it count as it (values under 2^-88)
-
-// ------------------------------------------------------------ the schedule ---
-
-__device__ __forceinline__ int seq_len(const Kv4Attn& a, int b)
-{
-    const int len = a.lens[b];
-    return len > a.max_len ? -1 : len;  // too long: raised by k_kv4_rows, left alone everywhere
-}
-
-// An item's work in units of a tile: `extra` units for its queries and its
-// result, its cached tiles, its step rows' tiles.
-__device__ __forceinline__ int item_units(const Kv4Attn& a, int len)
-{
-    return len < 0 ? 0 : a.extra + (len + kKeys - 1) / kKeys + (a.T + 15) / 16;
-}
-
-struct Start {
-    int b;
-    long long off, count;  // offset in the units of sequence b's items; units of the team
-    long long total;       // units of all items
-};
-
-// Where each of the CTA's teams begins: teams t0 .. t0 + n - 1 of a.nteams
-// take equal runs of all items' units in (sequence, item) order.
-__device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long long* scratch)
-{
-    const int items = a.Hkv * a.mtiles, per = ceil_div(a.B, (int)blockDim.x), b0 = threadIdx.x * per;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    long long mine = 0;
-    for (int b = b0; b < min(b0 + per, a.B); b++) mine += (long long)items * item_units(a, seq_len(a, b));
-    if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    long long before = x - mine, total = 0;
-    for (int w = 0; w < nw; w++) {
-        if (w < warp) before += scratch[w];
-        total += scratch[w];
-    }
-    if (mine) {
-        for (int i = 0; i < n; i++) {
-            const long long u0 = total * (t0 + i) / a.nteams, u1 = total * (t0 + i + 1) / a.nteams;
-            if (u0 >= u1 || u0 < before || u0 >= before + mine) continue;
-            long long at = before;
-            for (int b = b0; b < min(b0 + per, a.B); b++) {
-                const long long c = (long long)items * item_units(a, seq_len(a, b));
-                if (u0 < at + c) {
-                    starts[i] = Start{b, u0 - at, u1 - u0, total};
-                    break;
-                }
-                at += c;
-            }
-        }
-    }
-    __syncthreads();
-}
-
-// The run of units of one item that a team works on, and its tiles t0 .. t1 - 1.
-struct Run {
-    int b, item, len, nu, u0, u1, t0, t1;
-    long long left;
-    __device__ __forceinline__ void cut(const Kv4Attn& a, int from)
-    {
-        u0 = from;
-        u1 = (int)min((long long)nu, u0 + left);
-        left -= u1 - u0;
-        t0 = max(u0 - a.extra, 0);
-        t1 = max(u1 - a.extra, 0);
-    }
-    __device__ __forceinline__ void begin(const Kv4Attn& a, const Start& s)
-    {
-        left = s.count;
-        b = s.b;
-        len = seq_len(a, b);
-        nu = item_units(a, len);
-        item = (int)(s.off / nu);
-        cut(a, (int)(s.off - (long long)item * nu));
-    }
-    __device__ __forceinline__ bool next(const Kv4Attn& a)
-    {
-        if (left <= 0) return false;
-        if (++item == a.Hkv * a.mtiles) {
-            item = 0;
-            do {
-                if (++b >= a.B) return false;  // only if the lengths change under the call
-                len = seq_len(a, b);
-                nu = item_units(a, len);
-            } while (nu == 0);
-        }
-        cut(a, 0);
-        return true;
-    }
-};
-
-// Items that several teams hold, one record per team, filled by the team that
-// holds the item's first tile.
-struct MergeRec {
-    int b, item, rest, pad;  // rest: the item's units that other teams hold (0: none begins here)
-    long long total;         // units of all items
-};
-
-__host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
 
 // ------------------------------------------------------------------ kernel ---
 
@@ -355,9 +220,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
     }
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.B; b += blockDim.x)
-            if (a.lens[b] > a.max_len) kv4_raise(a.status, LA_ERR_ARG);
+    if (blockIdx.x == 0) raise_long(a);
     // (its barriers also publish the mbarriers)
     find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, (long long*)(starts + kWarps));
     if (warp == kWarps) {
@@ -833,14 +696,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
 // slot and the first slots of the teams after it, until the item's tiles are
 // all accounted for.  Weights exp2(m - M) of the parts in team order.
 
+constexpr int kMergeChunks = 4;
+
 template <int D, int R>
 __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
 {
     pdl_wait();
     pdl_trigger();
-    // one warp per team and 128 floats of the item's rows
-    const int chunks = ceil_div(min(R, a.rows) * D, 128), w = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int i0 = w / chunks;
+    // one warp per team and kMergeChunks x 128 floats of the item's rows
+    const int chunks = ceil_div(min(R, a.rows) * D, 128), groups = ceil_div(chunks, kMergeChunks);
+    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), i0 = w / groups;
     if (i0 >= a.nteams) return;
     const MergeRec* recs = (const MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
     const MergeRec rec = recs[i0];
@@ -850,24 +715,28 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
     int last = i0 + 1;  // teams i0 .. last hold a part
     while (total * (last + 1) / a.nteams < end) last++;
     const int head = rec.item / a.mtiles, mt = rec.item % a.mtiles, group = a.H / a.Hkv;
-    const int at = (w % chunks) * 128 + (threadIdx.x & 31) * 4, lr = at / D, c = at % D, gr = mt * R + lr;
-    if (lr >= R || gr >= a.rows) return;
-    // running join in team order
-    float mx = kNoRef, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = i0; i <= last; i++) {
-        if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;  // a team without units
-        const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
-        const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
-        const float4 v = *(const float4*)(part + (size_t)lr * D + c);
-        const float top = fmaxf(mx, ml.x), f = ex2(mx - top), h = ex2(ml.x - top);
-        mx = top;
-        sum = sum * f + ml.y * h;
-        acc.x = acc.x * f + v.x * h, acc.y = acc.y * f + v.y * h, acc.z = acc.z * f + v.z * h, acc.w = acc.w * f + v.w * h;
+    const int c0 = (w % groups) * kMergeChunks;
+#pragma unroll
+    for (int ch = 0; ch < kMergeChunks; ch++) {
+        const int at = (c0 + ch) * 128 + (threadIdx.x & 31) * 4, lr = at / D, c = at % D, gr = mt * R + lr;
+        if (lr >= R || gr >= a.rows) return;
+        // running join in team order
+        float mx = kNoRef, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = i0; i <= last; i++) {
+            if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;  // a team without units
+            const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
+            const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
+            const float4 v = *(const float4*)(part + (size_t)lr * D + c);
+            const float top = fmaxf(mx, ml.x), f = ex2(mx - top), h = ex2(ml.x - top);
+            mx = top;
+            sum = sum * f + ml.y * h;
+            acc.x = acc.x * f + v.x * h, acc.y = acc.y * f + v.y * h, acc.z = acc.z * f + v.z * h, acc.w = acc.w * f + v.w * h;
+        }
+        const float inv = 1.f / sum;
+        *(uint2*)(a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
-    const float inv = 1.f / sum;
-    *(uint2*)(a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // ---------------------------------------------------------------- launches ---
@@ -926,7 +795,7 @@ int attn_ready()
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
         if (!(set_smem<128, 1, 1>() && set_smem<128, 1, kWarps>() && set_smem<128, 2, 1>() && set_smem<128, 2, kWarps>() &&
-              set_smem<64, 1, 1>() && set_smem<64, 1, kWarps>() && set_smem<64, 2, 1>() && set_smem<64, 2, kWarps>()))
+              set_smem<64, 1, 1>() && set_smem<64, 1, kWarps>() && set_smem<64, 2, 1>() && set_smem<64, 2, kWarps>() && kv4_tc_init()))
             return LA_ERR_CUDA;
         g_ready[dev] = 1;
     }
@@ -938,34 +807,57 @@ cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
     cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, NB, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, 1>::kBytes, s, k)
                               : launch_pdl(k_kv4_rows<D, NB, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, kWarps>::kBytes, s, k);
-    if (e == cudaSuccess && p.merge) {
-        const int chunks = ceil_div(std::min(8 * NB, k.rows) * D, 128);
-        e = launch_pdl(k_kv4_merge<D, 8 * NB>, dim3(ceil_div(p.nteams * chunks, 8)), dim3(256), 0, s, k);
-    }
+    if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, D, 8 * NB);
     return e;
 }
 
 }  // namespace
 
-size_t kv4_attn_bytes(const la_kv4_desc& c, const la_kv4_attn& a) { return a.batch ? plan_of(c, a).bytes : 0; }
+cudaError_t launch_kv4_merge(cudaStream_t s, const Kv4Attn& k, int D, int R)
+{
+    const int chunks = ceil_div(std::min(R, k.rows) * D, 128), groups = ceil_div(chunks, kMergeChunks);
+    auto kern = D == 128 ? (R == 8 ? k_kv4_merge<128, 8> : R == 16 ? k_kv4_merge<128, 16> : k_kv4_merge<128, 128>)
+                         : (R == 8 ? k_kv4_merge<64, 8> : R == 16 ? k_kv4_merge<64, 16> : k_kv4_merge<64, 128>);
+    return launch_pdl(kern, dim3(ceil_div(k.nteams * groups, 8)), dim3(256), 0, s, k);
+}
+
+namespace {
+
+// Rows of one KV head: up to 8 fill the narrow side of mma.sync; more go to
+// the 128-row tiles of tcgen05.
+bool many_rows(const la_kv4_desc& c, const la_kv4_attn& a)
+{
+    return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > 16;
+}
+
+}  // namespace
+
+size_t kv4_attn_bytes(const la_kv4_desc& c, const la_kv4_attn& a)
+{
+    if (!a.batch) return 0;
+    return many_rows(c, a) ? kv4_tc_bytes(c, a) : plan_of(c, a).bytes;
+}
 
 int launch_kv4_attn(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a)
 {
     if (int rc = attn_ready()) return rc;
-    const Plan p = plan_of(c, a);
     Kv4Attn k;
     k.pages = (const uint8_t*)c.pages;
     k.q = (const __nv_bfloat16*)a.q, k.ks = (const __nv_bfloat16*)a.k_step, k.vs = (const __nv_bfloat16*)a.v_step;
     k.out = (__nv_bfloat16*)a.out;
     k.lens = a.lens, k.table = a.table, k.status = c.status;
-    k.part = p.merge ? (float*)a.workspace : nullptr;
     k.B = a.batch, k.H = a.n_heads, k.Hkv = c.n_kv_heads;
     k.W = a.W, k.n1 = a.N - 1, k.T = 1 + (a.W + a.G) * k.n1;
     k.q_ld = a.q_ld, k.kv_ld = a.kv_ld;
     k.n_pages = c.n_pages, k.max_pages = c.max_pages, k.max_len = max_len_of(c, a);
     k.blk_log2 = c.page == 16 ? 0 : c.page == 32 ? 1 : c.page == 64 ? 2 : 3;
-    k.rows = k.T * (a.n_heads / c.n_kv_heads), k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = p.extra;
+    k.rows = k.T * (a.n_heads / c.n_kv_heads);
     k.sl2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
+    if (many_rows(c, a)) return launch_kv4_tc(s, c, a, k);
+    const Plan p = plan_of(c, a);
+    k.part = p.merge ? (float*)a.workspace : nullptr;
+    k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = p.extra;
+    k.tile_log2 = kKeysLog2, k.step_tiles = (k.T + 15) / 16;
     const cudaError_t e = c.head_dim == 128 ? (p.nb == 1 ? go<128, 1>(s, p, k) : go<128, 2>(s, p, k))
                                             : (p.nb == 1 ? go<64, 1>(s, p, k) : go<64, 2>(s, p, k));
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;

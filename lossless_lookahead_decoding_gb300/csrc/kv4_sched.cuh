@@ -1,0 +1,163 @@
+// kv4_sched.cuh -- how the attention kernels over the 4-bit cache share their
+// work: items (sequence, KV head, row tile) are laid end to end in units of a
+// tile and cut into equal runs, one per team; and small helpers of both.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+
+namespace la {
+namespace {
+
+using namespace ptx;
+
+constexpr int kSMs = 152;
+constexpr float kNoRef = -3e38f;  // below every score: exp2(-inf - kNoRef) = 0
+constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;  // a pair of codes as fp16: c 2^-24, c 2^-20
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// ------------------------------------------------------------ the schedule ---
+
+__device__ __forceinline__ int seq_len(const Kv4Attn& a, int b)
+{
+    const int len = a.lens[b];
+    return len > a.max_len ? -1 : len;  // too long: raised by raise_long(), left alone everywhere
+}
+
+// An item's work in units of a tile: `extra` units for its queries and its
+// result, its cached tiles, its step rows' tiles.
+__device__ __forceinline__ int item_units(const Kv4Attn& a, int len)
+{
+    return len < 0 ? 0 : a.extra + ((len + (1 << a.tile_log2) - 1) >> a.tile_log2) + a.step_tiles;
+}
+
+// Sequences whose length is over its bound (one CTA calls it).
+__device__ __forceinline__ void raise_long(const Kv4Attn& a)
+{
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+        if (a.lens[b] > a.max_len) kv4_raise(a.status, LA_ERR_ARG);
+}
+
+struct Start {
+    int b;
+    long long off, count;  // offset in the units of sequence b's items; units of the team
+    long long total;       // units of all items
+};
+
+// Where each of the CTA's teams begins: teams t0 .. t0 + n - 1 of a.nteams
+// take equal runs of all items' units in (sequence, item) order.
+__device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long long* scratch)
+{
+    const int items = a.Hkv * a.mtiles, per = ceil_div(a.B, (int)blockDim.x), b0 = threadIdx.x * per;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    long long mine = 0;
+    for (int b = b0; b < min(b0 + per, a.B); b++) mine += (long long)items * item_units(a, seq_len(a, b));
+    if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+    for (int w = 0; w < nw; w++) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    if (mine) {
+        for (int i = 0; i < n; i++) {
+            const long long u0 = total * (t0 + i) / a.nteams, u1 = total * (t0 + i + 1) / a.nteams;
+            if (u0 >= u1 || u0 < before || u0 >= before + mine) continue;
+            long long at = before;
+            for (int b = b0; b < min(b0 + per, a.B); b++) {
+                const long long c = (long long)items * item_units(a, seq_len(a, b));
+                if (u0 < at + c) {
+                    starts[i] = Start{b, u0 - at, u1 - u0, total};
+                    break;
+                }
+                at += c;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The run of units of one item that a team works on, and its tiles t0 .. t1 - 1.
+struct Run {
+    int b, item, len, nu, u0, u1, t0, t1;
+    long long left;
+    __device__ __forceinline__ void cut(const Kv4Attn& a, int from)
+    {
+        u0 = from;
+        u1 = (int)min((long long)nu, u0 + left);
+        left -= u1 - u0;
+        t0 = max(u0 - a.extra, 0);
+        t1 = max(u1 - a.extra, 0);
+    }
+    __device__ __forceinline__ void begin(const Kv4Attn& a, const Start& s)
+    {
+        left = s.count;
+        b = s.b;
+        len = seq_len(a, b);
+        nu = item_units(a, len);
+        item = (int)(s.off / nu);
+        cut(a, (int)(s.off - (long long)item * nu));
+    }
+    __device__ __forceinline__ bool next(const Kv4Attn& a)
+    {
+        if (left <= 0) return false;
+        if (++item == a.Hkv * a.mtiles) {
+            item = 0;
+            do {
+                if (++b >= a.B) return false;  // only if the lengths change under the call
+                len = seq_len(a, b);
+                nu = item_units(a, len);
+            } while (nu == 0);
+        }
+        cut(a, 0);
+        return true;
+    }
+};
+
+// Items that several teams hold, one record per team, filled by the team that
+// holds the item's first tile.
+struct MergeRec {
+    int b, item, rest, pad;  // rest: the item's units that other teams hold (0: none begins here)
+    long long total;         // units of all items
+};
+
+__host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
+
+}  // namespace
+
+// Joins the parts of split items (kv4_attn.cu); R: rows of an item's tile.
+cudaError_t launch_kv4_merge(cudaStream_t s, const Kv4Attn& k, int D, int R);
+
+// The kernel for many rows per KV head (kv4_attn_tc.cu).
+size_t kv4_tc_bytes(const la_kv4_desc& c, const la_kv4_attn& a);
+bool kv4_tc_init();
+int launch_kv4_tc(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a, Kv4Attn k);
+
+}  // namespace la
