@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 #include "kv4_sched.cuh"
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                 }
             const bool whole = run.u0 == 0 && run.u1 == run.nu;
             float* part = a.part + ((size_t)team * 2 + (run.u0 == 0 ? 1 : 0)) * part_floats(R, D);
-            if (run.u0 == 0 && !whole && writes_rec) *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, starts[TW == 1 ? warp : 0].total};
+            if (run.u0 == 0 && !whole && writes_rec) *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, starts[TW == 1 ? warp : 0].sh};
             // channel c (of DV, from DV g) of row 2t + r
             auto chan = [&](int nb, int r, int c) -> float {
                 const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
@@ -703,29 +704,56 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
 {
     pdl_wait();
     pdl_trigger();
-    // one warp per team and kMergeChunks x 128 floats of the item's rows
-    const int chunks = ceil_div(min(R, a.rows) * D, 128), groups = ceil_div(chunks, kMergeChunks);
-    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), i0 = w / groups;
+    // one warp per team and 128 floats of the item's rows (R <= 16: of 4 kMergeChunks channels),
+    // or 32 rows x 8 channels (R = 128)
+    constexpr bool kCols = R == 128;
+    const int rows = min(R, a.rows);
+    const int groups = kCols ? (rows + 31) / 32 * (D / 8) : ceil_div(ceil_div(rows * D, 128), kMergeChunks);
+    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), i0 = w / groups, lane = threadIdx.x & 31;
     if (i0 >= a.nteams) return;
     const MergeRec* recs = (const MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
     const MergeRec rec = recs[i0];
     if (rec.rest == 0) return;
-    const long long total = rec.total;
-    const long long end = total * (i0 + 1) / a.nteams + rec.rest;  // where the item ends
-    int last = i0 + 1;  // teams i0 .. last hold a part
-    while (total * (last + 1) / a.nteams < end) last++;
+    const Shares sh = rec.sh;
+    const long long end = sh.at(i0 + 1) + rec.rest;  // where the item ends
     const int head = rec.item / a.mtiles, mt = rec.item % a.mtiles, group = a.H / a.Hkv;
+    auto out_at = [&](int gr, int c) {
+        return a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c;
+    };
+    // the parts: team i0's second one, then the first ones of the teams after it up to the item's end
+    auto part_of = [&](int i) { return a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D); };
+    if (kCols) {
+        const int g = w % groups, lr = g / (D / 8) * 32 + lane, c = g % (D / 8) * 8, gr = mt * R + lr;
+        if (gr >= a.rows) return;
+        float mx = kNoRef, sum = 0.f, acc[8] = {};
+        for (int i = i0; i == i0 || sh.at(i) < end; i++) {
+            if (sh.at(i) == sh.at(i + 1)) continue;  // a team without units
+            const float* part = part_of(i);
+            const float m = part[(size_t)R * D + lr], l = part[(size_t)R * D + R + lr];
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) v[k] = part[(size_t)(c + k) * R + lr];
+            const float top = fmaxf(mx, m), f = ex2(mx - top), h = ex2(m - top);
+            mx = top;
+            sum = sum * f + l * h;
+#pragma unroll
+            for (int k = 0; k < 8; k++) acc[k] = acc[k] * f + v[k] * h;
+        }
+        const float inv = 1.f / sum;
+        *(uint4*)out_at(gr, c) = make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                                            pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+        return;
+    }
     const int c0 = (w % groups) * kMergeChunks;
 #pragma unroll
     for (int ch = 0; ch < kMergeChunks; ch++) {
-        const int at = (c0 + ch) * 128 + (threadIdx.x & 31) * 4, lr = at / D, c = at % D, gr = mt * R + lr;
+        const int at = (c0 + ch) * 128 + lane * 4, lr = at / D, c = at % D, gr = mt * R + lr;
         if (lr >= R || gr >= a.rows) return;
-        // running join in team order
         float mx = kNoRef, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = i0; i <= last; i++) {
-            if (total * i / a.nteams == total * (i + 1) / a.nteams) continue;  // a team without units
-            const float* part = a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D);
+        for (int i = i0; i == i0 || sh.at(i) < end; i++) {
+            if (sh.at(i) == sh.at(i + 1)) continue;
+            const float* part = part_of(i);
             const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
             const float4 v = *(const float4*)(part + (size_t)lr * D + c);
             const float top = fmaxf(mx, ml.x), f = ex2(mx - top), h = ex2(ml.x - top);
@@ -734,8 +762,7 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
             acc.x = acc.x * f + v.x * h, acc.y = acc.y * f + v.y * h, acc.z = acc.z * f + v.z * h, acc.w = acc.w * f + v.w * h;
         }
         const float inv = 1.f / sum;
-        *(uint2*)(a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        *(uint2*)out_at(gr, c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
 }
 
@@ -815,7 +842,8 @@ cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 
 cudaError_t launch_kv4_merge(cudaStream_t s, const Kv4Attn& k, int D, int R)
 {
-    const int chunks = ceil_div(std::min(R, k.rows) * D, 128), groups = ceil_div(chunks, kMergeChunks);
+    const int rows = std::min(R, k.rows);
+    const int groups = R == 128 ? (rows + 31) / 32 * (D / 8) : ceil_div(ceil_div(rows * D, 128), kMergeChunks);
     auto kern = D == 128 ? (R == 8 ? k_kv4_merge<128, 8> : R == 16 ? k_kv4_merge<128, 16> : k_kv4_merge<128, 128>)
                          : (R == 8 ? k_kv4_merge<64, 8> : R == 16 ? k_kv4_merge<64, 16> : k_kv4_merge<64, 128>);
     return launch_pdl(kern, dim3(ceil_div(k.nteams * groups, 8)), dim3(256), 0, s, k);
@@ -827,7 +855,7 @@ namespace {
 // the 128-row tiles of tcgen05.
 bool many_rows(const la_kv4_desc& c, const la_kv4_attn& a)
 {
-    return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > 16;
+    return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > (getenv("KV_T") ? atoi(getenv("KV_T")) : 16);
 }
 
 }  // namespace

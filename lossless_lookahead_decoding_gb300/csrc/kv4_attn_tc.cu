@@ -19,11 +19,19 @@
 // for V, into the running reference M, which moves only when a p V unit
 // exceeds 2^8.
 //
-// Tensor bound for full row tiles (128 x 128 x D x 2 products a tile, 1024
-// cycles at D = 128), HBM and unpacking bound for few rows.  All roles run at
-// once on neighbouring tiles, one CTA per SM: warps 0-7 softmax (a row per
-// thread and half of the columns), 8-15 unpack, 16 issues the MMAs, 17 copies
-// code blocks ahead.  S, K and V are double buffered, codes triple.
+// Tensor and exponential bound for full row tiles (128 x 128 x D x 2 products
+// and 128 x 128 exponentials a tile: about 1024 cycles each at D = 128), HBM and
+// unpacking bound for few rows.  All roles run at once on neighbouring tiles,
+// one CTA per SM: warps 0-7 softmax (a row per thread; warps 0-3 the even
+// tiles, 4-7 the odd ones, so that one group's exponentials run while the
+// other waits), 8-11 unpack K, 12-15 V, 16 issues the MMAs, 17 copies code
+// blocks ahead and finds the tiles' powers of two.  S, P, K and V are double
+// buffered, codes triple.
+//
+// Two ways to share an item's tiles: equal runs of all items' units over the
+// SMs, parts joined by k_kv4_merge (ragged batches); or a cluster of CTAs per
+// item that join their outputs through distributed shared memory (few items:
+// one launch, no workspace).
 #include <algorithm>
 #include <cmath>
 
@@ -43,13 +51,33 @@ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
     return idesc_bf16(M, N, b_mn) & ~((1u << 7) | (1u << 10));  // A and B in fp16
 }
 
-// D += A B with A (fp16 pairs, K along the columns) in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+// The MMAs of one product of a tile, by one elected lane.  The operands'
+// descriptors advance by constants; the warp keeps everything uniform, so that
+// nothing but an add goes before each instruction (issued by a single lane's
+// code path with addresses of its own, an MMA cost 165 cycles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// D += A B, A and B in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-            d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc));
+}
+
+// D += A B with A (fp16 pairs, K along the columns) in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc));
 }
 
 // 16 columns of this thread's lane of tensor memory.
@@ -61,7 +89,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
                  "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_try_wait that may sleep up to 0.1 ms: a dozen warps that poll take the
+// issue slots of those that work.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 
 __device__ __forceinline__ float pow2i(int e)  // 2^e, e in -126 .. 127
 {
@@ -71,8 +135,8 @@ __device__ __forceinline__ float pow2i(int e)  // 2^e, e in -126 .. 127
 // x 2^e for any e that two such factors reach
 __device__ __forceinline__ float scale2(float x, int e) { return x * pow2i(e >> 1) * pow2i(e - (e >> 1)); }
 
-// What the softmax needs to know of a tile; four in turn (a tile's entry is
-// written again four tiles later, when its softmax is long done).
+// What the softmax needs to know of a tile; eight in turn (an entry is written
+// again when the softmax of the tile five after it is done).
 struct TileInfo {
     int live, bad;        // keys, and a bit per block of 16 whose page is not in the pool
     int ek, ev;           // powers of two of K and V
@@ -88,16 +152,19 @@ struct TcSmem {
     static constexpr int kStage = 8 * kv4_block_bytes(D);
     static constexpr int kVis = kCodes + kRing * kStage;      // [step row][4]: step rows it sees
     static constexpr int kRowF = kVis + 128 * 16;             // [2 runs] per row: what undoes q's power of two
-    static constexpr int kRed = kRowF + 2 * 128 * 4;              // [2 tiles][2 halves][128 rows]
-    static constexpr int kInfo = kRed + 4 * 128 * 4;          // TileInfo[4]
-    static constexpr int kBar = kInfo + 4 * (int)sizeof(TileInfo);
+    static constexpr int kRowM = kRowF + 2 * 128 * 4;         // per row: the reference M
+    static constexpr int kRowL = kRowM + 128 * 4;             // [2 groups] per row: sums
+    static constexpr int kInfo = kRowL + 2 * 128 * 4;         // TileInfo[8]
+    static constexpr int kBar = kInfo + 8 * (int)sizeof(TileInfo);
     static constexpr int kMisc = kBar + 32 * 8;               // ring info, reduction words, start, scan scratch
     static constexpr int kBytes = kMisc + 512 + 1024;         // 1024: to align the base
 };
 
 enum {  // barriers
-    kFull = 0, kEmpty = 3, kKReady = 6, kVReady = 8, kSDone = 10, kODone = 12, kPReady = 14, kQReady = 16, kOFree = 17, kEnd = 18
+    kFull = 0, kEmpty = 3, kInfoReady = 6, kKReady = 9, kVReady = 11, kSDone = 13, kODone = 15, kPReady = 17, kQReady = 19,
+    kOFree = 20, kEnd = 21
 };
+constexpr uint32_t kColO = 256, kColP = 384;  // tensor memory: S [2][128], O [D], P [2][64]
 
 // 8 codes of a word as fp16 (c - z) s 2^-E: pairs 0, 2 by lo, 1, 3 by hi.
 __device__ __forceinline__ uint4 unpack8(uint32_t w, __half2 lo, __half2 hi, __half2 off)
@@ -110,7 +177,66 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, __half2 lo, __half2 hi, __h
     return make_uint4(one(w & kLo, lo), one(w & kHi, hi), one(h & kLo, lo), one(h & kHi, hi));
 }
 
-template <int D>
+// Adds what is not finite among the values of the step rows (bits of odd and see
+// both set) to 32 channels from col.
+__device__ __noinline__ void add_odd_to(const Kv4Attn& a, const uint32_t* odd, const uint32_t* see, int b, int col, float* o)
+{
+    for (int key = 0; key < a.T; key++) {
+        if (!(((odd[key >> 5] & see[key >> 5]) >> (key & 31)) & 1)) continue;
+        const __nv_bfloat16* v = a.vs + (size_t)(b * (long long)a.T + key) * a.kv_ld + col;
+        for (int i = 0; i < 32; i++) {
+            const float x = __bfloat162float(v[i]);
+            if (!(fabsf(x) < INFINITY)) o[i] += x;
+        }
+    }
+}
+
+__device__ __forceinline__ void add_odd(const Kv4Attn& a, const uint32_t* odd, const uint32_t* see, int b, int col, float (&o)[32])
+{
+    float t[32];  // (in memory for the call; o stays in registers)
+#pragma unroll
+    for (int i = 0; i < 32; i++) t[i] = o[i];
+    add_odd_to(a, odd, see, b, col, t);
+#pragma unroll
+    for (int i = 0; i < 32; i++) o[i] = t[i];
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+// the address of p in the shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// CL: one item per cluster; its CTAs take equal runs of the item's tiles.
+template <int D, bool CL>
 __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 {
     using L = TcSmem<D>;
@@ -119,9 +245,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     uint64_t* bar = (uint64_t*)(sm + L::kBar);
     TileInfo* info = (TileInfo*)(sm + L::kInfo);
     uint32_t* vis = (uint32_t*)(sm + L::kVis);
-    float* rowf = (float*)(sm + L::kRowF);
+    float *rowf = (float*)(sm + L::kRowF), *row_m = (float*)(sm + L::kRowM), *row_l = (float*)(sm + L::kRowL);
     int* ring_info = (int*)(sm + L::kMisc);                // [3]: live | bad << 16
-    uint32_t* red_e = (uint32_t*)(sm + L::kMisc + 16);     // [2][8]: largest exponents of the unpacking warps
+    uint32_t* red_e = (uint32_t*)(sm + L::kMisc + 16);     // [2][4]: largest exponents of the unpacking warps
     uint32_t* tmem_slot = (uint32_t*)(sm + L::kMisc + 80);
     volatile int* abort_flag = (volatile int*)(sm + L::kMisc + 84);
     Start* start = (Start*)(sm + L::kMisc + 96);
@@ -129,14 +255,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.H / a.Hkv;
 
+    if (warp == 16) tmem_alloc(tmem_slot, 512);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; i++) mbar_init(bar + kFull + i, 1), mbar_init(bar + kEmpty + i, 8);
+        for (int i = 0; i < 3; i++) mbar_init(bar + kFull + i, 1), mbar_init(bar + kEmpty + i, 8), mbar_init(bar + kInfoReady + i, 1);
         for (int i = 0; i < 2; i++) {
-            mbar_init(bar + kKReady + i, 8);
-            mbar_init(bar + kVReady + i, 8);
+            mbar_init(bar + kKReady + i, 4);
+            mbar_init(bar + kVReady + i, 4);
             mbar_init(bar + kSDone + i, 1);
             mbar_init(bar + kODone + i, 1);
-            mbar_init(bar + kPReady + i, 8);
+            mbar_init(bar + kPReady + i, 4);
         }
         mbar_init(bar + kQReady, 8);
         mbar_init(bar + kOFree, 8);
@@ -144,19 +271,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 16) tmem_alloc(tmem_slot, 512);
-    for (int i = threadIdx.x; i < a.T; i += kTcThreads) {
-        // the step rows that step row i sees (the mask, as bits)
-        uint32_t m[4] = {1u, 0u, 0u, 0u};
-        auto set = [&](int j) { m[0] |= j < 32 ? 1u << j : 0u, m[1] |= j >= 32 && j < 64 ? 1u << (j - 32) : 0u,
-                                m[2] |= j >= 64 && j < 96 ? 1u << (j - 64) : 0u, m[3] |= j >= 96 ? 1u << (j - 96) : 0u; };
+    for (int i = threadIdx.x - 32; i >= 0 && i < a.T; i += kTcThreads) {
+        // the step rows that step row i sees (the mask), as bits
+        uint32_t m[4];
         const int nl = a.W * a.n1;
-        if (i >= 1 && i <= nl) {
-            const int lv = (i - 1) / a.W, c = (i - 1) % a.W;
-            for (int j = 1; j <= 1 + c; j++) set(j);
-            for (int v = 1; v <= lv; v++) set(1 + v * a.W + c);
-        } else if (i > nl) {
-            for (int j = i - (i - 1 - nl) % a.n1; j <= i; j++) set(j);
+        int lo, hi;  // besides row 0: lo .. hi, and column c of the levels up to lv
+        int lv = 0, c = 0;
+        if (i <= nl) lv = i ? (i - 1) / a.W : 0, c = i ? (i - 1) % a.W : 0, lo = 1, hi = i ? 1 + c : 0;
+        else lo = i - (i - 1 - nl) % a.n1, hi = i;
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            const int x = max(lo - 32 * w, 0), y = min(hi - 32 * w, 31);
+            m[w] = x <= y ? (~0u << x) & (~0u >> (31 - y)) : 0u;
+        }
+        m[0] |= 1u;
+        for (int v = 1; v <= lv; v++) {
+            const int j = 1 + v * a.W + c;
+#pragma unroll
+            for (int w = 0; w < 4; w++) m[w] |= j >> 5 == w ? 1u << (j & 31) : 0u;
         }
         *(uint4*)(vis + 4 * i) = make_uint4(m[0], m[1], m[2], m[3]);
     }
@@ -164,204 +296,246 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     pdl_trigger();
     if (blockIdx.x == 0) raise_long(a);
     tc_fence_before();
-    find_starts(a, blockIdx.x, 1, start, scratch);
+    Run first;
+    first.left = 0;
+    bool work;
+    MergeRec* rec = nullptr;
+    Shares shares{0, 0, 0};
+    if (CL) {
+        __syncthreads();
+        const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+        const int x = blockIdx.x / cs, items = a.Hkv * a.mtiles;
+        first.b = x / items;
+        first.item = x - first.b * items;
+        first.len = seq_len(a, first.b);
+        const int nt = first.len < 0 ? 0 : (first.len + kTile - 1) / kTile + 1;
+        first.nu = nt, first.u0 = first.t0 = nt * rank / cs, first.u1 = first.t1 = nt * (rank + 1) / cs;
+        work = first.t1 > first.t0;
+    } else {
+        find_starts(a, blockIdx.x, 1, start, scratch);
+        const Start st = *start;
+        work = st.count > 0;
+        shares = st.sh;
+        if (work) first.begin(a, st);
+        rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(kRowsTc, D)) + blockIdx.x;
+        if (a.part && threadIdx.x == 0) rec->rest = 0;
+    }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Start st = *start;
-    MergeRec* rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(kRowsTc, D)) + blockIdx.x;
-    if (a.part && threadIdx.x == 0) rec->rest = 0;
 
-    Run run;
-    run.left = 0;
     // A wait that gives up ends every later one at once, but no role leaves its
     // loops: the named barriers keep their counts.
     bool ok = true;
     auto wait = [&](int b, int parity) {
-        if (ok && !mbar_wait(bar + b, parity, abort_flag)) {
-            ok = false;
-            *abort_flag = 1;
-            kv4_raise(a.status, LA_ERR_TIMEOUT);
+        if (!ok || try_wait_long(bar + b, parity)) return;
+        const unsigned long long t0 = globaltimer();
+        while (!try_wait_long(bar + b, parity)) {
+            if (*abort_flag || globaltimer() - t0 > kWaitNs) {
+                ok = false;
+                *abort_flag = 1;
+                kv4_raise(a.status, LA_ERR_TIMEOUT);
+                return;
+            }
         }
     };
     int n = 0;     // tiles so far: n & 1 is the buffer, (n >> 1) & 1 its phase
     int segs = 0;  // runs with tiles so far
-    if (st.count > 0 && warp < 8) {
+    float out_m = kNoRef, out_l = 0.f;  // CL: this thread's row
+    Run run = first;
+    if (work && warp < 8) {
         // ------------------------------------------------------------ softmax
-        const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+        const int q = warp & 3, grp = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-        float* red = (float*)(sm + L::kRed);
-        run.begin(a, st);
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile, gr = mt * kRowsTc + row;
             const bool any = mt * kRowsTc + q * 32 < a.rows;  // some row of this warp is there
+            const int n0 = n;
             float m = kNoRef, l = 0.f;
             for (int tile = run.t0; tile < run.t1; tile++, n++) {
-                const int b = n & 1, ph = (n >> 1) & 1;
+                if ((n & 1) != grp) continue;
+                const int b = grp, ph = (n >> 1) & 1;
+                const bool step = tile >= ntc;
                 wait(kSDone + b, ph);
+                if (step) wait(kVReady + b, ph);  // (its entry has parts from both unpacking groups)
                 tc_fence_after();
                 if (any) {
-                    const TileInfo* ti = info + (n & 3);
+                    const TileInfo* ti = info + (n & 7);
                     const int live = ti->live, bad = ti->bad, iev = ti->ev;
                     const float f = fmaxf(scale2(rowf[(segs & 1) * 128 + row], ti->ek), 1e-37f), ev = (float)iev;
-                    const bool step = tile >= ntc;
-                    uint2 see = make_uint2(~0u, ~0u);  // the columns of this half that count
-                    if (step) {
-                        see = *(const uint2*)(vis + 4 * min(gr / group, a.T - 1) + 2 * half);
-                    } else if (live < kTile || bad) {
-                        const int left = live - half * 64;
-                        see.x = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-                        see.y = left >= 64 ? ~0u : left <= 32 ? 0u : (1u << (left - 32)) - 1u;
-                        const int hb = bad >> (half * 4);
-                        see.x &= ~((hb & 1 ? 0xffffu : 0u) | (hb & 2 ? 0xffff0000u : 0u));
-                        see.y &= ~((hb & 4 ? 0xffffu : 0u) | (hb & 8 ? 0xffff0000u : 0u));
-                    }
                     const bool part = step || live < kTile || bad;
-                    // 32 columns at a time, read again after the row's maximum is known
+                    const uint32_t* see = vis + 4 * min(gr / group, a.T - 1);
                     float x[32];
-                    auto load = [&](int c) {
-                        tmem_ld32(trow + b * 128 + half * 64 + c * 32, x);
+                    auto load = [&](int c) {  // 32 scores
+                        tmem_ld32(trow + b * 128 + c * 32, x);
                         if (part) {
-                            const uint32_t s = c ? see.y : see.x;
+                            uint32_t s;  // which of them count
+                            if (step) {
+                                s = see[c];
+                            } else {
+                                const int left = live - c * 32, hb = bad >> (2 * c);
+                                s = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                                s &= ~((hb & 1 ? 0xffffu : 0u) | (hb & 2 ? 0xffff0000u : 0u));
+                            }
 #pragma unroll
                             for (int j = 0; j < 32; j++)
                                 if (!((s >> j) & 1)) x[j] = -INFINITY;
                         }
                     };
-                    float t0 = -INFINITY, t1 = -INFINITY;
+                    // Weigh with the reference as it is, P going to its own columns; only where
+                    // a row outgrows it (2^15; and in the first tile) find the row's largest
+                    // and weigh again.  The other group may have moved it in the tile before:
+                    // its decision is waited for with the results in hand.
+                    const bool lead = n == n0;
+                    float sum = 0.f;
+                    auto weigh = [&]() {
+                        const float c0 = ev - m;
+                        float s0 = 0.f, s1 = 0.f;
+                        __half2 top = __float2half2_rn(0.f);
+#pragma unroll 1
+                        for (int c = 0; c < 4; c++) {
+                            load(c);
+                            uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        load(c);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            t0 = fmaxf(t0, fmaxf(x[j], x[j + 1]));
-                            t1 = fmaxf(t1, fmaxf(x[j + 2], x[j + 3]));
-                        }
-                    }
-                    red[(b * 2 + half) * 128 + row] = fmaxf(t0, t1);
-                    named_sync(1 + q, 64);
-                    const float y = fmaxf(red[b * 2 * 128 + row], red[(b * 2 + 1) * 128 + row]) * f + ev;
-                    const bool up = y > m + 8.f;
-                    if (__any_sync(0xffffffffu, up)) {
-                        // the same rows, and so the same vote, in both halves
-                        const float c = up ? ex2(m - y) : 1.f;
-                        if (up) m = y;
-                        l *= c;
-                        if (tile > run.t0) {
-                            wait(kODone + (b ^ 1), ((n - 1) >> 1) & 1);
-                            tc_fence_after();
-#pragma unroll
-                            for (int j = 0; j < D / 2; j += 32) {
-                                tmem_ld32(trow + 256 + half * (D / 2) + j, x);
-#pragma unroll
-                                for (int i = 0; i < 32; i++) x[i] *= c;
-                                uint32_t y[32];
-#pragma unroll
-                                for (int i = 0; i < 32; i++) y[i] = __float_as_uint(x[i]);
-                                tmem_st16(trow + 256 + half * (D / 2) + j, y);
-                                tmem_st16(trow + 256 + half * (D / 2) + j + 16, y + 16);
+                            for (int j = 0; j < 32; j += 2) {
+                                const float e0 = ex2(fmaf(x[j], f, c0)), e1 = ex2(fmaf(x[j + 1], f, c0));
+                                s0 += e0, s1 += e1;
+                                p[j / 2] = pack_f16(e0, e1);
+                                top = __hmax2(top, *reinterpret_cast<const __half2*>(&p[j / 2]));
                             }
-                            tmem_st_wait();
+                            tmem_st16(trow + kColP + b * 64 + c * 16, p);
                         }
-                    }
-                    const float c0 = ev - m;
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        load(c);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float e0 = ex2(fmaf(x[j], f, c0)), e1 = ex2(fmaf(x[j + 1], f, c0));
-                            s0 += e0, s1 += e1;
-                            p[j / 2] = pack_f16(e0, e1);
+                        sum = s0 + s1;
+                        return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(32768.f));
+                    };
+                    bool again = lead;
+                    if (!lead) {
+                        if (n == n0 + 1) {
+                            wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
+                            m = row_m[row];
+                            again = weigh();
+                        } else {
+                            again = weigh();
+                            wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
+                            const float mm = row_m[row];
+                            if (mm != m) l *= ex2(m - mm), m = mm, again = true;
                         }
-                        tmem_st16(trow + b * 128 + half * 64 + c * 16, p);
+                        again = __any_sync(0xffffffffu, again);
                     }
-                    l += scale2(s0 + s1, -iev);
+                    if (again) {
+                        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 4; c++) {
+                            load(c);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                t0 = fmaxf(t0, fmaxf(x[j], x[j + 1]));
+                                t1 = fmaxf(t1, fmaxf(x[j + 2], x[j + 3]));
+                            }
+                        }
+                        const float y = fmaxf(t0, t1) * f + ev;
+                        const bool up = y > m + 8.f;
+                        if (__any_sync(0xffffffffu, up)) {
+                            const float c = up ? ex2(m - y) : 1.f;
+                            if (up) m = y;
+                            l *= c;
+                            row_m[row] = m;
+                            if (!lead) {
+                                wait(kODone + (b ^ 1), ((n - 1) >> 1) & 1);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int j = 0; j < D; j += 8) {
+                                    uint32_t o[8];
+                                    tmem_ld8(trow + kColO + j, o);
+#pragma unroll
+                                    for (int i = 0; i < 8; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                                    tmem_st8(trow + kColO + j, o);
+                                }
+                            }
+                        }
+                        if (lead) row_m[row] = m;
+                        weigh();
+                    }
+                    l += scale2(sum, -iev);
                     tmem_st_wait();
+                } else if (n > n0) {
+                    wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);  // in tile order, like the others
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + kPReady + b);
             }
-            // ---- the run's result
+            // ---- the run's result: group grp takes half of the channels
             const bool tiles = run.t1 > run.t0, whole = run.u0 == 0 && run.u1 == run.nu;
+            const int last = n - 1;
             if (tiles) {
-                const int last = n - 1;
                 wait(kODone + (last & 1), (last >> 1) & 1);
                 tc_fence_after();
             }
             if (any) {
-                red[(2 * (segs & 1) + half) * 128 + row] = l;  // free: its last readers have arrived at kPReady
+                const float mm = tiles ? row_m[row] : kNoRef;
+                row_l[grp * 128 + row] = l * (m == mm ? 1.f : ex2(m - mm));
+                m = mm;
                 named_sync(1 + q, 64);
-                const float sum = red[2 * (segs & 1) * 128 + row] + red[(2 * (segs & 1) + 1) * 128 + row];
+                const float sum = row_l[row] + row_l[128 + row];
                 named_sync(1 + q, 64);
-                float* part = a.part + ((size_t)blockIdx.x * 2 + (run.u0 == 0 ? 1 : 0)) * part_floats(kRowsTc, D);
-                const float inv = 1.f / sum;
-                const size_t orow = ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
-                // the step tile, if it is there, is the last one; its products are done, so its entry is complete
-                const uint32_t* odd = info[(n - 1) & 3].odd;
-                const bool fix = run.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+                if (CL) {
+                    out_m = m, out_l = sum;
+                } else {
+                    float* part = a.part + ((size_t)blockIdx.x * 2 + (run.u0 == 0 ? 1 : 0)) * part_floats(kRowsTc, D);
+                    const float inv = 1.f / sum;
+                    __nv_bfloat16* orow = a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
+                    // the step tile, if it is there, is the last one; its products are done, so its entry is complete
+                    const uint32_t* odd = info[last & 7].odd;
+                    const bool fix = run.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+#pragma unroll 1
+                    for (int j = 0; j < D / 2; j += 32) {
+                        float o[32];
+                        const int c = grp * (D / 2) + j;
+                        __syncwarp();
+                        if (tiles) {
+                            tmem_ld32(trow + kColO + c, o);
+                        } else {
 #pragma unroll
-                for (int j = 0; j < D / 2; j += 32) {
-                    float o[32];
-                    __syncwarp();
-                    if (tiles) {
-                        tmem_ld32(trow + 256 + half * (D / 2) + j, o);
-                    } else {
+                            for (int i = 0; i < 32; i++) o[i] = 0.f;
+                        }
+                        if (fix && gr < a.rows) add_odd(a, odd, vis + 4 * (gr / group), run.b, head * D + c, o);
+                        if (gr < a.rows && whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) o[i] = 0.f;
-                    }
-                    const int c = half * (D / 2) + j;
-                    if (fix && gr < a.rows) {
-                        // values that are not finite, of the step rows this row sees
-                        for (int key = 0; key < a.T; key++) {
-                            if (!(((odd[key >> 5] & vis[4 * (gr / group) + (key >> 5)]) >> (key & 31)) & 1)) continue;
-                            const __nv_bfloat16* v = a.vs + (size_t)(run.b * (long long)a.T + key) * a.kv_ld + (size_t)head * D + c;
+                            for (int i = 0; i < 32; i += 8)
+                                *(uint4*)(orow + c + i) =
+                                    make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                                               pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+                        } else if (gr < a.rows) {
 #pragma unroll
-                            for (int i = 0; i < 32; i++) {
-                                const float x = __bfloat162float(v[i]);
-                                if (!(fabsf(x) < INFINITY)) o[i] += x;
-                            }
+                            for (int i = 0; i < 32; i++) part[(size_t)(c + i) * kRowsTc + row] = o[i];  // a line per warp
                         }
                     }
-                    if (gr < a.rows && whole) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *(uint4*)(a.out + orow + c + i) =
-                                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
-                    } else if (gr < a.rows) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *(float4*)(part + (size_t)row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    }
+                    if (!whole && grp == 0 && gr < a.rows)
+                        part[(size_t)kRowsTc * D + row] = m, part[(size_t)kRowsTc * (D + 1) + row] = sum;
                 }
-                if (!whole && half == 0 && gr < a.rows) *(float2*)(part + (size_t)kRowsTc * D + 2 * row) = make_float2(m, sum);
             }
-            if (run.u0 == 0 && !whole && a.part && threadIdx.x == 0)
-                *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, st.total};
+            if (!CL && run.u0 == 0 && !whole && a.part && threadIdx.x == 0)
+                *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, shares};
             if (tiles) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + kOFree);
                 segs++;
             }
-        } while (run.next(a));
-    } else if (st.count > 0 && warp < 16) {
+        } while (!CL && run.next(a));
+    } else if (work && warp < 16) {
         // ------------------------------------------------------------- unpack
-        const int tid = threadIdx.x - 256, row = tid >> 1, h = tid & 1, uw = warp - 8;
+        const int kv = warp >= 12, tid = threadIdx.x - 256 - kv * 128, h = tid & 1, uw = warp & 3;
         int fills = 0;  // ring stages taken
-        run.begin(a, st);
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile;
             if (run.t1 <= run.t0) continue;
-            // ---- the rows' queries: row by a power of two, channels 32 h + 64 p .. of row `row`
+            // ---- the rows' queries, each by a power of two: channels 32 h + 64 p .. of row `row`
             if (n > 0) wait(kSDone + ((n - 1) & 1), ((n - 1) >> 1) & 1);  // the last tile's S has read the old ones
             {
-                const int gr = mt * kRowsTc + row;
+                const int row = (threadIdx.x - 256) >> 1, gr = mt * kRowsTc + row;
                 const __nv_bfloat16* src = a.q + (size_t)(run.b * (long long)a.T + gr / group) * a.q_ld +
                                            (size_t)(head * group + gr % group) * D + 32 * h;
                 uint4 u[L::kAtoms][4];
@@ -369,8 +543,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 #pragma unroll
                 for (int p = 0; p < L::kAtoms; p++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
+                    for (int i = 0; i < 4; i++)
                         u[p][i] = gr < a.rows ? *(const uint4*)(src + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int p = 0; p < L::kAtoms; p++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
                         const uint32_t* w = (const uint32_t*)&u[p][i];
 #pragma unroll
                         for (int k = 0; k < 4; k++) top = max(top, max((w[k] << 16) & 0x7f800000u, w[k] & 0x7f800000u));
@@ -397,113 +575,87 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             }
             for (int tile = run.t0; tile < run.t1; tile++, n++) {
                 const int b = n & 1, ph = (n >> 1) & 1;
-                uint8_t* kt = sm + L::kK + b * L::kOperand + row * 128;
-                uint8_t* vt = sm + L::kV + b * L::kOperand + row * 128;
-                TileInfo* ti = info + (n & 3);
+                uint8_t* dst = sm + (kv ? L::kV : L::kK) + b * L::kOperand;
+                TileInfo* ti = info + (n & 7);
                 if (tile < ntc) {
-                    const int s = fills % kRing;
-                    wait(kFull + s, (fills / kRing) & 1);
+                    const int s = fills % kRing, sp = (fills / kRing) & 1;
+                    wait(kInfoReady + s, sp);
+                    wait(kFull + s, sp);
                     const uint8_t* stage = sm + L::kCodes + s * L::kStage;
-                    const int ri = ring_info[s], live = ri & 0xffff, bad = ri >> 16;
-                    // the largest scales' exponents of the tile (of keys that count)
-                    uint32_t ek = 0, ev = 0;
+                    const int live = ti->live, bad = ti->bad, E = kv ? ti->ev : ti->ek;
+                    if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);  // tile n - 2's product has read the buffer
+                    // key rows tid / 2 and 64 + tid / 2, half of each 64-channel panel
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int key = lane + 32 * i;
-                        if (key < live && !((bad >> (key >> 4)) & 1)) {
-                            const uint32_t* par = (const uint32_t*)(stage + (key >> 4) * kv4_block_bytes(D) + 16 * D) + (key & 15);
-                            const uint32_t k0 = par[0] >> 23, v0 = par[16] >> 23;
-                            ek = max(ek, k0 < 255 ? k0 : 0u);
-                            ev = max(ev, v0 < 255 ? v0 : 0u);
-                        }
-                    }
-                    ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
-                    const int Ek = max((int)ek, 20) - 118, Ev = max((int)ev, 20) - 118;  // s 2^-E < 2^-8
-                    const uint8_t* blk = stage + (row >> 4) * kv4_block_bytes(D);
-                    const uint8_t* crow = blk + (row & 15) * 32 + h * 16;
-                    const bool here = row < live && !((bad >> (row >> 4)) & 1);
-                    auto factors = [&](uint32_t par, int E, __half2& lo, __half2& hi, __half2& off) {
+                    for (int r2 = 0; r2 < 2; r2++) {
+                        const int row = (tid >> 1) + 64 * r2;
+                        const uint8_t* blk = stage + (row >> 4) * kv4_block_bytes(D);
+                        const uint32_t par = ((const uint32_t*)(blk + 16 * D))[16 * kv + (row & 15)];
+                        const bool here = row < live && !((bad >> (row >> 4)) & 1);
                         const float sc = here ? scale2(__uint_as_float(par & 0xffff0000u), -E) : 0.f;
-                        lo = __float2half2_rn(sc * 0x1p24f);
-                        hi = __float2half2_rn(sc * 0x1p20f);
-                        off = __float2half2_rn(-(float)(par & 15u) * sc);
-                    };
-                    const uint32_t* par = (const uint32_t*)(blk + 16 * D) + (row & 15);
-                    __half2 lo, hi, off;
-                    factors(par[0], Ek, lo, hi, off);
-                    if (n >= 2) wait(kSDone + b, ph ^ 1);  // S of tile n - 2 has read this K
+                        const __half2 lo = __float2half2_rn(sc * 0x1p24f), hi = __float2half2_rn(sc * 0x1p20f),
+                                      off = __float2half2_rn(-(float)(par & 15u) * sc);
+                        uint4 w[L::kAtoms];
 #pragma unroll
-                    for (int p = 0; p < L::kAtoms; p++) {
-                        const uint4 w = *(const uint4*)(crow + p * 512);
-                        const uint32_t* u = (const uint32_t*)&w;
+                        for (int p = 0; p < L::kAtoms; p++)
+                            w[p] = *(const uint4*)(blk + kv * 8 * D + p * 512 + (row & 15) * 32 + h * 16);
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            *(uint4*)(kt + p * (128 * 128) + (((4 * h + i) ^ (row & 7)) << 4)) = unpack8(u[i], lo, hi, off);
-                    }
-                    if (tid == 0) ti->live = live, ti->bad = bad, ti->ek = Ek, ti->ev = Ev;
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar + kKReady + b);
-                    factors(par[16], Ev, lo, hi, off);
-                    if (n >= 2) wait(kODone + b, ph ^ 1);  // O of tile n - 2 has read this V
+                        for (int p = 0; p < L::kAtoms; p++) {
+                            const uint32_t* u = (const uint32_t*)&w[p];
 #pragma unroll
-                    for (int p = 0; p < L::kAtoms; p++) {
-                        const uint4 w = *(const uint4*)(crow + 8 * D + p * 512);
-                        const uint32_t* u = (const uint32_t*)&w;
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            *(uint4*)(vt + p * (128 * 128) + (((4 * h + i) ^ (row & 7)) << 4)) = unpack8(u[i], lo, hi, off);
+                            for (int i = 0; i < 4; i++)
+                                *(uint4*)(dst + p * (128 * 128) + row * 128 + (((4 * h + i) ^ (row & 7)) << 4)) = unpack8(u[i], lo, hi, off);
+                        }
                     }
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(bar + kVReady + b);
+                        mbar_arrive(bar + (kv ? kVReady : kKReady) + b);
                         mbar_arrive(bar + kEmpty + s);
                     }
                     fills++;
                 } else {
                     // the step's own rows: bf16 to fp16 by the tile's largest finite exponent
-                    const bool here = row < a.T;
-                    const size_t at = (size_t)(run.b * (long long)a.T + row) * a.kv_ld + (size_t)head * D + 32 * h;
-                    uint32_t e[2] = {0, 0};
-#pragma unroll
-                    for (int kv = 0; kv < 2; kv++) {
-                        const __nv_bfloat16* src = (kv ? a.vs : a.ks) + at;
+                    const __nv_bfloat16* src = (kv ? a.vs : a.ks) + (size_t)run.b * a.T * a.kv_ld + (size_t)head * D + 32 * h;
+                    uint32_t e = 0;
+#pragma unroll 1
+                    for (int r2 = 0; r2 < 2; r2++) {
+                        const int row = (tid >> 1) + 64 * r2;
 #pragma unroll
                         for (int p = 0; p < L::kAtoms; p++)
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
-                                const uint4 u = here ? *(const uint4*)(src + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
+                                const uint4 u = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
                                 const uint32_t* w = (const uint32_t*)&u;
 #pragma unroll
                                 for (int k = 0; k < 4; k++) {
                                     const uint32_t x0 = (w[k] >> 7) & 255u, x1 = (w[k] >> 23) & 255u;
-                                    e[kv] = max(e[kv], max(x0 < 255 ? x0 : 0u, x1 < 255 ? x1 : 0u));
+                                    e = max(e, max(x0 < 255 ? x0 : 0u, x1 < 255 ? x1 : 0u));
                                 }
                             }
-                        e[kv] = __reduce_max_sync(0xffffffffu, e[kv]);
-                        if (lane == 0) red_e[kv * 8 + uw] = e[kv];
                     }
-                    if (tid < 4) ti->odd[tid] = 0;
-                    named_sync(5, 256);
+                    e = __reduce_max_sync(0xffffffffu, e);
+                    if (lane == 0) red_e[kv * 4 + uw] = e;
+                    if (kv && tid < 4) ti->odd[tid] = 0;
+                    named_sync(5 + kv, 128);
 #pragma unroll
-                    for (int kv = 0; kv < 2; kv++)
-#pragma unroll
-                        for (int i = 0; i < 8; i++) e[kv] = max(e[kv], red_e[kv * 8 + i]);
-                    named_sync(5, 256);  // red_e may be written again
-                    const int E[2] = {max((int)e[0], 28) - 135, max((int)e[1], 28) - 135};  // the largest comes to [2^8, 2^9)
-                    if (tid == 0) ti->live = kTile, ti->bad = 0, ti->ek = E[0], ti->ev = E[1];
-#pragma unroll
-                    for (int kv = 0; kv < 2; kv++) {
-                        if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);
-                        const __nv_bfloat16* src = (kv ? a.vs : a.ks) + at;
-                        const float f = pow2i(-E[kv]);
+                    for (int i = 0; i < 4; i++) e = max(e, red_e[kv * 4 + i]);
+                    named_sync(5 + kv, 128);  // red_e may be written again
+                    const int E = max((int)e, 28) - 135;  // the largest comes to [2^8, 2^9)
+                    if (tid == 0) {
+                        if (kv) ti->ev = E;
+                        else ti->ek = E, ti->live = kTile, ti->bad = 0;
+                    }
+                    if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);
+                    const float f = pow2i(-E);
+#pragma unroll 1
+                    for (int r2 = 0; r2 < 2; r2++) {
+                        const int row = (tid >> 1) + 64 * r2;
                         bool odd = false;
 #pragma unroll
                         for (int p = 0; p < L::kAtoms; p++)
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
-                                const uint4 u = here ? *(const uint4*)(src + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
+                                const uint4 u = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
                                 const uint32_t* w = (const uint32_t*)&u;
                                 uint32_t y[4];
 #pragma unroll
@@ -516,83 +668,125 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                                     }
                                     y[k] = pack_f16(x0 * f, x1 * f);
                                 }
-                                *(uint4*)((kv ? vt : kt) + p * (128 * 128) + (((4 * h + i) ^ (row & 7)) << 4)) =
-                                    make_uint4(y[0], y[1], y[2], y[3]);
+                                *(uint4*)(dst + p * (128 * 128) + row * 128 + (((4 * h + i) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                             }
                         if (odd) atomicOr(&ti->odd[row >> 5], 1u << (row & 31));
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar + (kv ? kVReady : kKReady) + b);
                     }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + (kv ? kVReady : kKReady) + b);
                 }
             }
-        } while (run.next(a));
-    } else if (st.count > 0 && warp == 16) {
+        } while (!CL && run.next(a));
+    } else if (work && warp == 16) {
         // ---------------------------------------------------------------- MMA
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16(128, kTile, false), id_o = idesc_f16(128, D, true);
-            auto scores = [&](bool first) {
-                const int b = n & 1;
-                wait(kKReady + b, (n >> 1) & 1);
-                if (first) wait(kQReady, segs & 1);
-                if (!ok) return;
-                tc_fence_after();
+        constexpr uint32_t id_s = idesc_f16(128, kTile, false), id_o = idesc_f16(128, D, true);
+        const uint32_t base = smem_u32(sm);
+        const uint64_t dk = desc_sw128_kmajor(base), dv = desc_sw128_mnmajor(base, 128 * 128);
+        const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+        const bool chosen = elect_one();
+        auto scores = [&](int b, int ph, bool lead) {
+            wait(kKReady + b, ph);
+            if (lead) wait(kQReady, segs & 1);
+            tc_fence_after();
+            if (chosen && ok) {
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
-                    const uint32_t qa = smem_u32(sm + L::kQ + (k >> 2) * (128 * 128)) + (k & 3) * 32;
-                    const uint32_t ka = smem_u32(sm + L::kK + b * L::kOperand + (k >> 2) * (128 * 128)) + (k & 3) * 32;
-                    mma_bf16(tmem + b * 128, desc_sw128_kmajor(qa), desc_sw128_kmajor(ka), id_s, k > 0);
+                    const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + b * 128, k_lo + (L::kQ >> 4) + at, k_lo + ((L::kK + b * L::kOperand) >> 4) + at, k_hi, id_s, k > 0);
                 }
                 mma_commit(bar + kSDone + b);
-            };
-            auto outputs = [&](int i, bool first) {  // tile i
-                const int b = i & 1, ph = (i >> 1) & 1;
-                wait(kPReady + b, ph);
-                wait(kVReady + b, ph);
-                if (first && segs > 0) wait(kOFree, (segs - 1) & 1);
-                if (!ok) return;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kTile / 16; k++) {
-                    const uint32_t va = smem_u32(sm + L::kV + b * L::kOperand) + k * 16 * 128;
-                    mma_ts(tmem + 256, tmem + b * 128 + (k >> 2) * 64 + (k & 3) * 8, desc_sw128_mnmajor(va, 128 * 128), id_o,
-                           !first || k > 0);
-                }
-                mma_commit(bar + kODone + b);
-            };
-            run.begin(a, st);
-            do {
-                if (run.t1 <= run.t0) continue;
-                scores(true);
-                for (int tile = run.t0; tile < run.t1; tile++) {
-                    const int i = n++;
-                    if (tile + 1 < run.t1) scores(false);  // of the next tile, while this one's softmax runs
-                    outputs(i, tile == run.t0);
-                }
-                segs++;
-            } while (run.next(a));
-            if (!ok) {
-                // let the products that were issued finish before the memory goes
-                mma_commit(bar + kEnd);
-                mbar_drain(bar + kEnd, 0);
             }
+            __syncwarp();
+        };
+        auto outputs = [&](int b, int ph, bool lead) {
+            wait(kPReady + b, ph);
+            wait(kVReady + b, ph);
+            if (lead && segs > 0) wait(kOFree, (segs - 1) & 1);
+            tc_fence_after();
+            if (chosen && ok) {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; k++)
+                    mma_ts(tmem + kColO, tmem + kColP + b * 64 + k * 8, v_lo + ((L::kV + b * L::kOperand + k * 16 * 128) >> 4), v_hi,
+                           id_o, !lead || k > 0);
+                mma_commit(bar + kODone + b);
+            }
+            __syncwarp();
+        };
+        do {
+            const int tiles = run.t1 - run.t0;
+            if (tiles <= 0) continue;
+            scores(n & 1, (n >> 1) & 1, true);
+            for (int i = 0; i < tiles; i++, n++) {
+                // the next tile's scores go first: they run while this one's softmax does
+                if (i + 1 < tiles) scores((n + 1) & 1, ((n + 1) >> 1) & 1, false);
+                outputs(n & 1, (n >> 1) & 1, i == 0);
+            }
+            segs++;
+        } while (!CL && run.next(a));
+        if (!ok && chosen) {
+            // let the products that were issued finish before the memory goes
+            mma_commit(bar + kEnd);
+            mbar_drain(bar + kEnd, 0);
         }
         __syncwarp();
-    } else if (st.count > 0) {
+    } else if (work) {
         // -------------------------------------------------------------- copies
         const uint64_t pol = policy_evict_first();
-        int fills = 0;
-        run.begin(a, st);
+        int fills = 0, known = 0;
+        int where[kRing] = {};  // the tile numbers of the stages in flight
+        auto find_powers = [&]() {  // of the oldest stage that is not done
+            const int s = known % kRing;
+            wait(kFull + s, (known / kRing) & 1);
+            const uint8_t* stage = sm + L::kCodes + s * L::kStage;
+            const int ri = ring_info[s], live = ri & 0xffff, bad = ri >> 16;
+            uint32_t ek = 0, ev = 0;  // the largest scales' exponents (of keys that count)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int key = lane + 32 * i;
+                const uint32_t* par = (const uint32_t*)(stage + (key >> 4) * kv4_block_bytes(D) + 16 * D) + (key & 15);
+                const uint32_t k0 = par[0] >> 23, v0 = par[16] >> 23;
+                const bool here = key < live && !((bad >> (key >> 4)) & 1);
+                ek = max(ek, here && k0 < 255 ? k0 : 0u);
+                ev = max(ev, here && v0 < 255 ? v0 : 0u);
+            }
+            ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
+            if (lane == 0) {
+                TileInfo* ti = info + ((s == 0 ? where[0] : s == 1 ? where[1] : where[2]) & 7);
+                ti->live = live, ti->bad = bad;
+                ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 20) - 118;  // s 2^-E < 2^-8
+                mbar_arrive(bar + kInfoReady + s);
+            }
+            __syncwarp();
+            known++;
+        };
         do {
             const int head = run.item / a.mtiles, ntc = (run.len + kTile - 1) / kTile;
-            for (int tile = run.t0; tile < min(run.t1, ntc); tile++) {
+            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+                if (tile >= ntc) continue;
                 const int s = fills % kRing, blk = tile * 8 + lane, live = min(run.len - tile * kTile, kTile);
                 const bool mine = lane < 8 && lane * 16 < live;
                 const int page = mine ? __ldg(a.table + (size_t)run.b * a.max_pages + (blk >> a.blk_log2)) : 0;
                 const bool bad = (unsigned)page >= (unsigned)a.n_pages;
                 const uint32_t bads = __ballot_sync(0xffffffffu, bad), who = __ballot_sync(0xffffffffu, mine);
-                if (fills >= kRing) wait(kEmpty + s, (fills / kRing - 1) & 1);
+                // until the stage is free, and after it: the powers of tiles that have landed
+                if (fills >= kRing) {
+                    const unsigned long long t0 = globaltimer();
+                    while (ok && !__all_sync(0xffffffffu, test_wait(bar + kEmpty + s, (fills / kRing - 1) & 1))) {
+                        if (known < fills && __all_sync(0xffffffffu, test_wait(bar + kFull + known % kRing, (known / kRing) & 1)))
+                            find_powers();
+                        const bool late = *abort_flag || globaltimer() - t0 > kWaitNs;
+                        if (__any_sync(0xffffffffu, late)) {
+                            ok = false;
+                            *abort_flag = 1;
+                            kv4_raise(a.status, LA_ERR_TIMEOUT);
+                        }
+                    }
+                }
                 if (!__all_sync(0xffffffffu, ok)) continue;
+                if (s == 0) where[0] = n;
+                else if (s == 1) where[1] = n;
+                else where[2] = n;
                 if (lane == 0) {
                     if (bads) kv4_raise(a.status, LA_ERR_ARG);
                     ring_info[s] = live | (int)bads << 16;
@@ -605,12 +799,66 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                               kv4_block_bytes(D), bar + kFull + s, pol);
                 __syncwarp();
                 fills++;
+                if (known < fills && __all_sync(0xffffffffu, test_wait(bar + kFull + known % kRing, (known / kRing) & 1))) find_powers();
             }
-        } while (run.next(a));
+        } while (!CL && run.next(a));
+        while (known < fills) find_powers();
         // no copy may still be on its way when the CTA ends
         for (int i = 1; i <= kRing && i <= fills; i++) mbar_drain(bar + kFull + (fills - i) % kRing, ((fills - i) / kRing) & 1);
     }
     __syncwarp();
+    if (CL) {
+        // ---- the cluster's parts meet: every CTA sums its share of the channels
+        const int cs = (int)cluster_size(), rank = (int)cluster_rank(), row = threadIdx.x & 127, grp = threadIdx.x >> 7;
+        const int head = first.item / a.mtiles, mt = first.item - head * a.mtiles, gr = mt * kRowsTc + row;
+        const int ntc = (first.len + kTile - 1) / kTile, slice = D / cs;
+        const bool mine = warp < 8 && gr < a.rows && first.len >= 0;
+        if (warp < 4) row_m[row] = out_m, row_l[row] = out_l;
+        cluster_sync();  // also: no CTA's products read K any more, where the parts go
+        float* parts = (float*)(sm + L::kK);  // [rank][slice][128 rows]
+        if (warp < 8) {
+            float top = kNoRef, sum = 0.f;
+            for (int r = 0; r < cs; r++) top = fmaxf(top, ld_peer(peer(row_m + row, r)));
+            for (int r = 0; r < cs; r++) sum += ld_peer(peer(row_l + row, r)) * ex2(ld_peer(peer(row_m + row, r)) - top);
+            const float w = ex2(out_m - top) / sum;
+            const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t* odd = info[(n - 1) & 7].odd;
+            const bool fix = work && first.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < D / 2; j += 32) {
+                float o[32];
+                const int c = grp * (D / 2) + j;
+                __syncwarp();
+                if (work) {
+                    tmem_ld32(trow + kColO + c, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = 0.f;
+                }
+                if (fix && mine) add_odd(a, odd, vis + 4 * (gr / group), first.b, head * D + c, o);
+                if (mine)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        // (8 channels are of one slice: a slice has 8 at least)
+                        const uint32_t to = peer(parts + ((size_t)rank * slice + (c + i) % slice) * 128 + row, (c + i) / slice);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) st_peer(to + k * 512, o[i + k] * w);
+                    }
+            }
+        }
+        cluster_sync();
+        if (mine) {
+            __nv_bfloat16* orow = a.out + ((size_t)(first.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + rank * slice;
+            for (int c = grp * 4; c < slice; c += 8) {
+                float v[4] = {};
+                for (int r = 0; r < cs; r++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) v[k] += parts[((size_t)r * slice + c + k) * 128 + row];
+                *(uint2*)(orow + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            }
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
@@ -620,7 +868,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 }
 
 struct TcPlan {
-    int nteams, mtiles;
+    int nteams, mtiles, cluster;  // cluster: CTAs per item, 0: equal runs over the SMs
+    long long items;
     bool merge;
     size_t bytes;
 };
@@ -632,13 +881,44 @@ TcPlan tc_plan(const la_kv4_desc& c, const la_kv4_attn& a)
     TcPlan p;
     const int T = 1 + (a.W + a.G) * (a.N - 1), rows = T * (a.n_heads / c.n_kv_heads);
     p.mtiles = ceil_div(rows, kRowsTc);
-    const long long items = (long long)a.batch * c.n_kv_heads * p.mtiles;
+    p.items = (long long)a.batch * c.n_kv_heads * p.mtiles;
     const int room = c.max_pages * c.page, max_len = a.max_len > 0 && a.max_len < room ? a.max_len : room;
-    const long long units = items * (kTcExtra + (max_len + kTile - 1) / kTile + 1);
-    p.nteams = (int)std::max(1LL, std::min((long long)kSMs, std::max(items, units / (kTcExtra + 2))));
-    p.merge = !(a.batch == 1 && items % p.nteams == 0);
+    const int tiles = (max_len + kTile - 1) / kTile + 1;  // of an item, at most
+    p.cluster = 0;
+    if (2 * p.items <= kSMs) {
+        p.cluster = 2;
+        while (p.cluster < 8 && 2 * p.cluster * p.items <= kSMs && p.cluster < tiles) p.cluster *= 2;
+    }
+    const long long units = p.items * (kTcExtra + tiles);
+    p.nteams = (int)std::max(1LL, std::min((long long)kSMs, std::max(p.items, units / (kTcExtra + 2))));
+    p.merge = !p.cluster && !(a.batch == 1 && p.items % p.nteams == 0);
     p.bytes = p.merge ? (size_t)p.nteams * (2 * part_floats(kRowsTc, c.head_dim) * 4 + sizeof(MergeRec)) : 0;
     return p;
+}
+
+template <int D>
+cudaError_t go(cudaStream_t s, const TcPlan& p, const Kv4Attn& k)
+{
+    if (!p.cluster) return launch_pdl(k_kv4_tc<D, false>, dim3(p.nteams), dim3(kTcThreads), TcSmem<D>::kBytes, s, k);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.items * p.cluster));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = TcSmem<D>::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)p.cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_kv4_tc<D, true>, k);
+}
+
+template <typename K>
+bool set_smem(K kern, int bytes)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
 }  // namespace
@@ -647,8 +927,8 @@ size_t kv4_tc_bytes(const la_kv4_desc& c, const la_kv4_attn& a) { return tc_plan
 
 bool kv4_tc_init()
 {
-    return cudaFuncSetAttribute(k_kv4_tc<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<128>::kBytes) == cudaSuccess &&
-           cudaFuncSetAttribute(k_kv4_tc<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<64>::kBytes) == cudaSuccess;
+    return set_smem(k_kv4_tc<128, false>, TcSmem<128>::kBytes) && set_smem(k_kv4_tc<128, true>, TcSmem<128>::kBytes) &&
+           set_smem(k_kv4_tc<64, false>, TcSmem<64>::kBytes) && set_smem(k_kv4_tc<64, true>, TcSmem<64>::kBytes);
 }
 
 int launch_kv4_tc(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a, Kv4Attn k)
@@ -657,9 +937,7 @@ int launch_kv4_tc(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a, Kv
     k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = kTcExtra;
     k.tile_log2 = kTileLog2, k.step_tiles = 1;
     k.part = p.merge ? (float*)a.workspace : nullptr;
-    cudaError_t e = c.head_dim == 128
-                        ? launch_pdl(k_kv4_tc<128>, dim3(p.nteams), dim3(kTcThreads), TcSmem<128>::kBytes, s, k)
-                        : launch_pdl(k_kv4_tc<64>, dim3(p.nteams), dim3(kTcThreads), TcSmem<64>::kBytes, s, k);
+    cudaError_t e = c.head_dim == 128 ? go<128>(s, p, k) : go<64>(s, p, k);
     if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, c.head_dim, kRowsTc);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }

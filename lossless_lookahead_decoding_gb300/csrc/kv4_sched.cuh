@@ -58,10 +58,29 @@ __device__ __forceinline__ void raise_long(const Kv4Attn& a)
         if (a.lens[b] > a.max_len) kv4_raise(a.status, LA_ERR_ARG);
 }
 
+// The equal runs: team t begins at unit q t + min(t, r) of all items' units
+// (q, r: their number divided by the teams').
+struct Shares {
+    long long q;
+    int r, pad;
+    __device__ __forceinline__ long long at(int t) const { return q * t + min(t, r); }
+};
+
+__device__ __forceinline__ Shares shares_of(long long total, int teams)
+{
+    // (a 64-bit division takes half a microsecond)
+    if (total < (1LL << 31)) {
+        const uint32_t q = (uint32_t)total / (uint32_t)teams;
+        return Shares{q, (int)((uint32_t)total - q * (uint32_t)teams), 0};
+    }
+    const long long q = total / teams;
+    return Shares{q, (int)(total - q * teams), 0};
+}
+
 struct Start {
     int b;
     long long off, count;  // offset in the units of sequence b's items; units of the team
-    long long total;       // units of all items
+    Shares sh;
 };
 
 // Where each of the CTA's teams begins: teams t0 .. t0 + n - 1 of a.nteams
@@ -87,14 +106,15 @@ __device__ void find_starts(const Kv4Attn& a, int t0, int n, Start* starts, long
         total += scratch[w];
     }
     if (mine) {
+        const Shares sh = shares_of(total, a.nteams);
         for (int i = 0; i < n; i++) {
-            const long long u0 = total * (t0 + i) / a.nteams, u1 = total * (t0 + i + 1) / a.nteams;
+            const long long u0 = sh.at(t0 + i), u1 = t0 + i < a.nteams ? sh.at(t0 + i + 1) : u0;
             if (u0 >= u1 || u0 < before || u0 >= before + mine) continue;
             long long at = before;
             for (int b = b0; b < min(b0 + per, a.B); b++) {
                 const long long c = (long long)items * item_units(a, seq_len(a, b));
                 if (u0 < at + c) {
-                    starts[i] = Start{b, u0 - at, u1 - u0, total};
+                    starts[i] = Start{b, u0 - at, u1 - u0, sh};
                     break;
                 }
                 at += c;
@@ -122,7 +142,7 @@ struct Run {
         b = s.b;
         len = seq_len(a, b);
         nu = item_units(a, len);
-        item = (int)(s.off / nu);
+        item = s.off < (1LL << 31) ? (int)((uint32_t)s.off / (uint32_t)nu) : (int)(s.off / nu);
         cut(a, (int)(s.off - (long long)item * nu));
     }
     __device__ __forceinline__ bool next(const Kv4Attn& a)
@@ -145,9 +165,11 @@ struct Run {
 // holds the item's first tile.
 struct MergeRec {
     int b, item, rest, pad;  // rest: the item's units that other teams hold (0: none begins here)
-    long long total;         // units of all items
+    Shares sh;
 };
 
+// A part: R rows of D outputs, each row's M and sum. R <= 16: [R][D], [R][2];
+// R = 128 (a thread per row): [D][R], [2][R].
 __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
 
 }  // namespace
