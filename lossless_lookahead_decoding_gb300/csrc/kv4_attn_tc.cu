@@ -80,7 +80,42 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc));
 }
 
-// 16 columns of this thread's lane of tensor memory.
+// 16 columns; the values are there after tmem_ld_wait(v)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+                   "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
+__device__ __forceinline__ void tmem_ld32x(uint32_t taddr, float (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld32_wait(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                   "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -116,6 +151,9 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity)
 {
@@ -165,6 +203,22 @@ enum {  // barriers
     kOFree = 20, kEnd = 21
 };
 constexpr uint32_t kColO = 256, kColP = 384;  // tensor memory: S [2][128], O [D], P [2][64]
+
+// Byte offset of 16-byte piece i (of a row's half h: 4 in each 64-channel
+// panel) from the row's place in the first panel, with the 128-byte swizzle.
+__device__ __forceinline__ int piece_at(int i, int h, int row)
+{
+    return (i >> 2) * (128 * 128) + (((4 * h + (i & 3)) ^ (row & 7)) << 4);
+}
+
+// the larger exponent of a bf16 pair, in place (bits 7 - 14)
+__device__ __forceinline__ uint32_t high_exp(uint32_t w) { return max(w & 0x7f80u, (w >> 16) & 0x7f80u); }
+
+// a bf16 pair times f, in fp16
+__device__ __forceinline__ uint32_t to_f16(uint32_t w, float f)
+{
+    return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
 
 // 8 codes of a word as fp16 (c - z) s 2^-E: pairs 0, 2 by lo, 1, 3 by hi.
 __device__ __forceinline__ uint4 unpack8(uint32_t w, __half2 lo, __half2 hi, __half2 off)
@@ -230,9 +284,9 @@ __device__ __forceinline__ float ld_peer(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float v)
+__device__ __forceinline__ void st_peer4(uint32_t addr, float x, float y, float z, float w)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
 // CL: one item per cluster; its CTAs take equal runs of the item's tiles.
@@ -299,17 +353,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     Run first;
     first.left = 0;
     bool work;
+    int stride = 1;  // between the CTA's tiles of an item
     MergeRec* rec = nullptr;
     Shares shares{0, 0, 0};
     if (CL) {
-        __syncthreads();
+        // tiles rank, rank + cs, ...: the first one does not depend on the length
         const int cs = (int)cluster_size(), rank = (int)cluster_rank();
         const int x = blockIdx.x / cs, items = a.Hkv * a.mtiles;
         first.b = x / items;
         first.item = x - first.b * items;
+        if (warp >= 8 && warp < 16) {
+            // what the unpacking warps read first and last
+            const int head = first.item / a.mtiles, kv = warp >= 12, i = (threadIdx.x - 256) & 127;
+            const int gr = (first.item - head * a.mtiles) * kRowsTc + ((threadIdx.x - 256) >> 1);
+            if (gr < a.rows)
+                prefetch_l1(a.q + (size_t)(first.b * (long long)a.T + gr / group) * a.q_ld + (size_t)(head * group + gr % group) * D +
+                            (D == 128 ? 64 * (threadIdx.x & 1) : 0));
+            if (i < a.T) {
+                const __nv_bfloat16* src = (kv ? a.vs : a.ks) + (size_t)(first.b * (long long)a.T + i) * a.kv_ld + (size_t)head * D;
+                prefetch_l2(src);
+                if (D == 128) prefetch_l2(src + 64);
+            }
+        } else if (warp == 17 && (rank * 8 + lane) >> a.blk_log2 < a.max_pages) {
+            prefetch_l1(a.table + (size_t)first.b * a.max_pages + ((rank * 8 + lane) >> a.blk_log2));
+        }
         first.len = seq_len(a, first.b);
         const int nt = first.len < 0 ? 0 : (first.len + kTile - 1) / kTile + 1;
-        first.nu = nt, first.u0 = first.t0 = nt * rank / cs, first.u1 = first.t1 = nt * (rank + 1) / cs;
+        first.nu = first.u1 = first.t1 = nt, first.u0 = 0, first.t0 = rank;
+        stride = cs;
+        __syncthreads();
         work = first.t1 > first.t0;
     } else {
         find_starts(a, blockIdx.x, 1, start, scratch);
@@ -352,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             const bool any = mt * kRowsTc + q * 32 < a.rows;  // some row of this warp is there
             const int n0 = n;
             float m = kNoRef, l = 0.f;
-            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 if ((n & 1) != grp) continue;
                 const int b = grp, ph = (n >> 1) & 1;
                 const bool step = tile >= ntc;
@@ -365,82 +437,61 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const float f = fmaxf(scale2(rowf[(segs & 1) * 128 + row], ti->ek), 1e-37f), ev = (float)iev;
                     const bool part = step || live < kTile || bad;
                     const uint32_t* see = vis + 4 * min(gr / group, a.T - 1);
-                    float x[32];
-                    auto load = [&](int c) {  // 32 scores
-                        tmem_ld32(trow + b * 128 + c * 32, x);
-                        if (part) {
-                            uint32_t s;  // which of them count
-                            if (step) {
-                                s = see[c];
-                            } else {
-                                const int left = live - c * 32, hb = bad >> (2 * c);
-                                s = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-                                s &= ~((hb & 1 ? 0xffffu : 0u) | (hb & 2 ? 0xffff0000u : 0u));
-                            }
-#pragma unroll
-                            for (int j = 0; j < 32; j++)
-                                if (!((s >> j) & 1)) x[j] = -INFINITY;
-                        }
+                    auto counts = [&](int c) -> uint32_t {  // which of the scores 16 c .. count
+                        if (step) return (see[c >> 1] >> (16 * (c & 1))) & 0xffffu;
+                        const int left = live - c * 16;
+                        return (bad >> c) & 1 ? 0u : left >= 16 ? 0xffffu : left <= 0 ? 0u : (1u << left) - 1u;
                     };
+                    auto hide = [&](int c, float (&x)[16]) {
+                        const uint32_t s = counts(c);
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            if (!((s >> j) & 1)) x[j] = -INFINITY;
+                    };
+                    auto hide2 = [&](int c, float (&x)[32]) {
+                        const uint32_t s = counts(c) | counts(c + 1) << 16;
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (!((s >> j) & 1)) x[j] = -INFINITY;
+                    };
+                    const uint32_t ts = trow + b * 128;
                     // Weigh with the reference as it is, P going to its own columns; only where
-                    // a row outgrows it (2^15; and in the first tile) find the row's largest
-                    // and weigh again.  The other group may have moved it in the tile before:
-                    // its decision is waited for with the results in hand.
+                    // a row outgrows it (a sum above 2^15, so that no P overflows) find the
+                    // row's largest and weigh again.  The first tile starts from the largest of
+                    // its first 32 scores.  The other group may have moved the reference in the
+                    // tile before: its decision is waited for with the results in hand.
                     const bool lead = n == n0;
                     float sum = 0.f;
-                    auto weigh = [&]() {
-                        const float c0 = ev - m;
-                        float s0 = 0.f, s1 = 0.f;
-                        __half2 top = __float2half2_rn(0.f);
-#pragma unroll 1
-                        for (int c = 0; c < 4; c++) {
-                            load(c);
-                            uint32_t p[16];
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float e0 = ex2(fmaf(x[j], f, c0)), e1 = ex2(fmaf(x[j + 1], f, c0));
-                                s0 += e0, s1 += e1;
-                                p[j / 2] = pack_f16(e0, e1);
-                                top = __hmax2(top, *reinterpret_cast<const __half2*>(&p[j / 2]));
-                            }
-                            tmem_st16(trow + kColP + b * 64 + c * 16, p);
-                        }
-                        sum = s0 + s1;
-                        return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(32768.f));
-                    };
-                    bool again = lead;
-                    if (!lead) {
-                        if (n == n0 + 1) {
-                            wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
-                            m = row_m[row];
-                            again = weigh();
-                        } else {
-                            again = weigh();
-                            wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
-                            const float mm = row_m[row];
-                            if (mm != m) l *= ex2(m - mm), m = mm, again = true;
-                        }
-                        again = __any_sync(0xffffffffu, again);
+                    int look = 0;  // scores / 16 to look for a row's largest in before weighing
+                    if (lead) {
+                        look = 2;
+                    } else if (n == n0 + 1) {
+                        wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
+                        m = row_m[row];
                     }
-                    if (again) {
-                        float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < 4; c++) {
-                            load(c);
+                    while (true) {
+                        if (look) {
+                            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < look; c++) {
+                                float x[16];
+                                tmem_ld16(ts + c * 16, x);
+                                tmem_ld_wait(x);
+                                if (part) hide(c, x);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                t0 = fmaxf(t0, fmaxf(x[j], x[j + 1]));
-                                t1 = fmaxf(t1, fmaxf(x[j + 2], x[j + 3]));
+                                for (int j = 0; j < 16; j += 4) {
+                                    t0 = fmaxf(t0, fmaxf(x[j], x[j + 1]));
+                                    t1 = fmaxf(t1, fmaxf(x[j + 2], x[j + 3]));
+                                }
                             }
-                        }
-                        const float y = fmaxf(t0, t1) * f + ev;
-                        const bool up = y > m + 8.f;
-                        if (__any_sync(0xffffffffu, up)) {
+                            const float y = fmaxf(t0, t1) * f + ev;
+                            const bool up = y > m + 8.f;
                             const float c = up ? ex2(m - y) : 1.f;
                             if (up) m = y;
                             l *= c;
                             row_m[row] = m;
-                            if (!lead) {
+                            if (!lead && __any_sync(0xffffffffu, up)) {
                                 wait(kODone + (b ^ 1), ((n - 1) >> 1) & 1);
                                 tc_fence_after();
 #pragma unroll 1
@@ -453,8 +504,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                                 }
                             }
                         }
-                        if (lead) row_m[row] = m;
-                        weigh();
+                        const float c0 = ev - m;
+                        float s0 = 0.f, s1 = 0.f, xa[32];
+                        // one load ahead of the exponentials: 32 scores are weighed while the next 32 come
+                        tmem_ld32x(ts, xa);
+#pragma unroll 1
+                        for (int c = 0; c < 8; c += 2) {
+                            float xb[32];
+                            tmem_ld32_wait(xa);
+#pragma unroll
+                            for (int j = 0; j < 32; j++) xb[j] = xa[j];
+                            if (c < 6) tmem_ld32x(ts + c * 16 + 32, xa);
+                            if (part) hide2(c, xb);
+                            uint32_t p[16];
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float e0 = ex2(fmaf(xb[j], f, c0)), e1 = ex2(fmaf(xb[j + 1], f, c0));
+                                s0 += e0, s1 += e1;
+                                p[j / 2] = pack_f16(e0, e1);
+                            }
+                            tmem_st16(trow + kColP + b * 64 + c * 8, p);
+                        }
+                        sum = s0 + s1;
+                        if (look == 8) break;
+                        bool again = sum > 32768.f || m == kNoRef;
+                        if (!look && n > n0 + 1) {
+                            wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
+                            const float mm = row_m[row];
+                            if (mm != m) l *= ex2(m - mm), m = mm, again = true;
+                        }
+                        if (!__any_sync(0xffffffffu, again)) break;
+                        look = 8;
                     }
                     l += scale2(sum, -iev);
                     tmem_st_wait();
@@ -532,48 +612,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile;
             if (run.t1 <= run.t0) continue;
+            // the step's rows are needed last: into L2 by then
+            if (!CL && run.t1 > ntc && tid < a.T) {
+                const __nv_bfloat16* src = (kv ? a.vs : a.ks) + (size_t)(run.b * (long long)a.T + tid) * a.kv_ld + (size_t)head * D;
+                prefetch_l2(src);
+                if (D == 128) prefetch_l2(src + 64);
+            }
             // ---- the rows' queries, each by a power of two: channels 32 h + 64 p .. of row `row`
             if (n > 0) wait(kSDone + ((n - 1) & 1), ((n - 1) >> 1) & 1);  // the last tile's S has read the old ones
             {
                 const int row = (threadIdx.x - 256) >> 1, gr = mt * kRowsTc + row;
                 const __nv_bfloat16* src = a.q + (size_t)(run.b * (long long)a.T + gr / group) * a.q_ld +
                                            (size_t)(head * group + gr % group) * D + 32 * h;
-                uint4 u[L::kAtoms][4];
+                // The rows go to their places as they are and are worked on there, in
+                // small loops: code that runs once a tile or less costs 8 cycles an
+                // instruction to fetch.
+                uint8_t* qrow = sm + L::kQ + row * 128;
+#pragma unroll
+                for (int i = 0; i < 4 * L::kAtoms; i++)
+                    *(uint4*)(qrow + piece_at(i, h, row)) =
+                        gr < a.rows ? *(const uint4*)(src + 64 * (i >> 2) + 8 * (i & 3)) : make_uint4(0, 0, 0, 0);
                 uint32_t top = 0;
-#pragma unroll
-                for (int p = 0; p < L::kAtoms; p++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        u[p][i] = gr < a.rows ? *(const uint4*)(src + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int p = 0; p < L::kAtoms; p++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t* w = (const uint32_t*)&u[p][i];
-#pragma unroll
-                        for (int k = 0; k < 4; k++) top = max(top, max((w[k] << 16) & 0x7f800000u, w[k] & 0x7f800000u));
-                    }
+#pragma unroll 1
+                for (int i = 0; i < 4 * L::kAtoms; i++) {
+                    const uint4 u = *(const uint4*)(qrow + piece_at(i, h, row));
+                    top = max(top, max(max(high_exp(u.x), high_exp(u.y)), max(high_exp(u.z), high_exp(u.w))));
+                }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                const int e = min(max((int)(top >> 23), 16), 236);
+                const int e = min(max((int)(top >> 7), 16), 236);
                 const float down = pow2i(11 + 127 - e);  // the largest comes to [2^11, 2^12)
-#pragma unroll
-                for (int p = 0; p < L::kAtoms; p++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t* w = (const uint32_t*)&u[p][i];
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            y[k] = pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-                        *(uint4*)(sm + L::kQ + p * (128 * 128) + row * 128 + (((4 * h + i) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+#pragma unroll 1
+                for (int i = 0; i < 4 * L::kAtoms; i++) {
+                    uint4* at = (uint4*)(qrow + piece_at(i, h, row));
+                    const uint4 u = *at;
+                    *at = make_uint4(to_f16(u.x, down), to_f16(u.y, down), to_f16(u.z, down), to_f16(u.w, down));
+                }
                 if (h == 0) rowf[(segs & 1) * 128 + row] = pow2i(e - 127 - 11) * a.sl2;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + kQReady);
                 segs++;
             }
-            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 const int b = n & 1, ph = (n >> 1) & 1;
                 uint8_t* dst = sm + (kv ? L::kV : L::kK) + b * L::kOperand;
                 TileInfo* ti = info + (n & 7);
@@ -585,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const int live = ti->live, bad = ti->bad, E = kv ? ti->ev : ti->ek;
                     if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);  // tile n - 2's product has read the buffer
                     // key rows tid / 2 and 64 + tid / 2, half of each 64-channel panel
-#pragma unroll
+#pragma unroll 1
                     for (int r2 = 0; r2 < 2; r2++) {
                         const int row = (tid >> 1) + 64 * r2;
                         const uint8_t* blk = stage + (row >> 4) * kv4_block_bytes(D);
@@ -616,22 +696,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 } else {
                     // the step's own rows: bf16 to fp16 by the tile's largest finite exponent
                     const __nv_bfloat16* src = (kv ? a.vs : a.ks) + (size_t)run.b * a.T * a.kv_ld + (size_t)head * D + 32 * h;
-                    uint32_t e = 0;
+                    uint32_t odd_rows = 0;  // this thread's two rows
+                    if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);  // tile n - 2's product has read the buffer
+                    // as they are, then worked on in place (see the queries): 16-byte pieces
+                    // i of the rows tid / 2 and 64 + tid / 2
+                    auto place = [&](int i) {
+                        const int row = (tid >> 1) + 64 * (i / (4 * L::kAtoms));
+                        return (uint4*)(dst + row * 128 + piece_at(i % (4 * L::kAtoms), h, row));
+                    };
+#pragma unroll
+                    for (int i = 0; i < 8 * L::kAtoms; i++) {
+                        const int row = (tid >> 1) + 64 * (i / (4 * L::kAtoms)), j = i % (4 * L::kAtoms);
+                        *place(i) = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * (j >> 2) + 8 * (j & 3)) : make_uint4(0, 0, 0, 0);
+                    }
+                    // the largest finite exponent; whether there are others
+                    uint32_t e = 0, all = 0;
 #pragma unroll 1
-                    for (int r2 = 0; r2 < 2; r2++) {
-                        const int row = (tid >> 1) + 64 * r2;
+                    for (int i = 0; i < 8 * L::kAtoms; i++) {
+                        const uint4 u = *place(i);
+                        const uint32_t x = max(max(high_exp(u.x), high_exp(u.y)), max(high_exp(u.z), high_exp(u.w)));
+                        all = max(all, x);
+                        if (x < 0x7f80u) e = max(e, x);
+                    }
+                    e >>= 7;
+                    if (__any_sync(0xffffffffu, all >= 0x7f80u)) {
+                        // (rare) per element: largest finite exponent; of V's, which rows have others
+#pragma unroll 1
+                        for (int i = 0; i < 8 * L::kAtoms; i++) {
+                            uint4* at = place(i);
+                            uint32_t w[4] = {at->x, at->y, at->z, at->w};
+                            bool found = false;
 #pragma unroll
-                        for (int p = 0; p < L::kAtoms; p++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const uint4 u = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
-                                const uint32_t* w = (const uint32_t*)&u;
-#pragma unroll
-                                for (int k = 0; k < 4; k++) {
-                                    const uint32_t x0 = (w[k] >> 7) & 255u, x1 = (w[k] >> 23) & 255u;
-                                    e = max(e, max(x0 < 255 ? x0 : 0u, x1 < 255 ? x1 : 0u));
-                                }
+                            for (int k = 0; k < 4; k++) {
+                                const uint32_t x0 = (w[k] >> 7) & 255u, x1 = (w[k] >> 23) & 255u;
+                                e = max(e, max(x0 < 255 ? x0 : 0u, x1 < 255 ? x1 : 0u));
+                                found |= x0 == 255 || x1 == 255;
+                                // zero times these is NaN: the product of V runs without them (TileInfo::odd)
+                                if (kv) w[k] &= (x0 == 255 ? 0xffff0000u : ~0u) & (x1 == 255 ? 0xffffu : ~0u);
                             }
+                            *at = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (found) odd_rows |= 1u << (i / (4 * L::kAtoms));
+                        }
                     }
                     e = __reduce_max_sync(0xffffffffu, e);
                     if (lane == 0) red_e[kv * 4 + uw] = e;
@@ -645,32 +750,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         if (kv) ti->ev = E;
                         else ti->ek = E, ti->live = kTile, ti->bad = 0;
                     }
-                    if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);
                     const float f = pow2i(-E);
 #pragma unroll 1
-                    for (int r2 = 0; r2 < 2; r2++) {
-                        const int row = (tid >> 1) + 64 * r2;
-                        bool odd = false;
-#pragma unroll
-                        for (int p = 0; p < L::kAtoms; p++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const uint4 u = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * p + 8 * i) : make_uint4(0, 0, 0, 0);
-                                const uint32_t* w = (const uint32_t*)&u;
-                                uint32_t y[4];
-#pragma unroll
-                                for (int k = 0; k < 4; k++) {
-                                    float x0 = __uint_as_float(w[k] << 16), x1 = __uint_as_float(w[k] & 0xffff0000u);
-                                    if (kv) {
-                                        // zero times these is NaN: the product runs without them (TileInfo::odd)
-                                        if (!(fabsf(x0) < INFINITY)) odd = true, x0 = 0.f;
-                                        if (!(fabsf(x1) < INFINITY)) odd = true, x1 = 0.f;
-                                    }
-                                    y[k] = pack_f16(x0 * f, x1 * f);
-                                }
-                                *(uint4*)(dst + p * (128 * 128) + row * 128 + (((4 * h + i) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                            }
-                        if (odd) atomicOr(&ti->odd[row >> 5], 1u << (row & 31));
+                    for (int i = 0; i < 8 * L::kAtoms; i++) {
+                        uint4* at = place(i);
+                        const uint4 u = *at;
+                        *at = make_uint4(to_f16(u.x, f), to_f16(u.y, f), to_f16(u.z, f), to_f16(u.w, f));
+                    }
+                    if (kv && odd_rows) {
+                        const int row = tid >> 1;
+                        if (odd_rows & 1) atomicOr(&ti->odd[row >> 5], 1u << (row & 31));
+                        if (odd_rows & 2) atomicOr(&ti->odd[(row >> 5) + 2], 1u << (row & 31));
                     }
                     fence_proxy_async();
                     __syncwarp();
@@ -714,7 +804,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             __syncwarp();
         };
         do {
-            const int tiles = run.t1 - run.t0;
+            const int tiles = (run.t1 - run.t0 + stride - 1) / stride;
             if (tiles <= 0) continue;
             scores(n & 1, (n >> 1) & 1, true);
             for (int i = 0; i < tiles; i++, n++) {
@@ -762,11 +852,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         };
         do {
             const int head = run.item / a.mtiles, ntc = (run.len + kTile - 1) / kTile;
-            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+            // the pages of four tiles' blocks at a time, and of the next four ahead
+            const int* pages = a.table + (size_t)run.b * a.max_pages;
+            auto look_up = [&](int tile) {
+                const int blk = (tile + (lane >> 3) * stride) * 8 + (lane & 7);
+                return blk * 16 < run.len ? __ldg(pages + (blk >> a.blk_log2)) : 0;
+            };
+            int pg = look_up(run.t0), pg_next = look_up(run.t0 + 4 * stride), turn = -1;
+            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 if (tile >= ntc) continue;
                 const int s = fills % kRing, blk = tile * 8 + lane, live = min(run.len - tile * kTile, kTile);
                 const bool mine = lane < 8 && lane * 16 < live;
-                const int page = mine ? __ldg(a.table + (size_t)run.b * a.max_pages + (blk >> a.blk_log2)) : 0;
+                turn = (turn + 1) & 3;
+                if (turn == 0 && tile > run.t0) pg = pg_next, pg_next = look_up(tile + 4 * stride);
+                const int page_of = __shfl_sync(0xffffffffu, pg, (8 * turn + lane) & 31), page = mine ? page_of : 0;
                 const bool bad = (unsigned)page >= (unsigned)a.n_pages;
                 const uint32_t bads = __ballot_sync(0xffffffffu, bad), who = __ballot_sync(0xffffffffu, mine);
                 // until the stage is free, and after it: the powers of tiles that have landed
@@ -811,19 +910,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         // ---- the cluster's parts meet: every CTA sums its share of the channels
         const int cs = (int)cluster_size(), rank = (int)cluster_rank(), row = threadIdx.x & 127, grp = threadIdx.x >> 7;
         const int head = first.item / a.mtiles, mt = first.item - head * a.mtiles, gr = mt * kRowsTc + row;
-        const int ntc = (first.len + kTile - 1) / kTile, slice = D / cs;
+        const int ntc = (first.len + kTile - 1) / kTile;
+        const int slice_log2 = __ffs(D / cs) - 1, slice = 1 << slice_log2;  // (cs is a power of two)
         const bool mine = warp < 8 && gr < a.rows && first.len >= 0;
         if (warp < 4) row_m[row] = out_m, row_l[row] = out_l;
         cluster_sync();  // also: no CTA's products read K any more, where the parts go
-        float* parts = (float*)(sm + L::kK);  // [rank][slice][128 rows]
+        float* parts = (float*)(sm + L::kK);  // [rank][slice / 4][128 rows][4]
         if (warp < 8) {
-            float top = kNoRef, sum = 0.f;
-            for (int r = 0; r < cs; r++) top = fmaxf(top, ld_peer(peer(row_m + row, r)));
-            for (int r = 0; r < cs; r++) sum += ld_peer(peer(row_l + row, r)) * ex2(ld_peer(peer(row_m + row, r)) - top);
+            float top = kNoRef, sum = 0.f, ms[8], ls[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++) {
+                ms[r] = kNoRef, ls[r] = 0.f;
+                if (r < cs) ms[r] = ld_peer(peer(row_m + row, r)), ls[r] = ld_peer(peer(row_l + row, r));
+            }
+#pragma unroll
+            for (int r = 0; r < 8; r++) top = fmaxf(top, ms[r]);
+#pragma unroll
+            for (int r = 0; r < 8; r++) sum += ls[r] * ex2(ms[r] - top);
             const float w = ex2(out_m - top) / sum;
             const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t* odd = info[(n - 1) & 7].odd;
-            const bool fix = work && first.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+            const bool fix = work && (ntc & (cs - 1)) == rank && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < D / 2; j += 32) {
@@ -839,23 +946,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 if (fix && mine) add_odd(a, odd, vis + 4 * (gr / group), first.b, head * D + c, o);
                 if (mine)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        // (8 channels are of one slice: a slice has 8 at least)
-                        const uint32_t to = peer(parts + ((size_t)rank * slice + (c + i) % slice) * 128 + row, (c + i) / slice);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) st_peer(to + k * 512, o[i + k] * w);
-                    }
+                    for (int i = 0; i < 32; i += 4)
+                        st_peer4(peer(parts + (((size_t)rank * slice + ((c + i) & (slice - 1))) * 32 + row) * 4, (c + i) >> slice_log2), o[i] * w,
+                                 o[i + 1] * w, o[i + 2] * w, o[i + 3] * w);
             }
         }
         cluster_sync();
         if (mine) {
             __nv_bfloat16* orow = a.out + ((size_t)(first.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + rank * slice;
-            for (int c = grp * 4; c < slice; c += 8) {
-                float v[4] = {};
-                for (int r = 0; r < cs; r++)
+            for (int c = grp * (slice / 2); c < (grp + 1) * (slice / 2); c += 4) {
+                float4 v[8], y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) v[k] += parts[((size_t)r * slice + c + k) * 128 + row];
-                *(uint2*)(orow + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                for (int r = 0; r < 8; r++)
+                    if (r < cs) v[r] = *(const float4*)(parts + (((size_t)r * slice + c) * 32 + row) * 4);
+#pragma unroll
+                for (int r = 0; r < 8; r++)
+                    if (r < cs) y.x += v[r].x, y.y += v[r].y, y.z += v[r].z, y.w += v[r].w;
+                *(uint2*)(orow + c) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
             }
         }
     }

@@ -66,6 +66,8 @@ struct Shares {
     __device__ __forceinline__ long long at(int t) const { return q * t + min(t, r); }
 };
 
+__device__ __noinline__ long long div_long(long long a, int b) { return a / b; }
+
 __device__ __forceinline__ Shares shares_of(long long total, int teams)
 {
     // (a 64-bit division takes half a microsecond)
@@ -73,7 +75,7 @@ __device__ __forceinline__ Shares shares_of(long long total, int teams)
         const uint32_t q = (uint32_t)total / (uint32_t)teams;
         return Shares{q, (int)((uint32_t)total - q * (uint32_t)teams), 0};
     }
-    const long long q = total / teams;
+    const long long q = div_long(total, teams);
     return Shares{q, (int)(total - q * teams), 0};
 }
 
@@ -142,7 +144,7 @@ struct Run {
         b = s.b;
         len = seq_len(a, b);
         nu = item_units(a, len);
-        item = s.off < (1LL << 31) ? (int)((uint32_t)s.off / (uint32_t)nu) : (int)(s.off / nu);
+        item = s.off < (1LL << 31) ? (int)((uint32_t)s.off / (uint32_t)nu) : (int)div_long(s.off, nu);
         cut(a, (int)(s.off - (long long)item * nu));
     }
     __device__ __forceinline__ bool next(const Kv4Attn& a)
