@@ -94,28 +94,6 @@ __device__ __forceinline__ void tmem_ld_wait(float (&v)[16])
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
                    "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
 }
-__device__ __forceinline__ void tmem_ld32x(uint32_t taddr, float (&v)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
-          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld32_wait(float (&v)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
-                   "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
-                 :
-                 : "memory");
-    asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -165,6 +143,27 @@ __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
+// packed pairs of fp32: one instruction for two
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float pow2i(int e)  // 2^e, e in -126 .. 127
 {
     return __uint_as_float((uint32_t)(e + 127) << 23);
@@ -204,11 +203,10 @@ enum {  // barriers
 };
 constexpr uint32_t kColO = 256, kColP = 384;  // tensor memory: S [2][128], O [D], P [2][64]
 
-// Byte offset of 16-byte piece i (of a row's half h: 4 in each 64-channel
-// panel) from the row's place in the first panel, with the 128-byte swizzle.
-__device__ __forceinline__ int piece_at(int i, int h, int row)
+// Byte offset of 16-byte piece i of a row in an operand, with the 128-byte swizzle.
+__device__ __forceinline__ int piece_at(int i, int row)
 {
-    return (i >> 2) * (128 * 128) + (((4 * h + (i & 3)) ^ (row & 7)) << 4);
+    return (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
 }
 
 // the larger exponent of a bf16 pair, in place (bits 7 - 14)
@@ -448,12 +446,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         for (int j = 0; j < 16; j++)
                             if (!((s >> j) & 1)) x[j] = -INFINITY;
                     };
-                    auto hide2 = [&](int c, float (&x)[32]) {
-                        const uint32_t s = counts(c) | counts(c + 1) << 16;
-#pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            if (!((s >> j) & 1)) x[j] = -INFINITY;
-                    };
                     const uint32_t ts = trow + b * 128;
                     // Weigh with the reference as it is, P going to its own columns; only where
                     // a row outgrows it (a sum above 2^15, so that no P overflows) find the
@@ -505,26 +497,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                             }
                         }
                         const float c0 = ev - m;
-                        float s0 = 0.f, s1 = 0.f, xa[32];
-                        // one load ahead of the exponentials: 32 scores are weighed while the next 32 come
-                        tmem_ld32x(ts, xa);
+                        uint64_t s2 = 0;  // two sums
+                        const uint64_t f2 = pair(f, f), c2 = pair(c0, c0);
 #pragma unroll 1
                         for (int c = 0; c < 8; c += 2) {
-                            float xb[32];
-                            tmem_ld32_wait(xa);
+                            float x[32];
+                            tmem_ld32(ts + c * 16, x);
+                            if (part) {
+                                const uint32_t s = counts(c) | counts(c + 1) << 16;
 #pragma unroll
-                            for (int j = 0; j < 32; j++) xb[j] = xa[j];
-                            if (c < 6) tmem_ld32x(ts + c * 16 + 32, xa);
-                            if (part) hide2(c, xb);
+                                for (int j = 0; j < 32; j++)
+                                    if (!((s >> j) & 1)) x[j] = -INFINITY;
+                            }
                             uint32_t p[16];
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
-                                const float e0 = ex2(fmaf(xb[j], f, c0)), e1 = ex2(fmaf(xb[j + 1], f, c0));
-                                s0 += e0, s1 += e1;
+                                float e0, e1;
+                                unpair(fma2(pair(x[j], x[j + 1]), f2, c2), e0, e1);
+                                e0 = ex2(e0), e1 = ex2(e1);
+                                s2 = add2(s2, pair(e0, e1));
                                 p[j / 2] = pack_f16(e0, e1);
                             }
                             tmem_st16(trow + kColP + b * 64 + c * 8, p);
                         }
+                        float s0, s1;
+                        unpair(s2, s0, s1);
                         sum = s0 + s1;
                         if (look == 8) break;
                         bool again = sum > 32768.f || m == kNoRef;
@@ -618,36 +615,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 prefetch_l2(src);
                 if (D == 128) prefetch_l2(src + 64);
             }
-            // ---- the rows' queries, each by a power of two: channels 32 h + 64 p .. of row `row`
+            // ---- the rows' queries, each by a power of two
             if (n > 0) wait(kSDone + ((n - 1) & 1), ((n - 1) >> 1) & 1);  // the last tile's S has read the old ones
             {
-                const int row = (threadIdx.x - 256) >> 1, gr = mt * kRowsTc + row;
-                const __nv_bfloat16* src = a.q + (size_t)(run.b * (long long)a.T + gr / group) * a.q_ld +
-                                           (size_t)(head * group + gr % group) * D + 32 * h;
-                // The rows go to their places as they are and are worked on there, in
-                // small loops: code that runs once a tile or less costs 8 cycles an
-                // instruction to fetch.
-                uint8_t* qrow = sm + L::kQ + row * 128;
+                // Neighbouring threads take neighbouring 16-byte pieces of a row (spread over
+                // rows, each load would touch 32 lines); short loops, because code that runs
+                // once costs 8 cycles an instruction to fetch.
+                constexpr int kPieces = D / 8, kPass = 256 / kPieces;
+                const int pc = (threadIdx.x - 256) % kPieces, r0 = (threadIdx.x - 256) / kPieces;
+                uint8_t* q0 = sm + L::kQ;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 128 / kPass; i0 += 4) {
+                    // (loads first: none moves above a store to shared memory by itself)
+                    uint4 u[4];
 #pragma unroll
-                for (int i = 0; i < 4 * L::kAtoms; i++)
-                    *(uint4*)(qrow + piece_at(i, h, row)) =
-                        gr < a.rows ? *(const uint4*)(src + 64 * (i >> 2) + 8 * (i & 3)) : make_uint4(0, 0, 0, 0);
-                uint32_t top = 0;
-#pragma unroll 1
-                for (int i = 0; i < 4 * L::kAtoms; i++) {
-                    const uint4 u = *(const uint4*)(qrow + piece_at(i, h, row));
-                    top = max(top, max(max(high_exp(u.x), high_exp(u.y)), max(high_exp(u.z), high_exp(u.w))));
+                    for (int i = 0; i < 4; i++) {
+                        const int gr = mt * kRowsTc + r0 + (i0 + i) * kPass;
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        if (gr < a.rows)
+                            u[i] = *(const uint4*)(a.q + (size_t)(run.b * (long long)a.T + gr / group) * a.q_ld + (size_t)(head * group + gr % group) * D + 8 * pc);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int row = r0 + (i0 + i) * kPass;
+                        uint32_t top = max(max(high_exp(u[i].x), high_exp(u[i].y)), max(high_exp(u[i].z), high_exp(u[i].w)));
+#pragma unroll
+                        for (int o = 1; o < kPieces; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = min(max((int)(top >> 7), 16), 236);
+                        const float down = pow2i(11 + 127 - e);  // the largest comes to [2^11, 2^12)
+                        *(uint4*)(q0 + piece_at(pc, row)) = make_uint4(to_f16(u[i].x, down), to_f16(u[i].y, down), to_f16(u[i].z, down), to_f16(u[i].w, down));
+                        if (pc == 0) rowf[(segs & 1) * 128 + row] = pow2i(e - 127 - 11) * a.sl2;
+                    }
                 }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                const int e = min(max((int)(top >> 7), 16), 236);
-                const float down = pow2i(11 + 127 - e);  // the largest comes to [2^11, 2^12)
-#pragma unroll 1
-                for (int i = 0; i < 4 * L::kAtoms; i++) {
-                    uint4* at = (uint4*)(qrow + piece_at(i, h, row));
-                    const uint4 u = *at;
-                    *at = make_uint4(to_f16(u.x, down), to_f16(u.y, down), to_f16(u.z, down), to_f16(u.w, down));
-                }
-                if (h == 0) rowf[(segs & 1) * 128 + row] = pow2i(e - 127 - 11) * a.sl2;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar + kQReady);
@@ -695,34 +694,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     fills++;
                 } else {
                     // the step's own rows: bf16 to fp16 by the tile's largest finite exponent
-                    const __nv_bfloat16* src = (kv ? a.vs : a.ks) + (size_t)run.b * a.T * a.kv_ld + (size_t)head * D + 32 * h;
-                    uint32_t odd_rows = 0;  // this thread's two rows
+                    constexpr int kPieces = D / 8, kPass = 128 / kPieces;
+                    const int pc = tid % kPieces, r0 = tid / kPieces;  // as the queries
+                    const __nv_bfloat16* src = (kv ? a.vs : a.ks) + ((size_t)run.b * a.T + r0) * a.kv_ld + (size_t)head * D + 8 * pc;
+                    uint32_t odd_rows = 0;  // bit i: of row r0 + i kPass
                     if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);  // tile n - 2's product has read the buffer
-                    // as they are, then worked on in place (see the queries): 16-byte pieces
-                    // i of the rows tid / 2 and 64 + tid / 2
-                    auto place = [&](int i) {
-                        const int row = (tid >> 1) + 64 * (i / (4 * L::kAtoms));
-                        return (uint4*)(dst + row * 128 + piece_at(i % (4 * L::kAtoms), h, row));
-                    };
-#pragma unroll
-                    for (int i = 0; i < 8 * L::kAtoms; i++) {
-                        const int row = (tid >> 1) + 64 * (i / (4 * L::kAtoms)), j = i % (4 * L::kAtoms);
-                        *place(i) = row < a.T ? *(const uint4*)(src + (size_t)row * a.kv_ld + 64 * (j >> 2) + 8 * (j & 3)) : make_uint4(0, 0, 0, 0);
-                    }
-                    // the largest finite exponent; whether there are others
+                    auto place = [&](int i) { return (uint4*)(dst + piece_at(pc, r0 + i * kPass)); };
+                    // to their places as they are; the largest finite exponent, and whether there are others
                     uint32_t e = 0, all = 0;
 #pragma unroll 1
-                    for (int i = 0; i < 8 * L::kAtoms; i++) {
-                        const uint4 u = *place(i);
-                        const uint32_t x = max(max(high_exp(u.x), high_exp(u.y)), max(high_exp(u.z), high_exp(u.w)));
-                        all = max(all, x);
-                        if (x < 0x7f80u) e = max(e, x);
+                    for (int i0 = 0; i0 < 128 / kPass; i0 += 8) {
+                        uint4 u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            u[i] = r0 + (i0 + i) * kPass < a.T ? *(const uint4*)(src + (size_t)((i0 + i) * kPass) * a.kv_ld) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const uint32_t x = max(max(high_exp(u[i].x), high_exp(u[i].y)), max(high_exp(u[i].z), high_exp(u[i].w)));
+                            all = max(all, x);
+                            if (x < 0x7f80u) e = max(e, x);
+                            *place(i0 + i) = u[i];
+                        }
                     }
                     e >>= 7;
                     if (__any_sync(0xffffffffu, all >= 0x7f80u)) {
                         // (rare) per element: largest finite exponent; of V's, which rows have others
 #pragma unroll 1
-                        for (int i = 0; i < 8 * L::kAtoms; i++) {
+                        for (int i = 0; i < 128 / kPass; i++) {
                             uint4* at = place(i);
                             uint32_t w[4] = {at->x, at->y, at->z, at->w};
                             bool found = false;
@@ -735,7 +733,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                                 if (kv) w[k] &= (x0 == 255 ? 0xffff0000u : ~0u) & (x1 == 255 ? 0xffffu : ~0u);
                             }
                             *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (found) odd_rows |= 1u << (i / (4 * L::kAtoms));
+                            if (found) odd_rows |= 1u << i;
                         }
                     }
                     e = __reduce_max_sync(0xffffffffu, e);
@@ -752,16 +750,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     }
                     const float f = pow2i(-E);
 #pragma unroll 1
-                    for (int i = 0; i < 8 * L::kAtoms; i++) {
-                        uint4* at = place(i);
-                        const uint4 u = *at;
-                        *at = make_uint4(to_f16(u.x, f), to_f16(u.y, f), to_f16(u.z, f), to_f16(u.w, f));
+                    for (int i0 = 0; i0 < 128 / kPass; i0 += 4) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) u[i] = *place(i0 + i);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            *place(i0 + i) = make_uint4(to_f16(u[i].x, f), to_f16(u[i].y, f), to_f16(u[i].z, f), to_f16(u[i].w, f));
                     }
-                    if (kv && odd_rows) {
-                        const int row = tid >> 1;
-                        if (odd_rows & 1) atomicOr(&ti->odd[row >> 5], 1u << (row & 31));
-                        if (odd_rows & 2) atomicOr(&ti->odd[(row >> 5) + 2], 1u << (row & 31));
-                    }
+                    if (kv)
+                        for (uint32_t left = odd_rows; left; left &= left - 1) {
+                            const int row = r0 + (__ffs(left) - 1) * kPass;
+                            atomicOr(&ti->odd[row >> 5], 1u << (row & 31));
+                        }
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + (kv ? kVReady : kKReady) + b);
