@@ -40,7 +40,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cstdlib>
 #include <mutex>
 
 #include "kv4_sched.cuh"
@@ -84,13 +83,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
 // bf16 pair with its NaNs and infinities replaced by 0; whether there were any
 __device__ __forceinline__ bool drop_nonfinite(uint32_t& u)
 {
@@ -100,20 +92,30 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& u)
     return lo || hi;
 }
 
-constexpr float kMinScale = 0x1p-92f;  // V scales below it count as it (values under 2^-88)
+constexpr float kMinScale = 0x1p-92f;  // added to V scales, so that their logarithm exists (values under 2^-88 differ)
 
 // ------------------------------------------------------------------ kernel ---
 
-template <int D, int NB, int TW>
+// Where a row of a KV head is, relative to its sequence and head, and which
+// step rows it sees (bits).
+constexpr int kMaxRows = 16;
+struct RowAt {
+    int q, out;
+    uint32_t sees;
+    int pad;
+};
+
+template <int D, int TW>
 struct RowsSmem {
-    static constexpr int kR = 8 * NB;
-    static constexpr int kStages = NB == 1 && TW > 1 ? 2 : 3;
+    static constexpr int kR = 8;
+    static constexpr int kStages = TW > 1 ? 2 : 3;
     static constexpr int kBlk = 2 * kv4_block_bytes(D);
     static constexpr int kRing = kWarps * kStages * kBlk;
     static constexpr int kBar = kRing;                                          // full, empty
     static constexpr int kLive = kBar + kWarps * kStages * 16;                  // keys of each stage's block
     static constexpr int kMisc = kLive + (kWarps * kStages * 4 + 15) / 16 * 16;  // starts and scan scratch
-    static constexpr int kMerge = kMisc + (kWarps * (int)sizeof(Start) + (kWarps + 2) * 8 + 15) / 16 * 16;
+    static constexpr int kTab = kMisc + (kWarps * (int)sizeof(Start) + (kWarps + 2) * 8 + 15) / 16 * 16;
+    static constexpr int kMerge = kTab + kMaxRows * (int)sizeof(RowAt);
     static constexpr int kMergeBytes = TW == 1 ? 0 : kWarps * kR * (D + 4) * 4;  // [warp][row][D | M, sum]
     static constexpr int kBytes = kMerge + kMergeBytes;
     static_assert(kMisc % 8 == 0 && kMerge % 16 == 0, "alignment");
@@ -147,7 +149,7 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
                 page = __ldg(entry);
                 left = r.len - t * kKeys;
                 page1 = left > 16 ? (a.blk_log2 ? page : __ldg(entry + 1)) : -2;
-                head = r.item / a.mtiles;
+                head = r.item >> (a.mtiles >> 1);
                 blk = (2 * t) & ((1 << a.blk_log2) - 1);
                 pend = true;
                 t += TW;
@@ -204,25 +206,32 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
     }
 }
 
-template <int D, int NB, int TW>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn a)
+template <int D, int TW>
+__global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
 {
-    using L = RowsSmem<D, NB, TW>;
+    using L = RowsSmem<D, TW>;
     constexpr int S = L::kStages, R = L::kR, PAN = D / 64, MB = D / 16, DV = D / 8, BLK = kv4_block_bytes(D);
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint64_t *full = (uint64_t*)(sm + L::kBar), *empty = full + kWarps * S;
     int* live_of = (int*)(sm + L::kLive);
     Start* starts = (Start*)(sm + L::kMisc);
+    RowAt* tab = (RowAt*)(sm + L::kTab);
+    const int group = a.H / a.Hkv;
     if (threadIdx.x < kWarps * S) {
         mbar_init(full + threadIdx.x, 1);
         mbar_init(empty + threadIdx.x, 1);
         mbar_fence_init();
+    } else if (threadIdx.x >= 64 && threadIdx.x < 64 + kMaxRows) {
+        const int r = threadIdx.x - 64, i = r / group;
+        uint32_t see = 0;
+        for (int j = 0; j < a.T; j++) see |= kv4_sees(i, j, a.W, a.n1) ? 1u << j : 0u;
+        tab[r] = RowAt{i * a.q_ld + (r - i * group) * D, (i * a.H + r - i * group) * D, see, 0};
     }
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0) raise_long(a);
-    // (its barriers also publish the mbarriers)
+    // (its barriers also publish the mbarriers and the table)
     find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, (long long*)(starts + kWarps));
     if (warp == kWarps) {
         const int w = min(lane, kWarps - 1);
@@ -234,12 +243,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
     const int wi = TW == 1 ? 0 : warp;  // this warp's place in its team
     const int team = TW == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
     const Start st = starts[TW == 1 ? warp : 0];
-    const uint8_t* ring = sm + warp * S * L::kBlk;
     full += warp * S, empty += warp * S, live_of += warp * S;
     MergeRec* rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D)) + team;
     const bool writes_rec = a.part && team < a.nteams && lane == 0 && wi == 0;
     if (writes_rec) rec->rest = 0;
-    const int group = a.H / a.Hkv;
     bool alive = true;  // no wait has given up
     int s = 0, phase = 0;
     Run run;
@@ -248,74 +255,65 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
         run.begin(a, st);
         bool first = true;
         do {
-            const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
+            const int mt = run.item & (a.mtiles - 1), head = run.item >> (a.mtiles >> 1);  // 1 or 2 row tiles
             const int ntc = (run.len + kKeys - 1) / kKeys;
-            // the step's rows of this KV head are needed last: have them near by then
-            if (run.t1 > ntc && lane < min(a.T, 16)) {
-                const size_t at = (size_t)(run.b * (long long)a.T + lane) * a.kv_ld + (size_t)head * D;
+            const __nv_bfloat16* q_base = a.q + (size_t)run.b * a.T * a.q_ld + (size_t)head * group * D;
+            // needed last: the step's rows of this KV head; then the next head's queries
+            const size_t step_at = (size_t)run.b * a.T * a.kv_ld + (size_t)head * D;
+            if (run.t1 > ntc && lane < a.T) {
+                const size_t at = step_at + (size_t)lane * a.kv_ld;
                 prefetch_l1(a.ks + at), prefetch_l1(a.vs + at);
                 if (D == 128) prefetch_l1(a.ks + at + 64), prefetch_l1(a.vs + at + 64);
             }
-            auto q_row = [&](int nb) {
-                const int r = mt * R + nb * 8 + g;
-                return a.q + (size_t)(run.b * (long long)a.T + r / group) * a.q_ld + (size_t)(head * group + r % group) * D + 16 * t;
-            };
-            float o[NB][MB][4], m[NB][2], l[NB][2];
+            const bool q_here = mt * R + g < a.rows;
+            const __nv_bfloat16* q_row = q_base + tab[mt * R + g].q + 16 * t;
+            if (q_here && t < PAN && head + 1 < a.Hkv) prefetch_l1(q_row + group * D + 48 * t);
+            float o[MB][4], m[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};  // rows 2t, 2t + 1
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++) {
-                m[nb][0] = m[nb][1] = kNoRef;
-                l[nb][0] = l[nb][1] = 0.f;
+            for (int i = 0; i < MB; i++)
 #pragma unroll
-                for (int i = 0; i < MB; i++)
+                for (int j = 0; j < 4; j++) o[i][j] = 0.f;
+            // Move the references to the largest y = log2(p s) of the tile (y: of this lane's).
+            auto raise_ref = [&](float y0, float y1) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) o[nb][i][j] = 0.f;
-            }
-            // Move the reference of row 2t + r to the largest y = log2(p s) of the tile; y(i) is
-            // the largest of this lane's for row 2t + (i & 1) of row block i >> 1.
-            auto raise_ref = [&](auto&& y) {
+                for (int r = 0; r < 2; r++) {
+                    float mx = r ? y1 : y0;
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    mx = fmaxf(mx, m[r]);
+                    const float c = ex2(m[r] - mx);
+                    m[r] = mx;
+                    l[r] *= c;
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        float mx = y(nb, r);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mx, m[nb][r]);
-                        const float c = ex2(m[nb][r] - mx);
-                        m[nb][r] = mx;
-                        l[nb][r] *= c;
-#pragma unroll
-                        for (int i = 0; i < MB; i++) o[nb][i][r] *= c, o[nb][i][r + 2] *= c;
-                    }
+                    for (int i = 0; i < MB; i++) o[i][r] *= c, o[i][r + 2] *= c;
+                }
             };
             if (run.t0 + wi < min(run.t1, ntc)) {
                 // ---------------------------------------------- cached keys
-                // this lane's part of the query rows: row 8 nb + g, channels 64 p + 16 t ..
-                uint32_t q[NB][PAN][8];
-                float qs[NB][2], qf[NB][2];  // rows 2t, 2t + 1: sum of q, what undoes q's and the codes' powers of two
-#pragma unroll
-                for (int nb = 0; nb < NB; nb++) {
-                    const bool valid = mt * R + nb * 8 + g < a.rows;
-                    const __nv_bfloat16* src = q_row(nb);
-                    uint32_t raw[PAN][8];
+                // this lane's part of the query rows: row g, channels 64 p + 16 t ..
+                uint32_t q[PAN][8];
+                float qs[2], qf[2];  // rows 2t, 2t + 1: sum of q, what undoes q's and the codes' powers of two
+                {
                     float sum = 0.f, top = 0.f;
 #pragma unroll
                     for (int p = 0; p < PAN; p++) {
                         uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-                        if (valid) {
-                            u0 = *(const uint4*)(src + 64 * p);
-                            u1 = *(const uint4*)(src + 64 * p + 8);
+                        if (q_here) {
+                            u0 = *(const uint4*)(q_row + 64 * p);
+                            u1 = *(const uint4*)(q_row + 64 * p + 8);
                         }
-                        raw[p][0] = u0.x, raw[p][1] = u0.y, raw[p][2] = u0.z, raw[p][3] = u0.w;
-                        raw[p][4] = u1.x, raw[p][5] = u1.y, raw[p][6] = u1.z, raw[p][7] = u1.w;
+                        q[p][0] = u0.x, q[p][1] = u0.y, q[p][2] = u0.z, q[p][3] = u0.w;
+                        q[p][4] = u1.x, q[p][5] = u1.y, q[p][6] = u1.z, q[p][7] = u1.w;
+                    }
+#pragma unroll
+                    for (int p = 0; p < PAN; p++)
 #pragma unroll
                         for (int i = 0; i < 8; i++) {
-                            const float lo = __uint_as_float(raw[p][i] << 16), hi = __uint_as_float(raw[p][i] & 0xffff0000u);
+                            const float lo = __uint_as_float(q[p][i] << 16), hi = __uint_as_float(q[p][i] & 0xffff0000u);
                             sum += lo + hi;
                             top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
                         }
-                    }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -329,13 +327,12 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
 #pragma unroll
                         for (int i = 0; i < 8; i++) {
                             const float f = i & 1 ? down * 0.0625f : down;
-                            q[nb][p][i] = pack_f16(__uint_as_float(raw[p][i] << 16) * f,
-                                                   __uint_as_float(raw[p][i] & 0xffff0000u) * f);
+                            q[p][i] = pack_f16(__uint_as_float(q[p][i] << 16) * f, __uint_as_float(q[p][i] & 0xffff0000u) * f);
                         }
-                    qs[nb][0] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t);
-                    qs[nb][1] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t + 4);
-                    qf[nb][0] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t);
-                    qf[nb][1] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t + 4);
+                    qs[0] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t);
+                    qs[1] = __shfl_sync(0xffffffffu, sum * a.sl2, 8 * t + 4);
+                    qf[0] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t);
+                    qf[1] = __shfl_sync(0xffffffffu, up * a.sl2, 8 * t + 4);
                 }
                 const int k0 = kv4_key(g), k1 = k0 + 8;
                 const int kA = t, kB = 4 + (t ^ 3);  // V's keys: probability slots 2t, 2t + 1; + 8: slots 2t + 8, 2t + 9
@@ -349,14 +346,14 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                                 break;
                             }
                     }
-                    const uint8_t* stage = ring + s * L::kBlk;
+                    const uint8_t* stage = sm + (warp * S + s) * L::kBlk;
                     const int live = live_of[s];
-                    float x[2][NB][4], sv[2][2];  // per block: scores; V scales of the keys k0, k1
+                    float x[2][4], sv[2][2];  // per block: scores; V scales of the keys k0, k1
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
                         const uint8_t* blk = stage + u * BLK;
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++) x[u][nb][0] = x[u][nb][1] = x[u][nb][2] = x[u][nb][3] = 0.f;
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};  // a second sum, to halve the chain of dependent products
+                        x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
 #pragma unroll
                         for (int p = 0; p < PAN; p++) {
                             const uint2 w0 = *(const uint2*)(blk + p * 512 + k0 * 32 + t * 8);
@@ -365,65 +362,55 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                             for (int i = 0; i < 4; i++) {
                                 uint32_t u0 = i < 2 ? w0.x : w0.y, u1 = i < 2 ? w1.x : w1.y;
                                 if (i & 1) u0 >>= 8, u1 >>= 8;
-#pragma unroll
-                                for (int nb = 0; nb < NB; nb++)
-                                    mma_f16(x[u][nb], u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, q[nb][p][2 * i], q[nb][p][2 * i + 1]);
+                                mma_f16(i & 1 ? y : x[u], u0 & kLo, u1 & kLo, u0 & kHi, u1 & kHi, q[p][2 * i], q[p][2 * i + 1]);
                             }
                         }
                         const uint32_t* par = (const uint32_t*)(blk + 16 * D);  // K, then V
                         const uint32_t p0 = par[k0], p1 = par[k1];
                         const float s0 = __uint_as_float(p0 & 0xffff0000u), s1 = __uint_as_float(p1 & 0xffff0000u);
                         const float z0 = 128.f - __uint_as_float(p0 << 16), z1 = 128.f - __uint_as_float(p1 << 16);  // -z
-                        sv[u][0] = max_nan(__uint_as_float(par[16 + k0] & 0xffff0000u), kMinScale);
-                        sv[u][1] = max_nan(__uint_as_float(par[16 + k1] & 0xffff0000u), kMinScale);
+                        sv[u][0] = __uint_as_float(par[16 + k0] & 0xffff0000u) + kMinScale;
+                        sv[u][1] = __uint_as_float(par[16 + k1] & 0xffff0000u) + kMinScale;
 #pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                            for (int r = 0; r < 2; r++) {
-                                x[u][nb][r] = s0 * fmaf(x[u][nb][r], qf[nb][r], z0 * qs[nb][r]);
-                                x[u][nb][r + 2] = s1 * fmaf(x[u][nb][r + 2], qf[nb][r], z1 * qs[nb][r]);
-                            }
+                        for (int r = 0; r < 2; r++) {
+                            x[u][r] = s0 * fmaf(x[u][r] + y[r], qf[r], z0 * qs[r]);
+                            x[u][r + 2] = s1 * fmaf(x[u][r + 2] + y[r + 2], qf[r], z1 * qs[r]);
+                        }
                     }
                     if (live != 0x1010) {
                         // the last blocks of a sequence (or a bad page): the rest may hold anything
 #pragma unroll
                         for (int u = 0; u < 2; u++) {
                             const int n = (live >> (8 * u)) & 255;
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                                for (int r = 0; r < 2; r++) {
-                                    if (k0 >= n) x[u][nb][r] = -INFINITY;
-                                    if (k1 >= n) x[u][nb][r + 2] = -INFINITY;
-                                }
-                            if (k0 >= n) sv[u][0] = kMinScale;
-                            if (k1 >= n) sv[u][1] = kMinScale;
+                            if (k0 >= n) x[u][0] = x[u][1] = -INFINITY, sv[u][0] = kMinScale;
+                            if (k1 >= n) x[u][2] = x[u][3] = -INFINITY, sv[u][1] = kMinScale;
                         }
                     }
-                    float e[2][NB][4];              // probabilities
-                    uint32_t b0[2][NB], b1[2][NB];  // p s of the keys k0 and k1, rows 2t and 2t + 1
-                    auto weigh = [&]() {            // whether some p s is above 2^8
-                        __half2 top = __float2half2_rn(0.f);
+                    float e[2][4];              // probabilities
+                    uint32_t b0[2], b1[2];      // p s of the keys k0 and k1, rows 2t and 2t + 1
+                    auto weigh = [&]() {  // the sum of this lane's p s: while it is at most 2^11, none is above that
+                        float all[2];
 #pragma unroll
-                        for (int u = 0; u < 2; u++)
+                        for (int u = 0; u < 2; u++) {
+                            float w[4];
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++) {
-#pragma unroll
-                                for (int i = 0; i < 4; i++) e[u][nb][i] = ex2(x[u][nb][i] - m[nb][i & 1]);
-                                b0[u][nb] = pack_f16(e[u][nb][0] * sv[u][0], e[u][nb][1] * sv[u][0]);
-                                b1[u][nb] = pack_f16(e[u][nb][2] * sv[u][1], e[u][nb][3] * sv[u][1]);
-                                top = __hmax2(top, __hmax2(*(__half2*)&b0[u][nb], *(__half2*)&b1[u][nb]));
+                            for (int i = 0; i < 4; i++) {
+                                e[u][i] = ex2(x[u][i] - m[i & 1]);
+                                w[i] = e[u][i] * sv[u][i >> 1];
                             }
-                        return !__hble2(top, __float2half2_rn(256.f));
+                            all[u] = (w[0] + w[1]) + (w[2] + w[3]);
+                            b0[u] = pack_f16(w[0], w[1]);
+                            b1[u] = pack_f16(w[2], w[3]);
+                        }
+                        return all[0] + all[1];
                     };
-                    if (__any_sync(0xffffffffu, weigh())) {
-                        raise_ref([&](int nb, int r) {
-                            float y = kNoRef;
+                    if (__any_sync(0xffffffffu, weigh() > 2048.f)) {
+                        float y[2];
 #pragma unroll
-                            for (int u = 0; u < 2; u++)
-                                y = fmaxf(y, fmaxf(x[u][nb][r] + __log2f(sv[u][0]), x[u][nb][r + 2] + __log2f(sv[u][1])));
-                            return y;
-                        });
+                        for (int r = 0; r < 2; r++)
+                            y[r] = fmaxf(fmaxf(x[0][r] + __log2f(sv[0][0]), x[0][r + 2] + __log2f(sv[0][1])),
+                                         fmaxf(x[1][r] + __log2f(sv[1][0]), x[1][r + 2] + __log2f(sv[1][1])));
+                        raise_ref(y[0], y[1]);
                         weigh();
                     }
 #pragma unroll
@@ -431,13 +418,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                         const uint8_t* blk = stage + u * BLK;
                         const uint32_t* vpar = (const uint32_t*)(blk + 16 * D + 64);
                         const uint32_t vA = vpar[kA], vB = vpar[kB], vC = vpar[8 + kA], vE = vpar[8 + kB];
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++) {
-                            l[nb][0] += e[u][nb][0] + e[u][nb][2];
-                            l[nb][1] += e[u][nb][1] + e[u][nb][3];
-                            b0[u][nb] = transpose8(b0[u][nb]);
-                            b1[u][nb] = transpose8(b1[u][nb]);
-                        }
+                        l[0] += e[u][0] + e[u][2];
+                        l[1] += e[u][1] + e[u][3];
+                        b0[u] = transpose8(b0[u]);
+                        b1[u] = transpose8(b1[u]);
                         // -z of the same keys as fp16 2^-24 z and 2^-20 z
                         const uint32_t zAB = __byte_perm(vA, vB, 0x5410) & kLo, zCE = __byte_perm(vC, vE, 0x5410) & kLo;
                         const uint32_t zl0 = zAB | 0x80008000u, zl1 = zCE | 0x80008000u;
@@ -456,9 +440,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                                 for (int j = 0; j < 4; j++) {
                                     const uint32_t mk = j & 1 ? kHi : kLo;
                                     if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
-#pragma unroll
-                                    for (int nb = 0; nb < NB; nb++)
-                                        mma_f16(o[nb][(hf * 4 + j) % MB], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u][nb], b1[u][nb]);
+                                    mma_f16(o[(hf * 4 + j) % MB], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u], b1[u]);
                                 }
                             }
                         } else {
@@ -471,215 +453,185 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
                             for (int j = 0; j < 4; j++) {
                                 const uint32_t mk = j & 1 ? kHi : kLo;
                                 if (j == 2) ab0 >>= 8, ab1 >>= 8, ce0 >>= 8, ce1 >>= 8;
-#pragma unroll
-                                for (int nb = 0; nb < NB; nb++)
-                                    mma_f16(o[nb][j], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u][nb], b1[u][nb]);
+                                mma_f16(o[j], ab0 & mk, ab1 & mk, ce0 & mk, ce1 & mk, b0[u], b1[u]);
                             }
                         }
 #pragma unroll
                         for (int j = 0; j < MB; j++)
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++)
-                                mma_f16(o[nb][j], j & 1 ? zh0 : zl0, j & 1 ? zh0 : zl0, j & 1 ? zh1 : zl1, j & 1 ? zh1 : zl1, b0[u][nb],
-                                        b1[u][nb]);
+                            mma_f16(o[j], j & 1 ? zh0 : zl0, j & 1 ? zh0 : zl0, j & 1 ? zh1 : zl1, j & 1 ? zh1 : zl1, b0[u], b1[u]);
                     }
                     __syncwarp();  // every lane has read the stage
                     if (lane == 0) mbar_arrive(empty + s);
                     if (++s == S) s = 0, phase ^= 1;
                 }
             }
-            // ------------------------------------------ the step's own rows
-            // (in bf16, with their values brought to the codes' powers of two)
-            int tile = run.t0 + wi;
-            if (tile < ntc) tile += (ntc - tile + TW - 1) / TW * TW;
-            for (; tile < run.t1; tile += TW) {
-                const int j0 = (tile - ntc) * 16;
-                const size_t col = (size_t)head * D;
-                auto row = [&](const __nv_bfloat16* base, int j) {
-                    return base + (size_t)(run.b * (long long)a.T + j) * a.kv_ld + col;
-                };
-                const int k0 = j0 + kv4_key(g), k1 = k0 + 8;
-                float x[NB][4];
-#pragma unroll
-                for (int nb = 0; nb < NB; nb++) x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.f;
+            // ------------------------------------------ the step's own rows (16 at most: one tile)
+            // in bf16, with their values brought to the codes' powers of two
+            if (run.t1 > ntc && (TW == 1 || (ntc - run.t0) % TW == wi)) {
+                const __nv_bfloat16 *ks = a.ks + step_at, *vs = a.vs + step_at;
+                const int k0 = kv4_key(g), k1 = k0 + 8;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int p = 0; p < PAN; p++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-                        if (k0 < a.T) u0 = *(const uint4*)(row(a.ks, k0) + 64 * p + 16 * t + 8 * i);
-                        if (k1 < a.T) u1 = *(const uint4*)(row(a.ks, k1) + 64 * p + 16 * t + 8 * i);
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++) {
-                            uint4 u = make_uint4(0, 0, 0, 0);
-                            if (mt * R + nb * 8 + g < a.rows) u = *(const uint4*)(q_row(nb) + 64 * p + 8 * i);
-                            mma_b16(x[nb], u0.x, u1.x, u0.y, u1.y, u.x, u.y);
-                            mma_b16(x[nb], u0.z, u1.z, u0.w, u1.w, u.z, u.w);
-                        }
+                        const int c = 64 * p + 16 * t + 8 * i;
+                        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0, u = u0;
+                        if (k0 < a.T) u0 = *(const uint4*)(ks + (size_t)k0 * a.kv_ld + c);
+                        if (k1 < a.T) u1 = *(const uint4*)(ks + (size_t)k1 * a.kv_ld + c);
+                        if (q_here) u = *(const uint4*)(q_row + 64 * p + 8 * i);
+                        mma_b16(x, u0.x, u1.x, u0.y, u1.y, u.x, u.y);
+                        mma_b16(x, u0.z, u1.z, u0.w, u1.w, u.z, u.w);
                     }
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const int i = (mt * R + nb * 8 + 2 * t + r) / group;  // the step row
-                        x[nb][r] = k0 < a.T && kv4_sees(i, k0, a.W, a.n1) ? x[nb][r] * a.sl2 : -INFINITY;
-                        x[nb][r + 2] = k1 < a.T && kv4_sees(i, k1, a.W, a.n1) ? x[nb][r + 2] * a.sl2 : -INFINITY;
-                    }
-                raise_ref([&](int nb, int r) { return fmaxf(x[nb][r], x[nb][r + 2]); });
-                uint32_t b0[NB][2], b1[NB][2];
-#pragma unroll
-                for (int nb = 0; nb < NB; nb++) {
-                    float e[4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) e[i] = ex2(x[nb][i] - m[nb][i & 1]);
-                    l[nb][0] += e[0] + e[2];
-                    l[nb][1] += e[1] + e[3];
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const float f = h ? 0x1p-20f : 0x1p-24f;
-                        b0[nb][h] = transpose8(pack_bf16(e[0] * f, e[1] * f));
-                        b1[nb][h] = transpose8(pack_bf16(e[2] * f, e[3] * f));
-                    }
+                for (int r = 0; r < 2; r++) {
+                    const uint32_t see = tab[mt * R + 2 * t + r].sees;  // (rows beyond T see none)
+                    x[r] = (see >> k0) & 1 ? x[r] * a.sl2 : -INFINITY;
+                    x[r + 2] = (see >> k1) & 1 ? x[r + 2] * a.sl2 : -INFINITY;
                 }
-                // A NaN or an infinity among the values must reach the rows that see its key
-                // and no others, and zero times it is NaN: the product runs without it
+                raise_ref(fmaxf(x[0], x[2]), fmaxf(x[1], x[3]));
+                uint32_t b0[2], b1[2];
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) e[i] = ex2(x[i] - m[i & 1]);
+                l[0] += e[0] + e[2];
+                l[1] += e[1] + e[3];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float f = h ? 0x1p-20f : 0x1p-24f;
+                    b0[h] = transpose8(pack_bf16(e[0] * f, e[1] * f));
+                    b1[h] = transpose8(pack_bf16(e[2] * f, e[3] * f));
+                }
                 bool odd = false;
-                const int key[4] = {j0 + t, j0 + 4 + (t ^ 3), j0 + 8 + t, j0 + 12 + (t ^ 3)};
+                const int key[4] = {t, 4 + (t ^ 3), 8 + t, 12 + (t ^ 3)};
 #pragma unroll
                 for (int half = 0; half < DV / 8; half++) {
                     // channels DV g + 8 half ..
-                    uint4 v[4];
+                    uint32_t v[4][4];
+                    __nv_bfloat162 zero = __float2bfloat162_rn(0.f), nan = zero;
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (key[i] < a.T) v[i] = *(const uint4*)(row(a.vs, key[i]) + DV * g + 8 * half);
-                        odd |= drop_nonfinite(v[i].x) | drop_nonfinite(v[i].y) | drop_nonfinite(v[i].z) | drop_nonfinite(v[i].w);
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (key[i] < a.T) u = *(const uint4*)(vs + (size_t)key[i] * a.kv_ld + DV * g + 8 * half);
+                        v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+#pragma unroll
+                        for (int k = 0; k < 4; k++) nan = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v[i][k]), zero, nan);
                     }
-                    const uint32_t* vA = (const uint32_t*)&v[0];
-                    const uint32_t* vB = (const uint32_t*)&v[1];
-                    const uint32_t* vC = (const uint32_t*)&v[2];
-                    const uint32_t* vE = (const uint32_t*)&v[3];
+                    if (!__hbeq2(nan, zero)) {
+                        // A NaN or an infinity among the values must reach the rows that see its key
+                        // and no others, and zero times it is NaN: the product runs without it
+                        odd = true;
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+#pragma unroll
+                            for (int k = 0; k < 4; k++) drop_nonfinite(v[i][k]);
+                    }
                     if (D == 128) {
                         // fragment rows g and g + 8 hold channels 16 g + 2j (+ 1) and 16 g + 8 + 2j (+ 1):
                         // half the fragment at a time, the other half zero
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
                             const uint32_t sel = j < 4 ? 0x5410 : 0x7632;
-                            const uint32_t ab = __byte_perm(vA[j & 3], vB[j & 3], sel);
-                            const uint32_t ce = __byte_perm(vC[j & 3], vE[j & 3], sel);
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++)
-                                mma_b16(o[nb][j % MB], half ? 0u : ab, half ? ab : 0u, half ? 0u : ce, half ? ce : 0u, b0[nb][j & 1],
-                                        b1[nb][j & 1]);
+                            const uint32_t ab = __byte_perm(v[0][j & 3], v[1][j & 3], sel);
+                            const uint32_t ce = __byte_perm(v[2][j & 3], v[3][j & 3], sel);
+                            mma_b16(o[j % MB], half ? 0u : ab, half ? ab : 0u, half ? 0u : ce, half ? ce : 0u, b0[j & 1], b1[j & 1]);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const uint32_t a0 = __byte_perm(vA[j], vB[j], 0x5410), a1 = __byte_perm(vA[j], vB[j], 0x7632);
-                            const uint32_t a2 = __byte_perm(vC[j], vE[j], 0x5410), a3 = __byte_perm(vC[j], vE[j], 0x7632);
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma_b16(o[nb][j], a0, a1, a2, a3, b0[nb][j & 1], b1[nb][j & 1]);
+                            const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
+                            const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
+                            mma_b16(o[j], a0, a1, a2, a3, b0[j & 1], b1[j & 1]);
                         }
                     }
                 }
                 if (__any_sync(0xffffffffu, odd)) {
-                    for (int j = j0; j < min(j0 + 16, a.T); j++) {
+                    for (int j = 0; j < a.T; j++) {
 #pragma unroll
                         for (int c = 0; c < DV; c++) {
-                            const float v = __bfloat162float(row(a.vs, j)[DV * g + c]);
-                            if (fabsf(v) < INFINITY) continue;
+                            const float v = __bfloat162float(vs[(size_t)j * a.kv_ld + DV * g + c]);
                             const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++)
+                            if (!(fabsf(v) < INFINITY))
 #pragma unroll
                                 for (int r = 0; r < 2; r++)
-                                    if (kv4_sees((mt * R + nb * 8 + 2 * t + r) / group, j, a.W, a.n1))
-                                        o[nb][mb % MB][r + 2 * hi] += v;
+                                    if ((tab[mt * R + 2 * t + r].sees >> j) & 1) o[mb % MB][r + 2 * hi] += v;
                         }
                     }
                 }
             }
             // ---- the item's (or the run's) result
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], 4);
-                    l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], 8);
-                    l[nb][r] += __shfl_xor_sync(0xffffffffu, l[nb][r], 16);
-                }
+            for (int r = 0; r < 2; r++) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+            }
             const bool whole = run.u0 == 0 && run.u1 == run.nu;
             float* part = a.part + ((size_t)team * 2 + (run.u0 == 0 ? 1 : 0)) * part_floats(R, D);
             if (run.u0 == 0 && !whole && writes_rec) *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, starts[TW == 1 ? warp : 0].sh};
-            // channel c (of DV, from DV g) of row 2t + r
-            auto chan = [&](int nb, int r, int c) -> float {
+            __nv_bfloat16* out_base = a.out + ((size_t)run.b * a.T * a.H + (size_t)head * group) * D;
+            // channel c (of DV, from DV g) of row 2t + r, times f
+            auto chan = [&](int r, int c, float f) -> float {
                 const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
-                return o[nb][mb % MB][r + 2 * hi] * (mb & 1 ? 0x1p20f : 0x1p24f);
+                return o[mb % MB][r + 2 * hi] * (mb & 1 ? f * 0x1p20f : f * 0x1p24f);
             };
-            auto out_row = [&](int gr) {
-                return a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
-            };
-            if (TW == 1) {
+            if (TW == 1 && whole) {
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++)
+                for (int r = 0; r < 2; r++) {
+                    const int lr = mt * R + 2 * t + r;
+                    const float inv = 1.f / l[r];
+                    uint32_t y[DV / 2];
 #pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const int lr = nb * 8 + 2 * t + r, gr = mt * R + lr;
-                        if (gr >= a.rows) continue;
-                        if (whole) {
-                            const float inv = 1.f / l[nb][r];
-                            uint32_t y[DV / 2];
+                    for (int c = 0; c < DV; c += 2) y[c / 2] = pack_bf16(chan(r, c, 1.f) * inv, chan(r, c + 1, 1.f) * inv);
+                    if (lr < a.rows) {
+                        __nv_bfloat16* dst = out_base + tab[lr].out + DV * g;
 #pragma unroll
-                            for (int c = 0; c < DV; c += 2)
-                                y[c / 2] = pack_bf16(chan(nb, r, c) * inv, chan(nb, r, c + 1) * inv);
-                            __nv_bfloat16* dst = out_row(gr) + DV * g;
-#pragma unroll
-                            for (int c = 0; c < DV / 2; c += 4) *(uint4*)(dst + 2 * c) = make_uint4(y[c], y[c + 1], y[c + 2], y[c + 3]);
-                        } else {
-                            float* dst = part + (size_t)lr * D + DV * g;
-#pragma unroll
-                            for (int c = 0; c < DV; c += 4)
-                                *(float4*)(dst + c) = make_float4(chan(nb, r, c), chan(nb, r, c + 1), chan(nb, r, c + 2), chan(nb, r, c + 3));
-                            if (g == 0) *(float2*)(part + (size_t)R * D + 2 * lr) = make_float2(m[nb][r], l[nb][r]);
-                        }
+                        for (int c = 0; c < DV / 2; c += 4) *(uint4*)(dst + 2 * c) = make_uint4(y[c], y[c + 1], y[c + 2], y[c + 3]);
                     }
+                }
             } else {
-                float* mg = (float*)(sm + L::kMerge);
-                if (!first) named_sync(1, kWarps * 32);  // the last item's results have been read
+                // [row][D], then the rows' references and sums: to the team's merge area, or as a part
+                float* to = TW == 1 ? part : (float*)(sm + L::kMerge) + (size_t)warp * R * (D + 4);
+                constexpr int kLd = TW == 1 ? D : D + 4;
+                if (TW > 1 && !first) named_sync(1, kWarps * 32);  // the last item's results have been read
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        float* dst = mg + ((size_t)warp * R + nb * 8 + 2 * t + r) * (D + 4);
+                for (int r = 0; r < 2; r++) {
+                    const int lr = 2 * t + r;
+                    if (TW > 1 || mt * R + lr < a.rows) {
 #pragma unroll
                         for (int c = 0; c < DV; c += 4)
-                            *(float4*)(dst + DV * g + c) = make_float4(chan(nb, r, c), chan(nb, r, c + 1), chan(nb, r, c + 2), chan(nb, r, c + 3));
-                        if (g == 0) *(float2*)(dst + D) = make_float2(m[nb][r], l[nb][r]);
+                            *(float4*)(to + (size_t)lr * kLd + DV * g + c) =
+                                make_float4(chan(r, c, 1.f), chan(r, c + 1, 1.f), chan(r, c + 2, 1.f), chan(r, c + 3, 1.f));
+                        if (g == 0) *(float2*)(TW == 1 ? to + (size_t)R * D + 2 * lr : to + (size_t)lr * kLd + D) = make_float2(m[r], l[r]);
                     }
+                }
+            }
+            if (TW > 1) {
+                const float* mg = (const float*)(sm + L::kMerge);
                 named_sync(1, kWarps * 32);
                 for (int i = threadIdx.x; i < R * D / 4; i += kWarps * 32) {
-                    const int lr = i / (D / 4), c = (i % (D / 4)) * 4, gr = mt * R + lr;
-                    if (gr >= a.rows) continue;
+                    const int lr = i / (D / 4), c = (i % (D / 4)) * 4;
+                    if (mt * R + lr >= a.rows) continue;
                     float2 ml[kWarps];
-                    float mx = -INFINITY;
+                    float mx = kNoRef;
 #pragma unroll
                     for (int w = 0; w < kWarps; w++) {
                         ml[w] = *(const float2*)(mg + ((size_t)w * R + lr) * (D + 4) + D);
                         mx = fmaxf(mx, ml[w].x);
                     }
-                    const float mu = fmaxf(mx, kNoRef);
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; w++) {
-                        const float f = ex2(ml[w].x - mu);
+                        const float f = ex2(ml[w].x - mx);
                         const float4 v = *(const float4*)(mg + ((size_t)w * R + lr) * (D + 4) + c);
                         sum += f * ml[w].y;
                         acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
                     }
                     if (whole) {
                         const float inv = 1.f / sum;
-                        *(uint2*)(out_row(gr) + c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                        *(uint2*)(out_base + tab[mt * R + lr].out + c) =
+                            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
                     } else {
                         *(float4*)(part + (size_t)lr * D + c) = acc;
                         if (c == 0) *(float2*)(part + (size_t)R * D + 2 * lr) = make_float2(mx, sum);
@@ -697,79 +649,74 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) k_kv4_rows(Kv4Attn 
 // slot and the first slots of the teams after it, until the item's tiles are
 // all accounted for.  Weights exp2(m - M) of the parts in team order.
 
-constexpr int kMergeChunks = 4;
-
 template <int D, int R>
 __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
 {
     pdl_wait();
     pdl_trigger();
-    // one warp per team and 128 floats of the item's rows (R <= 16: of 4 kMergeChunks channels),
-    // or 32 rows x 8 channels (R = 128)
+    // one warp per team and 128 floats of the item's rows, or (R = 128) 32 rows x 8 channels
     constexpr bool kCols = R == 128;
+    constexpr int kBatch = kCols ? 4 : 8;  // parts loaded together: one after the other, each costs a trip to L2
     const int rows = min(R, a.rows);
-    const int groups = kCols ? (rows + 31) / 32 * (D / 8) : ceil_div(ceil_div(rows * D, 128), kMergeChunks);
-    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), i0 = w / groups, lane = threadIdx.x & 31;
+    const int groups = kCols ? (rows + 31) / 32 * (D / 8) : ceil_div(rows * D, 128);
+    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), i0 = w / groups, grp = w - i0 * groups, lane = threadIdx.x & 31;
     if (i0 >= a.nteams) return;
     const MergeRec* recs = (const MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D));
     const MergeRec rec = recs[i0];
     if (rec.rest == 0) return;
     const Shares sh = rec.sh;
     const long long end = sh.at(i0 + 1) + rec.rest;  // where the item ends
-    const int head = rec.item / a.mtiles, mt = rec.item % a.mtiles, group = a.H / a.Hkv;
-    auto out_at = [&](int gr, int c) {
-        return a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c;
-    };
-    // the parts: team i0's second one, then the first ones of the teams after it up to the item's end
-    auto part_of = [&](int i) { return a.part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * part_floats(R, D); };
-    if (kCols) {
-        const int g = w % groups, lr = g / (D / 8) * 32 + lane, c = g % (D / 8) * 8, gr = mt * R + lr;
-        if (gr >= a.rows) return;
-        float mx = kNoRef, sum = 0.f, acc[8] = {};
-        for (int i = i0; i == i0 || sh.at(i) < end; i++) {
-            if (sh.at(i) == sh.at(i + 1)) continue;  // a team without units
-            const float* part = part_of(i);
-            const float m = part[(size_t)R * D + lr], l = part[(size_t)R * D + R + lr];
-            float v[8];
+    const int head = rec.item / a.mtiles, mt = rec.item - head * a.mtiles, group = a.H / a.Hkv;
+    const int lr = kCols ? grp / (D / 8) * 32 + lane : (grp * 128 + lane * 4) / D;
+    const int c = kCols ? grp % (D / 8) * 8 : (grp * 128 + lane * 4) % D, gr = mt * R + lr;
+    if (lr >= R || gr >= a.rows) return;
+    constexpr int kV = kCols ? 8 : 4;
+    float mx = kNoRef, sum = 0.f, acc[kV] = {};
+    // the parts: team i0's second one, then the first ones of the teams after it up to the
+    // item's end; joined in team order
+#pragma unroll 1
+    for (int i = i0; i == i0 || sh.at(i) < end; i += kBatch) {
+        float m[kBatch], l[kBatch], v[kBatch][kV];
 #pragma unroll
-            for (int k = 0; k < 8; k++) v[k] = part[(size_t)(c + k) * R + lr];
-            const float top = fmaxf(mx, m), f = ex2(mx - top), h = ex2(m - top);
-            mx = top;
-            sum = sum * f + l * h;
+        for (int j = 0; j < kBatch; j++) {
+            m[j] = kNoRef, l[j] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; k++) acc[k] = acc[k] * f + v[k] * h;
+            for (int k = 0; k < kV; k++) v[j][k] = 0.f;
+            const long long at = sh.at(i + j);
+            if (at >= end || at == sh.at(i + j + 1)) continue;  // past the item, or a team without units
+            const float* part = a.part + ((size_t)(i + j) * 2 + (i + j == i0 ? 1 : 0)) * part_floats(R, D);
+            if (kCols) {
+                m[j] = part[(size_t)R * D + lr], l[j] = part[(size_t)R * D + R + lr];
+#pragma unroll
+                for (int k = 0; k < kV; k++) v[j][k] = part[(size_t)(c + k) * R + lr];
+            } else {
+                const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
+                const float4 x = *(const float4*)(part + (size_t)lr * D + c);
+                m[j] = ml.x, l[j] = ml.y, v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+            }
         }
-        const float inv = 1.f / sum;
-        *(uint4*)out_at(gr, c) = make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
-                                            pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
-        return;
-    }
-    const int c0 = (w % groups) * kMergeChunks;
 #pragma unroll
-    for (int ch = 0; ch < kMergeChunks; ch++) {
-        const int at = (c0 + ch) * 128 + lane * 4, lr = at / D, c = at % D, gr = mt * R + lr;
-        if (lr >= R || gr >= a.rows) return;
-        float mx = kNoRef, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = i0; i == i0 || sh.at(i) < end; i++) {
-            if (sh.at(i) == sh.at(i + 1)) continue;
-            const float* part = part_of(i);
-            const float2 ml = *(const float2*)(part + (size_t)R * D + 2 * lr);
-            const float4 v = *(const float4*)(part + (size_t)lr * D + c);
-            const float top = fmaxf(mx, ml.x), f = ex2(mx - top), h = ex2(ml.x - top);
+        for (int j = 0; j < kBatch; j++) {
+            const float top = fmaxf(mx, m[j]), f = ex2(mx - top), h = ex2(m[j] - top);
             mx = top;
-            sum = sum * f + ml.y * h;
-            acc.x = acc.x * f + v.x * h, acc.y = acc.y * f + v.y * h, acc.z = acc.z * f + v.z * h, acc.w = acc.w * f + v.w * h;
+            sum = sum * f + l[j] * h;
+#pragma unroll
+            for (int k = 0; k < kV; k++) acc[k] = acc[k] * f + v[j][k] * h;
         }
-        const float inv = 1.f / sum;
-        *(uint2*)out_at(gr, c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
+    const float inv = 1.f / sum;
+    uint32_t y[kV / 2];
+#pragma unroll
+    for (int k = 0; k < kV; k += 2) y[k / 2] = pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+    __nv_bfloat16* dst = a.out + ((size_t)(rec.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D + c;
+    if (kCols) *(uint4*)dst = make_uint4(y[0], y[1], y[kV / 2 - 2], y[kV / 2 - 1]);
+    else *(uint2*)dst = make_uint2(y[0], y[1]);
 }
 
 // ---------------------------------------------------------------- launches ---
 
 struct Plan {
-    int nb, tw, grid, nteams, mtiles, extra;
+    int tw, grid, nteams, mtiles, extra;
     bool merge;
     size_t bytes;
 };
@@ -784,34 +731,36 @@ Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
 {
     Plan p;
     const int T = 1 + (a.W + a.G) * (a.N - 1), rows = T * (a.n_heads / c.n_kv_heads);
-    p.nb = rows <= 8 ? 1 : 2;
-    p.mtiles = ceil_div(rows, 8 * p.nb);
+    p.mtiles = ceil_div(rows, 8);  // 1 or 2
     const long long items = (long long)a.batch * c.n_kv_heads * p.mtiles;
-    const long long tiles = items * ((max_len_of(c, a) + kKeys - 1) / kKeys + (T + 15) / 16);  // at most
-    const int ctas = p.nb == 1 ? 2 * kSMs : kSMs;  // resident at once
-    p.tw = items >= (long long)ctas * kWarps ? 1 : kWarps;
+    const int ctas = 2 * kSMs;  // resident at once
+    // A warp per team spares the CTA's barriers but splits few items too finely: 13B lookahead x 9 (720
+    // items) 36 against 39 us, 7B greedy x 16 (512 items) 19.4 against 20.1, 34B greedy x 32 (256 items)
+    // 45 against 28
+    p.tw = items >= 512 ? 1 : kWarps;
     // an item's queries and result take as long as so many tiles (32 keys); without them the teams
-    // that get many short sequences finish last.  128 greedy 7B sequences: 86 us at 0, 66 at 4, 71 at 8;
-    // CTA teams on 16 long 34B sequences of 1 to 64 K: 124 us at 0, 117 at 21, 118 at 42
-    p.extra = p.tw == 1 ? 4 : 18;
+    // that get many short sequences finish last.  Warps: 128 greedy 7B sequences 64 us at 0, 57 at 1,
+    // 61 at 4; CTAs: 16 long 34B sequences of 1 to 64 K tokens 132 us at 0, 121 at 14, 122 at 24
+    p.extra = p.tw == 1 ? 1 : 14;
     const long long teams = (long long)ctas * (p.tw == 1 ? kWarps : 1);
+    const long long tiles = items * ((max_len_of(c, a) + kKeys - 1) / kKeys + 1);  // at most
     p.nteams = (int)std::max(1LL, std::min(teams, std::max(items, tiles / kWarps)));
     p.grid = p.tw == 1 ? ceil_div(p.nteams, kWarps) : p.nteams;
     // one sequence: every item has the same tiles, so whole items a team stay whole
     p.merge = !(a.batch == 1 && items % p.nteams == 0);
-    p.bytes = p.merge ? (size_t)p.nteams * (2 * part_floats(8 * p.nb, c.head_dim) * 4 + sizeof(MergeRec)) : 0;
+    p.bytes = p.merge ? (size_t)p.nteams * (2 * part_floats(8, c.head_dim) * 4 + sizeof(MergeRec)) : 0;
     return p;
 }
 
 std::mutex g_mu;
 unsigned char g_ready[256];
 
-template <int D, int NB, int TW>
+template <int D, int TW>
 bool set_smem()
 {
-    return cudaFuncSetAttribute(k_kv4_rows<D, NB, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                RowsSmem<D, NB, TW>::kBytes) == cudaSuccess &&
-           cudaFuncSetAttribute(k_kv4_rows<D, NB, TW>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
+    return cudaFuncSetAttribute(k_kv4_rows<D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, TW>::kBytes) ==
+               cudaSuccess &&
+           cudaFuncSetAttribute(k_kv4_rows<D, TW>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
 }
 
 // The kernels' shared-memory limits, once per device.
@@ -821,20 +770,19 @@ int attn_ready()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return LA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
-        if (!(set_smem<128, 1, 1>() && set_smem<128, 1, kWarps>() && set_smem<128, 2, 1>() && set_smem<128, 2, kWarps>() &&
-              set_smem<64, 1, 1>() && set_smem<64, 1, kWarps>() && set_smem<64, 2, 1>() && set_smem<64, 2, kWarps>() && kv4_tc_init()))
+        if (!(set_smem<128, 1>() && set_smem<128, kWarps>() && set_smem<64, 1>() && set_smem<64, kWarps>() && kv4_tc_init()))
             return LA_ERR_CUDA;
         g_ready[dev] = 1;
     }
     return LA_OK;
 }
 
-template <int D, int NB>
+template <int D>
 cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
-    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, NB, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, 1>::kBytes, s, k)
-                              : launch_pdl(k_kv4_rows<D, NB, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, NB, kWarps>::kBytes, s, k);
-    if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, D, 8 * NB);
+    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, 1>::kBytes, s, k)
+                              : launch_pdl(k_kv4_rows<D, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, kWarps>::kBytes, s, k);
+    if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, D, 8);
     return e;
 }
 
@@ -843,9 +791,9 @@ cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 cudaError_t launch_kv4_merge(cudaStream_t s, const Kv4Attn& k, int D, int R)
 {
     const int rows = std::min(R, k.rows);
-    const int groups = R == 128 ? (rows + 31) / 32 * (D / 8) : ceil_div(ceil_div(rows * D, 128), kMergeChunks);
-    auto kern = D == 128 ? (R == 8 ? k_kv4_merge<128, 8> : R == 16 ? k_kv4_merge<128, 16> : k_kv4_merge<128, 128>)
-                         : (R == 8 ? k_kv4_merge<64, 8> : R == 16 ? k_kv4_merge<64, 16> : k_kv4_merge<64, 128>);
+    const int groups = R == 128 ? (rows + 31) / 32 * (D / 8) : ceil_div(rows * D, 128);
+    auto kern = D == 128 ? (R == 8 ? k_kv4_merge<128, 8> : k_kv4_merge<128, 128>)
+                         : (R == 8 ? k_kv4_merge<64, 8> : k_kv4_merge<64, 128>);
     return launch_pdl(kern, dim3(ceil_div(k.nteams * groups, 8)), dim3(256), 0, s, k);
 }
 
@@ -855,7 +803,7 @@ namespace {
 // the 128-row tiles of tcgen05.
 bool many_rows(const la_kv4_desc& c, const la_kv4_attn& a)
 {
-    return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > (getenv("KV_T") ? atoi(getenv("KV_T")) : 16);
+    return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > 16;
 }
 
 }  // namespace
@@ -885,9 +833,8 @@ int launch_kv4_attn(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a)
     const Plan p = plan_of(c, a);
     k.part = p.merge ? (float*)a.workspace : nullptr;
     k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = p.extra;
-    k.tile_log2 = kKeysLog2, k.step_tiles = (k.T + 15) / 16;
-    const cudaError_t e = c.head_dim == 128 ? (p.nb == 1 ? go<128, 1>(s, p, k) : go<128, 2>(s, p, k))
-                                            : (p.nb == 1 ? go<64, 1>(s, p, k) : go<64, 2>(s, p, k));
+    k.tile_log2 = kKeysLog2, k.step_tiles = 1;
+    const cudaError_t e = c.head_dim == 128 ? go<128>(s, p, k) : go<64>(s, p, k);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

@@ -170,7 +170,7 @@ struct MergeRec {
     Shares sh;
 };
 
-// A part: R rows of D outputs, each row's M and sum. R <= 16: [R][D], [R][2];
+// A part: R rows of D outputs, each row's M and sum. R = 8: [R][D], [R][2];
 // R = 128 (a thread per row): [D][R], [2][R].
 __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
 
