@@ -25,7 +25,7 @@
 // one CTA per SM: warps 0-7 softmax (a row per thread; warps 0-3 the even
 // tiles, 4-7 the odd ones, so that one group's exponentials run while the
 // other waits), 8-11 unpack K, 12-15 V, 16 issues the MMAs, 17 copies code
-// blocks ahead and finds the tiles' powers of two.  S, P, K and V are double
+// blocks ahead, 18 finds the tiles' powers of two.  S, P, K and V are double
 // buffered, codes triple.
 //
 // Two ways to share an item's tiles: equal runs of all items' units over the
@@ -41,7 +41,7 @@ namespace la {
 
 namespace {
 
-constexpr int kTcThreads = 576;
+constexpr int kTcThreads = 608;
 constexpr int kTileLog2 = 7, kTile = 128;
 constexpr int kRowsTc = 128;
 constexpr int kRing = 3;
@@ -132,16 +132,6 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity)
 
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
 
 // packed pairs of fp32: one instruction for two
 __device__ __forceinline__ uint64_t pair(float a, float b)
@@ -293,7 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 {
     using L = TcSmem<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023);  // (by an offset: a pointer made from an integer is generic)
     uint64_t* bar = (uint64_t*)(sm + L::kBar);
     TileInfo* info = (TileInfo*)(sm + L::kInfo);
     uint32_t* vis = (uint32_t*)(sm + L::kVis);
@@ -821,36 +811,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             mbar_drain(bar + kEnd, 0);
         }
         __syncwarp();
-    } else if (work) {
+    } else if (work && warp == 17) {
         // -------------------------------------------------------------- copies
         const uint64_t pol = policy_evict_first();
-        int fills = 0, known = 0;
-        int where[kRing] = {};  // the tile numbers of the stages in flight
-        auto find_powers = [&]() {  // of the oldest stage that is not done
-            const int s = known % kRing;
-            wait(kFull + s, (known / kRing) & 1);
-            const uint8_t* stage = sm + L::kCodes + s * L::kStage;
-            const int ri = ring_info[s], live = ri & 0xffff, bad = ri >> 16;
-            uint32_t ek = 0, ev = 0;  // the largest scales' exponents (of keys that count)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int key = lane + 32 * i;
-                const uint32_t* par = (const uint32_t*)(stage + (key >> 4) * kv4_block_bytes(D) + 16 * D) + (key & 15);
-                const uint32_t k0 = par[0] >> 23, v0 = par[16] >> 23;
-                const bool here = key < live && !((bad >> (key >> 4)) & 1);
-                ek = max(ek, here && k0 < 255 ? k0 : 0u);
-                ev = max(ev, here && v0 < 255 ? v0 : 0u);
-            }
-            ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
-            if (lane == 0) {
-                TileInfo* ti = info + ((s == 0 ? where[0] : s == 1 ? where[1] : where[2]) & 7);
-                ti->live = live, ti->bad = bad;
-                ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 20) - 118;  // s 2^-E < 2^-8
-                mbar_arrive(bar + kInfoReady + s);
-            }
-            __syncwarp();
-            known++;
-        };
+        int fills = 0;
         do {
             const int head = run.item / a.mtiles, ntc = (run.len + kTile - 1) / kTile;
             // the pages of four tiles' blocks at a time, and of the next four ahead
@@ -860,8 +824,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 return blk * 16 < run.len ? __ldg(pages + (blk >> a.blk_log2)) : 0;
             };
             int pg = look_up(run.t0), pg_next = look_up(run.t0 + 4 * stride), turn = -1;
-            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
-                if (tile >= ntc) continue;
+            for (int tile = run.t0; tile < min(run.t1, ntc); tile += stride) {
                 const int s = fills % kRing, blk = tile * 8 + lane, live = min(run.len - tile * kTile, kTile);
                 const bool mine = lane < 8 && lane * 16 < live;
                 turn = (turn + 1) & 3;
@@ -869,24 +832,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 const int page_of = __shfl_sync(0xffffffffu, pg, (8 * turn + lane) & 31), page = mine ? page_of : 0;
                 const bool bad = (unsigned)page >= (unsigned)a.n_pages;
                 const uint32_t bads = __ballot_sync(0xffffffffu, bad), who = __ballot_sync(0xffffffffu, mine);
-                // until the stage is free, and after it: the powers of tiles that have landed
-                if (fills >= kRing) {
-                    const unsigned long long t0 = globaltimer();
-                    while (ok && !__all_sync(0xffffffffu, test_wait(bar + kEmpty + s, (fills / kRing - 1) & 1))) {
-                        if (known < fills && __all_sync(0xffffffffu, test_wait(bar + kFull + known % kRing, (known / kRing) & 1)))
-                            find_powers();
-                        const bool late = *abort_flag || globaltimer() - t0 > kWaitNs;
-                        if (__any_sync(0xffffffffu, late)) {
-                            ok = false;
-                            *abort_flag = 1;
-                            kv4_raise(a.status, LA_ERR_TIMEOUT);
-                        }
-                    }
-                }
+                if (fills >= kRing) wait(kEmpty + s, (fills / kRing - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) continue;
-                if (s == 0) where[0] = n;
-                else if (s == 1) where[1] = n;
-                else where[2] = n;
                 if (lane == 0) {
                     if (bads) kv4_raise(a.status, LA_ERR_ARG);
                     ring_info[s] = live | (int)bads << 16;
@@ -899,12 +846,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                               kv4_block_bytes(D), bar + kFull + s, pol);
                 __syncwarp();
                 fills++;
-                if (known < fills && __all_sync(0xffffffffu, test_wait(bar + kFull + known % kRing, (known / kRing) & 1))) find_powers();
             }
         } while (!CL && run.next(a));
-        while (known < fills) find_powers();
         // no copy may still be on its way when the CTA ends
         for (int i = 1; i <= kRing && i <= fills; i++) mbar_drain(bar + kFull + (fills - i) % kRing, ((fills - i) / kRing) & 1);
+    } else if (work) {
+        // ------------------------------------------------- the powers of two
+        int fills = 0;
+        do {
+            const int ntc = (run.len + kTile - 1) / kTile;
+            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
+                if (tile >= ntc) continue;
+                const int s = fills % kRing;
+                wait(kFull + s, (fills / kRing) & 1);
+                const uint8_t* stage = sm + L::kCodes + s * L::kStage;
+                const int ri = ring_info[s], live = ri & 0xffff, bad = ri >> 16;
+                uint32_t ek = 0, ev = 0;  // the largest scales' exponents (of keys that count)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = lane + 32 * i;
+                    const uint32_t* par = (const uint32_t*)(stage + (key >> 4) * kv4_block_bytes(D) + 16 * D) + (key & 15);
+                    const uint32_t k0 = par[0] >> 23, v0 = par[16] >> 23;
+                    const bool here = key < live && !((bad >> (key >> 4)) & 1);
+                    ek = max(ek, here && k0 < 255 ? k0 : 0u);
+                    ev = max(ev, here && v0 < 255 ? v0 : 0u);
+                }
+                ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
+                if (lane == 0) {
+                    TileInfo* ti = info + (n & 7);
+                    ti->live = live, ti->bad = bad;
+                    ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 20) - 118;  // s 2^-E < 2^-8
+                    mbar_arrive(bar + kInfoReady + s);
+                }
+                __syncwarp();
+                fills++;
+            }
+        } while (!CL && run.next(a));
     }
     __syncwarp();
     if (CL) {
