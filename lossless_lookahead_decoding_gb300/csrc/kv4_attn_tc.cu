@@ -189,7 +189,7 @@ struct TcSmem {
 
 enum {  // barriers
     kFull = 0, kEmpty = 3, kInfoReady = 6, kKReady = 9, kVReady = 11, kSDone = 13, kODone = 15, kPReady = 17, kQReady = 19,
-    kOFree = 20, kEnd = 21
+    kOFree = 20, kEnd = 21, kStepReady = 22
 };
 constexpr uint32_t kColO = 256, kColP = 384;  // tensor memory: S [2][128], O [D], P [2][64]
 
@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         mbar_init(bar + kQReady, 8);
         mbar_init(bar + kOFree, 8);
         mbar_init(bar + kEnd, 1);
+        mbar_init(bar + kStepReady, 2);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, grp = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+        int steps = 0;  // step tiles so far
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile, gr = mt * kRowsTc + row;
@@ -413,11 +415,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             const int n0 = n;
             float m = kNoRef, l = 0.f;
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
-                if ((n & 1) != grp) continue;
-                const int b = grp, ph = (n >> 1) & 1;
                 const bool step = tile >= ntc;
+                if ((n & 1) != grp) {
+                    steps += step;
+                    continue;
+                }
+                const int b = grp, ph = (n >> 1) & 1;
                 wait(kSDone + b, ph);
-                if (step) wait(kVReady + b, ph);  // (its entry has parts from both unpacking groups)
+                if (step) wait(kStepReady, steps & 1), steps++;  // (its entry has parts from both unpacking groups)
                 tc_fence_after();
                 if (any) {
                     const TileInfo* ti = info + (n & 7);
@@ -614,6 +619,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 constexpr int kPieces = D / 8, kPass = 256 / kPieces;
                 const int pc = (threadIdx.x - 256) % kPieces, r0 = (threadIdx.x - 256) / kPieces;
                 uint8_t* q0 = sm + L::kQ;
+                // step row and head of the group, advanced by kPass rows at a time
+                int si = (mt * kRowsTc + r0) / group, sj = mt * kRowsTc + r0 - si * group;
+                const int di = kPass / group, dj = kPass - di * group;
 #pragma unroll 1
                 for (int i0 = 0; i0 < 128 / kPass; i0 += 4) {
                     // (loads first: none moves above a store to shared memory by itself)
@@ -623,7 +631,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         const int gr = mt * kRowsTc + r0 + (i0 + i) * kPass;
                         u[i] = make_uint4(0, 0, 0, 0);
                         if (gr < a.rows)
-                            u[i] = *(const uint4*)(a.q + (size_t)(run.b * (long long)a.T + gr / group) * a.q_ld + (size_t)(head * group + gr % group) * D + 8 * pc);
+                            u[i] = *(const uint4*)(a.q + ((size_t)run.b * a.T + si) * a.q_ld + (size_t)(head * group + sj) * D + 8 * pc);
+                        si += di, sj += dj;
+                        if (sj >= group) sj -= group, si++;
                     }
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
@@ -733,12 +743,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 #pragma unroll
                     for (int i = 0; i < 4; i++) e = max(e, red_e[kv * 4 + i]);
                     named_sync(5 + kv, 128);  // red_e may be written again
-                    const int E = max((int)e, 28) - 135;  // the largest comes to [2^8, 2^9)
+                    // The largest comes to [2^-4, 2^-3), as the cached tiles' do: P carries the tiles'
+                    // powers of two of V, and a step tile far from the others would push its P (or
+                    // theirs) to where fp16 has fewer bits.
+                    const int E = max((int)e, 28) - 123;
                     if (tid == 0) {
                         if (kv) ti->ev = E;
                         else ti->ek = E, ti->live = kTile, ti->bad = 0;
+                        mbar_arrive(bar + kStepReady);
                     }
-                    const float f = pow2i(-E);
+                    const float f = scale2(1.f, -E);
 #pragma unroll 1
                     for (int i0 = 0; i0 < 128 / kPass; i0 += 4) {
                         uint4 u[4];
@@ -852,9 +866,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         for (int i = 1; i <= kRing && i <= fills; i++) mbar_drain(bar + kFull + (fills - i) % kRing, ((fills - i) / kRing) & 1);
     } else if (work) {
         // ------------------------------------------------- the powers of two
+        // (and, with time to spare, the next item's queries and step rows into L2)
         int fills = 0;
         do {
             const int ntc = (run.len + kTile - 1) / kTile;
+            if (!CL && run.left > 0 && run.item + 1 < a.Hkv * a.mtiles) {
+                const int item = run.item + 1, head = item / a.mtiles, r0 = (item - head * a.mtiles) * kRowsTc;
+                for (int r = lane; r < min(kRowsTc, a.rows - r0); r += 32) {
+                    const int i = (r0 + r) / group, j = r0 + r - i * group;
+                    const __nv_bfloat16* src = a.q + ((size_t)run.b * a.T + i) * a.q_ld + (size_t)(head * group + j) * D;
+                    prefetch_l2(src);
+                    if (D == 128) prefetch_l2(src + 64);
+                }
+                if (r0 == 0)
+                    for (int r = lane; r < a.T; r += 32) {
+                        const size_t at = ((size_t)run.b * a.T + r) * a.kv_ld + (size_t)head * D;
+                        prefetch_l2(a.ks + at), prefetch_l2(a.vs + at);
+                        if (D == 128) prefetch_l2(a.ks + at + 64), prefetch_l2(a.vs + at + 64);
+                    }
+            }
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 if (tile >= ntc) continue;
                 const int s = fills % kRing;
