@@ -80,20 +80,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc));
 }
 
-// 16 columns; the values are there after tmem_ld_wait(v)
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-                   "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait(float (&v)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -277,6 +263,12 @@ __device__ __forceinline__ void st_peer4(uint32_t addr, float x, float y, float 
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
+template <int D>
+__device__ __forceinline__ MergeRec* merge_rec(const Kv4Attn& a)
+{
+    return (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(kRowsTc, D)) + blockIdx.x;
+}
+
 // CL: one item per cluster; its CTAs take equal runs of the item's tiles.
 template <int D, bool CL>
 __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
@@ -343,8 +335,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     first.left = 0;
     bool work;
     int stride = 1;  // between the CTA's tiles of an item
-    MergeRec* rec = nullptr;
-    Shares shares{0, 0, 0};
     if (CL) {
         // tiles rank, rank + cs, ...: the first one does not depend on the length
         const int cs = (int)cluster_size(), rank = (int)cluster_rank();
@@ -376,10 +366,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         find_starts(a, blockIdx.x, 1, start, scratch);
         const Start st = *start;
         work = st.count > 0;
-        shares = st.sh;
         if (work) first.begin(a, st);
-        rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(kRowsTc, D)) + blockIdx.x;
-        if (a.part && threadIdx.x == 0) rec->rest = 0;
+        if (a.part && threadIdx.x == 0) merge_rec<D>(a)->rest = 0;
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -430,16 +418,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const float f = fmaxf(scale2(rowf[(segs & 1) * 128 + row], ti->ek), 1e-37f), ev = (float)iev;
                     const bool part = step || live < kTile || bad;
                     const uint32_t* see = vis + 4 * min(gr / group, a.T - 1);
-                    auto counts = [&](int c) -> uint32_t {  // which of the scores 16 c .. count
-                        if (step) return (see[c >> 1] >> (16 * (c & 1))) & 0xffffu;
-                        const int left = live - c * 16;
-                        return (bad >> c) & 1 ? 0u : left >= 16 ? 0xffffu : left <= 0 ? 0u : (1u << left) - 1u;
-                    };
-                    auto hide = [&](int c, float (&x)[16]) {
-                        const uint32_t s = counts(c);
-#pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (!((s >> j) & 1)) x[j] = -INFINITY;
+                    const int n32 = (live + 31) >> 5;  // groups of 32 scores that hold any (P V stops there, too)
+                    auto counts = [&](int c) -> uint32_t {  // which of the scores 32 c .. count
+                        if (step) return see[c];
+                        const int left = live - c * 32, off = bad >> (2 * c);
+                        const uint32_t s = left >= 32 ? ~0u : (1u << left) - 1u;
+                        return s & ~((off & 1 ? 0xffffu : 0u) | (off & 2 ? 0xffff0000u : 0u));
                     };
                     const uint32_t ts = trow + b * 128;
                     // Weigh with the reference as it is, P going to its own columns; only where
@@ -449,9 +433,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     // tile before: its decision is waited for with the results in hand.
                     const bool lead = n == n0;
                     float sum = 0.f;
-                    int look = 0;  // scores / 16 to look for a row's largest in before weighing
+                    int look = 0;  // scores / 32 to look for a row's largest in before weighing
                     if (lead) {
-                        look = 2;
+                        look = 1;
                     } else if (n == n0 + 1) {
                         wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
                         m = row_m[row];
@@ -461,13 +445,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         if (look) {
                             float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll 1
-                            for (int c = 0; c < look; c++) {
-                                float x[16];
-                                tmem_ld16(ts + c * 16, x);
-                                tmem_ld_wait(x);
-                                if (part) hide(c, x);
+                            for (int c = 0; c < min(look, n32); c++) {
+                                float x[32];
+                                tmem_ld32(ts + c * 32, x);
+                                if (part) {
+                                    const uint32_t s = counts(c);
 #pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
+                                    for (int j = 0; j < 32; j++)
+                                        if (!((s >> j) & 1)) x[j] = -INFINITY;
+                                }
+#pragma unroll
+                                for (int j = 0; j < 32; j += 4) {
                                     t0 = fmaxf(t0, fmaxf(x[j], x[j + 1]));
                                     t1 = fmaxf(t1, fmaxf(x[j + 2], x[j + 3]));
                                 }
@@ -494,16 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         const float c0 = ev - m;
                         uint64_t s2 = 0;  // two sums
                         const uint64_t f2 = pair(f, f), c2 = pair(c0, c0);
-#pragma unroll 1
-                        for (int c = 0; c < 8; c += 2) {
-                            float x[32];
-                            tmem_ld32(ts + c * 16, x);
-                            if (part) {
-                                const uint32_t s = counts(c) | counts(c + 1) << 16;
-#pragma unroll
-                                for (int j = 0; j < 32; j++)
-                                    if (!((s >> j) & 1)) x[j] = -INFINITY;
-                            }
+                        auto weigh = [&](int c, float (&x)[32]) {
                             uint32_t p[16];
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
@@ -513,12 +492,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                                 s2 = add2(s2, pair(e0, e1));
                                 p[j / 2] = pack_f16(e0, e1);
                             }
-                            tmem_st16(trow + kColP + b * 64 + c * 8, p);
+                            tmem_st16(trow + kColP + b * 64 + c * 16, p);
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < n32; c++) {
+                            float x[32];
+                            tmem_ld32(ts + c * 32, x);
+                            if (part) {
+                                const uint32_t s = counts(c);
+#pragma unroll
+                                for (int j = 0; j < 32; j++)
+                                    if (!((s >> j) & 1)) x[j] = -INFINITY;
+                            }
+                            weigh(c, x);
                         }
                         float s0, s1;
                         unpair(s2, s0, s1);
                         sum = s0 + s1;
-                        if (look == 8) break;
+                        if (look == 4) break;
                         bool again = sum > 32768.f || m == kNoRef;
                         if (!look && n > n0 + 1) {
                             wait(kPReady + (b ^ 1), ((n - 1) >> 1) & 1);
@@ -526,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                             if (mm != m) l *= ex2(m - mm), m = mm, again = true;
                         }
                         if (!__any_sync(0xffffffffu, again)) break;
-                        look = 8;
+                        look = 4;
                     }
                     l += scale2(sum, -iev);
                     tmem_st_wait();
@@ -588,7 +579,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 }
             }
             if (!CL && run.u0 == 0 && !whole && a.part && threadIdx.x == 0)
-                *rec = MergeRec{run.b, run.item, run.nu - run.u1, 0, shares};
+                *merge_rec<D>(a) = MergeRec{run.b, run.item, run.nu - run.u1, 0, start->sh};
             if (tiles) {
                 tc_fence_before();
                 __syncwarp();
@@ -667,6 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
 #pragma unroll 1
                     for (int r2 = 0; r2 < 2; r2++) {
                         const int row = (tid >> 1) + 64 * r2;
+                        if ((row & ~15) >= live) break;
                         const uint8_t* blk = stage + (row >> 4) * kv4_block_bytes(D);
                         const uint32_t par = ((const uint32_t*)(blk + 16 * D))[16 * kv + (row & 15)];
                         const bool here = row < live && !((bad >> (row >> 4)) & 1);
@@ -749,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const int E = max((int)e, 28) - 123;
                     if (tid == 0) {
                         if (kv) ti->ev = E;
-                        else ti->ek = E, ti->live = kTile, ti->bad = 0;
+                        else ti->ek = E, ti->live = a.T, ti->bad = 0;
                         mbar_arrive(bar + kStepReady);
                     }
                     const float f = scale2(1.f, -E);
@@ -798,12 +790,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             wait(kPReady + b, ph);
             wait(kVReady + b, ph);
             if (lead && segs > 0) wait(kOFree, (segs - 1) & 1);
+            const int live = info[n & 7].live;  // only these keys' products
             tc_fence_after();
             if (chosen && ok) {
-#pragma unroll
-                for (int k = 0; k < kTile / 16; k++)
+                auto step16 = [&](int k) {
                     mma_ts(tmem + kColO, tmem + kColP + b * 64 + k * 8, v_lo + ((L::kV + b * L::kOperand + k * 16 * 128) >> 4), v_hi,
                            id_o, !lead || k > 0);
+                };
+                if (live > kTile - 16) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; k++) step16(k);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k * 16 < live; k++) step16(k);
+                }
                 mma_commit(bar + kODone + b);
             }
             __syncwarp();
