@@ -39,6 +39,27 @@ __host__ __device__ __forceinline__ size_t kv4_block_at(int page, int head, int 
     return ((((size_t)page * n_kv_heads + head) << blk_log2) + blk) * kv4_block_bytes(D);
 }
 
+// packed pairs of fp32: one instruction for two
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Whether step row j is visible to step row i (the combined 2D-window +
 // verification mask): every row sees row 0; lookahead row (l, c) sees level 0
 // up to column c and column c up to level l; verification row (g, i) sees its

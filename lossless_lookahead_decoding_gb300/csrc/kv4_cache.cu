@@ -231,67 +231,58 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_release(ReleaseArgs a)
 // One vector is quantised by D / 16 neighbouring lanes, 16 channels a lane,
 // with four tokens (D = 128) or eight (D = 64) of the same head in a warp: a
 // warp reads whole vectors, and writes the neighbouring 32-byte panel rows of
-// consecutive slots.  K and V of a token are in flight together.
-// HBM bound by design: one pass, extremes by packed max/min, no division per
-// element.  The decisions are exact (the codes are those of exact
+// consecutive slots.  K and V of a token are in flight together, and even
+// lanes work out K's parameters while odd ones work out V's.
+// HBM bound by design: one pass, extremes by packed max/min, and 3.5
+// instructions an element for the codes: they stay in pairs, the way the
+// format keeps them (channel 2i in bits 4i, 2i + 1 in bits 16 + 4i).
+// The decisions are exact (the codes are those of exact
 // arithmetic, whatever the inputs):
 //  * s: 15 s against hi - lo with the rounding error of the subtraction;
 //  * bf16 inputs: x / s is either a tie or at least 2^-10 away from one (both
 //    have 8 significant bits and |x| >= s / 2 where a tie is near), so x * (1
-//    / s), off by less than 2^-18, rounded to multiples of 2^-11 is a tie
+//    / s), off by less than 2^-17, rounded to multiples of 2^-11 is a tie
 //    exactly when x / s is;
 //  * fp32 inputs: the residual x - k s is exact in one fused multiply-add
 //    (12 bits in k s), and is compared with s / 2.
 
 constexpr float kRound11 = 6144.f;       // 1.5 x 2^12: adding it rounds to multiples of 2^-11
-constexpr float kRound0 = 12582912.f;    // 1.5 x 2^23: adding it rounds to whole numbers, ties to even
-
-struct Quant {
-    float s, inv;   // scale as the elements are compared with it, its reciprocal
-    int z;
-    uint32_t param;
-    bool some;      // codes differ from z (s is neither 0 nor NaN)
-    bool tiny;      // the elements are to be multiplied by 2^64
-};
+constexpr float kRound0 = 12582912.f;    // 1.5 x 2^23: adding it rounds to whole numbers, ties to even; its bits' lower half is 0
+constexpr uint32_t kKvNan = 0x7fc04300u; // the parameter word of a vector with a NaN or an infinity
 
 template <bool F32>
 __device__ __forceinline__ int nearest(float x, float s, float inv)
 {
-    if (!F32) {
-        const float t = (__fmul_rn(x, inv) + kRound11) - kRound11;
-        return __float_as_int(t + kRound0) - 0x4B400000;
-    }
+    if (!F32) return __float_as_int(__fadd_rn(__fmaf_rn(x, inv, kRound11), kRound0 - kRound11)) - 0x4B400000;
     int k = __float_as_int(__fmul_rn(x, inv) + kRound0) - 0x4B400000;
     const float r = 2.f * __fmaf_rn(-(float)k, s, x);
     if (fabsf(r) > s || (fabsf(r) == s && (k & 1))) k += r > 0.f ? 1 : -1;
     return k;
 }
 
-// Scale, zero point and parameter word from the extremes (hi or lo NaN or
-// infinite when the vector holds such a value).
+__device__ __forceinline__ float scale_of(uint32_t param) { return __uint_as_float(param & 0xffff0000u); }
+// scales below this are compared with elements times 2^64 (their reciprocals would not fit)
+__device__ __forceinline__ bool tiny_scale(float s) { return s < 0x1p-100f; }
+
+// Parameter word and reciprocal of the scale from the extremes hi = max x and
+// nlo = -min x (NaN or infinite when the vector holds such a value).
 template <bool F32>
-__device__ __forceinline__ Quant quant_params(float hi, float lo)
+__device__ __forceinline__ uint32_t quant_params(float hi, float nlo, float* inv)
 {
-    Quant q;
-    hi = fmaxf(hi, 0.f) + (hi - hi);  // NaN and infinity stay
-    lo = fminf(lo, 0.f) + (lo - lo);
-    q.tiny = false;
-    if (!(hi < INFINITY) || !(lo > -INFINITY)) {
-        q.s = q.inv = 0.f;
-        q.z = 0;
-        q.param = 0x7fc00000u | 0x4300u;
-        q.some = false;
-        return q;
-    }
+    *inv = 0.f;
+    if (!(hi < INFINITY) || !(nlo < INFINITY)) return kKvNan;
+    hi = fmaxf(hi, 0.f);
+    nlo = fmaxf(nlo, 0.f);
     // the span of values near the type's end does not fit: take 2^-8 of both
-    const bool huge = hi > 1e38f || lo < -1e38f;
-    float h = hi, l = lo;
+    const bool huge = fmaxf(hi, nlo) > 1e38f;
+    float h = hi, l = nlo;
     if (huge) {
         h = fmaxf(h * 0x1p-8f, h > 0.f ? 0x1p-149f : 0.f);
-        l = fminf(l * 0x1p-8f, l < 0.f ? -0x1p-149f : 0.f);
+        l = fmaxf(l * 0x1p-8f, l > 0.f ? 0x1p-149f : 0.f);
     }
-    const float sp = h - l, bb = sp - h, err = (h - (sp - bb)) + (-l - bb);  // sp + err = h - l
-    uint32_t c = __float_as_uint(__fdiv_rn(sp, 15.f)) & 0xffff0000u;
+    const float sp = h + l, bb = sp - h, err = (h - (sp - bb)) + (l - bb);  // sp + err = h + l
+    // sp / 15 to within an ulp; cut to bf16 it is at most two steps low and never high
+    uint32_t c = __float_as_uint(sp * (1.f / 15.f)) & 0xffff0000u;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const float d = 15.f * __uint_as_float(c) - sp;  // exact: 12 bits, and near sp
@@ -299,78 +290,130 @@ __device__ __forceinline__ Quant quant_params(float hi, float lo)
     }
     float s = __uint_as_float(c);
     if (huge) s *= 256.f;
-    q.some = s > 0.f;
-    q.tiny = s < 0x1p-100f;
-    const float s0 = s;
-    if (q.tiny) s *= 0x1p64f, lo *= 0x1p64f;
-    q.s = s;
-    q.inv = q.some ? __frcp_rn(s) : 0.f;
-    q.z = q.some ? nearest<F32>(-lo, s, q.inv) : 0;
-    q.param = __float_as_uint(s0) | 0x4300u | (uint32_t)q.z;
-    return q;
+    c = __float_as_uint(s);
+    if (c == 0) return 0x4300u;
+    if (tiny_scale(s)) s *= 0x1p64f, nlo *= 0x1p64f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(*inv) : "f"(s));  // s and 1 / s are normal numbers
+    return c | 0x4300u | (uint32_t)nearest<F32>(nlo, s, *inv);
 }
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmax2_nan(*(const __nv_bfloat162*)&a, *(const __nv_bfloat162*)&b);
+    return *(const uint32_t*)&r;
+}
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmin2_nan(*(const __nv_bfloat162*)&a, *(const __nv_bfloat162*)&b);
+    return *(const uint32_t*)&r;
+}
+
+// max x and -min x of some channels: one word of two bf16 numbers, or two of fp32
+template <bool F32>
+struct Ends {
+    uint32_t w[F32 ? 2 : 1];
+    __device__ __forceinline__ void join(const Ends& o)
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); i++)
+            w[i] = F32 ? __float_as_uint(max_nan(__uint_as_float(w[i]), __uint_as_float(o.w[i]))) : max_nan2(w[i], o.w[i]);
+    }
+    __device__ __forceinline__ Ends from(int lane_xor) const
+    {
+        Ends r;
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); i++) r.w[i] = __shfl_xor_sync(0xffffffffu, w[i], lane_xor);
+        return r;
+    }
+    __device__ __forceinline__ float hi() const { return __uint_as_float(F32 ? w[0] : w[0] << 16); }
+    __device__ __forceinline__ float nlo() const { return __uint_as_float(F32 ? w[F32 ? 1 : 0] : w[0] & 0xffff0000u); }
+};
 
 template <bool F32>
 struct Elems {
     // 16 channels of one lane
-    uint4 w[F32 ? 4 : 2];
+    uint32_t w[F32 ? 16 : 8];
     __device__ __forceinline__ void load(const void* p)
     {
-        const uint4* s = (const uint4*)p;
 #pragma unroll
-        for (int i = 0; i < (F32 ? 4 : 2); i++) w[i] = __ldg(s + i);
+        for (int i = 0; i < (F32 ? 4 : 2); i++) {
+            const uint4 x = __ldg((const uint4*)p + i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
     }
-    __device__ __forceinline__ float at(int i) const
+    __device__ __forceinline__ void zero()
     {
-        const uint32_t* u = (const uint32_t*)w;
-        if (F32) return __uint_as_float(u[i]);
-        return __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 16 : 8); i++) w[i] = 0;
     }
-    __device__ __forceinline__ void extremes(float& hi, float& lo) const
+    __device__ __forceinline__ Ends<F32> ends() const
     {
-        const uint32_t* u = (const uint32_t*)w;
+        Ends<F32> r;
         if (F32) {
-            hi = lo = __uint_as_float(u[0]);
-            bool bad = !(fabsf(hi) < INFINITY);
+            float hi = __uint_as_float(w[0]), nlo = -hi;
 #pragma unroll
             for (int i = 1; i < 16; i++) {
-                const float x = __uint_as_float(u[i]);
-                hi = fmaxf(hi, x);
-                lo = fminf(lo, x);
-                bad |= !(fabsf(x) < INFINITY);
+                hi = max_nan(hi, __uint_as_float(w[F32 ? i : 0]));
+                nlo = max_nan(nlo, -__uint_as_float(w[F32 ? i : 0]));
             }
-            if (bad) hi = lo = __uint_as_float(0x7fc00000u);
+            r.w[0] = __float_as_uint(hi);
+            r.w[F32 ? 1 : 0] = __float_as_uint(nlo);
         } else {
-            __nv_bfloat162 h = *(const __nv_bfloat162*)&u[0], l = h;
+            uint32_t h = w[0], l = w[0];
 #pragma unroll
-            for (int i = 1; i < 8; i++) {
-                const __nv_bfloat162 x = *(const __nv_bfloat162*)&u[i];
-                h = __hmax2_nan(h, x);
-                l = __hmin2_nan(l, x);
+            for (int i = 1; i < 8; i++) h = max_nan2(h, w[i]), l = min_nan2(l, w[i]);
+            l ^= 0x80008000u;
+            r.w[0] = max_nan2(__byte_perm(h, l, 0x5410), __byte_perm(h, l, 0x7632));
+        }
+        return r;
+    }
+    __device__ __forceinline__ void times_2_64()
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 16 : 8); i++) {
+            if (F32) {
+                w[i] = __float_as_uint(__uint_as_float(w[i]) * 0x1p64f);
+            } else {  // exact: these vectors' elements are below 2^-96
+                const float a = __uint_as_float(w[i] << 16) * 0x1p64f, b = __uint_as_float(w[i] & 0xffff0000u) * 0x1p64f;
+                w[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
             }
-            const float2 hf = __bfloat1622float2(h), lf = __bfloat1622float2(l);
-            hi = fmaxf(hf.x, hf.y) + (hf.x - hf.x) + (hf.y - hf.y);
-            lo = fminf(lf.x, lf.y) + (lf.x - lf.x) + (lf.y - lf.y);
+        }
+    }
+    // The codes, 8 a word, of a vector with a scale.
+    __device__ __forceinline__ void codes(uint32_t param, float inv, uint32_t* word) const
+    {
+        const int z = param & 15;
+        float s = scale_of(param);
+        if (tiny_scale(s)) s *= 0x1p64f;
+        const uint64_t inv2 = pair(inv, inv), r11 = pair(kRound11, kRound11), r0 = pair(kRound0 - kRound11, kRound0 - kRound11);
+#pragma unroll
+        for (int wd = 0; wd < 2; wd++) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                uint32_t k2;  // two codes less z, 16 bits each
+                if (F32) {
+                    const uint32_t* x = w + (F32 ? 8 * wd + 2 * i : 0);
+                    const int k0 = nearest<F32>(__uint_as_float(x[0]), s, inv), k1 = nearest<F32>(__uint_as_float(x[1]), s, inv);
+                    k2 = __byte_perm((uint32_t)k0, (uint32_t)k1, 0x5410);
+                } else {
+                    const uint32_t x = w[F32 ? 0 : 4 * wd + i];
+                    float t0, t1;
+                    unpair(add2(fma2(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2, r11), r0), t0, t1);
+                    k2 = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x5410);
+                }
+                u += __viaddmin_s16x2_relu(k2, (uint32_t)z * 0x10001u, 0x000f000fu) << (4 * i);
+            }
+            word[wd] = u;
         }
     }
 };
-
-template <bool F32>
-__device__ __forceinline__ void quantise(const Elems<F32>& e, const Quant& q, uint32_t* word)
-{
-#pragma unroll
-    for (int wd = 0; wd < 2; wd++) {
-        uint32_t u = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            float x = e.at(wd * 8 + i);
-            if (q.tiny) x *= 0x1p64f;
-            const int c = __vimin_s32_relu(nearest<F32>(x, q.s, q.inv) + q.z, 15);
-            u |= (uint32_t)c << (4 * (i >> 1) + 16 * (i & 1));
-        }
-        word[wd] = q.some ? u : 0u;  // s = 0 or NaN: every code 0
-    }
-}
 
 struct AppendArgs {
     uint8_t* pages;
@@ -378,9 +421,10 @@ struct AppendArgs {
     const int *rows, *slots;
     int* status;
     long long row_bytes;
-    int n, n_rows, Hkv, page_log2, blk_log2, n_slots;
+    int n, n_rows, Hkv, page_log2, blk_log2, n_slots, heads_log2;
 };
 
+// A CTA's 8 warps: 2^heads_log2 heads by 8 / 2^heads_log2 groups of tokens.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) k_kv4_append(AppendArgs a)
 {
@@ -388,58 +432,68 @@ __global__ void __launch_bounds__(256) k_kv4_append(AppendArgs a)
     constexpr int E = F32 ? 4 : 2;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
-    const long long tasks = (long long)((a.n + TOK - 1) / TOK) * a.Hkv;
-    for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += (long long)gridDim.x * 8) {
-        const int h = (int)(task % a.Hkv), i = (int)(task / a.Hkv) * TOK + grp;
-        int slot = -1, row = i;
-        if (i < a.n) {
-            slot = a.slots[i];
-            if (a.rows) row = a.rows[i];
-            if (slot >= a.n_slots || (slot >= 0 && (row < 0 || row >= a.n_rows))) {
-                kv4_raise(a.status, LA_ERR_ARG);
-                slot = -1;
-            }
+    const int lane = threadIdx.x & 31, sub = lane % L, warp = threadIdx.x >> 5;
+    const int h = (blockIdx.y << a.heads_log2) + (warp & ((1 << a.heads_log2) - 1));
+    const long long group = ((long long)blockIdx.x << (3 - a.heads_log2)) + (warp >> a.heads_log2), i = group * TOK + lane / L;
+    if (h >= a.Hkv || group * TOK >= a.n) return;
+    int slot = -1;
+    long long row = i;
+    if (i < a.n) {
+        slot = a.slots[i];
+        if (a.rows) row = a.rows[i];
+        if (slot >= a.n_slots || (slot >= 0 && (row < 0 || row >= a.n_rows))) {
+            kv4_raise(a.status, LA_ERR_ARG);
+            slot = -1;
         }
-        const bool live = slot >= 0;
-        Elems<F32> e[2];
-        if (live) {
-            const size_t at = (size_t)row * a.row_bytes + ((size_t)h * D + sub * 16) * E;
-            e[0].load(a.k + at);
-            e[1].load(a.v + at);
-        } else {
+    }
+    const bool live = slot >= 0;
+    Elems<F32> e[2];
+    if (live) {
+        const size_t at = (size_t)row * a.row_bytes + ((size_t)h * D + sub * 16) * E;
+        e[0].load(a.k + at);
+        e[1].load(a.v + at);
+    } else {
+        e[0].zero();
+        e[1].zero();
+    }
+    // K's extremes to the even lanes, V's to the odd ones
+    const bool odd = lane & 1;
+    const Ends<F32> ek = e[0].ends(), ev = e[1].ends();
+    Ends<F32> m = odd ? ev : ek;
+    m.join((odd ? ek : ev).from(1));
 #pragma unroll
-            for (int p = 0; p < 2; p++)
+    for (int o = 2; o < L; o <<= 1) m.join(m.from(o));
+    float inv[2];
+    uint32_t param[2];
+    {
+        float mine;
+        const uint32_t p = quant_params<F32>(m.hi(), m.nlo(), &mine);
+        const uint32_t p2 = __shfl_xor_sync(0xffffffffu, p, 1);
+        const float other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        param[0] = odd ? p2 : p, param[1] = odd ? p : p2;
+        inv[0] = odd ? other : mine, inv[1] = odd ? mine : other;
+    }
+    if (!live) return;
+    const int in_page = slot & ((1 << a.page_log2) - 1), tok = slot & 15;
+    uint8_t* blk = a.pages + kv4_block_at(slot >> a.page_log2, h, in_page >> 4, a.Hkv, a.blk_log2, D);
 #pragma unroll
-                for (int j = 0; j < (F32 ? 4 : 2); j++) e[p].w[j] = make_uint4(0, 0, 0, 0);
-        }
-        const int in_page = slot & ((1 << a.page_log2) - 1), tok = slot & 15;
-        uint8_t* blk = a.pages + kv4_block_at(slot >> a.page_log2, h, in_page >> 4, a.Hkv, a.blk_log2, D);
-#pragma unroll
-        for (int p = 0; p < 2; p++) {
-            float hi, lo;
-            e[p].extremes(hi, lo);
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) {
-                const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
-                hi = fmaxf(hi, h2) + ((hi - hi) + (h2 - h2));
-                lo = fminf(lo, l2) + ((lo - lo) + (l2 - l2));
-            }
-            const Quant q = quant_params<F32>(hi, lo);
-            uint32_t w[2];
-            quantise<F32>(e[p], q, w);
-            if (live) {
-                *(uint2*)(blk + p * 8 * D + (sub >> 2) * 512 + tok * 32 + (sub & 3) * 8) = make_uint2(w[0], w[1]);
-                if (sub == 0) *(uint32_t*)(blk + 16 * D + p * 64 + tok * 4) = q.param;
-            }
-        }
+    for (int p = 0; p < 2; p++) {
+        uint32_t w[2];
+        if (tiny_scale(scale_of(param[p]))) e[p].times_2_64();
+        e[p].codes(param[p], inv[p], w);
+        if (!(scale_of(param[p]) > 0.f)) w[0] = w[1] = 0;  // scale 0 or NaN: every code 0
+        *(uint2*)(blk + p * 8 * D + (sub >> 2) * 512 + tok * 32 + (sub & 3) * 8) = make_uint2(w[0], w[1]);
+        if (sub == p) *(uint32_t*)(blk + 16 * D + p * 64 + tok * 4) = param[p];
     }
 }
 
 // ------------------------------------------------------------------ read ---
 //
 // The values (c - z) s of tokens, in fp32 (exact: 4 + 8 bits) or rounded to
-// bf16.  The mirror image of append; HBM bound.
+// bf16 (once: c - z is exact in bf16, too, so the packed product there rounds
+// the exact value).  One word of codes is 8 channels and 16 bytes of bf16: a
+// lane takes the same word of two tokens, K and V, so that a warp's loads and
+// stores cover whole lines.  HBM bound.
 
 struct ReadArgs {
     const uint8_t* pages;
@@ -447,62 +501,68 @@ struct ReadArgs {
     const int* slots;
     int* status;
     long long row_bytes;
-    int n, Hkv, page_log2, blk_log2, n_slots;
+    int n, Hkv, page_log2, blk_log2, n_slots, heads_log2;
 };
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) k_kv4_read(ReadArgs a)
 {
-    constexpr int L = D / 16, TOK = 32 / L, E = F32 ? 4 : 2;
+    constexpr int L = D / 8, TOK = 32 / L, E = F32 ? 4 : 2;  // a warp: TOK tokens at a time, two times
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
-    const long long tasks = (long long)((a.n + TOK - 1) / TOK) * a.Hkv;
-    for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += (long long)gridDim.x * 8) {
-        const int h = (int)(task % a.Hkv), i = (int)(task / a.Hkv) * TOK + grp;
-        if (i >= a.n) continue;
-        const int slot = a.slots[i];
-        if (slot < 0) continue;
+    const int lane = threadIdx.x & 31, sub = lane % L, warp = threadIdx.x >> 5;
+    const int h = (blockIdx.y << a.heads_log2) + (warp & ((1 << a.heads_log2) - 1));
+    const long long group = ((long long)blockIdx.x << (3 - a.heads_log2)) + (warp >> a.heads_log2);
+    const long long i0 = group * 2 * TOK + lane / L;
+    if (h >= a.Hkv) return;
+    uint32_t w[2][2], prm[2][2];
+    bool live[2];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const long long i = i0 + t * TOK;
+        int slot = i < a.n ? a.slots[i] : -1;
         if (slot >= a.n_slots) {
             kv4_raise(a.status, LA_ERR_ARG);
-            continue;
+            slot = -1;
         }
+        live[t] = slot >= 0;
+        if (!live[t]) continue;
         const int in_page = slot & ((1 << a.page_log2) - 1), tok = slot & 15;
         const uint8_t* blk = a.pages + kv4_block_at(slot >> a.page_log2, h, in_page >> 4, a.Hkv, a.blk_log2, D);
-        uint2 w[2];
-        uint32_t prm[2];
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-            w[p] = *(const uint2*)(blk + p * 8 * D + (sub >> 2) * 512 + tok * 32 + (sub & 3) * 8);
-            prm[p] = *(const uint32_t*)(blk + 16 * D + p * 64 + tok * 4);
+            w[t][p] = *(const uint32_t*)(blk + p * 8 * D + (sub >> 3) * 512 + tok * 32 + (sub & 7) * 4);
+            prm[t][p] = *(const uint32_t*)(blk + 16 * D + p * 64 + tok * 4);
         }
-        const size_t at = (size_t)i * a.row_bytes + ((size_t)h * D + sub * 16) * E;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        if (!live[t]) continue;
+        const size_t at = (size_t)(i0 + t * TOK) * a.row_bytes + ((size_t)h * D + sub * 8) * E;
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-            const float s = __uint_as_float(prm[p] & 0xffff0000u);
-            const float z = __uint_as_float(prm[p] << 16);  // 128 + z
-            float x[16];
-#pragma unroll
-            for (int c = 0; c < 16; c++) {
-                const uint32_t u = c < 8 ? w[p].x : w[p].y;
-                const uint32_t code = (u >> (4 * ((c & 7) >> 1) + 16 * (c & 1))) & 15u;
-                // code into the mantissa of 128 (fp32: 2^16 per unit)
-                x[c] = (__uint_as_float(0x43000000u | code << 16) - z) * s;
-            }
+            const uint32_t u = w[t][p], q = prm[t][p];
             uint8_t* dst = (p ? a.v : a.k) + at;
+            // a code in the mantissa of 128 (bf16: 1 a unit; fp32: 2^16 a unit), less 128 + z
             if (F32) {
+                const float s = scale_of(q), z = __uint_as_float(q << 16);
+                float x[8];
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    *(float4*)(dst + 16 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                for (int c = 0; c < 8; c++)
+                    x[c] = (__uint_as_float(0x43000000u | ((u >> (4 * (c >> 1) + 16 * (c & 1))) & 15u) << 16) - z) * s;
+                *(float4*)dst = make_float4(x[0], x[1], x[2], x[3]);
+                *(float4*)(dst + 16) = make_float4(x[4], x[5], x[6], x[7]);
             } else {
-                uint32_t y[8];
+                const uint32_t s2 = __byte_perm(q, q, 0x3232), z2 = __byte_perm(q, q, 0x1010);
+                uint32_t y[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                    y[j] = *(uint32_t*)&b;
+                for (int c = 0; c < 4; c++) {
+                    const uint32_t x = (u >> (4 * c) & 0x000f000fu) | 0x43004300u;
+                    const __nv_bfloat162 r = __hmul2_rn(__hsub2_rn(*(const __nv_bfloat162*)&x, *(const __nv_bfloat162*)&z2),
+                                                        *(const __nv_bfloat162*)&s2);
+                    y[c] = *(const uint32_t*)&r;
                 }
                 *(uint4*)dst = make_uint4(y[0], y[1], y[2], y[3]);
-                *(uint4*)(dst + 16) = make_uint4(y[4], y[5], y[6], y[7]);
             }
         }
     }
@@ -531,6 +591,15 @@ int plan_ready()
         g_plan_ready[dev] = true;
     }
     return LA_OK;
+}
+
+// The CTAs of append and read: 8 warps each, a warp 512 / D tokens of a head,
+// the heads of a token next to each other (their rows are).
+dim3 token_grid(const la_kv4_desc& c, int n, int* heads_log2)
+{
+    *heads_log2 = std::min(3, log2_of(c.n_kv_heads));
+    const long long tokens = (512LL / c.head_dim) << (3 - *heads_log2), heads = 1 << *heads_log2;
+    return dim3((unsigned)((n + tokens - 1) / tokens), (unsigned)((c.n_kv_heads + heads - 1) / heads));
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
@@ -568,10 +637,8 @@ int launch_kv4_append(cudaStream_t s, const la_kv4_desc& c, const void* k, const
     const bool f32 = dtype == LA_FP32;
     AppendArgs a{(uint8_t*)c.pages, (const uint8_t*)k, (const uint8_t*)v, rows, slots, c.status,
                  (long long)ld * (f32 ? 4 : 2), n, n_rows, c.n_kv_heads, log2_of(c.page), log2_of(c.page / 16),
-                 c.n_pages * c.page};
-    const int tok = 512 / c.head_dim;
-    const long long tasks = (n + (long long)tok - 1) / tok * c.n_kv_heads;
-    const dim3 grid((unsigned)std::min((tasks + 7) / 8, 152LL * 8));
+                 c.n_pages * c.page, 0};
+    const dim3 grid = token_grid(c, n, &a.heads_log2);
     auto kern = c.head_dim == 128 ? (f32 ? k_kv4_append<128, true> : k_kv4_append<128, false>)
                                   : (f32 ? k_kv4_append<64, true> : k_kv4_append<64, false>);
     return done(launch_pdl(kern, grid, dim3(256), 0, s, a));
@@ -581,10 +648,8 @@ int launch_kv4_read(cudaStream_t s, const la_kv4_desc& c, const int* slots, int 
 {
     const bool f32 = dtype == LA_FP32;
     ReadArgs a{(const uint8_t*)c.pages, (uint8_t*)k, (uint8_t*)v, slots, c.status, (long long)ld * (f32 ? 4 : 2), n,
-               c.n_kv_heads, log2_of(c.page), log2_of(c.page / 16), c.n_pages * c.page};
-    const int tok = 512 / c.head_dim;
-    const long long tasks = (n + (long long)tok - 1) / tok * c.n_kv_heads;
-    const dim3 grid((unsigned)std::min((tasks + 7) / 8, 152LL * 8));
+               c.n_kv_heads, log2_of(c.page), log2_of(c.page / 16), c.n_pages * c.page, 0};
+    const dim3 grid = token_grid(c, n, &a.heads_log2);
     auto kern = c.head_dim == 128 ? (f32 ? k_kv4_read<128, true> : k_kv4_read<128, false>)
                                   : (f32 ? k_kv4_read<64, true> : k_kv4_read<64, false>);
     return done(launch_pdl(kern, grid, dim3(256), 0, s, a));
