@@ -24,14 +24,14 @@ using namespace ptx;
 // Latency bound: a few kilobytes in, the slots out.  So every CTA scans all
 // sequences by itself (the lengths come out of L2) and keeps both sums in
 // shared memory; no CTA waits for another.  Work is then split over slots,
-// four neighbouring ones a thread (one search, one 16-byte store), and over
-// new pages.  One CTA serves up to 16 K slots; beyond that one more for every 8 K.
+// eight neighbouring ones a thread, and over new pages.  One CTA serves up to 16 K slots; beyond that one more for every 8 K.
 // The new lengths are written by CTA 0 of the same launch when they go to
 // buffers of their own; updated in place they are written by a second,
 // one-CTA launch (kCommit) because other CTAs may still be reading them.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxBatch = 8192;
+constexpr int kPlanPer = 8;  // slots a thread: one search, whole 16-byte stores
 enum PlanMode { kPlanAll, kPlanMap, kPlanCommit };
 
 struct PlanArgs {
@@ -125,38 +125,44 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_plan(PlanArgs a)
     __syncthreads();
     const int tid = blockIdx.x * kPlanThreads + threadIdx.x, nthr = gridDim.x * kPlanThreads;
     if (a.mode != kPlanCommit) {
-        // slots, four at a time
+        // slots, eight at a time, in runs of neighbours: tokens of one sequence and page,
+        // or places that no token takes
         const int live = ok ? (a.stride ? a.B * a.stride : (int)total.a) : 0;
         const bool wide = ((uintptr_t)a.slots & 15) == 0;
-        for (int t0 = tid * 4; t0 < a.n_slots; t0 += nthr * 4) {
-            int s[4] = {-1, -1, -1, -1};
-            if (t0 < live) {
-                int b = a.stride ? t0 / a.stride : last_not_above(first_tok, a.B, t0), seen = -1;
-                int len = 0, n = 0, base = 0;
+        for (long long at0 = (long long)tid * kPlanPer; at0 < a.n_slots; at0 += (long long)nthr * kPlanPer) {
+            const int t0 = (int)at0, t1 = min(a.n_slots - t0, kPlanPer);
+            int s[kPlanPer];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int t = t0 + i;
-                    if (t >= live) break;
-                    if (a.stride) b = t / a.stride;
-                    else
-                        while (b + 1 < a.B && first_tok[b + 1] <= t) b++;
-                    if (b != seen) {
-                        seen = b;
-                        len = a.lens[b];
-                        n = len < 0 ? 0 : a.n_new[b];
-                        base = a.stride ? b * a.stride : first_tok[b];
-                    }
-                    if (t - base >= n) continue;
-                    const int pos = len + (t - base), had = (len + page - 1) >> a.page_log2, j = pos >> a.page_log2;
+            for (int i = 0; i < kPlanPer; i++) s[i] = -1;
+            int b = t0 >= live ? 0 : a.stride ? t0 / a.stride : last_not_above(first_tok, a.B, t0);
+#pragma unroll 1
+            for (int i0 = 0; i0 < t1 && t0 + i0 < live;) {
+                const int len = a.lens[b], n = len < 0 ? 0 : a.n_new[b];
+                const int off = t0 + i0 - (a.stride ? b * a.stride : first_tok[b]);
+                int run = a.stride - off, slot = -1;  // to the sequence's end
+                if (off < n) {
+                    const int pos = len + off, had = (len + page - 1) >> a.page_log2, j = pos >> a.page_log2;
                     const int pg = j < had ? a.table[(size_t)b * a.max_pages + j]
                                            : a.free_pages[n_free - 1 - first_page[b] - (j - had)];
-                    s[i] = pg < 0 ? -1 : (pg << a.page_log2) + (pos & (page - 1));
+                    if (pg >= 0) slot = (pg << a.page_log2) + (pos & (page - 1));
+                    run = min(page - (pos & (page - 1)), n - off);
                 }
+                const int i1 = i0 + min(run, kPlanPer - i0);
+#pragma unroll
+                for (int i = 0; i < kPlanPer; i++)
+                    if (i >= i0 && i < i1 && slot >= 0) s[i] = slot + (i - i0);
+                i0 = i1;
+                if (a.stride) b += off + run == a.stride;
+                else
+                    while (b + 1 < a.B && first_tok[b + 1] <= t0 + i0) b++;
             }
-            if (wide && t0 + 4 <= a.n_slots) {
-                *(int4*)(a.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
+            if (wide && t1 == kPlanPer) {
+#pragma unroll
+                for (int i = 0; i < kPlanPer; i += 4) *(int4*)(a.slots + t0 + i) = make_int4(s[i], s[i + 1], s[i + 2], s[i + 3]);
             } else {
-                for (int i = 0; i < 4 && t0 + i < a.n_slots; i++) a.slots[t0 + i] = s[i];
+#pragma unroll
+                for (int i = 0; i < kPlanPer; i++)
+                    if (i < t1) a.slots[t0 + i] = s[i];
             }
         }
         // new pages into the block table
