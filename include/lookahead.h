@@ -435,7 +435,7 @@ typedef struct la_kv4_desc {
     int n_kv_heads, head_dim; /* head_dim 64 or 128, n_kv_heads <= 1024             */
     int page;                 /* tokens per page: 16, 32, 64 or 128                 */
     int n_pages;              /* pages; n_pages * page < 2^31                       */
-    int max_pages;            /* block-table entries of one sequence                */
+    int max_pages;            /* block-table entries of one sequence; max_pages * page <= 2^30 */
     void* pages;              /* DEVICE, n_pages * la_kv4_page_bytes(), 16-byte aligned */
     int32_t* status;          /* DEVICE int32, 0 at first, or NULL: the first error */
 } la_kv4_desc;
@@ -463,7 +463,8 @@ LA_API size_t la_kv4_page_bytes(const la_kv4_desc* c);
  *   pages_left  DEVICE int32: *n_free less the pages taken (may be n_free)
  * All or nothing: if the pages, a table row, n_slots or slot_stride do not
  * suffice (LA_ERR_CAPACITY in *status) or a count is negative (LA_ERR_ARG),
- * every slot is -1 and the table, lengths and page count stay.  desc.pages is
+ * every slot is -1 and the table, lengths and page count stay.  Tokens of a
+ * page index outside 0..n_pages-1 get slot -1 (LA_ERR_ARG).  desc.pages is
  * not used.  batch <= 8192.  LA_ERR_ARG also for output buffers that overlap
  * others than said. */
 LA_API int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int32_t* n_new, int batch,
@@ -529,7 +530,7 @@ LA_API size_t la_kv4_attention_bytes(const la_kv4_desc* c, const la_kv4_attn* a)
  * 2D-window + verification mask lets it see (never none: each row sees row
  * 0), scaled by 1 / sqrt(head_dim).  Positions past a length are never used,
  * whatever bytes they hold, and a NaN or infinity in a step row reaches only
- * rows that see it.  A length above its bound leaves that sequence's rows
+ * rows that see it.  out overlaps no other buffer.  A length above its bound leaves that sequence's rows
  * alone, a page index outside the pool counts as no keys (LA_ERR_ARG in
  * *status).  Asynchronous on `stream`; the order of sums depends on the
  * shapes and lengths alone, so equal calls give equal bits.  Two calls that

@@ -100,9 +100,9 @@ constexpr float kMinScale = 0x1p-92f;  // added to V scales, so that their logar
 // step rows it sees (bits).
 constexpr int kMaxRows = 16;
 struct RowAt {
-    int q, out;
+    long long q;
+    int out;
     uint32_t sees;
-    int pad;
 };
 
 template <int D, int TW>
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
         const int r = threadIdx.x - 64, i = r / group;
         uint32_t see = 0;
         for (int j = 0; j < a.T; j++) see |= kv4_sees(i, j, a.W, a.n1) ? 1u << j : 0u;
-        tab[r] = RowAt{i * a.q_ld + (r - i * group) * D, (i * a.H + r - i * group) * D, see, 0};
+        tab[r] = RowAt{(long long)i * a.q_ld + (r - i * group) * D, (i * a.H + r - i * group) * D, see};
     }
     pdl_wait();
     pdl_trigger();

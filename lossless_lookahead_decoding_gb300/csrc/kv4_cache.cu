@@ -37,7 +37,7 @@ enum PlanMode { kPlanAll, kPlanMap, kPlanCommit };
 struct PlanArgs {
     const int *lens, *n_new, *free_pages, *n_free;
     int *table, *slots, *new_lens, *left, *status;
-    int B, page_log2, max_pages, n_slots, stride, mode;
+    int B, page_log2, max_pages, n_pages, n_slots, stride, mode;
 };
 
 struct Scan2 {
@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_plan(PlanArgs a)
                     const int pos = len + off, had = (len + page - 1) >> a.page_log2, j = pos >> a.page_log2;
                     const int pg = j < had ? a.table[(size_t)b * a.max_pages + j]
                                            : a.free_pages[n_free - 1 - first_page[b] - (j - had)];
-                    if (pg >= 0) slot = (pg << a.page_log2) + (pos & (page - 1));
+                    if ((unsigned)pg < (unsigned)a.n_pages) slot = (pg << a.page_log2) + (pos & (page - 1));
+                    else kv4_raise(a.status, LA_ERR_ARG);
                     run = min(page - (pos & (page - 1)), n - off);
                 }
                 const int i1 = i0 + min(run, kPlanPer - i0);
@@ -617,7 +618,7 @@ int launch_kv4_plan(cudaStream_t s, const la_kv4_desc& c, const int* lens, const
 {
     if (int rc = plan_ready()) return rc;
     PlanArgs a{lens, n_new, free_pages, n_free, table, slots, new_lens, left, c.status, B, log2_of(c.page), c.max_pages,
-               n_slots, stride, kPlanAll};
+               c.n_pages, n_slots, stride, kPlanAll};
     const size_t smem = (size_t)B * 8;
     const int grid = n_slots <= 16384 ? 1 : (int)std::min(152LL, (n_slots + 8191LL) / 8192);
     const bool in_place = new_lens == lens || left == n_free;
@@ -674,7 +675,7 @@ bool desc_ok(const la_kv4_desc* c)
     if (!c || (c->head_dim != 64 && c->head_dim != 128) || c->n_kv_heads < 1 || c->n_kv_heads > 1024) return false;
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
     if (c->n_pages < 1 || (long long)c->n_pages * c->page >= (1LL << 31)) return false;
-    return c->max_pages >= 1 && (long long)c->max_pages * c->page < (1LL << 31);
+    return c->max_pages >= 1 && (long long)c->max_pages * c->page <= (1LL << 30);  // (lengths in tiles stay within an int)
 }
 
 bool aligned(const void* p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }

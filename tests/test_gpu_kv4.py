@@ -511,6 +511,93 @@ def test_attention_refuses_wrong_tensors():
                     out=out, workspace=ws)
 
 
+@pytest.mark.parametrize("shape,step,lens", [
+    ((8, 8, 128), (0, 103, 1), [30]), ((8, 8, 64), (0, 40, 1), [3, 700, 0]), ((8, 2, 128), (15, 5, 15), [300]),
+    ((8, 8, 128), (7, 5, 7), [129] * 11), ((32, 4, 128), (0, 2, 0), [777, 30]), ((16, 16, 64), (2, 4, 2), [500, 31])], ids=str)
+def test_attention_error_is_that_of_the_output(shape, step, lens):
+    """Over many rows of normal data the error is little more than the output's
+    rounding to bf16.  That one: uniform within half a step, relative 2^-8 / m
+    at a mantissa m in [1, 2), and m log-uniform: rms 2^-8 / sqrt(3) sqrt(3 /
+    (8 ln 2)) = 1.66e-3.  The fp16 roundings of probabilities, values and keys
+    (rms 2^-11 / sqrt(3) or less of p v each, the keys' times scores of
+    order 1) add in squares 3 (2.8e-4)^2: 1.73e-3.  Bound: 1.2 times the first."""
+    H, Hkv, D = shape
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, lens, 32, 17)
+    out = _call(c, qkv, dl, dt, H, *step)
+    c.check()
+    T = 1 + (step[0] + step[2]) * (step[1] - 1)
+    x = qkv.double().cpu().numpy().reshape(len(lens), T, H + 2 * Hkv, D)
+    got, at, num, den = out.double().cpu().numpy().reshape(len(lens), T, H, D), 0, 0.0, 0.0
+    for b, n in enumerate(lens):
+        want, _ = R.attention(x[b, :, :H], x[b, :, H:H + Hkv], x[b, :, H + Hkv:], vals[0][at:at + n], vals[1][at:at + n], *step)
+        num, den, at = num + ((got[b] - want) ** 2).sum(), den + (want ** 2).sum(), at + n
+    bound = 1.2 * 2.0 ** -8 / np.sqrt(3) * np.sqrt(3 / (8 * np.log(2)))
+    assert np.sqrt(num / den) <= bound, (np.sqrt(num / den), bound)
+
+
+@pytest.mark.parametrize("step,H", [((0, 16, 1), 1), ((0, 16, 1), 2), ((7, 3, 0), 1)], ids=str)
+def test_attention_rows_past_32_bit_offsets(step, H):
+    """Step rows so far apart that row offsets pass 2^31 elements."""
+    import torch
+    D, W, N, G = 64, *step
+    T, ld = 1 + (W + G) * (N - 1), 1 << 28
+    c, qkv, dl, dt, vals = _attend_case(H, 1, D, *step, [70], 16, 23)
+    far = torch.empty((T - 1) * ld + (H + 2) * D, dtype=torch.bfloat16, device="cuda").as_strided((T, (H + 2) * D), (ld, 1))
+    far.copy_(qkv)
+    out = _call(c, far, dl, dt, H, *step, out=torch.full((T, H * D), 77.0, dtype=torch.bfloat16, device="cuda"))
+    c.check()
+    assert torch.equal(out, _call(c, qkv, dl, dt, H, *step))
+    _verify(out, qkv, [70], vals, H, 1, D, *step)
+
+
+@pytest.mark.parametrize("heads,D", [(2, 64), (9, 128), (13, 64), (40, 128)])
+def test_append_and_read_many_heads(heads, D):
+    """Numbers of heads that leave parts of the last workers idle."""
+    import torch
+    n, page = 101, 16
+    g = np.random.default_rng(heads)
+    c = _cache(9, heads, D, page, 9, fill=0x5A)
+    slots = g.permutation(9 * page)[:n]
+    k, v = (torch.from_numpy(g.standard_normal((n, heads, D)).astype(np.float32)).cuda().to(torch.bfloat16) for _ in range(2))
+    c.append(k, v, _i32(slots))
+    want = R.pack(*(x.double().cpu().numpy() for x in (k, v)), 9, page, slots, fill=0x5A)
+    assert np.array_equal(c.pages.cpu().numpy(), want)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    c.read(_i32(slots), ko, vo)
+    c.check()
+    for x, o in ((k, ko), (v, vo)):
+        cd, s, z = R.quantise(x.double().cpu().numpy())
+        assert torch.equal(o.cpu(), torch.from_numpy((cd - z[..., None]) * s[..., None]).to(torch.bfloat16))
+
+
+def test_plan_reports_pages_outside_the_pool():
+    """A page index outside the pool, held or newly taken: its tokens get no
+    slot (and none of another page's), the rest as ever."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    for bad in (-1, 6, 1 << 28, -(1 << 28)):
+        c = _cache(6, 1, 64, 16, 4)
+        lens, new = [20, 10, 0], [3, 10, 17]
+        table = np.array([[0, 1, -1, -1], [2, -1, -1, -1], [-1] * 4])
+        free = np.array([3, bad, 4])
+        for held in (False, True):
+            tb, fr = table.copy(), free.copy()
+            if held:
+                tb[0, 1], fr[1] = bad, 5
+            slots = torch.full((33,), 99, dtype=torch.int32, device="cuda")
+            nl, left, dt = _i32([0] * 3), _i32([0]), _i32(tb)
+            c.plan(_i32(lens), _i32(new), _i32(fr), _i32([3]), dt, slots, nl, left)
+            with pytest.raises(LA.LAError) as e:
+                c.check()
+            assert e.value.code == LA.LA_ERR_ARG
+            got = slots.cpu().numpy()
+            # pages taken from the top: sequence 1 gets 4, sequence 2 gets fr[1], then 3
+            want = np.r_[(-1, -1, -1) if held else (20, 21, 22), 42:48, 64:68,
+                         np.arange(80, 96) if held else np.full(16, -1), 48, [-1] * 3]
+            assert np.array_equal(got, want), (bad, held, got)
+            assert nl.cpu().numpy().tolist() == [23, 20, 17] and int(left) == 0
+
+
 # ------------------------------------------------------- all of them together
 
 def _serve(graph, steps=6):
@@ -627,3 +714,59 @@ def test_two_graphs_with_their_own_workspaces_run_side_by_side():
                 cg.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("step", [(4, 3, 4), (0, 64, 1)], ids=str)
+def test_calls_on_two_streams_with_their_own_workspaces(step):
+    """Many rows per KV head: calls that overlap on two streams."""
+    import torch
+    H, Hkv, D = 16, 8, 128
+    cases = [_attend_case(H, Hkv, D, *step, [n] + [77, 300] * 8, 64, s) for n, s in ((900, 1), (1500, 2))]
+    want = [_call(c, qkv, dl, dt, H, *step) for c, qkv, dl, dt, _ in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    ws = [torch.zeros(c.attention_bytes(17, H, *step), dtype=torch.uint8, device="cuda") for c, *_ in cases]
+    assert all(w.numel() for w in ws)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (c, qkv, dl, dt, _), o, w, s in zip(cases, outs, ws, streams):
+            with torch.cuda.stream(s):
+                _call(c, qkv, dl, dt, H, *step, out=o, ws=w)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to run before a capture: kernels are set up while it goes on."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, lossless_lookahead_decoding_gb300 as LA
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+c = LA.KV4Cache(LA.KV4Cache.empty_pages(4, 2, 128, 16), 16, 4)
+lens, new, free, nf, table = i32([0]), i32([5]), i32([3, 2, 1, 0]), i32([4]), i32([[-1] * 4])
+slots = i32([0] * 8)
+k = torch.randn((8, 256), device="cuda").to(torch.bfloat16)
+q, q2 = torch.randn((1, 512), device="cuda").to(torch.bfloat16), torch.randn((40, 512), device="cuda").to(torch.bfloat16)
+k2 = torch.randn((40, 256), device="cuda").to(torch.bfloat16)
+o, o2 = torch.zeros_like(q), torch.zeros_like(q2)
+b = [torch.empty(max(16, c.attention_bytes(1, 4, 0, n, g)), dtype=torch.uint8, device="cuda") for n, g in ((2, 0), (40, 1))]
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    c.plan(lens, new, free, nf, table, slots, lens, nf, stride=8)
+    c.append(k, k, slots)
+    c.attention(q, k[:1], k[:1], lens, table, 0, 2, 0, out=o, workspace=b[0])
+    c.attention(q2, k2, k2, lens, table, 0, 40, 1, out=o2, workspace=b[1])
+gr.replay()
+torch.cuda.synchronize()
+c.check()
+assert int(lens) == 5 and int(nf) == 3 and bool(o.any()) and bool(o2.any())
+gr.replay()
+torch.cuda.synchronize()
+c.check()
+assert int(lens) == 10 and int(nf) == 3
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
