@@ -978,10 +978,17 @@ TcPlan tc_plan(const la_kv4_desc& c, const la_kv4_attn& a)
     p.items = (long long)a.batch * c.n_kv_heads * p.mtiles;
     const int room = c.max_pages * c.page, max_len = a.max_len > 0 && a.max_len < room ? a.max_len : room;
     const int tiles = (max_len + kTile - 1) / kTile + 1;  // of an item, at most
-    p.cluster = 0;
-    if (2 * p.items <= kSMs) {
-        p.cluster = 2;
-        while (p.cluster < 8 && 2 * p.cluster * p.items <= kSMs && p.cluster < tiles) p.cluster *= 2;
+    // Clusters of 4 and 8 leave some of a GPC's SMs over: 38 items of 1 K tokens in fours took two rounds
+    // (25.9 us against 15.7 in twos), 16 in eights, too (24.5; 14: 13.2).  32 and 14 fit.  A cluster's time goes with the longest item, equal runs' with all tiles, and 10 tiles'
+    // time on top for parts and their merge; of a batch, three quarters of the longest length are
+    // taken for the average.  D = 128, 100 rows (us, cluster / runs): 8 items of 4 K tokens 15.8 / 20.8,
+    // of 32 K 44.6 / 37.1; 28 of 16 K 45.5 / 44.1, of 32 K 77.5 / 71.4; 28 of 4 to 32 K 76.4 / 48.3;
+    // 70 of 16 K 78.4 / 85.5.
+    p.cluster = p.items <= 14 ? 8 : p.items <= 32 ? 4 : 2 * p.items <= kSMs ? 2 : 0;
+    while (p.cluster > 2 && p.cluster >= 2 * tiles) p.cluster /= 2;
+    if (p.cluster) {
+        const long long all = p.items * tiles * (a.batch > 1 ? 3 : 4) / 4;
+        if (tiles / p.cluster > all / kSMs + 10) p.cluster = 0;
     }
     const long long units = p.items * (kTcExtra + tiles);
     p.nteams = (int)std::max(1LL, std::min((long long)kSMs, std::max(p.items, units / (kTcExtra + 2))));
