@@ -127,16 +127,11 @@ constexpr int kThreads = (kWarps + 1) * 32;
 // Warp kWarps: lane w fills the ring of warp w, block by block in the order in
 // which that warp takes them.  The lanes poll their rings' empty barriers in
 // turn; the page of the next block is looked up a round ahead.
-template <int D, int TW, int S>
-__device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        int* live, int wi)
+template <int D, bool CL, int S>
+__device__ __forceinline__ void produce(const Kv4Attn& a, Run r, bool more, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                        int* live, int wi, int stride)
 {
     const uint64_t pol = policy_evict_first();
-    Run r;
-    r.left = 0;
-    r.t0 = r.t1 = 0;
-    bool more = st.count > 0;
-    if (more) r.begin(a, st);
     constexpr int BLK = kv4_block_bytes(D);
     int t = r.t0 + wi, page = 0, page1 = 0, head = 0, left = 0, blk = 0, n = 0;
     bool pend = false;
@@ -153,10 +148,10 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
                 head = r.item >> (a.mtiles >> 1);
                 blk = (2 * t) & ((1 << a.blk_log2) - 1);
                 pend = true;
-                t += TW;
+                t += stride;
                 return;
             }
-            more = r.next(a);
+            more = !CL && r.next(a);
             t = r.t0 + wi;
         }
     };
@@ -207,7 +202,9 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, const Start& st, uint8
     }
 }
 
-template <int D, int TW>
+// CL: one item per cluster of CTAs, whose warps take its tiles in turn and whose results meet in
+// distributed shared memory: one launch, no workspace.
+template <int D, int TW, bool CL>
 __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
 {
     using L = RowsSmem<D, TW>;
@@ -232,28 +229,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0) raise_long(a);
-    // (its barriers also publish the mbarriers and the table)
-    find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, (long long*)(starts + kWarps));
+    const int cs = CL ? (int)cluster_size() : 1, rank = CL ? (int)cluster_rank() : 0;
+    // the lane's warp in the producer, this warp otherwise; its place in its team, and how many there are
+    const int w = warp == kWarps ? min(lane, kWarps - 1) : warp;
+    const int wi = TW == 1 ? 0 : rank * TW + w, stride = TW * cs;
+    Run run;
+    run.left = 0, run.t0 = run.t1 = 0;
+    bool work;
+    if (CL) {
+        const int x = blockIdx.x / cs, items = a.Hkv * a.mtiles;
+        run.b = x / items;
+        run.item = x - run.b * items;
+        run.len = seq_len(a, run.b);
+        work = run.len >= 0;
+        run.nu = run.u1 = run.t1 = (run.len + kKeys - 1) / kKeys + 1, run.u0 = 0;
+        __syncthreads();  // the mbarriers and the table
+    } else {
+        // (its barriers also publish the mbarriers and the table)
+        find_starts(a, TW == 1 ? blockIdx.x * kWarps : blockIdx.x, TW == 1 ? kWarps : 1, starts, (long long*)(starts + kWarps));
+        const Start st = starts[TW == 1 ? w : 0];
+        work = st.count > 0;
+        if (work) run.begin(a, st);
+    }
     if (warp == kWarps) {
-        const int w = min(lane, kWarps - 1);
-        Start st = starts[TW == 1 ? w : 0];
-        if (lane >= kWarps) st.count = 0;
-        produce<D, TW, S>(a, st, sm + w * S * L::kBlk, full + w * S, empty + w * S, live_of + w * S, TW == 1 ? 0 : w);
+        produce<D, CL, S>(a, run, work && lane < kWarps, sm + w * S * L::kBlk, full + w * S, empty + w * S, live_of + w * S, wi, stride);
         return;
     }
-    const int wi = TW == 1 ? 0 : warp;  // this warp's place in its team
     const int team = TW == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
-    const Start st = starts[TW == 1 ? warp : 0];
     full += warp * S, empty += warp * S, live_of += warp * S;
     MergeRec* rec = (MergeRec*)(a.part + (size_t)a.nteams * 2 * part_floats(R, D)) + team;
-    const bool writes_rec = a.part && team < a.nteams && lane == 0 && wi == 0;
+    const bool writes_rec = !CL && a.part && team < a.nteams && lane == 0 && wi == 0;
     if (writes_rec) rec->rest = 0;
     bool alive = true;  // no wait has given up
     int s = 0, phase = 0;
-    Run run;
-    run.left = 0;
-    if (st.count > 0) {
-        run.begin(a, st);
+    if (work) {
         bool first = true;
         do {
             const int mt = run.item & (a.mtiles - 1), head = run.item >> (a.mtiles >> 1);  // 1 or 2 row tiles
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                 }
                 const int k0 = kv4_key(g), k1 = k0 + 8;
                 const int kA = t, kB = 4 + (t ^ 3);  // V's keys: probability slots 2t, 2t + 1; + 8: slots 2t + 8, 2t + 9
-                for (int tile = run.t0 + wi; tile < min(run.t1, ntc); tile += TW) {
+                for (int tile = run.t0 + wi; tile < min(run.t1, ntc); tile += stride) {
                     if (alive && !mbar_try_wait(full + s, phase)) {
                         const unsigned long long since = globaltimer();
                         while (!mbar_try_wait(full + s, phase))
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
             }
             // ------------------------------------------ the step's own rows (16 at most: one tile)
             // in bf16, with their values brought to the codes' powers of two
-            if (run.t1 > ntc && (TW == 1 || (ntc - run.t0) % TW == wi)) {
+            if (run.t1 > ntc && (TW == 1 || (ntc - run.t0) % stride == wi)) {
                 const __nv_bfloat16 *ks = a.ks + step_at, *vs = a.vs + step_at;
                 const int k0 = kv4_key(g), k1 = k0 + 8;
                 float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                 }
             }
             if (TW > 1) {
-                const float* mg = (const float*)(sm + L::kMerge);
+                float* mg = (float*)(sm + L::kMerge);
                 named_sync(1, kWarps * 32);
                 for (int i = threadIdx.x; i < R * D / 4; i += kWarps * 32) {
                     const int lr = i / (D / 4), c = (i % (D / 4)) * 4;
@@ -636,7 +645,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                         sum += f * ml[w].y;
                         acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
                     }
-                    if (whole) {
+                    if (CL && cs > 1) {
+                        // over the first warp's (no other thread reads these four); the rest of the row's padding
+                        *(float4*)(mg + (size_t)lr * (D + 4) + c) = acc;
+                        if (c == 0) *(float2*)(mg + (size_t)lr * (D + 4) + D + 2) = make_float2(mx, sum);
+                    } else if (whole) {
                         const float inv = 1.f / sum;
                         *(uint2*)(out_base + tab[mt * R + lr].out + c) =
                             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -647,7 +660,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                 }
                 first = false;
             }
-        } while (run.next(a));
+            if (CL && cs > 1) {
+                // every CTA joins its share of the item's outputs
+                __syncwarp();
+                cluster_sync();
+                const int share = R * D / 4 / cs;
+                for (int i = threadIdx.x; i < share; i += kWarps * 32) {
+                    const int at = rank * share + i, lr = at / (D / 4), c = (at % (D / 4)) * 4;
+                    if (mt * R + lr >= a.rows) continue;
+                    const float* row = (const float*)(sm + L::kMerge) + (size_t)lr * (D + 4);
+                    float2 ml[8];
+                    float4 v[8];
+                    float mx = kNoRef, sum = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 8; r++) {
+                        ml[r] = make_float2(kNoRef, 0.f), v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (r < cs) ml[r] = ld_peer2(peer(row + D + 2, r)), v[r] = ld_peer4(peer(row + c, r));
+                    }
+#pragma unroll
+                    for (int r = 0; r < 8; r++) mx = fmaxf(mx, ml[r].x);
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int r = 0; r < 8; r++) {
+                        const float f = ex2(ml[r].x - mx);
+                        sum += f * ml[r].y;
+                        acc.x += f * v[r].x, acc.y += f * v[r].y, acc.z += f * v[r].z, acc.w += f * v[r].w;
+                    }
+                    const float inv = 1.f / sum;
+                    *(uint2*)(out_base + tab[mt * R + lr].out + c) =
+                        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                }
+                __syncwarp();
+                cluster_sync();  // no CTA leaves while others read its results
+            }
+        } while (!CL && run.next(a));
     }
 }
 
@@ -727,6 +773,7 @@ __global__ void __launch_bounds__(256) k_kv4_merge(Kv4Attn a)
 
 struct Plan {
     int tw, grid, nteams, mtiles, extra;
+    int cluster;  // CTAs per item, 0: equal runs over the teams
     bool merge;
     size_t bytes;
 };
@@ -735,6 +782,27 @@ int max_len_of(const la_kv4_desc& c, const la_kv4_attn& a)
 {
     const int room = c.max_pages * c.page;
     return a.max_len > 0 && a.max_len < room ? a.max_len : room;
+}
+
+// CTAs per item, or 0 for equal runs, by what both cost in rounds of a tile per warp (1.55 us with two
+// CTAs on an SM, about half of that while there is one).  A cluster goes as long as the longest item and 2
+// rounds for queries and result, again for every 304 items; equal runs as long as all tiles and 7 rounds
+// for the search of the starts, the parts and their merge.  Of a batch, three quarters of the longest
+// length are taken for the average.  D = 128, 4 rows (us, clusters / runs):
+//   1 sequence of 8 items: 400 tokens 4.5 / 8.3, 4 K 6.2 / 10.4, 16 K 11.3 / 15.0, 64 K 34.1 / 23.4
+//   1 sequence of 100 items: 400 tokens 6.2 / 10.8, 4 K 18.0 / 18.0, 16 K 58.0 / 46.0
+//   1/8 to full length, 250 sequences: to 400 tokens 6.1 / 12.1, to 4 K 28.5 / 24.1, to 16 K 103 / 62
+//   likewise 900: to 400 tokens 15.1 / 18.6, 1200 to 1 K: 31.2 / 29.9, 2000 to 400: 31.3 / 28.4
+int cluster_of(long long items, long long tiles, bool ragged)
+{
+    const double mean = ragged ? 0.75 : 1.0, ctas = 2.0 * kSMs;
+    // (not all of a GPC's SMs fit into clusters of 4 and 8)
+    int cs = items <= 32 ? 8 : items <= 64 ? 4 : items <= kSMs ? 2 : 1;
+    while (cs > 1 && cs * kWarps >= 2 * tiles) cs /= 2;
+    const double waves = std::ceil(items / ctas), shared = items * cs > kSMs / 2 ? 1.0 : 0.55;
+    const double rounds = (double)tiles / (cs * kWarps) * shared * (waves > 1 ? waves * mean : 1.0);
+    const double clusters = rounds + 2 * std::max(1.0, items / ctas), runs = items * tiles * mean / (ctas * kWarps) + 7;
+    return clusters <= runs ? cs : 0;
 }
 
 Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
@@ -748,6 +816,7 @@ Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
     // items) 36 against 39 us, 7B greedy x 16 (512 items) 19.4 against 20.1, 34B greedy x 32 (256 items)
     // 45 against 28
     p.tw = items >= 512 ? 1 : kWarps;
+    p.cluster = cluster_of(items, (max_len_of(c, a) + kKeys - 1) / kKeys + 1, a.batch > 1);
     // an item's queries and result take as long as so many tiles (32 keys); without them the teams
     // that get many short sequences finish last.  Warps: 128 greedy 7B sequences 64 us at 0, 57 at 1,
     // 61 at 4; CTAs: 16 long 34B sequences of 1 to 64 K tokens 132 us at 0, 121 at 14, 122 at 24
@@ -757,7 +826,7 @@ Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
     p.nteams = (int)std::max(1LL, std::min(teams, std::max(items, tiles / kWarps)));
     p.grid = p.tw == 1 ? ceil_div(p.nteams, kWarps) : p.nteams;
     // one sequence: every item has the same tiles, so whole items a team stay whole
-    p.merge = !(a.batch == 1 && items % p.nteams == 0);
+    p.merge = !p.cluster && !(a.batch == 1 && items % p.nteams == 0);
     p.bytes = p.merge ? (size_t)p.nteams * (2 * part_floats(8, c.head_dim) * 4 + sizeof(MergeRec)) : 0;
     return p;
 }
@@ -765,12 +834,12 @@ Plan plan_of(const la_kv4_desc& c, const la_kv4_attn& a)
 std::mutex g_mu;
 unsigned char g_ready[256];
 
-template <int D, int TW>
+template <int D, int TW, bool CL>
 bool set_smem()
 {
-    return cudaFuncSetAttribute(k_kv4_rows<D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, TW>::kBytes) ==
-               cudaSuccess &&
-           cudaFuncSetAttribute(k_kv4_rows<D, TW>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
+    auto kern = k_kv4_rows<D, TW, CL>;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, TW>::kBytes) == cudaSuccess &&
+           cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
 }
 
 // The kernels' shared-memory limits, once per device.
@@ -780,7 +849,8 @@ int attn_ready()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return LA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
-        if (!(set_smem<128, 1>() && set_smem<128, kWarps>() && set_smem<64, 1>() && set_smem<64, kWarps>() && kv4_tc_init()))
+        if (!(set_smem<128, 1, false>() && set_smem<128, kWarps, false>() && set_smem<128, kWarps, true>() &&
+              set_smem<64, 1, false>() && set_smem<64, kWarps, false>() && set_smem<64, kWarps, true>() && kv4_tc_init()))
             return LA_ERR_CUDA;
         g_ready[dev] = 1;
     }
@@ -790,8 +860,11 @@ int attn_ready()
 template <int D>
 cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
-    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, 1>, dim3(p.grid), dim3(kThreads), RowsSmem<D, 1>::kBytes, s, k)
-                              : launch_pdl(k_kv4_rows<D, kWarps>, dim3(p.grid), dim3(kThreads), RowsSmem<D, kWarps>::kBytes, s, k);
+    if (p.cluster)
+        return launch_cluster(k_kv4_rows<D, kWarps, true>, (unsigned)(k.B * k.Hkv * k.mtiles), (unsigned)p.cluster, kThreads,
+                              RowsSmem<D, kWarps>::kBytes, s, k);
+    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, 1, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, 1>::kBytes, s, k)
+                              : launch_pdl(k_kv4_rows<D, kWarps, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, kWarps>::kBytes, s, k);
     if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, D, 8);
     return e;
 }

@@ -208,29 +208,6 @@ __device__ __forceinline__ void add_odd(const Kv4Attn& a, const uint32_t* odd, c
     for (int i = 0; i < 32; i++) o[i] = t[i];
 }
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-// the address of p in the shared memory of CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank)
-{
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
 __device__ __forceinline__ float ld_peer(uint32_t addr)
 {
     float v;
@@ -1003,19 +980,7 @@ template <int D>
 cudaError_t go(cudaStream_t s, const TcPlan& p, const Kv4Attn& k)
 {
     if (!p.cluster) return launch_pdl(k_kv4_tc<D, false>, dim3(p.nteams), dim3(kTcThreads), TcSmem<D>::kBytes, s, k);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.items * p.cluster));
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = TcSmem<D>::kBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)p.cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_kv4_tc<D, true>, k);
+    return launch_cluster(k_kv4_tc<D, true>, (unsigned)p.items, (unsigned)p.cluster, kTcThreads, TcSmem<D>::kBytes, s, k);
 }
 
 template <typename K>

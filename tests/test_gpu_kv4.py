@@ -598,6 +598,48 @@ def test_plan_reports_pages_outside_the_pool():
             assert nl.cpu().numpy().tolist() == [23, 20, 17] and int(left) == 0
 
 
+@pytest.mark.parametrize("case", [
+    dict(H=4, Hkv=2, D=64, step=(0, 2, 0), lens=[40000, 3, 200, 0, -1, 1111], page=16),
+    dict(H=4, Hkv=4, D=128, step=(2, 4, 2), lens=[30001, 0, 77, -1, 2050], page=128),
+    dict(H=32, Hkv=32, D=64, step=(0, 2, 0), lens=[1000 - 50 * i for i in range(20)], page=32),
+    dict(H=32, Hkv=32, D=64, step=(0, 2, 2), lens=[1500 - 170 * i for i in range(9)] + [0, -1, 16], page=64, runs=False),
+    dict(H=48, Hkv=48, D=64, step=(0, 2, 2), lens=[3000 - 300 * i for i in range(10)] + [0, -1, 16], page=64),
+    dict(H=2, Hkv=2, D=64, step=(15, 5, 15), lens=[33000, 12, 129, -1], page=64),
+], ids=lambda c: f"{c['H']}x{c['Hkv']}x{c['D']}-{c['step']}-{len(c['lens'])}")
+def test_attention_equal_runs(case):
+    """Shapes whose items are cut into equal runs and joined from parts (and one
+    that takes them whole), on two streams at once with a workspace each; the
+    workspace's bytes do not matter."""
+    import torch
+    H, Hkv, D, step, lens = case["H"], case["Hkv"], case["D"], case["step"], case["lens"]
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, lens, case["page"], 31)
+    assert (c.attention_bytes(len(lens), H, *step) > 0) == case.get("runs", True)
+    out = _call(c, qkv, dl, dt, H, *step)
+    c.check()
+    _verify(out, qkv, lens, vals, H, Hkv, D, *step, only=set(range(0, len(lens), max(1, len(lens) // 6))))
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.full_like(out, 77.0) for _ in range(2)]
+    ws = [torch.zeros(c.attention_bytes(len(lens), H, *step), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o, w in zip(streams, outs, ws):
+            with torch.cuda.stream(s):
+                _call(c, qkv, dl, dt, H, *step, out=o, ws=w)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 100, 225, 449, 897, 1800])
+@pytest.mark.parametrize("shape", [(3, 3, 64), (16, 2, 128), (40, 40, 128), (130, 65, 64), (200, 200, 64)], ids=str)
+def test_attention_one_sequence(shape, n):
+    """Single tokens over lengths around the tiles that a cluster's warps take,
+    for every cluster size; without a workspace where none is asked for."""
+    H, Hkv, D = shape
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, 0, 2, 0, [n], 64, 37)
+    out = _call(c, qkv, dl, dt, H, 0, 2, 0)
+    c.check()
+    _verify(out, qkv, [n], vals, H, Hkv, D, 0, 2, 0)
+
+
 # ------------------------------------------------------- all of them together
 
 def _serve(graph, steps=6):

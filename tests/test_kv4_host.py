@@ -105,11 +105,11 @@ def test_plan_and_release_refusals():
 def test_attention_refusals_and_sizing():
     import lossless_lookahead_decoding_gb300 as LA
     E = LA.LA_ERR_ARG
-    d, a = _desc(), _attn()
+    d, a = _desc(), _attn(batch=400)
     need = LA.la_kv4_attention_bytes(d, a)
-    assert need > 0  # two sequences may have any lengths: items can be split
+    assert need > 0  # many sequences of any lengths: items are split
     for bad in BAD_DESC + [dict(pages=None), dict(pages=FAKE + 4), dict(status=FAKE + 1)]:
-        assert LA.la_kv4_attention(_desc(**bad), _attn(workspace=FAKE, ws_bytes=need)) == E, bad
+        assert LA.la_kv4_attention(_desc(**bad), _attn(batch=400, workspace=FAKE, ws_bytes=need)) == E, bad
     shapes = [dict(batch=-1), dict(batch=65536), dict(n_heads=0), dict(n_heads=12), dict(W=-1), dict(G=-1), dict(N=1), dict(N=129),
               dict(W=40, N=5), dict(W=127, N=3), dict(max_len=-1), dict(W=64, G=64, N=2)]
     for bad in shapes:
@@ -118,7 +118,7 @@ def test_attention_refusals_and_sizing():
                          dict(q=FAKE + 2), dict(k_step=FAKE + 8), dict(v_step=FAKE + 4), dict(out=FAKE + 8),
                          dict(q_ld=64 * 128 - 8), dict(q_ld=64 * 128 + 4), dict(kv_ld=1016), dict(kv_ld=1028),
                          dict(workspace=None), dict(ws_bytes=need - 1), dict(workspace=FAKE + 8)]:
-        assert LA.la_kv4_attention(d, _attn(**{**dict(workspace=FAKE, ws_bytes=need), **bad})) == E, bad
+        assert LA.la_kv4_attention(d, _attn(**{**dict(batch=400, workspace=FAKE, ws_bytes=need), **bad})) == E, bad
     assert LA.lib().la_kv4_attention(None, C.byref(a), None) == E and LA.lib().la_kv4_attention(C.byref(d), None, None) == E
     assert LA.la_kv4_attention(d, _attn(batch=0)) == 0
     # the widest steps and longest chains are accepted
