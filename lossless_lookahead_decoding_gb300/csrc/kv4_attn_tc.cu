@@ -6,7 +6,7 @@
 // its keys come in tiles of 128: cached ones, then one tile of the step's own
 // rows under the mask.  Per tile, in fp16 with fp32 sums:
 //   S = Q K^T          Q and K in shared memory, S in tensor memory
-//   P = exp2(S f - M)  written over S
+//   P = exp2(S f - M)  into columns of its own
 //   O += P V           P from tensor memory, V in shared memory
 // K and V are unpacked by 8 warps, one key row per two threads: masking two
 // codes out of a word leaves fp16 subnormals (c 2^-24 or c 2^-20), and one
@@ -16,8 +16,8 @@
 // 2^-25 absolute below.  Rounding: q exact (a power of two per row), K and V
 // values 2^-11 relative, P 2^-11, the output to bf16; S, the softmax sums and
 // O stay in fp32.  The tiles' powers of two go into the exponent of exp2 and,
-// for V, into the running reference M, which moves only when a p V unit
-// exceeds 2^8.
+// for V, into the running reference M, which moves only when a row's P of a
+// tile sum to more than 2^15.
 //
 // Tensor and exponential bound for full row tiles (128 x 128 x D x 2 products
 // and 128 x 128 exponentials a tile: about 1024 cycles each at D = 128), HBM and
@@ -29,9 +29,19 @@
 // buffered, codes triple.
 //
 // Two ways to share an item's tiles: equal runs of all items' units over the
-// SMs, parts joined by k_kv4_merge (ragged batches); or a cluster of CTAs per
-// item that join their outputs through distributed shared memory (few items:
-// one launch, no workspace).
+// SMs, parts joined by k_kv4_merge (many items, long ragged batches); or a
+// cluster of 1 to 8 CTAs per item that join their outputs through distributed
+// shared memory (up to 152 items: one launch, no workspace).
+//
+// Measured on one GB300.  121 rows of 32 heads over 2048 tokens (128 CTAs, 4 or
+// 5 tiles each): 17.0 us, 2.1 of them by the tensor cores' rate; the rest is a
+// chain of latencies (launch and first loads 3 us, 6 us a CTA for queries, first
+// tile and unpacking, 2.5 us for the cluster's join).  6 such sequences: 52 us,
+// 0.24 of the tensor cores' rate in steady state (1.6 us a tile): the softmax
+// groups and the unpacking warps alternate on the schedulers (45 % of issue
+// slots, tensor pipe 25 %); short prompt blocks: 128 rows over at most 11 tokens,
+// 1872 items, 118 us = 9.6 us an item, the step's rows' way through bf16 to fp16
+// and the queries' being the longest chain.
 #include <algorithm>
 #include <cmath>
 
@@ -962,8 +972,10 @@ TcPlan tc_plan(const la_kv4_desc& c, const la_kv4_attn& a)
     // time on top for parts and their merge; of a batch, three quarters of the longest length are
     // taken for the average.  D = 128, 100 rows (us, cluster / runs): 8 items of 4 K tokens 15.8 / 20.8,
     // of 32 K 44.6 / 37.1; 28 of 16 K 45.5 / 44.1, of 32 K 77.5 / 71.4; 28 of 4 to 32 K 76.4 / 48.3;
-    // 70 of 16 K 78.4 / 85.5.
-    p.cluster = p.items <= 14 ? 8 : p.items <= 32 ? 4 : 2 * p.items <= kSMs ? 2 : 0;
+    // 70 of 16 K 78.4 / 85.5; 114 sequences (one CTA each) of 60 to 500 tokens 16.9 / 24.2, of 250 to 2 K
+    // 29.2 / 31.2, of 500 to 4 K 45.8 / 38.1.  Where every run is a whole item, runs need no parts: 152
+    // items of 130 tokens 14.7 us, in clusters of one 15.7.
+    p.cluster = p.items <= 14 ? 8 : p.items <= 32 ? 4 : 2 * p.items <= kSMs ? 2 : p.items <= kSMs ? 1 : 0;
     while (p.cluster > 2 && p.cluster >= 2 * tiles) p.cluster /= 2;
     if (p.cluster) {
         const long long all = p.items * tiles * (a.batch > 1 ? 3 : 4) / 4;
@@ -971,6 +983,7 @@ TcPlan tc_plan(const la_kv4_desc& c, const la_kv4_attn& a)
     }
     const long long units = p.items * (kTcExtra + tiles);
     p.nteams = (int)std::max(1LL, std::min((long long)kSMs, std::max(p.items, units / (kTcExtra + 2))));
+    if (p.cluster == 1 && a.batch == 1 && p.nteams == p.items) p.cluster = 0;
     p.merge = !p.cluster && !(a.batch == 1 && p.items % p.nteams == 0);
     p.bytes = p.merge ? (size_t)p.nteams * (2 * part_floats(kRowsTc, c.head_dim) * 4 + sizeof(MergeRec)) : 0;
     return p;

@@ -760,14 +760,13 @@ def test_two_graphs_with_their_own_workspaces_run_side_by_side():
 
 @pytest.mark.parametrize("step", [(4, 3, 4), (0, 64, 1)], ids=str)
 def test_calls_on_two_streams_with_their_own_workspaces(step):
-    """Many rows per KV head: calls that overlap on two streams."""
+    """Many rows per KV head: calls that overlap on two streams (some shapes need no workspace)."""
     import torch
     H, Hkv, D = 16, 8, 128
     cases = [_attend_case(H, Hkv, D, *step, [n] + [77, 300] * 8, 64, s) for n, s in ((900, 1), (1500, 2))]
     want = [_call(c, qkv, dl, dt, H, *step) for c, qkv, dl, dt, _ in cases]
     outs = [torch.zeros_like(w) for w in want]
     ws = [torch.zeros(c.attention_bytes(17, H, *step), dtype=torch.uint8, device="cuda") for c, *_ in cases]
-    assert all(w.numel() for w in ws)
     streams = [torch.cuda.Stream() for _ in cases]
     torch.cuda.synchronize()
     for _ in range(20):
