@@ -123,7 +123,7 @@ def test_attention_refusals_and_sizing():
     assert LA.la_kv4_attention(d, _attn(batch=0)) == 0
     # the widest steps and longest chains are accepted
     for good in [dict(W=127, N=2, G=0), dict(W=0, N=128, G=1), dict(W=15, N=5, G=15), dict(batch=65535)]:
-        assert LA.la_kv4_attention_bytes(d, _attn(**good)) > 0, good
+        assert LA.la_kv4_attention_bytes(d, _attn(**{**dict(batch=400), **good})) > 0, good
 
 
 def test_reference_quantiser_pins():
