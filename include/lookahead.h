@@ -530,9 +530,11 @@ LA_API size_t la_kv4_attention_bytes(const la_kv4_desc* c, const la_kv4_attn* a)
  * 2D-window + verification mask lets it see (never none: each row sees row
  * 0), scaled by 1 / sqrt(head_dim).  Positions past a length are never used,
  * whatever bytes they hold, and a NaN or infinity in a step row reaches only
- * rows that see it.  out overlaps no other buffer.  A length above its bound leaves that sequence's rows
- * alone, a page index outside the pool counts as no keys (LA_ERR_ARG in
- * *status).  Asynchronous on `stream`; the order of sums depends on the
+ * rows that see it.  Values of V below 2^-50 in magnitude lose accuracy, and
+ * where a sequence holds some above 2^50, keys of far smaller ones may lose
+ * their weight.  out overlaps no other buffer.  A length above its bound
+ * leaves that sequence's rows alone, a page index outside the pool counts as
+ * no keys (LA_ERR_ARG in *status).  Asynchronous on `stream`; the order of sums depends on the
  * shapes and lengths alone, so equal calls give equal bits.  Two calls that
  * may run at the same time (two streams, two captured graphs) need a
  * workspace each. */

@@ -104,7 +104,10 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& u)
     return lo || hi;
 }
 
-constexpr float kMinScale = 0x1p-92f;  // added to V scales, so that their logarithm exists (values under 2^-88 differ)
+// Added to V scales, so that their logarithm exists (values under 2^-50 differ).  Not smaller: a warp's
+// reference over keys without a value is that of this scale, and beside one of values near 2^50 its keys
+// must keep their weight in fp32.
+constexpr float kMinScale = 0x1p-64f;
 
 // ------------------------------------------------------------------ kernel ---
 

@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     // The largest comes to [2^-4, 2^-3), as the cached tiles' do: P carries the tiles'
                     // powers of two of V, and a step tile far from the others would push its P (or
                     // theirs) to where fp16 has fewer bits.
-                    const int E = max((int)e, 28) - 123;
+                    const int E = max((int)e, kv ? 82 : 28) - 123;
                     if (tid == 0) {
                         if (kv) ti->ev = E;
                         else ti->ek = E, ti->live = a.T, ti->bad = 0;
@@ -871,7 +871,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 if (lane == 0) {
                     TileInfo* ti = info + (n & 7);
                     ti->live = live, ti->bad = bad;
-                    ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 20) - 118;  // s 2^-E < 2^-8
+                    // s 2^-E < 2^-8.  V's not below 2^-41, where the values under 2^-50 lose bits: the weights of
+                    // a tile without values must still be fp32 numbers beside one of values near 2^50.
+                    ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 77) - 118;
                     mbar_arrive(bar + kInfoReady + s);
                 }
                 __syncwarp();

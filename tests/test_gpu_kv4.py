@@ -640,6 +640,104 @@ def test_attention_one_sequence(shape, n):
     _verify(out, qkv, [n], vals, H, Hkv, D, 0, 2, 0)
 
 
+def _store(c, dt, n, k, v):
+    """Tokens 0..n-1 of sequence 0 from [n, heads, D] arrays; the values held."""
+    import torch
+    slots = dt[0].cpu().numpy()[np.arange(n) // c.page] * c.page + np.arange(n) % c.page
+    t = lambda a: torch.from_numpy(a.reshape(n, -1).astype(np.float32)).cuda()  # noqa: E731
+    c.append(t(k), t(v), _i32(slots))
+    vals = []
+    for x in (k, v):
+        cd, s, z = R.quantise(x.astype(np.float32))
+        vals.append((cd - z[..., None]) * s[..., None])
+    return vals
+
+
+@pytest.mark.parametrize("step", [(0, 2, 0), (2, 4, 2), (7, 5, 7)], ids=str)
+@pytest.mark.parametrize("big", [2.0 ** 10, 2.0 ** 14, 2.0 ** 40, 2.0 ** -40])
+@pytest.mark.parametrize("first", [True, False])
+def test_attention_values_of_very_different_size(step, big, first):
+    """Whole tiles of keys without a value (V = 0) next to large or small ones: they
+    still take their share of the weights."""
+    H, Hkv, D, n = 4, 2, 128, 384
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, [n], 64, 41)
+    g = np.random.default_rng(41)
+    k, v = g.standard_normal((2, n, Hkv, D))
+    v *= big
+    v[:256] *= first
+    if first:
+        v[128:256] = 0
+    qkv[:, (H + Hkv) * D: (H + 2 * Hkv) * D] *= big
+    held = _store(c, dt, n, k, v)
+    out = _call(c, qkv, dl, dt, H, *step)
+    c.check()
+    _verify(out, qkv, [n], held, H, Hkv, D, *step)
+
+
+@pytest.mark.parametrize("step", [(0, 2, 0), (2, 4, 2), (7, 5, 7)], ids=str)
+def test_attention_nonfinite_cache_and_queries(step):
+    """A cached vector with a NaN makes its head's rows NaN and no others; a
+    query row with a NaN is NaN in its head, every other row as before."""
+    import torch
+    H, Hkv, D, n = 4, 2, 64, 300
+    T = 1 + (step[0] + step[2]) * (step[1] - 1)
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, [n, 40], 32, 43)
+    clean = _call(c, qkv, dl, dt, H, *step)
+    bad = qkv.clone()
+    bad[T - 1, 2 * D + 5] = float("nan")
+    out = _call(c, bad, dl, dt, H, *step).reshape(2 * T, H, D)
+    assert torch.isnan(out[T - 1, 2]).all()
+    out[T - 1, 2] = clean.reshape(2 * T, H, D)[T - 1, 2]
+    assert torch.equal(out.reshape(2 * T, -1), clean)
+    for part in range(2):
+        k, v = (x[:n].copy() for x in vals)
+        (k, v)[part][171, 1, 9] = np.nan
+        with np.errstate(invalid="ignore"):
+            slots = dt[0].cpu().numpy()[171 // 32] * 32 + 171 % 32
+        t = lambda a: torch.from_numpy(a[171:172].reshape(1, -1).astype(np.float32)).cuda()  # noqa: E731
+        c.append(t(k), t(v), _i32([slots]))
+        out = _call(c, qkv, dl, dt, H, *step).reshape(2 * T, H, D)
+        assert torch.isnan(out[:T, 2:]).all()
+        assert torch.equal(out[:T, :2], clean.reshape(2 * T, H, D)[:T, :2]) and torch.equal(out[T:].reshape(T, -1), clean[T:])
+        c.append(t(vals[0]), t(vals[1]), _i32([slots]))
+        assert torch.equal(_call(c, qkv, dl, dt, H, *step), clean)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_read_of_hard_vectors(D):
+    """Scales from the smallest subnormal to the largest, NaN: fp32 exact, bf16
+    rounded once."""
+    import torch
+    x = _hard_vectors(D, np.random.default_rng(D), True)
+    n = len(x)
+    c = _cache(-(-n // 16), 1, D, 16, 1)
+    k = torch.from_numpy(x).cuda()
+    c.append(k, k, _i32(np.arange(n)))
+    want = np.full((n, D), np.nan)
+    for i in range(n):
+        cd, s, z = R.quantise_exact(x[i])
+        if not np.isnan(s):
+            want[i] = (cd.astype(np.float64) - z) * float(s)
+    with np.errstate(over="ignore"):
+        w32 = torch.from_numpy(want.astype(np.float32))
+    for dt, ref in ((torch.float32, w32), (torch.bfloat16, torch.from_numpy(want).to(torch.bfloat16))):
+        ko, vo = torch.zeros((n, D), dtype=dt, device="cuda"), torch.zeros((n, D), dtype=dt, device="cuda")
+        c.read(_i32(np.arange(n)), ko, vo)
+        for o in (ko.cpu(), vo.cpu()):
+            assert torch.equal(torch.isnan(o), torch.isnan(ref))
+            assert torch.equal(torch.nan_to_num(o, 0.0), torch.nan_to_num(ref, 0.0))
+    c.check()
+
+
+@pytest.mark.parametrize("step,B", [((0, 2, 0), 9000), ((0, 17, 1), 2000)], ids=str)
+def test_attention_many_sequences(step, B):
+    lens = [b % 23 - 1 for b in range(B)]
+    c, qkv, dl, dt, vals = _attend_case(1, 1, 64, *step, lens, 16, 47)
+    out = _call(c, qkv, dl, dt, 1, *step)
+    c.check()
+    _verify(out, qkv, lens, vals, 1, 1, 64, *step, only=set(range(0, B, B // 40)) | {B - 1})
+
+
 # ------------------------------------------------------- all of them together
 
 def _serve(graph, steps=6):
