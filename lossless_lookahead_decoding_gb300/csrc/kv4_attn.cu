@@ -42,7 +42,7 @@
 // take a cluster of 1 to 8 CTAs each (cluster_of).
 //
 // Measured on one GB300: 16 sequences of 1 to 64 K tokens, 8 KV heads of 8 query
-// heads, D = 128: 107 us = 5.4 TB/s (80 % of a plain copy's rate); 128 sequences
+// heads, D = 128: 103 us = 5.7 TB/s (83 % of a plain copy's rate); 128 sequences
 // of 31 to 768 tokens, 32 heads: 53.4 us = 4.2 TB/s; one sequence of 2 K tokens, 32
 // heads: 7.1 us.  At two CTAs of 128 registers a thread on an SM the schedulers
 // issue in 55 % of their cycles with 3.6 warps each to choose from, half the
@@ -120,10 +120,15 @@ struct RowAt {
     uint32_t sees;
 };
 
-template <int D, int TW>
+// A team's results meet in areas of their own, fewer than its warps, so that the rings have three stages
+// (with two, 16 sequences of 1 to 64 K tokens took 107.0 us instead of 102.7); the last warps' results
+// go through the first ones'.  A cluster has two stages and an area a warp: its few tiles a warp gain
+// nothing from the third, and its one result a warp loses 0.3 us of 4.0 on the way.
+template <int D, int TW, bool CL>
 struct RowsSmem {
     static constexpr int kR = 8;
-    static constexpr int kStages = TW > 1 ? 2 : 3;
+    static constexpr int kStages = CL ? 2 : 3;
+    static constexpr int kAreas = CL ? kWarps : 5;
     static constexpr int kBlk = 2 * kv4_block_bytes(D);
     static constexpr int kRing = kWarps * kStages * kBlk;
     static constexpr int kBar = kRing;                                          // full, empty
@@ -131,7 +136,7 @@ struct RowsSmem {
     static constexpr int kMisc = kLive + (kWarps * kStages * 4 + 15) / 16 * 16;  // starts and scan scratch
     static constexpr int kTab = kMisc + (kWarps * (int)sizeof(Start) + (kWarps + 2) * 8 + 15) / 16 * 16;
     static constexpr int kMerge = kTab + kMaxRows * (int)sizeof(RowAt);
-    static constexpr int kMergeBytes = TW == 1 ? 0 : kWarps * kR * (D + 4) * 4;  // [warp][row][D | M, sum]
+    static constexpr int kMergeBytes = TW == 1 ? 0 : kAreas * kR * (D + 4) * 4;  // [area][row][D | M, sum]
     static constexpr int kBytes = kMerge + kMergeBytes;
     static_assert(kMisc % 8 == 0 && kMerge % 16 == 0, "alignment");
 };
@@ -221,7 +226,7 @@ __device__ __forceinline__ void produce(const Kv4Attn& a, Run r, bool more, uint
 template <int D, int TW, bool CL>
 __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
 {
-    using L = RowsSmem<D, TW>;
+    using L = RowsSmem<D, TW, CL>;
     constexpr int S = L::kStages, R = L::kR, PAN = D / 64, MB = D / 16, DV = D / 8, BLK = kv4_block_bytes(D);
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -621,19 +626,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                     }
                 }
             } else {
-                // [row][D], then the rows' references and sums: to the team's merge area, or as a part
-                float* to = TW == 1 ? part : (float*)(sm + L::kMerge) + (size_t)warp * R * (D + 4);
-                constexpr int kLd = TW == 1 ? D : D + 4;
+                // [row][D], then the rows' references and sums: to a merge area of the team, or as a part
+                constexpr int kLd = TW == 1 ? D : D + 4, kAreas = L::kAreas;
+                constexpr bool kTwice = TW > 1 && kAreas < kWarps;
+                const int area = warp < kAreas ? warp : warp - kAreas;
+                float* to = TW == 1 ? part : (float*)(sm + L::kMerge) + (size_t)area * R * (D + 4);
                 if (TW > 1 && !first) named_sync(1, kWarps * 32);  // the last item's results have been read
+#pragma unroll 1
+                for (int late = 0; late < (kTwice ? 2 : 1); late++) {  // the last warps' results first
+                    if (kTwice && late == 1) {
+                        named_sync(1, kWarps * 32);
+                        if (warp < kWarps - kAreas) {
+                            // the same lane of the late warp wrote the same elements
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const int lr = 2 * t + r;
-                    if (TW > 1 || mt * R + lr < a.rows) {
+                            for (int r = 0; r < 2; r++) {
+                                const float* row = to + (size_t)(2 * t + r) * kLd;
+                                const float2 ml = *(const float2*)(row + D);
+                                const float mx = fmaxf(m[r], ml.x), f = ex2(m[r] - mx), h = ex2(ml.x - mx);
+                                l[r] = l[r] * f + ml.y * h;
+                                m[r] = mx;
 #pragma unroll
-                        for (int c = 0; c < DV; c += 4)
-                            *(float4*)(to + (size_t)lr * kLd + DV * g + c) =
-                                make_float4(chan(r, c, 1.f), chan(r, c + 1, 1.f), chan(r, c + 2, 1.f), chan(r, c + 3, 1.f));
-                        if (g == 0) *(float2*)(TW == 1 ? to + (size_t)R * D + 2 * lr : to + (size_t)lr * kLd + D) = make_float2(m[r], l[r]);
+                                for (int c = 0; c < DV; c++) {
+                                    const int mb = D == 128 ? ((c & 7) >> 1) + 4 * (c & 1) : c >> 1, hi = D == 128 ? c >> 3 : c & 1;
+                                    float& x = o[mb % MB][r + 2 * hi];
+                                    x = x * f + row[DV * g + c] * (mb & 1 ? h * 0x1p-20f : h * 0x1p-24f);
+                                }
+                            }
+                            __syncwarp();  // every lane has read the references
+                        }
+                    }
+                    if (kTwice && (warp < kAreas) != (late == 1)) continue;
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const int lr = 2 * t + r;
+                        if (TW > 1 || mt * R + lr < a.rows) {
+#pragma unroll
+                            for (int c = 0; c < DV; c += 4)
+                                *(float4*)(to + (size_t)lr * kLd + DV * g + c) =
+                                    make_float4(chan(r, c, 1.f), chan(r, c + 1, 1.f), chan(r, c + 2, 1.f), chan(r, c + 3, 1.f));
+                            if (g == 0) *(float2*)(TW == 1 ? to + (size_t)R * D + 2 * lr : to + (size_t)lr * kLd + D) = make_float2(m[r], l[r]);
+                        }
                     }
                 }
             }
@@ -643,17 +675,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                 for (int i = threadIdx.x; i < R * D / 4; i += kWarps * 32) {
                     const int lr = i / (D / 4), c = (i % (D / 4)) * 4;
                     if (mt * R + lr >= a.rows) continue;
-                    float2 ml[kWarps];
+                    float2 ml[L::kAreas];
                     float mx = kNoRef;
 #pragma unroll
-                    for (int w = 0; w < kWarps; w++) {
+                    for (int w = 0; w < L::kAreas; w++) {
                         ml[w] = *(const float2*)(mg + ((size_t)w * R + lr) * (D + 4) + D);
                         mx = fmaxf(mx, ml[w].x);
                     }
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; w++) {
+                    for (int w = 0; w < L::kAreas; w++) {
                         const float f = ex2(ml[w].x - mx);
                         const float4 v = *(const float4*)(mg + ((size_t)w * R + lr) * (D + 4) + c);
                         sum += f * ml[w].y;
@@ -852,7 +884,7 @@ template <int D, int TW, bool CL>
 bool set_smem()
 {
     auto kern = k_kv4_rows<D, TW, CL>;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, TW>::kBytes) == cudaSuccess &&
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, TW, CL>::kBytes) == cudaSuccess &&
            cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
 }
 
@@ -876,9 +908,9 @@ cudaError_t go(cudaStream_t s, const Plan& p, const Kv4Attn& k)
 {
     if (p.cluster)
         return launch_cluster(k_kv4_rows<D, kWarps, true>, (unsigned)(k.B * k.Hkv * k.mtiles), (unsigned)p.cluster, kThreads,
-                              RowsSmem<D, kWarps>::kBytes, s, k);
-    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, 1, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, 1>::kBytes, s, k)
-                              : launch_pdl(k_kv4_rows<D, kWarps, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, kWarps>::kBytes, s, k);
+                              RowsSmem<D, kWarps, true>::kBytes, s, k);
+    cudaError_t e = p.tw == 1 ? launch_pdl(k_kv4_rows<D, 1, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, 1, false>::kBytes, s, k)
+                              : launch_pdl(k_kv4_rows<D, kWarps, false>, dim3(p.grid), dim3(kThreads), RowsSmem<D, kWarps, false>::kBytes, s, k);
     if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, D, 8);
     return e;
 }
