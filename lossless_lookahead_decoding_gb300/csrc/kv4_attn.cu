@@ -42,7 +42,7 @@
 // take a cluster of 1 to 8 CTAs each (cluster_of).
 //
 // Measured on one GB300: 16 sequences of 1 to 64 K tokens, 8 KV heads of 8 query
-// heads, D = 128: 103 us = 5.7 TB/s (83 % of a plain copy's rate); 128 sequences
+// heads, D = 128: 103 us = 5.6 TB/s (83 % of a plain copy's rate); 128 sequences
 // of 31 to 768 tokens, 32 heads: 53.4 us = 4.2 TB/s; one sequence of 2 K tokens, 32
 // heads: 7.1 us.  At two CTAs of 128 registers a thread on an SM the schedulers
 // issue in 55 % of their cycles with 3.6 warps each to choose from, half the

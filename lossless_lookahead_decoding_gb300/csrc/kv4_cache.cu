@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_release(ReleaseArgs a)
 // HBM bound by design: one pass, extremes by packed max/min, and 3.5
 // instructions an element for the codes: they stay in pairs, the way the
 // format keeps them (channel 2i in bits 4i, 2i + 1 in bits 16 + 4i).
-// 18 K tokens of 8 heads (bf16, D = 128): 18 us, 94 MB; integer pipe 70 % busy,
-// issue 74 %, so a little above the 14 us its bytes take.
+// 18 K tokens of 8 heads, D = 128: bf16 14.7 us (96 MB: 14.1 us at a plain copy's
+// rate; integer pipe 70 % busy), fp32 29.9 us (171 MB: 25.2).
 // The decisions are exact (the codes are those of exact
 // arithmetic, whatever the inputs):
 //  * s: 15 s against hi - lo with the rounding error of the subtraction;
@@ -255,8 +255,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_release(ReleaseArgs a)
 //    have 8 significant bits and |x| >= s / 2 where a tie is near), so x * (1
 //    / s), off by less than 2^-17, rounded to multiples of 2^-11 is a tie
 //    exactly when x / s is;
-//  * fp32 inputs: the residual x - k s is exact in one fused multiply-add
-//    (12 bits in k s), and is compared with s / 2.
+//  * fp32 inputs: x (1 / s) decides where it is further than 2^-17 from a tie;
+//    for a lane that holds another, the residual x - k s, exact in one fused
+//    multiply-add (12 bits in k s), is compared with s / 2.
 
 constexpr float kRound11 = 6144.f;       // 1.5 x 2^12: adding it rounds to multiples of 2^-11
 constexpr float kRound0 = 12582912.f;    // 1.5 x 2^23: adding it rounds to whole numbers, ties to even; its bits' lower half is 0
@@ -400,29 +401,46 @@ struct Elems {
     // The codes, 8 a word, of a vector with a scale.
     __device__ __forceinline__ void codes(uint32_t param, float inv, uint32_t* word) const
     {
-        const int z = param & 15;
-        float s = scale_of(param);
-        if (tiny_scale(s)) s *= 0x1p64f;
-        const uint64_t inv2 = pair(inv, inv), r11 = pair(kRound11, kRound11), r0 = pair(kRound0 - kRound11, kRound0 - kRound11);
+        const uint32_t z2 = (param & 15) * 0x10001u;
+        const uint64_t inv2 = pair(inv, inv);
+        // two codes less z, 16 bits each, to their places
+        auto put = [&](int i, uint32_t k2) {
+            const uint32_t c = __viaddmin_s16x2_relu(k2, z2, 0x000f000fu) << (4 * (i & 3));
+            word[i >> 2] = i & 3 ? word[i >> 2] + c : c;
+        };
+        if (F32) {
+            uint32_t k2[8];
+            // x (1 / s) is off by less than 2^-18, so only next to a tie the nearest number is in doubt
+            const uint64_t up = pair(kRound0, kRound0), down = pair(-kRound0, -kRound0), minus = pair(-1.f, -1.f);
+            float far = 0.f;  // the largest distance from the number taken
 #pragma unroll
-        for (int wd = 0; wd < 2; wd++) {
-            uint32_t u = 0;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint32_t k2;  // two codes less z, 16 bits each
-                if (F32) {
-                    const uint32_t* x = w + (F32 ? 8 * wd + 2 * i : 0);
-                    const int k0 = nearest<F32>(__uint_as_float(x[0]), s, inv), k1 = nearest<F32>(__uint_as_float(x[1]), s, inv);
-                    k2 = __byte_perm((uint32_t)k0, (uint32_t)k1, 0x5410);
-                } else {
-                    const uint32_t x = w[F32 ? 0 : 4 * wd + i];
-                    float t0, t1;
-                    unpair(add2(fma2(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2, r11), r0), t0, t1);
-                    k2 = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x5410);
-                }
-                u += __viaddmin_s16x2_relu(k2, (uint32_t)z * 0x10001u, 0x000f000fu) << (4 * i);
+            for (int i = 0; i < 8; i++) {
+                const uint64_t x = pair(__uint_as_float(w[F32 ? 2 * i : 0]), __uint_as_float(w[F32 ? 2 * i + 1 : 0]));
+                const uint64_t k = fma2(x, inv2, up);
+                float k0, k1, d0, d1;
+                unpair(k, k0, k1);
+                unpair(fma2(x, inv2, fma2(add2(k, down), minus, 0)), d0, d1);
+                far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
+                k2[i] = __byte_perm(__float_as_uint(k0), __float_as_uint(k1), 0x5410);
             }
-            word[wd] = u;
+            if (far > 0.5f - 0x1p-17f) {
+                float s = scale_of(param);
+                if (tiny_scale(s)) s *= 0x1p64f;
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    k2[i] = __byte_perm((uint32_t)nearest<F32>(__uint_as_float(w[F32 ? 2 * i : 0]), s, inv),
+                                        (uint32_t)nearest<F32>(__uint_as_float(w[F32 ? 2 * i + 1 : 0]), s, inv), 0x5410);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) put(i, k2[i]);
+        } else {
+            const uint64_t r11 = pair(kRound11, kRound11), r0 = pair(kRound0 - kRound11, kRound0 - kRound11);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                float t0, t1;
+                unpair(add2(fma2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), inv2, r11), r0), t0, t1);
+                put(i, __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x5410));
+            }
         }
     }
 };
@@ -504,9 +522,9 @@ __global__ void __launch_bounds__(256) k_kv4_append(AppendArgs a)
 // The values (c - z) s of tokens, in fp32 (exact: 4 + 8 bits) or rounded to
 // bf16 (once: c - z is exact in bf16, too, so the packed product there rounds
 // the exact value).  One word of codes is 8 channels and 16 bytes of bf16: a
-// lane takes the same word of two tokens, K and V, so that a warp's loads and
-// stores cover whole lines.  HBM bound: 18 K tokens of 8 heads into bf16, 94 MB,
-// 15 us of the 14 that the bytes take.
+// lane takes the same word of two tokens, K and V (or, for fp32, halves of two
+// words of them), so that a warp's loads and stores cover whole lines.  HBM bound: 18 K tokens of 8 heads, D = 128, into bf16
+// 13.6 us (96 MB: 14.1 us at a plain copy's rate), into fp32 27.1 us (171 MB: 25.2).
 
 struct ReadArgs {
     const uint8_t* pages;
@@ -528,7 +546,8 @@ __global__ void __launch_bounds__(256) k_kv4_read(ReadArgs a)
     const long long group = ((long long)blockIdx.x << (3 - a.heads_log2)) + (warp >> a.heads_log2);
     const long long i0 = group * 2 * TOK + lane / L;
     if (h >= a.Hkv) return;
-    uint32_t w[2][2], prm[2][2];
+    constexpr int NW = F32 ? 2 : 1;
+    uint32_t w[2][2][NW], prm[2][2];
     bool live[2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
@@ -544,33 +563,40 @@ __global__ void __launch_bounds__(256) k_kv4_read(ReadArgs a)
         const uint8_t* blk = a.pages + kv4_block_at(slot >> a.page_log2, h, in_page >> 4, a.Hkv, a.blk_log2, D);
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-            w[t][p] = *(const uint32_t*)(blk + p * 8 * D + (sub >> 3) * 512 + tok * 32 + (sub & 7) * 4);
+#pragma unroll
+            for (int j = 0; j < NW; j++) {
+                const int wd = F32 ? (j * L + sub) >> 1 : sub;
+                w[t][p][j] = *(const uint32_t*)(blk + p * 8 * D + (wd >> 3) * 512 + tok * 32 + (wd & 7) * 4);
+            }
             prm[t][p] = *(const uint32_t*)(blk + 16 * D + p * 64 + tok * 4);
         }
     }
 #pragma unroll
     for (int t = 0; t < 2; t++) {
         if (!live[t]) continue;
-        const size_t at = (size_t)(i0 + t * TOK) * a.row_bytes + ((size_t)h * D + sub * 8) * E;
+        const size_t at = (size_t)(i0 + t * TOK) * a.row_bytes + (size_t)h * D * E + sub * 16;
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-            const uint32_t u = w[t][p], q = prm[t][p];
+            const uint32_t q = prm[t][p];
             uint8_t* dst = (p ? a.v : a.k) + at;
             // a code in the mantissa of 128 (bf16: 1 a unit; fp32: 2^16 a unit), less 128 + z
             if (F32) {
                 const float s = scale_of(q), z = __uint_as_float(q << 16);
-                float x[8];
 #pragma unroll
-                for (int c = 0; c < 8; c++)
-                    x[c] = (__uint_as_float(0x43000000u | ((u >> (4 * (c >> 1) + 16 * (c & 1))) & 15u) << 16) - z) * s;
-                *(float4*)dst = make_float4(x[0], x[1], x[2], x[3]);
-                *(float4*)(dst + 16) = make_float4(x[4], x[5], x[6], x[7]);
+                for (int j = 0; j < NW; j++) {
+                    const uint32_t u = w[t][p][j] >> (8 * (sub & 1));
+                    float x[4];
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        x[c] = (__uint_as_float(0x43000000u | ((u >> (4 * (c >> 1) + 16 * (c & 1))) & 15u) << 16) - z) * s;
+                    *(float4*)(dst + j * L * 16) = make_float4(x[0], x[1], x[2], x[3]);
+                }
             } else {
                 const uint32_t s2 = __byte_perm(q, q, 0x3232), z2 = __byte_perm(q, q, 0x1010);
                 uint32_t y[4];
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    const uint32_t x = (u >> (4 * c) & 0x000f000fu) | 0x43004300u;
+                    const uint32_t x = (w[t][p][0] >> (4 * c) & 0x000f000fu) | 0x43004300u;
                     const __nv_bfloat162 r = __hmul2_rn(__hsub2_rn(*(const __nv_bfloat162*)&x, *(const __nv_bfloat162*)&z2),
                                                         *(const __nv_bfloat162*)&s2);
                     y[c] = *(const uint32_t*)&r;
