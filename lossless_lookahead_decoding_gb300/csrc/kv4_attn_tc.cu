@@ -137,13 +137,23 @@ __device__ __forceinline__ float pow2i(int e)  // 2^e, e in -126 .. 127
 // x 2^e for any e that two such factors reach
 __device__ __forceinline__ float scale2(float x, int e) { return x * pow2i(e >> 1) * pow2i(e - (e >> 1)); }
 
-// What the softmax needs to know of a tile; eight in turn (an entry is written
-// again when the softmax of the tile five after it is done).
+// What the softmax needs to know of a tile.
 struct TileInfo {
     int live, bad;        // keys, and a bit per block of 16 whose page is not in the pool
     int ek, ev;           // powers of two of K and V
     uint32_t odd[4];      // step rows with a NaN or an infinity among their values
 };
+
+// Cached tiles' entries, eight in turn by the number of cached tiles before them: the copies, and so the
+// search for the powers of two, run at most three cached tiles ahead of the unpacking warps, and these at
+// most two tiles ahead of the softmax, so at most five cached tiles are in use.  (Counted over all tiles,
+// that would not hold: items without cached tiles pass the copying warp without a wait.)
+// Step tiles' entries, four in turn by the number of tiles: the unpacking warps write tile n + 4's when
+// tile n + 2's scores (K) or products (V) are done.  By then tile n's weights are taken, and for V, as
+// the step tile is its run's last, its run's results are out, which is when `odd` is read.
+constexpr int kCachedInfos = 8, kStepInfos = 4;
+__device__ __forceinline__ TileInfo* cached_info(TileInfo* info, int fill) { return info + (fill & (kCachedInfos - 1)); }
+__device__ __forceinline__ TileInfo* step_info(TileInfo* info, int n) { return info + kCachedInfos + (n & (kStepInfos - 1)); }
 
 template <int D>
 struct TcSmem {
@@ -156,8 +166,8 @@ struct TcSmem {
     static constexpr int kRowF = kVis + 128 * 16;             // [2 runs] per row: what undoes q's power of two
     static constexpr int kRowM = kRowF + 2 * 128 * 4;         // per row: the reference M
     static constexpr int kRowL = kRowM + 128 * 4;             // [2 groups] per row: sums
-    static constexpr int kInfo = kRowL + 2 * 128 * 4;         // TileInfo[8]
-    static constexpr int kBar = kInfo + 8 * (int)sizeof(TileInfo);
+    static constexpr int kInfo = kRowL + 2 * 128 * 4;         // cached tiles' entries, step tiles'
+    static constexpr int kBar = kInfo + (kCachedInfos + kStepInfos) * (int)sizeof(TileInfo);
     static constexpr int kMisc = kBar + 32 * 8;               // ring info, reduction words, start, scan scratch
     static constexpr int kBytes = kMisc + 512 + 1024;         // 1024: to align the base
 };
@@ -361,7 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, grp = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-        int steps = 0;  // step tiles so far
+        int steps = 0, fills = 0;  // step tiles and cached tiles so far
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile, gr = mt * kRowsTc + row;
@@ -370,6 +380,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             float m = kNoRef, l = 0.f;
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 const bool step = tile >= ntc;
+                const TileInfo* ti = step ? step_info(info, n) : cached_info(info, fills);
+                fills += !step;
                 if ((n & 1) != grp) {
                     steps += step;
                     continue;
@@ -379,7 +391,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 if (step) wait(kStepReady, steps & 1), steps++;  // (its entry has parts from both unpacking groups)
                 tc_fence_after();
                 if (any) {
-                    const TileInfo* ti = info + (n & 7);
                     const int live = ti->live, bad = ti->bad, iev = ti->ev;
                     const float f = fmaxf(scale2(rowf[(segs & 1) * 128 + row], ti->ek), 1e-37f), ev = (float)iev;
                     const bool part = step || live < kTile || bad;
@@ -515,7 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const float inv = 1.f / sum;
                     __nv_bfloat16* orow = a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
                     // the step tile, if it is there, is the last one; its products are done, so its entry is complete
-                    const uint32_t* odd = info[last & 7].odd;
+                    const uint32_t* odd = step_info(info, last)->odd;
                     const bool fix = run.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
 #pragma unroll 1
                     for (int j = 0; j < D / 2; j += 32) {
@@ -612,8 +623,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 const int b = n & 1, ph = (n >> 1) & 1;
                 uint8_t* dst = sm + (kv ? L::kV : L::kK) + b * L::kOperand;
-                TileInfo* ti = info + (n & 7);
                 if (tile < ntc) {
+                    const TileInfo* ti = cached_info(info, fills);
                     const int s = fills % kRing, sp = (fills / kRing) & 1;
                     wait(kInfoReady + s, sp);
                     wait(kFull + s, sp);
@@ -652,6 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     fills++;
                 } else {
                     // the step's own rows: bf16 to fp16 by the tile's largest finite exponent
+                    TileInfo* ti = step_info(info, n);
                     constexpr int kPieces = D / 8, kPass = 128 / kPieces;
                     const int pc = tid % kPieces, r0 = tid / kPieces;  // as the queries
                     const __nv_bfloat16* src = (kv ? a.vs : a.ks) + ((size_t)run.b * a.T + r0) * a.kv_ld + (size_t)head * D + 8 * pc;
@@ -752,11 +764,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             }
             __syncwarp();
         };
-        auto outputs = [&](int b, int ph, bool lead) {
+        auto outputs = [&](int b, int ph, bool lead, const TileInfo* ti) {
             wait(kPReady + b, ph);
             wait(kVReady + b, ph);
             if (lead && segs > 0) wait(kOFree, (segs - 1) & 1);
-            const int live = info[n & 7].live;  // only these keys' products
+            const int live = ti->live;  // only these keys' products
             tc_fence_after();
             if (chosen && ok) {
                 auto step16 = [&](int k) {
@@ -774,14 +786,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             }
             __syncwarp();
         };
+        int fills = 0;  // cached tiles so far
         do {
-            const int tiles = (run.t1 - run.t0 + stride - 1) / stride;
+            const int tiles = (run.t1 - run.t0 + stride - 1) / stride, ntc = (run.len + kTile - 1) / kTile;
             if (tiles <= 0) continue;
             scores(n & 1, (n >> 1) & 1, true);
             for (int i = 0; i < tiles; i++, n++) {
                 // the next tile's scores go first: they run while this one's softmax does
                 if (i + 1 < tiles) scores((n + 1) & 1, ((n + 1) >> 1) & 1, false);
-                outputs(n & 1, (n >> 1) & 1, i == 0);
+                const bool step = run.t0 + i * stride >= ntc;
+                outputs(n & 1, (n >> 1) & 1, i == 0, step ? step_info(info, n) : cached_info(info, fills));
+                fills += !step;
             }
             segs++;
         } while (!CL && run.next(a));
@@ -851,8 +866,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                         if (D == 128) prefetch_l2(a.ks + at + 64), prefetch_l2(a.vs + at + 64);
                     }
             }
-            for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
-                if (tile >= ntc) continue;
+            for (int tile = run.t0; tile < min(run.t1, ntc); tile += stride) {
                 const int s = fills % kRing;
                 wait(kFull + s, (fills / kRing) & 1);
                 const uint8_t* stage = sm + L::kCodes + s * L::kStage;
@@ -869,7 +883,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 }
                 ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
                 if (lane == 0) {
-                    TileInfo* ti = info + (n & 7);
+                    TileInfo* ti = cached_info(info, fills);
                     ti->live = live, ti->bad = bad;
                     // s 2^-E < 2^-8.  V's not below 2^-41, where the values under 2^-50 lose bits: the weights of
                     // a tile without values must still be fp32 numbers beside one of values near 2^50.
@@ -905,7 +919,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             for (int r = 0; r < 8; r++) sum += ls[r] * ex2(ms[r] - top);
             const float w = ex2(out_m - top) / sum;
             const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t* odd = info[(n - 1) & 7].odd;
+            const uint32_t* odd = step_info(info, n - 1)->odd;
             const bool fix = work && (ntc & (cs - 1)) == rank && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
             tc_fence_after();
 #pragma unroll 1

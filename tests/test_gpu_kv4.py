@@ -909,3 +909,29 @@ assert int(lens) == 10 and int(nf) == 3
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
+
+
+# ------------------------------------- many rows, sequences without cached tokens
+
+EMPTY_BETWEEN = [  # heads, KV heads, head_dim, step, lens: more than 152 items, so equal runs of them
+    (8, 8, 64, (0, 128, 1), [0] + [64] * 40),
+    (5, 5, 128, (0, 128, 1), ([0, 0, 11, 0, 300, 0, 0, 0, 5] + [0] * 9 + [129, 0, 250]) * 3),
+    (32, 32, 64, (0, 17, 1), ([0] * 7 + [3, 0, 0, 40, 1]) * 3),
+    (8, 1, 128, (2, 4, 2), [0, 0, 0, 0, 0, 7] * 30 + [0] * 20 + [200, 0, 0, 0, 13]),
+    (64, 4, 128, (7, 5, 7), [0, 30, 0, 0, 400, 0]),
+]
+
+
+@pytest.mark.parametrize("case", EMPTY_BETWEEN, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}-{c[3]}-{len(c[4])}")
+def test_attention_empty_sequences_between_others(case):
+    """First blocks of prompts in a batch with running sequences: items that hold
+    the step's own rows only, many in a row, before, between and after others."""
+    import torch
+    H, Hkv, D, step, lens = case
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, lens, 16, 61)
+    out = _call(c, qkv, dl, dt, H, *step)
+    c.check()
+    _verify(out, qkv, lens, vals, H, Hkv, D, *step)
+    for _ in range(3):
+        assert torch.equal(out, _call(c, qkv, dl, dt, H, *step))
+    c.check()
