@@ -174,7 +174,7 @@ struct TcSmem {
 
 enum {  // barriers
     kFull = 0, kEmpty = 3, kInfoReady = 6, kKReady = 9, kVReady = 11, kSDone = 13, kODone = 15, kPReady = 17, kQReady = 19,
-    kOFree = 20, kEnd = 21, kStepReady = 22
+    kOFree = 20, kEnd = 21, kStepReady = 22  // (22, 23: a step tile's power of two of V, by the tile's parity)
 };
 constexpr uint32_t kColO = 256, kColP = 384;  // tensor memory: S [2][128], O [D], P [2][64]
 
@@ -274,11 +274,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             mbar_init(bar + kSDone + i, 1);
             mbar_init(bar + kODone + i, 1);
             mbar_init(bar + kPReady + i, 4);
+            mbar_init(bar + kStepReady + i, 1);
         }
         mbar_init(bar + kQReady, 8);
         mbar_init(bar + kOFree, 8);
         mbar_init(bar + kEnd, 1);
-        mbar_init(bar + kStepReady, 2);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, grp = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-        int steps = 0, fills = 0;  // step tiles and cached tiles so far
+        int steps = 0, fills = 0;  // this group's step tiles, and both groups' cached tiles so far
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile, gr = mt * kRowsTc + row;
@@ -382,13 +382,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 const bool step = tile >= ntc;
                 const TileInfo* ti = step ? step_info(info, n) : cached_info(info, fills);
                 fills += !step;
-                if ((n & 1) != grp) {
-                    steps += step;
-                    continue;
-                }
+                if ((n & 1) != grp) continue;
                 const int b = grp, ph = (n >> 1) & 1;
-                wait(kSDone + b, ph);
-                if (step) wait(kStepReady, steps & 1), steps++;  // (its entry has parts from both unpacking groups)
+                wait(kSDone + b, ph);  // (so K's part of a step tile's entry is there; V's may not be)
+                // A barrier a group: V's part of tile n + 2 waits for tile n's products, so for this wait
+                if (step) wait(kStepReady + grp, steps & 1), steps++;
                 tc_fence_after();
                 if (any) {
                     const int live = ti->live, bad = ti->bad, iev = ti->ev;
@@ -718,9 +716,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     // theirs) to where fp16 has fewer bits.
                     const int E = max((int)e, kv ? 82 : 28) - 123;
                     if (tid == 0) {
-                        if (kv) ti->ev = E;
+                        // K's part is waited for with the scores, which need all of K
+                        if (kv) ti->ev = E, mbar_arrive(bar + kStepReady + b);
                         else ti->ek = E, ti->live = a.T, ti->bad = 0;
-                        mbar_arrive(bar + kStepReady);
                     }
                     const float f = scale2(1.f, -E);
 #pragma unroll 1

@@ -935,3 +935,28 @@ def test_attention_empty_sequences_between_others(case):
     for _ in range(3):
         assert torch.equal(out, _call(c, qkv, dl, dt, H, *step))
     c.check()
+
+
+@pytest.mark.parametrize("case", EMPTY_BETWEEN[:3], ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}-{c[3]}-{len(c[4])}")
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attention_nonfinite_values_of_empty_sequences(case, value):
+    """A value that is not finite in the last own row of sequences without cached
+    tokens reaches that row and channel alone: everything else is as with a zero
+    in its place, bit for bit."""
+    import torch
+    H, Hkv, D, step, lens = case
+    T = 1 + (step[0] + step[2]) * (step[1] - 1)
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, *step, lens, 16, 67)
+    rows = torch.tensor([b * T + T - 1 for b, n in enumerate(lens) if n == 0], device="cuda")
+    at = (H + Hkv) * D + torch.arange(Hkv, device="cuda") * D + 3
+    qkv[rows[:, None], at[None]] = 0.0
+    clean = _call(c, qkv, dl, dt, H, *step)
+    _verify(clean, qkv, lens, vals, H, Hkv, D, *step)
+    odd = qkv.clone()
+    odd[rows[:, None], at[None]] = value
+    out = _call(c, odd, dl, dt, H, *step)
+    c.check()
+    touched = torch.arange(H, device="cuda") * D + 3
+    assert not torch.isfinite(out[rows[:, None], touched[None]]).any()
+    out[rows[:, None], touched[None]] = clean[rows[:, None], touched[None]]
+    assert torch.equal(out, clean)
