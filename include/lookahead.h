@@ -449,8 +449,9 @@ LA_API size_t la_kv4_page_bytes(const la_kv4_desc* c);
  *   lens        DEVICE int32[batch]: tokens held (< 0: not a sequence; it is
  *               left alone and its n_new is not read as a count)
  *   n_new       DEVICE int32[batch] >= 0
- *   free_pages  DEVICE int32[]: a stack of free page indexes, *n_free of them
- *   n_free      DEVICE int32
+ *   free_pages  DEVICE int32[]: a stack of free page indexes, at least *n_free
+ *               of them
+ *   n_free      DEVICE int32, 0..n_pages
  *   table       DEVICE int32[batch][max_pages]: entries of new pages are
  *               written, taken from the stack's top, b ascending and each
  *               sequence's pages in order; the others are left
@@ -462,8 +463,8 @@ LA_API size_t la_kv4_page_bytes(const la_kv4_desc* c);
  *   new_lens    DEVICE int32[batch]: lens + n_new (may be lens itself)
  *   pages_left  DEVICE int32: *n_free less the pages taken (may be n_free)
  * All or nothing: if the pages, a table row, n_slots or slot_stride do not
- * suffice (LA_ERR_CAPACITY in *status) or a count is negative (LA_ERR_ARG),
- * every slot is -1 and the table, lengths and page count stay.  Tokens of a
+ * suffice (LA_ERR_CAPACITY in *status), a count is negative or *n_free over
+ * n_pages (LA_ERR_ARG), every slot is -1 and the table, lengths and page count stay.  Tokens of a
  * page index outside 0..n_pages-1 get slot -1 (LA_ERR_ARG).  desc.pages is
  * not used.  batch <= 8192.  LA_ERR_ARG also for output buffers that overlap
  * others than said. */

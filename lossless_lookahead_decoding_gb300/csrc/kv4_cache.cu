@@ -111,9 +111,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv4_plan(PlanArgs a)
     Scan2 total;
     Scan2 at = block_scan2(mine, &total);
     if (!bad && ((!a.stride && total.a > a.n_slots) || total.b > n_free)) bad = LA_ERR_CAPACITY;
-    const bool any_arg = __syncthreads_or(bad == LA_ERR_ARG), ok = !__syncthreads_or(bad != 0);
+    const bool any_arg = __syncthreads_or(bad == LA_ERR_ARG), any = __syncthreads_or(bad != 0);
+    const bool ok = !any && n_free <= a.n_pages;  // (a higher stack than there are pages is not read)
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0 && a.mode != kPlanCommit)
-        kv4_raise(a.status, any_arg ? LA_ERR_ARG : LA_ERR_CAPACITY);
+        kv4_raise(a.status, any_arg || !any ? LA_ERR_ARG : LA_ERR_CAPACITY);
     if (ok && a.mode != kPlanCommit) {
         for (int b = b0; b < min(b0 + per, a.B); b++) {
             first_tok[b] = (int)at.a;

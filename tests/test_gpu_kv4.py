@@ -960,3 +960,30 @@ def test_attention_nonfinite_values_of_empty_sequences(case, value):
     assert not torch.isfinite(out[rows[:, None], touched[None]]).any()
     out[rows[:, None], touched[None]] = clean[rows[:, None], touched[None]]
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_new", [3, 20000])
+def test_plan_refuses_more_free_pages_than_there_are(n_new, in_place):
+    """A page count over n_pages: nothing is planned; the count itself is allowed."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    page, n_pages = 128, 200
+    c = _cache(n_pages, 1, 64, page, n_pages)
+    free = np.r_[np.arange(n_pages), np.zeros(8, int)]
+    for n_free in (n_pages + 1, n_pages + 8, 1 << 30, n_pages):
+        lens, nf = _i32([0]), _i32([n_free])
+        table = torch.full((1, n_pages), -7, dtype=torch.int32, device="cuda")
+        slots = torch.full((n_new,), 99, dtype=torch.int32, device="cuda")
+        nl, left = (lens, nf) if in_place else (_i32([5]), _i32([5]))
+        c.plan(lens, _i32([n_new]), _i32(free), nf, table, slots, nl, left)
+        if n_free == n_pages:
+            c.check()
+            pages = -(-n_new // page)
+            assert int(nl) == n_new and int(left) == n_pages - pages
+            assert table[0, :pages].tolist() == list(range(n_pages - 1, n_pages - 1 - pages, -1)) and int(slots[0]) == (n_pages - 1) * page
+            continue
+        with pytest.raises(LA.LAError) as e:
+            c.check()
+        assert e.value.code == LA.LA_ERR_ARG
+        assert bool((slots == -1).all()) and bool((table == -7).all()) and int(nl) == 0 and int(left) == n_free
