@@ -464,10 +464,12 @@ LA_API size_t la_kv4_page_bytes(const la_kv4_desc* c);
  *   pages_left  DEVICE int32: *n_free less the pages taken (may be n_free)
  * All or nothing: if the pages, a table row, n_slots or slot_stride do not
  * suffice (LA_ERR_CAPACITY in *status), a count is negative or *n_free over
- * n_pages (LA_ERR_ARG), every slot is -1 and the table, lengths and page count stay.  Tokens of a
- * page index outside 0..n_pages-1 get slot -1 (LA_ERR_ARG).  desc.pages is
- * not used.  batch <= 8192.  LA_ERR_ARG also for output buffers that overlap
- * others than said. */
+ * n_pages (LA_ERR_ARG), every slot is -1 and the table, lengths and page count
+ * stay.  Tokens of a page index outside 0..n_pages-1 get slot -1 (LA_ERR_ARG).
+ * desc.pages is not used.  batch <= 8192.  LA_ERR_ARG also for output buffers
+ * that overlap others than said (of free_pages, whose size the call does not
+ * know, the first entry is compared; an output over later ones is the caller's
+ * error). */
 LA_API int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int32_t* n_new, int batch,
                        const int32_t* free_pages, const int32_t* n_free, int32_t* table, int32_t* slots, int n_slots,
                        int slot_stride, int32_t* new_lens, int32_t* pages_left, void* stream);
@@ -478,7 +480,8 @@ LA_API int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int32_t*
  * ascending, each sequence's pages in order; their lens become 0 and *n_free
  * grows.  Sequences with lens[b] < 0 hold no pages.  Nothing is given back
  * (LA_ERR_ARG in *status) when a sequence would hold more than max_pages
- * pages or the stack more than n_pages.  batch <= 8192. */
+ * pages or the stack more than n_pages.  batch <= 8192.  LA_ERR_ARG also for
+ * buffers that overlap (lens may be done itself: every sequence ends). */
 LA_API int la_kv4_release(const la_kv4_desc* c, const int32_t* done, int batch, int32_t* lens, const int32_t* table,
                           int32_t* free_pages, int32_t* n_free, void* stream);
 

@@ -743,6 +743,10 @@ extern "C" int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int3
         overlap(table, new_lens, tab, batch) || overlap(pages_left, lens, 1, batch) || overlap(pages_left, n_new, 1, batch) ||
         overlap(pages_left, new_lens, 1, batch) || overlap(pages_left, slots, 1, n_slots) || overlap(pages_left, table, 1, tab))
         return LA_ERR_ARG;
+    // (of free_pages only its first entry is known to be there)
+    for (const int* in : {n_free, free_pages})
+        if (overlap(in, slots, 1, n_slots) || overlap(in, table, 1, tab) || overlap(in, new_lens, 1, batch)) return LA_ERR_ARG;
+    if (overlap(pages_left, free_pages, 1, 1)) return LA_ERR_ARG;
     return launch_kv4_plan((cudaStream_t)stream, *c, lens, n_new, batch, free_pages, n_free, table, slots, n_slots,
                            slot_stride, new_lens, pages_left);
 }
@@ -753,6 +757,11 @@ extern "C" int la_kv4_release(const la_kv4_desc* c, const int32_t* done, int bat
     if (!desc_ok(c) || batch < 0 || batch > kPlanMaxBatch) return LA_ERR_ARG;
     if (batch == 0) return LA_OK;
     if (!done || !lens || !table || !free_pages || !n_free) return LA_ERR_ARG;
+    const size_t tab = (size_t)batch * c->max_pages, room = c->n_pages;
+    if (overlap(free_pages, lens, room, batch) || overlap(free_pages, done, room, batch) || overlap(free_pages, table, room, tab) ||
+        overlap(free_pages, n_free, room, 1) || overlap(lens, table, batch, tab) || (lens != done && overlap(lens, done, batch, batch)) ||
+        overlap(n_free, lens, 1, batch) || overlap(n_free, done, 1, batch) || overlap(n_free, table, 1, tab))
+        return LA_ERR_ARG;
     return launch_kv4_release((cudaStream_t)stream, *c, done, batch, lens, table, free_pages, n_free);
 }
 

@@ -71,6 +71,13 @@ const at::Tensor& ints(const Handle& h, PyObject* o)
 const int32_t* data(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
 int32_t* out(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
 
+// whether two contiguous tensors share memory
+bool share(const at::Tensor& a, const at::Tensor& b)
+{
+    const char *p = static_cast<const char*>(a.data_ptr()), *q = static_cast<const char*>(b.data_ptr());
+    return p < q + b.nbytes() && q < p + a.nbytes();
+}
+
 // Row stride (elements) of [rows, heads * D] or [rows, heads, D] with dense rows.
 long row_stride(const Handle& h, const at::Tensor& t, long heads, const char* what)
 {
@@ -120,6 +127,9 @@ int call_plan(PyObject* const* a)
     if (n_new.numel() != B || new_lens.numel() != B) throw Refused{"plan: lens, n_new and new_lens of one length"};
     if (n_free.numel() < 1 || left.numel() < 1) throw Refused{"plan: n_free and pages_left hold one number"};
     rows_of_table(h, table, B);
+    // (the C call does not know how far free_pages goes)
+    for (const at::Tensor* t : {&table, &slots, &new_lens, &left})
+        if (share(free_pages, *t)) throw Refused{"plan: free_pages shares memory with an output"};
     return la_kv4_plan(&h.desc, data(lens), data(n_new), (int)B, data(free_pages), data(n_free), out(table), out(slots),
                        (int)count(slots), (int)int_of(a[9]), out(new_lens), out(left), stream_of(h));
 }

@@ -987,3 +987,25 @@ def test_plan_refuses_more_free_pages_than_there_are(n_new, in_place):
             c.check()
         assert e.value.code == LA.LA_ERR_ARG
         assert bool((slots == -1).all()) and bool((table == -7).all()) and int(nl) == 0 and int(left) == n_free
+
+
+def test_plan_refuses_an_output_over_the_free_pages():
+    """KV4Cache knows how long the stack's buffer is; neighbours in one buffer are fine."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    c = _cache(6, 1, 64, 16, 4)
+    buf = torch.zeros(40, dtype=torch.int32, device="cuda")
+    free, lens, new = buf[:6], _i32([0, 5]), _i32([2, 12])
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    free.copy_(torch.arange(6))
+    other = dict(table=table, slots=_i32([9] * 14), new_lens=_i32([9, 9]), left=_i32([9]))
+    table[1, 0] = 5
+    for bad in (dict(slots=buf[5:19]), dict(slots=buf[2:16]), dict(table=buf[4:12].view(2, 4)), dict(new_lens=buf[5:7]),
+                dict(left=buf[3:4])):
+        a = {**other, **bad}
+        with pytest.raises((ValueError, LA.LAError)):
+            c.plan(lens, new, free, _i32([5]), a["table"], a["slots"], a["new_lens"], a["left"])
+    assert free.tolist() == list(range(6))
+    c.plan(lens, new, free, _i32([5]), table, buf[6:20], buf[20:22], buf[22:23])
+    c.check()
+    assert buf[6:23].tolist() == [64, 65, *range(85, 96), 48, 2, 17, 3] and table[:, 0].tolist() == [4, 5] and int(table[1, 1]) == 3

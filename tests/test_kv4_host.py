@@ -171,3 +171,31 @@ def test_reference_mask_matches_the_oracle_controller():
         _, _, vis = k.rows(3, 0)
         for i in range(len(vis)):
             assert np.nonzero(vis[i])[0].tolist() == sorted(R.visible(W, N, G, i)), (W, N, G, i)
+
+
+def test_plan_and_release_refuse_shared_buffers():
+    """The free pages and their number under an output; all of release's buffers."""
+    import lossless_lookahead_decoding_gb300 as LA
+    E = LA.LA_ERR_ARG
+    p = [FAKE + 0x10000 * i for i in range(8)]
+    ok = dict(lens=p[0], n_new=p[1], batch=4, free=p[2], n_free=p[3], table=p[4], slots=p[5], n_slots=32, stride=8,
+              new_lens=p[6], left=p[7], done=p[1])
+
+    def plan(**kw):
+        a = {**ok, **kw}
+        return LA.la_kv4_plan(_desc(), a["lens"], a["n_new"], a["batch"], a["free"], a["n_free"], a["table"],
+                              a["slots"], a["n_slots"], a["stride"], a["new_lens"], a["left"])
+
+    for bad in [dict(n_free=p[5]), dict(n_free=p[5] + 31 * 4), dict(n_free=p[4] + 63 * 4), dict(n_free=p[6] + 12),
+                dict(slots=p[3] - 31 * 4), dict(table=p[3] - 63 * 4), dict(new_lens=p[3] - 12),
+                dict(free=p[5] + 31 * 4), dict(slots=p[2]), dict(table=p[2] - 63 * 4), dict(new_lens=p[2] - 4), dict(left=p[2])]:
+        assert plan(**bad) == E, bad
+
+    def release(**kw):
+        a = {**ok, **kw}
+        return LA.la_kv4_release(_desc(), a["done"], a["batch"], a["lens"], a["table"], a["free"], a["n_free"])
+
+    for bad in [dict(lens=p[2]), dict(lens=p[2] + 99 * 4), dict(done=p[2] - 12), dict(table=p[2] + 99 * 4),
+                dict(table=p[2] - 63 * 4), dict(n_free=p[2]), dict(n_free=p[2] + 99 * 4), dict(lens=p[4] + 63 * 4),
+                dict(lens=p[1] + 4), dict(lens=p[1] - 12), dict(n_free=p[0] + 12), dict(n_free=p[1]), dict(n_free=p[4] + 4)]:
+        assert release(**bad) == E, bad
