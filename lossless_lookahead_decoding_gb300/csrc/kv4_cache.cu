@@ -713,6 +713,13 @@ bool desc_ok(const la_kv4_desc* c)
 
 bool aligned(const void* p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }
 
+// every address one of an int (a misaligned access would end the context)
+template <typename... P>
+bool ints_aligned(const P*... p)
+{
+    return (aligned(p, 4) && ...);
+}
+
 bool pool_ok(const la_kv4_desc* c) { return desc_ok(c) && c->pages && aligned(c->pages, 16) && aligned(c->status, 4); }
 
 // do [a, a + n) and [b, b + n) of ints share memory
@@ -733,6 +740,7 @@ extern "C" int la_kv4_plan(const la_kv4_desc* c, const int32_t* lens, const int3
     if (!desc_ok(c) || batch < 0 || batch > kPlanMaxBatch || n_slots < 0 || slot_stride < 0) return LA_ERR_ARG;
     if (!n_free || !pages_left || (batch && (!lens || !n_new || !free_pages || !table || !new_lens))) return LA_ERR_ARG;
     if (n_slots && !slots) return LA_ERR_ARG;
+    if (!ints_aligned(lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left, c->status)) return LA_ERR_ARG;
     if (slot_stride && (long long)batch * slot_stride != n_slots) return LA_ERR_ARG;
     // the lengths and the page count may be updated in place; anything else
     // written over something read is refused
@@ -757,6 +765,7 @@ extern "C" int la_kv4_release(const la_kv4_desc* c, const int32_t* done, int bat
     if (!desc_ok(c) || batch < 0 || batch > kPlanMaxBatch) return LA_ERR_ARG;
     if (batch == 0) return LA_OK;
     if (!done || !lens || !table || !free_pages || !n_free) return LA_ERR_ARG;
+    if (!ints_aligned(done, lens, table, free_pages, n_free, c->status)) return LA_ERR_ARG;
     const size_t tab = (size_t)batch * c->max_pages, room = c->n_pages;
     if (overlap(free_pages, lens, room, batch) || overlap(free_pages, done, room, batch) || overlap(free_pages, table, room, tab) ||
         overlap(free_pages, n_free, room, 1) || overlap(lens, table, batch, tab) || (lens != done && overlap(lens, done, batch, batch)) ||
@@ -770,7 +779,7 @@ extern "C" int la_kv4_append(const la_kv4_desc* c, const void* k, const void* v,
 {
     if (!pool_ok(c) || n < 0 || n_rows < 0 || (dtype != LA_FP32 && dtype != LA_BF16)) return LA_ERR_ARG;
     if (n == 0) return LA_OK;
-    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16)) return LA_ERR_ARG;
+    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !ints_aligned(rows, slots)) return LA_ERR_ARG;
     if (ld < c->n_kv_heads * c->head_dim || (ld * (dtype == LA_FP32 ? 4LL : 2LL)) % 16) return LA_ERR_ARG;
     if (!rows && n > n_rows) return LA_ERR_ARG;
     return launch_kv4_append((cudaStream_t)stream, *c, k, v, dtype, ld, n_rows, rows, slots, n);
@@ -781,7 +790,7 @@ extern "C" int la_kv4_read(const la_kv4_desc* c, const int32_t* slots, int n, vo
 {
     if (!pool_ok(c) || n < 0 || (dtype != LA_FP32 && dtype != LA_BF16)) return LA_ERR_ARG;
     if (n == 0) return LA_OK;
-    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16)) return LA_ERR_ARG;
+    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !ints_aligned(slots)) return LA_ERR_ARG;
     if (ld < c->n_kv_heads * c->head_dim || (ld * (dtype == LA_FP32 ? 4LL : 2LL)) % 16) return LA_ERR_ARG;
     return launch_kv4_read((cudaStream_t)stream, *c, slots, n, k, v, dtype, ld);
 }
@@ -809,6 +818,7 @@ extern "C" int la_kv4_attention(const la_kv4_desc* c, const la_kv4_attn* a, void
     if (!pool_ok(c) || !attn_shape_ok(c, a)) return LA_ERR_ARG;
     if (a->batch == 0) return LA_OK;
     if (!a->q || !a->k_step || !a->v_step || !a->out || !a->lens || !a->table) return LA_ERR_ARG;
+    if (!ints_aligned(a->lens, a->table)) return LA_ERR_ARG;
     if (!aligned(a->q, 16) || !aligned(a->k_step, 16) || !aligned(a->v_step, 16) || !aligned(a->out, 16)) return LA_ERR_ARG;
     if (a->q_ld < a->n_heads * c->head_dim || a->q_ld % 8 || a->kv_ld < c->n_kv_heads * c->head_dim || a->kv_ld % 8)
         return LA_ERR_ARG;

@@ -199,3 +199,25 @@ def test_plan_and_release_refuse_shared_buffers():
                 dict(table=p[2] - 63 * 4), dict(n_free=p[2]), dict(n_free=p[2] + 99 * 4), dict(lens=p[4] + 63 * 4),
                 dict(lens=p[1] + 4), dict(lens=p[1] - 12), dict(n_free=p[0] + 12), dict(n_free=p[1]), dict(n_free=p[4] + 4)]:
         assert release(**bad) == E, bad
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_index_arrays_are_refused(off):
+    """Every int32 array of every call, and the status, at an address that is no int's."""
+    import lossless_lookahead_decoding_gb300 as LA
+    E = LA.LA_ERR_ARG
+    p = [FAKE + 0x10000 * i for i in range(8)]
+    for i in range(8):
+        a = [x + off * (i == j) for j, x in enumerate(p)]
+        assert LA.la_kv4_plan(_desc(), a[0], a[1], 4, a[2], a[3], a[4], a[5], 32, 8, a[6], a[7]) == E, i
+    for i in range(5):
+        a = [x + off * (i == j) for j, x in enumerate(p)]
+        assert LA.la_kv4_release(_desc(), a[0], 4, a[1], a[2], a[3], a[4]) == E, i
+    d = _desc(status=FAKE + off)
+    assert LA.la_kv4_plan(d, *p[:2], 4, *p[2:6], 32, 8, *p[6:]) == E and LA.la_kv4_release(d, p[0], 4, *p[1:5]) == E
+    for rows, slots in ((FAKE + off, FAKE), (None, FAKE + off)):
+        assert LA.la_kv4_append(_desc(), FAKE, FAKE, LA.LA_BF16, 1024, 5, rows, slots, 5) == E
+    assert LA.la_kv4_read(_desc(), FAKE + off, 5, FAKE, FAKE, LA.LA_BF16, 1024) == E
+    ws = dict(workspace=FAKE, ws_bytes=1 << 40)
+    assert LA.la_kv4_attention(_desc(), _attn(lens=FAKE + off, **ws)) == E
+    assert LA.la_kv4_attention(_desc(), _attn(table=FAKE + off, **ws)) == E
