@@ -4,7 +4,8 @@ Each csrc/*.cu is compiled in parallel into _build/, then linked into
 lossless_lookahead_decoding_gb300/liblookahead.so against the shared CUDA
 runtime.  Rebuilds only what changed (object newer than its source and every
 header).  csrc/kv4_torch.cpp becomes _kv4.so, the Python module behind
-KV4Cache, compiled by the host compiler against torch's headers.
+KV4Cache, compiled by the host compiler against torch's headers; without a
+CUDA build of torch, which KV4Cache needs, it is left out.
 """
 from __future__ import annotations
 
@@ -31,8 +32,10 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)  # without importing it
+def torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")  # without importing it
+    at = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    return at if os.path.exists(os.path.join(at, "include", "c10", "cuda", "CUDAStream.h")) else None
 
 
 def cuda_include() -> str:
@@ -63,10 +66,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     # the binding's object: as the others, with the host compiler
     bsrc, bobj = os.path.join(CSRC, "kv4_torch.cpp"), os.path.join(BUILD, "kv4_torch.o")
-    binding = force or not os.path.exists(bobj) or os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_t)
+    torch = torch_dir()
+    binding = torch and (force or not os.path.exists(bobj) or os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_t))
 
     def cc_binding():
-        t = os.path.join(torch_dir(), "include")
+        t = os.path.join(torch, "include")
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-c", bsrc, "-o", bobj, "-I", t,
                "-I", os.path.join(t, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
                "-I", cuda_include(), "-I", os.path.join(ROOT, "include")]
@@ -77,8 +81,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
         other = ex.submit(cc_binding) if binding else None
         logs = list(ex.map(cc, jobs))
-        if other:
-            other.result()
     if verbose:
         for log in logs:
             print(log)
@@ -87,8 +89,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".{os.getpid()}.tmp"
         subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if binding or not os.path.exists(BINDING):
-        lib = os.path.join(torch_dir(), "lib")
+    if other:
+        other.result()
+    if torch and (binding or not os.path.exists(BINDING)):
+        lib = os.path.join(torch, "lib")
         tmp = BINDING + f".{os.getpid()}.tmp"
         subprocess.check_call(["g++", "-shared", "-o", tmp, bobj, "-L", HERE, "-llookahead", "-Wl,-rpath,$ORIGIN",
                                "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
