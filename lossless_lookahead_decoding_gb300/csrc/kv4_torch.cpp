@@ -11,7 +11,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
-#include <algorithm>
 #include <exception>
 
 #include "../../include/lookahead.h"
@@ -87,10 +86,10 @@ long row_stride(const Handle& h, const at::Tensor& t, long heads, const char* wh
     if (t.dim() == 2) ok = t.size(1) == heads * D && t.stride(1) == 1;
     else if (t.dim() == 3) ok = t.size(1) == heads && t.size(2) == D && t.stride(2) == 1 && (heads == 1 || t.stride(1) == D);
     if (!ok) throw Refused{what};
-    // the stride of a single row says nothing
-    const long ld = t.size(0) < 2 ? std::max<long>(t.stride(0), heads * D) : t.stride(0);
+    // the stride of a single row says nothing, and may differ between tensors of one layout
+    const long ld = t.size(0) < 2 ? heads * D : t.stride(0);
     if (ld > INT32_MAX || t.size(0) > INT32_MAX) throw Refused{what};
-    return t.size(0) < 2 && ld % 8 ? heads * D : ld;
+    return ld;
 }
 
 int dtype_of(const at::Tensor& t)

@@ -1009,3 +1009,34 @@ def test_plan_refuses_an_output_over_the_free_pages():
     c.plan(lens, new, free, _i32([5]), table, buf[6:20], buf[20:22], buf[22:23])
     c.check()
     assert buf[6:23].tolist() == [64, 65, *range(85, 96), 48, 2, 17, 3] and table[:, 0].tolist() == [4, 5] and int(table[1, 1]) == 3
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_single_rows_of_any_stride(f32):
+    """One token whose k is a tensor of its own and whose v (and q) are views into
+    a projection: a single row has no stride to differ in."""
+    import torch
+    H = Hkv = 2
+    D, n = 64, 20
+    c, qkv, dl, dt, vals = _attend_case(H, Hkv, D, 0, 2, 0, [n], 16, 71, extra=8)
+    want = _call(c, qkv, dl, dt, H, 0, 2, 0)
+    q, v = qkv[:, :H * D], qkv[:, 2 * H * D: 3 * H * D]
+    k = v.new_empty((1, H * D)).copy_(qkv[:, H * D: 2 * H * D])
+    assert k.stride(0) != v.stride(0)
+    ws = torch.zeros(max(16, c.attention_bytes(1, H, 0, 2, 0)), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(want)
+    c.attention(q, k, v, dl, dt, 0, 2, 0, out=out, workspace=ws)
+    assert torch.equal(out, want)
+    dtype = torch.float32 if f32 else torch.bfloat16
+    k, x = k.to(dtype), torch.cat([v, v, v[:, :8]], 1).to(dtype)
+    v = x[:, H * D: 2 * H * D]
+    assert k.stride(0) != v.stride(0)
+    slot = dt[0, :1] * 16 + 3
+    c.append(k, v, slot)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(x)[:, :H * D]
+    c.read(slot, ko, vo)
+    c.check()
+    for a, b in ((k, ko), (v, vo)):
+        cd, s, z = R.quantise(a.double().cpu().numpy().reshape(1, Hkv, D))
+        ref = torch.from_numpy(((cd - z[..., None]) * s[..., None]).reshape(1, -1)).to(dtype)
+        assert torch.equal(b.cpu(), ref)
