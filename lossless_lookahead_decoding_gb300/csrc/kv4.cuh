@@ -87,7 +87,7 @@ struct Kv4Attn {
     int q_ld, kv_ld;
     int n_pages, max_pages, max_len, blk_log2;
     int rows, mtiles;        // rows of one KV head (T x heads per KV head), row tiles
-    int tile_log2, step_tiles;  // keys of a tile; tiles of the step's rows
+    int tile_log2;           // keys of a tile (the step's rows are one tile)
     int nteams, extra;       // teams that share the items; tiles an item counts for beyond its own
     float sl2;               // log2(e) / sqrt(D)
 };

@@ -964,7 +964,7 @@ int launch_kv4_attn(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a)
     const Plan p = plan_of(c, a);
     k.part = p.merge ? (float*)a.workspace : nullptr;
     k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = p.extra;
-    k.tile_log2 = kKeysLog2, k.step_tiles = 1;
+    k.tile_log2 = kKeysLog2;
     const cudaError_t e = c.head_dim == 128 ? go<128>(s, p, k) : go<64>(s, p, k);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }

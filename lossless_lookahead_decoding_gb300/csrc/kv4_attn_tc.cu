@@ -1030,7 +1030,7 @@ int launch_kv4_tc(cudaStream_t s, const la_kv4_desc& c, const la_kv4_attn& a, Kv
 {
     const TcPlan p = tc_plan(c, a);
     k.mtiles = p.mtiles, k.nteams = p.nteams, k.extra = kTcExtra;
-    k.tile_log2 = kTileLog2, k.step_tiles = 1;
+    k.tile_log2 = kTileLog2;
     k.part = p.merge ? (float*)a.workspace : nullptr;
     cudaError_t e = c.head_dim == 128 ? go<128>(s, p, k) : go<64>(s, p, k);
     if (e == cudaSuccess && p.merge) e = launch_kv4_merge(s, k, c.head_dim, kRowsTc);

@@ -100,10 +100,10 @@ __device__ __forceinline__ int seq_len(const Kv4Attn& a, int b)
 }
 
 // An item's work in units of a tile: `extra` units for its queries and its
-// result, its cached tiles, its step rows' tiles.
+// result, its cached tiles, its step rows' tile.
 __device__ __forceinline__ int item_units(const Kv4Attn& a, int len)
 {
-    return len < 0 ? 0 : a.extra + ((len + (1 << a.tile_log2) - 1) >> a.tile_log2) + a.step_tiles;
+    return len < 0 ? 0 : a.extra + ((len + (1 << a.tile_log2) - 1) >> a.tile_log2) + 1;
 }
 
 // Sequences whose length is over its bound (one CTA calls it).
