@@ -137,23 +137,18 @@ __device__ __forceinline__ float pow2i(int e)  // 2^e, e in -126 .. 127
 // x 2^e for any e that two such factors reach
 __device__ __forceinline__ float scale2(float x, int e) { return x * pow2i(e >> 1) * pow2i(e - (e >> 1)); }
 
-// What the softmax needs to know of a tile.
-struct TileInfo {
+// What the softmax needs to know of a tile; four in turn.  The unpacking warps fill tile n + 4's in when
+// tile n + 2's scores (K's side: all but `odd`, and a step tile's `ev`) or products (V's side: those) are
+// done.  By then tile n's weights are taken, and for V's side, as a step tile is its run's last, the run's
+// results are out, which is when `odd` is read.  What is known of a cached tile's codes comes with their
+// ring stage: the warp that finds it runs ahead of the others, by any number of tiles where items without
+// cached ones are passed.
+struct alignas(16) TileInfo {
     int live, bad;        // keys, and a bit per block of 16 whose page is not in the pool
     int ek, ev;           // powers of two of K and V
     uint32_t odd[4];      // step rows with a NaN or an infinity among their values
 };
-
-// Cached tiles' entries, eight in turn by the number of cached tiles before them: the copies, and so the
-// search for the powers of two, run at most three cached tiles ahead of the unpacking warps, and these at
-// most two tiles ahead of the softmax, so at most five cached tiles are in use.  (Counted over all tiles,
-// that would not hold: items without cached tiles pass the copying warp without a wait.)
-// Step tiles' entries, four in turn by the number of tiles: the unpacking warps write tile n + 4's when
-// tile n + 2's scores (K) or products (V) are done.  By then tile n's weights are taken, and for V, as
-// the step tile is its run's last, its run's results are out, which is when `odd` is read.
-constexpr int kCachedInfos = 8, kStepInfos = 4;
-__device__ __forceinline__ TileInfo* cached_info(TileInfo* info, int fill) { return info + (fill & (kCachedInfos - 1)); }
-__device__ __forceinline__ TileInfo* step_info(TileInfo* info, int n) { return info + kCachedInfos + (n & (kStepInfos - 1)); }
+constexpr int kInfos = 4;
 
 template <int D>
 struct TcSmem {
@@ -166,10 +161,11 @@ struct TcSmem {
     static constexpr int kRowF = kVis + 128 * 16;             // [2 runs] per row: what undoes q's power of two
     static constexpr int kRowM = kRowF + 2 * 128 * 4;         // per row: the reference M
     static constexpr int kRowL = kRowM + 128 * 4;             // [2 groups] per row: sums
-    static constexpr int kInfo = kRowL + 2 * 128 * 4;         // cached tiles' entries, step tiles'
-    static constexpr int kBar = kInfo + (kCachedInfos + kStepInfos) * (int)sizeof(TileInfo);
+    static constexpr int kInfo = kRowL + 2 * 128 * 4;         // TileInfo[kInfos]
+    static constexpr int kBar = kInfo + kInfos * (int)sizeof(TileInfo);
     static constexpr int kMisc = kBar + 32 * 8;               // ring info, reduction words, start, scan scratch
     static constexpr int kBytes = kMisc + 512 + 1024;         // 1024: to align the base
+    static_assert(kInfo % 16 == 0 && kMisc % 16 == 0, "alignment");
 };
 
 enum {  // barriers
@@ -262,6 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
     volatile int* abort_flag = (volatile int*)(sm + L::kMisc + 84);
     Start* start = (Start*)(sm + L::kMisc + 96);
     long long* scratch = (long long*)(sm + L::kMisc + 160);  // one per warp
+    int4* stage_info = (int4*)(sm + L::kMisc + 320);         // [3]: live, bad, ek, ev of the stage's tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.H / a.Hkv;
 
@@ -371,7 +368,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, grp = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-        int steps = 0, fills = 0;  // this group's step tiles, and both groups' cached tiles so far
+        int steps = 0;  // this group's step tiles so far
         do {
             const int head = run.item / a.mtiles, mt = run.item - head * a.mtiles;
             const int ntc = (run.len + kTile - 1) / kTile, gr = mt * kRowsTc + row;
@@ -379,16 +376,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             const int n0 = n;
             float m = kNoRef, l = 0.f;
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
-                const bool step = tile >= ntc;
-                const TileInfo* ti = step ? step_info(info, n) : cached_info(info, fills);
-                fills += !step;
                 if ((n & 1) != grp) continue;
+                const bool step = tile >= ntc;
                 const int b = grp, ph = (n >> 1) & 1;
-                wait(kSDone + b, ph);  // (so K's part of a step tile's entry is there; V's may not be)
+                wait(kSDone + b, ph);  // (so K's part of the tile's entry is there; V's of a step tile may not be)
                 // A barrier a group: V's part of tile n + 2 waits for tile n's products, so for this wait
                 if (step) wait(kStepReady + grp, steps & 1), steps++;
                 tc_fence_after();
                 if (any) {
+                    const TileInfo* ti = info + (n & (kInfos - 1));
                     const int live = ti->live, bad = ti->bad, iev = ti->ev;
                     const float f = fmaxf(scale2(rowf[(segs & 1) * 128 + row], ti->ek), 1e-37f), ev = (float)iev;
                     const bool part = step || live < kTile || bad;
@@ -524,7 +520,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     const float inv = 1.f / sum;
                     __nv_bfloat16* orow = a.out + ((size_t)(run.b * (long long)a.T + gr / group) * a.H + head * group + gr % group) * D;
                     // the step tile, if it is there, is the last one; its products are done, so its entry is complete
-                    const uint32_t* odd = step_info(info, last)->odd;
+                    const uint32_t* odd = info[last & (kInfos - 1)].odd;
                     const bool fix = run.t1 > ntc && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
 #pragma unroll 1
                     for (int j = 0; j < D / 2; j += 32) {
@@ -621,14 +617,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             for (int tile = run.t0; tile < run.t1; tile += stride, n++) {
                 const int b = n & 1, ph = (n >> 1) & 1;
                 uint8_t* dst = sm + (kv ? L::kV : L::kK) + b * L::kOperand;
+                TileInfo* ti = info + (n & (kInfos - 1));
                 if (tile < ntc) {
-                    const TileInfo* ti = cached_info(info, fills);
                     const int s = fills % kRing, sp = (fills / kRing) & 1;
                     wait(kInfoReady + s, sp);
                     wait(kFull + s, sp);
                     const uint8_t* stage = sm + L::kCodes + s * L::kStage;
-                    const int live = ti->live, bad = ti->bad, E = kv ? ti->ev : ti->ek;
+                    const int4 known = stage_info[s];
+                    const int live = known.x, bad = known.y, E = kv ? known.w : known.z;
                     if (n >= 2) wait((kv ? kODone : kSDone) + b, ph ^ 1);  // tile n - 2's product has read the buffer
+                    if (tid == 0 && !kv) *(int4*)ti = known;
                     // key rows tid / 2 and 64 + tid / 2, half of each 64-channel panel
 #pragma unroll 1
                     for (int r2 = 0; r2 < 2; r2++) {
@@ -661,7 +659,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                     fills++;
                 } else {
                     // the step's own rows: bf16 to fp16 by the tile's largest finite exponent
-                    TileInfo* ti = step_info(info, n);
                     constexpr int kPieces = D / 8, kPass = 128 / kPieces;
                     const int pc = tid % kPieces, r0 = tid / kPieces;  // as the queries
                     const __nv_bfloat16* src = (kv ? a.vs : a.ks) + ((size_t)run.b * a.T + r0) * a.kv_ld + (size_t)head * D + 8 * pc;
@@ -762,11 +759,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             }
             __syncwarp();
         };
-        auto outputs = [&](int b, int ph, bool lead, const TileInfo* ti) {
+        auto outputs = [&](int b, int ph, bool lead) {
             wait(kPReady + b, ph);
             wait(kVReady + b, ph);
             if (lead && segs > 0) wait(kOFree, (segs - 1) & 1);
-            const int live = ti->live;  // only these keys' products
+            const int live = info[n & (kInfos - 1)].live;  // only these keys' products
             tc_fence_after();
             if (chosen && ok) {
                 auto step16 = [&](int k) {
@@ -784,17 +781,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             }
             __syncwarp();
         };
-        int fills = 0;  // cached tiles so far
         do {
-            const int tiles = (run.t1 - run.t0 + stride - 1) / stride, ntc = (run.len + kTile - 1) / kTile;
+            const int tiles = (run.t1 - run.t0 + stride - 1) / stride;
             if (tiles <= 0) continue;
             scores(n & 1, (n >> 1) & 1, true);
             for (int i = 0; i < tiles; i++, n++) {
                 // the next tile's scores go first: they run while this one's softmax does
                 if (i + 1 < tiles) scores((n + 1) & 1, ((n + 1) >> 1) & 1, false);
-                const bool step = run.t0 + i * stride >= ntc;
-                outputs(n & 1, (n >> 1) & 1, i == 0, step ? step_info(info, n) : cached_info(info, fills));
-                fills += !step;
+                outputs(n & 1, (n >> 1) & 1, i == 0);
             }
             segs++;
         } while (!CL && run.next(a));
@@ -881,11 +875,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
                 }
                 ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
                 if (lane == 0) {
-                    TileInfo* ti = cached_info(info, fills);
-                    ti->live = live, ti->bad = bad;
                     // s 2^-E < 2^-8.  V's not below 2^-41, where the values under 2^-50 lose bits: the weights of
                     // a tile without values must still be fp32 numbers beside one of values near 2^50.
-                    ti->ek = max((int)ek, 20) - 118, ti->ev = max((int)ev, 77) - 118;
+                    stage_info[s] = make_int4(live, bad, max((int)ek, 20) - 118, max((int)ev, 77) - 118);
                     mbar_arrive(bar + kInfoReady + s);
                 }
                 __syncwarp();
@@ -917,7 +909,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv4_tc(Kv4Attn a)
             for (int r = 0; r < 8; r++) sum += ls[r] * ex2(ms[r] - top);
             const float w = ex2(out_m - top) / sum;
             const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t* odd = step_info(info, n - 1)->odd;
+            const uint32_t* odd = info[(n - 1) & (kInfos - 1)].odd;
             const bool fix = work && (ntc & (cs - 1)) == rank && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
             tc_fence_after();
 #pragma unroll 1
