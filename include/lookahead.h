@@ -417,8 +417,10 @@ LA_API void la_pool_destroy(la_pool* pool);
  * hi = max(0, max x) and lo = min(0, min x), s is the smallest bf16 number
  * with 15 s >= hi - lo, z the nearest integer to -lo / s and c the nearest
  * integer to x / s (ties to even) plus z, clamped to 0..15.  hi = lo gives
- * zeros.  A vector that holds a NaN or an infinity reads back as NaN.  The
- * decisions are those of exact arithmetic.  Pages: [n_pages][n_kv_heads]
+ * zeros.  (Next to the type's largest number (c - z) s may pass it and read
+ * as an infinity: 15 s is up to 2^-7 above hi - lo.)  A vector that holds a
+ * NaN or an infinity reads back as NaN.  The decisions are those of exact
+ * arithmetic.  Pages: [n_pages][n_kv_heads]
  * [page / 16] blocks of 16 head_dim + 128 bytes for 16 tokens: K codes
  * [head_dim / 64][16 tokens][32 bytes], V codes likewise, 16 K parameter
  * words, 16 V parameter words.  8 codes of channels 8w..8w+7 are one 32-bit
@@ -534,12 +536,17 @@ LA_API size_t la_kv4_attention_bytes(const la_kv4_desc* c, const la_kv4_attn* a)
  * 2D-window + verification mask lets it see (never none: each row sees row
  * 0), scaled by 1 / sqrt(head_dim).  Positions past a length are never used,
  * whatever bytes they hold, and a NaN or infinity in a step row reaches only
- * rows that see it.  Values of V below 2^-50 in magnitude lose accuracy, and
+ * rows that see it.  The step rows' own K and V are used as they are given,
+ * not as their codes; once appended they are seen through them.  So a row of a
+ * step and the same token decoded by itself after its predecessors were
+ * appended differ by the 4-bit rounding of those: over this cache lookahead
+ * decoding is close to decoding one token at a time, not equal to it (la_step,
+ * on its bf16 cache, is).  Values of V below 2^-50 in magnitude lose accuracy, and
  * where a sequence holds some above 2^50, keys of far smaller ones may lose
  * their weight.  out overlaps no other buffer.  A length above its bound
  * leaves that sequence's rows alone, a page index outside the pool counts as
- * no keys (LA_ERR_ARG in *status).  Asynchronous on `stream`; the order of sums depends on the
- * shapes and lengths alone, so equal calls give equal bits.  Two calls that
+ * no keys (LA_ERR_ARG in *status).  Asynchronous on `stream`; the order of sums
+ * depends on the shapes and lengths alone, so equal calls give equal bits.  Two calls that
  * may run at the same time (two streams, two captured graphs) need a
  * workspace each. */
 LA_API int la_kv4_attention(const la_kv4_desc* c, const la_kv4_attn* a, void* stream);

@@ -14,8 +14,9 @@
 //  * q is scaled by a power of two per row (largest magnitude in [2^11, 2^12))
 //    and, for the channels at bits 4-7, by 1/16: exact for every element
 //    within 2^-18 of the row's largest, and off by 2^-36 of it below;
-//  * p s goes to fp16: relative 2^-11, or 2^-25 absolute where the running
-//    reference keeps the largest between 1 and 2^8 (bf16 would cost 2^-8);
+//  * p s goes to fp16: relative 2^-11, or 2^-25 absolute, where the running
+//    reference keeps a row's largest so far between 1 and 2^11 (bf16 would cost
+//    2^-8);
 //  * -z sum(p s) is a product of its own, with -z in place of the codes of all
 //    channels, added to the outputs' sums after every tile: these return near
 //    zero (they shrink as the context grows, z sum(p s) does not).  Added by
@@ -502,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv4_rows(Kv4Attn a)
                 }
             }
             // ------------------------------------------ the step's own rows (16 at most: one tile)
-            // in bf16, with their values brought to the codes' powers of two
+            // in bf16, with the probabilities brought to the codes' powers of two.  V is bf16 of any
+            // exponent, so both operands of P V are, and P rounds by 2^-8 of itself (as in la_attention);
+            // fp16 would need V scaled by the tile's largest first, for the few keys of a step.
             if (run.t1 > ntc && (TW == 1 || (ntc - run.t0) % stride == wi)) {
                 const __nv_bfloat16 *ks = a.ks + step_at, *vs = a.vs + step_at;
                 const int k0 = kv4_key(g), k1 = k0 + 8;
@@ -930,8 +933,8 @@ cudaError_t launch_kv4_merge(cudaStream_t s, const Kv4Attn& k, int D, int R)
 
 namespace {
 
-// Rows of one KV head: up to 8 fill the narrow side of mma.sync; more go to
-// the 128-row tiles of tcgen05.
+// Rows of one KV head: up to 16, one or two tiles of the narrow side of
+// mma.sync; more go to the 128-row tiles of tcgen05.
 bool many_rows(const la_kv4_desc& c, const la_kv4_attn& a)
 {
     return (1 + (a.W + a.G) * (a.N - 1)) * (a.n_heads / c.n_kv_heads) > 16;

@@ -34,13 +34,13 @@
 // shared memory (up to 152 items: one launch, no workspace).
 //
 // Measured on one GB300.  121 rows of 32 heads over 2048 tokens (128 CTAs, 4 or
-// 5 tiles each): 17.0 us, 2.1 of them by the tensor cores' rate; the rest is a
+// 5 tiles each): 17.0 us in a graph, 2.1 of them by the tensor cores' rate; the rest is a
 // chain of latencies (launch and first loads 3 us, 6 us a CTA for queries, first
 // tile and unpacking, 2.5 us for the cluster's join).  6 such sequences: 52 us,
 // 0.24 of the tensor cores' rate in steady state (1.6 us a tile): the softmax
 // groups and the unpacking warps alternate on the schedulers (45 % of issue
 // slots, tensor pipe 25 %); short prompt blocks: 128 rows over at most 11 tokens,
-// 1872 items, 118 us = 9.6 us an item, the step's rows' way through bf16 to fp16
+// 1872 items, 119 us = 9.7 us an item, the step's rows' way through bf16 to fp16
 // and the queries' being the longest chain.
 #include <algorithm>
 #include <cmath>
@@ -962,7 +962,7 @@ struct TcPlan {
 };
 
 // An item's queries and result take as long as so many tiles: 30 sequences of 30 to 2000 tokens, 57 rows
-// of 8 heads each: 234 us at 0, 160 at 2, 146 at 4, 151 at 9; 6 sequences of 2303: 56.0, 54.3, 53.9, 55.1.
+// of 8 heads each: 230 us at 0, 156 at 2, 142 at 4, 146 at 9; 6 sequences of 2303: 55.6, 53.6, 53.3, 55.0.
 constexpr int kTcExtra = 4;
 
 TcPlan tc_plan(const la_kv4_desc& c, const la_kv4_attn& a)
