@@ -551,6 +551,129 @@ LA_API size_t la_kv4_attention_bytes(const la_kv4_desc* c, const la_kv4_attn* a)
  * workspace each. */
 LA_API int la_kv4_attention(const la_kv4_desc* c, const la_kv4_attn* a, void* stream);
 
+/* ---- paged bf16 KV cache: tokens turned to their positions on the way in,
+ * and the step attention of a batch whose sequences share prefixes ----
+ * For serving with a loop of one's own where the cache is to hold keys and
+ * values as they were computed.  One layer's pages are one la_kv16_desc; all
+ * layers share the block tables and the slots.  la_kv4_plan and la_kv4_release
+ * serve this cache, too: they do not look at the pages, so an la_kv4_desc of
+ * the same n_kv_heads, head_dim, page, n_pages, max_pages and status does.
+ *
+ * A prefix (a system prompt, a document) that several sequences begin with is
+ * held once, in pages of its own: plan and append it as a sequence, then name
+ * its pages and length as a prefix.  A sequence's own table and length start
+ * behind its prefix, its positions go on from the prefix's length.
+ *
+ * A step of a batch: la_kv16_append turns the step's queries and keys to their
+ * positions (k_out, q_out), la_kv16_attention attends; after verification
+ * la_kv4_plan gives the accepted rows their slots and la_kv16_append without a
+ * rope copies them there.  A prompt's rows can be written in the first call.
+ * Everything is asynchronous on `stream` and can be captured.
+ *
+ * Format.  k_pages and v_pages are bf16 [n_pages][n_kv_heads][page][head_dim];
+ * slot = page index * page + offset in the page.  Errors met on the device go
+ * to *status as those of the 4-bit cache do, and nothing outside the buffers
+ * given is read or written for such values. */
+typedef struct la_kv16_desc {
+    int n_kv_heads, head_dim; /* head_dim 64 or 128, n_kv_heads <= 1024             */
+    int page;                 /* tokens per page: 16, 32, 64 or 128                 */
+    int n_pages;              /* pages; n_pages * page < 2^31                       */
+    int max_pages;            /* block-table entries of one sequence; max_pages * page <= 2^30 */
+    void *k_pages, *v_pages;  /* DEVICE, n_pages * la_kv16_page_bytes() each, 16-byte aligned */
+    int32_t* status;          /* DEVICE int32, 0 at first, or NULL: the first error */
+} la_kv16_desc;
+
+/* No counterpart on the pages: sizing of this library's device memory.
+ * Bytes of one page of k_pages (needs no GPU); 0 for unsupported shapes. */
+LA_API size_t la_kv16_page_bytes(const la_kv16_desc* c);
+
+/* A position rotation: pair i of the first rot_dim channels turns by turn[i] /
+ * 2^64 of a circle per position; the other channels stay.  Filled by
+ * la_rope_init, plain data. */
+typedef struct la_rope {
+    int rot_dim;       /* 16, 32, ..., head_dim                                    */
+    int neighbours;    /* 0: pair i is channels i, i + rot_dim / 2 (as la_model_desc's); 1: 2 i, 2 i + 1 */
+    uint64_t turn[64]; /* rot_dim / 2 of them                                      */
+} la_rope;
+
+/* No counterpart on the pages: position rotation of a caller's own layer loop.
+ * HOST only.  freq: HOST double[rot_dim / 2], radians per position, or NULL:
+ * theta^(-2 i / rot_dim).  The angle of a position is formed as an exact
+ * multiple of turn, modulo a circle, so far positions lose nothing.
+ * LA_ERR_ARG for rot_dim not a multiple of 16 in 16..128, theta not above 0,
+ * frequencies not finite or above 2^20. */
+LA_API int la_rope_init(la_rope* r, int rot_dim, int neighbours, double theta, const double* freq);
+
+/* Rows to turn and to keep.  Row i of the call is row rows[i] of k, v and q. */
+typedef struct la_kv16_rows {
+    const void *k, *v;         /* DEVICE dtype [n_rows][n_kv_heads][head_dim], rows k_ld, v_ld apart */
+    const void* q;             /* DEVICE dtype [n_rows][n_heads][head_dim], rows q_ld apart; NULL: none */
+    int dtype;                 /* LA_BF16 or LA_FP32                                                */
+    int n_rows, n_heads;
+    int k_ld, v_ld, q_ld;      /* elements; rows 16-byte aligned                                    */
+    int n;                     /* rows of the call                                                  */
+    const int32_t* rows;       /* DEVICE int32[n], or NULL: row i                                   */
+    const int32_t* slots;      /* DEVICE int32[n], < 0: not kept; NULL: none is kept (v not read)   */
+    const int32_t* positions;  /* DEVICE int32[n]; not read without rope                            */
+    const la_rope* rope;       /* HOST, or NULL: nothing turns                                      */
+    void *k_out, *q_out;       /* DEVICE bf16, row i of the call at i * ld; NULL: not wanted        */
+    int k_out_ld, q_out_ld;
+} la_kv16_rows;
+
+/* No counterpart on the pages (their rotary embedding and KV commit, for this
+ * cache).  Keys of the call's rows, turned to their positions, go to their
+ * slots and to k_out, queries to q_out; values go to the slots as they are.
+ * Sums are fp32, rounded once to bf16.  A row or slot outside its range
+ * (LA_ERR_ARG in *status) leaves that row out, a slot may appear once.  q_out
+ * may be q itself and k_out k itself (bf16, equal ld, rows NULL); other
+ * outputs that overlap anything are refused. */
+LA_API int la_kv16_append(const la_kv16_desc* c, const la_kv16_rows* r, void* stream);
+
+/* A step's rows, where they are, and what their sequences share.  As
+ * la_kv4_attn, and prefixes: sequences prefix_first[p] .. prefix_first[p+1]-1
+ * begin with prefix p; those before prefix_first[0] or from
+ * prefix_first[n_prefix] on have none. */
+typedef struct la_kv16_attn {
+    const void* q;        /* DEVICE bf16 [batch * T][n_heads][head_dim], rows q_ld apart  */
+    const void* k_step;   /* DEVICE bf16 [batch * T][n_kv_heads][head_dim], k_ld apart    */
+    const void* v_step;   /* likewise, v_ld apart                                         */
+    void* out;            /* DEVICE bf16 [batch * T][n_heads * head_dim]                  */
+    const int32_t* lens;  /* DEVICE int32[batch]: cached tokens of its own; < 0: rows left alone */
+    const int32_t* table; /* DEVICE int32[batch][max_pages]                               */
+    int batch, n_heads;   /* batch <= 8192, n_heads a multiple of n_kv_heads, <= 128 times it */
+    int W, N, G;          /* T = 1 + (W+G)(N-1) <= 128, 2 <= N <= 128                     */
+    int q_ld, k_ld, v_ld; /* multiples of 8                                               */
+    int max_len;          /* no length is above it (0: max_pages * page)                  */
+    int n_prefix;         /* <= 8192; 0: none, the next three are not read                */
+    int prefix_pages;     /* entries of a prefix's row of prefix_table; times page <= 2^30 */
+    int max_prefix_len;   /* no prefix is longer (0: prefix_pages * page)                 */
+    const int32_t* prefix_lens;  /* DEVICE int32[n_prefix] >= 0                           */
+    const int32_t* prefix_table; /* DEVICE int32[n_prefix][prefix_pages]                  */
+    const int32_t* prefix_first; /* DEVICE int32[n_prefix + 1], ascending in 0..batch     */
+    void* workspace;      /* DEVICE, la_kv16_attention_bytes(), 16-byte aligned           */
+    size_t ws_bytes;
+} la_kv16_attn;
+
+/* No counterpart on the pages: sizing of this library's device memory.
+ * Workspace of la_kv16_attention for these shapes (needs no GPU; pointers are
+ * not looked at); 0 when none is needed or the shape is unsupported. */
+LA_API size_t la_kv16_attention_bytes(const la_kv16_desc* c, const la_kv16_attn* a);
+
+/* Pages: "Summary" (both branches share one forward pass under one mask).
+ * la_attention for a batch over the paged bf16 cache: row i of sequence b
+ * attends to its prefix's tokens, to the lens[b] tokens of its own and to the
+ * step rows the 2D-window + verification mask lets it see (never none: each
+ * row sees row 0), scaled by 1 / sqrt(head_dim).  A prefix is read once for
+ * all of its sequences, not once for each.  Positions past a length are never
+ * used, whatever bytes they hold, and a NaN or infinity in a step row reaches
+ * only rows that see it.  out overlaps no other buffer.  A length above its
+ * bound (of a prefix: for all of its sequences) leaves a sequence's rows alone,
+ * a page index outside the pool counts as no keys, prefix_first out of order
+ * leaves every row alone (each LA_ERR_ARG in *status).  Asynchronous on
+ * `stream`; equal calls give equal bits.  Two calls that may run at the same
+ * time (two streams, two captured graphs) need a workspace each. */
+LA_API int la_kv16_attention(const la_kv16_desc* c, const la_kv16_attn* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

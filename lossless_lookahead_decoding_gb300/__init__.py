@@ -32,7 +32,8 @@ EXPORTS = ("la_workspace_bytes", "la_create", "la_prefill", "la_step", "la_gener
            "la_last_error", "la_destroy", "la_attention", "la_attention_noalloc", "la_pool_create", "la_pool_insert", "la_pool_lookup", "la_pool_size",
            "la_pool_destroy",
            "la_kv4_page_bytes", "la_kv4_plan", "la_kv4_release", "la_kv4_append", "la_kv4_read", "la_kv4_attention_bytes",
-           "la_kv4_attention")
+           "la_kv4_attention",
+           "la_kv16_page_bytes", "la_rope_init", "la_kv16_append", "la_kv16_attention_bytes", "la_kv16_attention")
 
 
 class LAError(RuntimeError):
@@ -69,6 +70,31 @@ class la_kv4_attn(C.Structure):
     _fields_ = [("q", C.c_void_p), ("k_step", C.c_void_p), ("v_step", C.c_void_p), ("out", C.c_void_p),
                 ("lens", C.c_void_p), ("table", C.c_void_p), ("batch", C.c_int), ("n_heads", C.c_int), ("W", C.c_int),
                 ("N", C.c_int), ("G", C.c_int), ("q_ld", C.c_int), ("kv_ld", C.c_int), ("max_len", C.c_int),
+                ("workspace", C.c_void_p), ("ws_bytes", C.c_size_t)]
+
+
+class la_kv16_desc(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("page", C.c_int), ("n_pages", C.c_int),
+                ("max_pages", C.c_int), ("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("status", C.c_void_p)]
+
+
+class la_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("neighbours", C.c_int), ("turn", C.c_uint64 * 64)]
+
+
+class la_kv16_rows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("q", C.c_void_p), ("dtype", C.c_int), ("n_rows", C.c_int),
+                ("n_heads", C.c_int), ("k_ld", C.c_int), ("v_ld", C.c_int), ("q_ld", C.c_int), ("n", C.c_int), ("rows", C.c_void_p),
+                ("slots", C.c_void_p), ("positions", C.c_void_p), ("rope", C.POINTER(la_rope)), ("k_out", C.c_void_p),
+                ("q_out", C.c_void_p), ("k_out_ld", C.c_int), ("q_out_ld", C.c_int)]
+
+
+class la_kv16_attn(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k_step", C.c_void_p), ("v_step", C.c_void_p), ("out", C.c_void_p),
+                ("lens", C.c_void_p), ("table", C.c_void_p), ("batch", C.c_int), ("n_heads", C.c_int), ("W", C.c_int),
+                ("N", C.c_int), ("G", C.c_int), ("q_ld", C.c_int), ("k_ld", C.c_int), ("v_ld", C.c_int), ("max_len", C.c_int),
+                ("n_prefix", C.c_int), ("prefix_pages", C.c_int), ("max_prefix_len", C.c_int),
+                ("prefix_lens", C.c_void_p), ("prefix_table", C.c_void_p), ("prefix_first", C.c_void_p),
                 ("workspace", C.c_void_p), ("ws_bytes", C.c_size_t)]
 
 
@@ -122,6 +148,11 @@ def lib():
             "la_kv4_read": (i32, [vp, vp, i32, vp, vp, i32, i32, vp]),
             "la_kv4_attention_bytes": (sz, [vp, vp]),
             "la_kv4_attention": (i32, [vp, vp, vp]),
+            "la_kv16_page_bytes": (sz, [vp]),
+            "la_rope_init": (i32, [vp, i32, i32, C.c_double, vp]),
+            "la_kv16_append": (i32, [vp, vp, vp]),
+            "la_kv16_attention_bytes": (sz, [vp, vp]),
+            "la_kv16_attention": (i32, [vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -375,6 +406,31 @@ def la_kv4_attention(desc: la_kv4_desc, attn: la_kv4_attn, stream: int = 0) -> i
     return lib().la_kv4_attention(C.byref(desc), C.byref(attn), stream or None)
 
 
+# The la_kv16_* calls, likewise; la_rope_init fills a structure of the caller's.
+
+def la_kv16_page_bytes(desc: la_kv16_desc) -> int:
+    return int(lib().la_kv16_page_bytes(C.byref(desc)))
+
+
+def la_rope_init(rope: la_rope, rot_dim: int, neighbours: int = 0, theta: float = 1e4, freq=None) -> int:
+    f = None if freq is None else np.ascontiguousarray(freq, dtype=np.float64)
+    if f is not None and f.size != rot_dim // 2:
+        return LA_ERR_ARG
+    return lib().la_rope_init(C.byref(rope), rot_dim, neighbours, theta, None if f is None else _p(f))
+
+
+def la_kv16_append(desc: la_kv16_desc, rows: la_kv16_rows, stream: int = 0) -> int:
+    return lib().la_kv16_append(C.byref(desc), C.byref(rows), stream or None)
+
+
+def la_kv16_attention_bytes(desc: la_kv16_desc, attn: la_kv16_attn) -> int:
+    return int(lib().la_kv16_attention_bytes(C.byref(desc), C.byref(attn)))
+
+
+def la_kv16_attention(desc: la_kv16_desc, attn: la_kv16_attn, stream: int = 0) -> int:
+    return lib().la_kv16_attention(C.byref(desc), C.byref(attn), stream or None)
+
+
 # ------------------------------------------------------------------ Decoder
 
 LAYER_ORDER = ("attn_norm", "wq", "wk", "wv", "wo", "ffn_norm", "wg", "wu", "wd")
@@ -571,3 +627,99 @@ class KV4Cache:
         rc = self._kv4.attention(self._handle, q, k_step, v_step, lens, table, W, N, G, out, workspace, max_len)
         if rc:
             self._done(rc, "la_kv4_attention")
+
+
+# ---------------------------------------------------------------- KV16Cache
+
+class Rope:
+    """A position rotation of the first ``rot_dim`` channels (``la_rope``): pair
+    i turns by ``theta ** (-2 i / rot_dim)`` radians per position, or by
+    ``freq[i]``; pairs are channels (i, i + rot_dim / 2), or neighbours."""
+
+    def __init__(self, rot_dim: int, theta: float = 1e4, neighbours: bool = False, freq=None):
+        self.rope = la_rope()
+        if la_rope_init(self.rope, rot_dim, int(neighbours), theta, freq) != LA_OK:
+            raise ValueError("rope: rot_dim a multiple of 16 up to 128, theta above 0, rot_dim / 2 finite frequencies")
+        self.rot_dim, self.address = rot_dim, C.addressof(self.rope)
+
+
+class KV16Cache:
+    """One layer's paged bf16 KV cache (``la_kv16_*``) over torch tensors.
+
+    ``k_pages``, ``v_pages``: bf16 ``[n_pages, n_kv_heads, page, head_dim]`` on
+    the GPU, see ``empty_pages``.  All index tensors are int32 on the same
+    device.  Every call runs on torch's current stream, is asynchronous and can
+    be captured into a CUDA graph; the device must be the current one.  Errors
+    found on the device (an index outside its range, too few pages) stay in
+    ``status``; ``check()`` waits and raises them."""
+
+    def __init__(self, k_pages, v_pages, max_pages: int):
+        import torch
+        for x in (k_pages, v_pages):
+            if x.dtype != torch.bfloat16 or x.dim() != 4 or not x.is_contiguous() or not x.is_cuda:
+                raise ValueError("pages: contiguous bf16 [n_pages, n_kv_heads, page, head_dim] on the GPU")
+        if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages of one shape, on one device")
+        n, heads, page, dim = k_pages.shape
+        self.k_pages, self.v_pages, self.page, self.max_pages = k_pages, v_pages, page, max_pages
+        self.n_kv_heads, self.head_dim, self.device = heads, dim, k_pages.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+        self.desc = la_kv16_desc(heads, dim, page, n, max_pages, k_pages.data_ptr(), v_pages.data_ptr(),
+                                 self.status.data_ptr())
+        if not la_kv16_page_bytes(self.desc):
+            raise ValueError("unsupported cache shape")
+        from . import _kv16
+        self._kv16, self._handle = _kv16, _kv16.handle(k_pages, v_pages, self.status, C.addressof(self.desc))
+
+    @staticmethod
+    def empty_pages(n_pages: int, n_kv_heads: int, head_dim: int, page: int, device="cuda"):
+        """k_pages and v_pages of a cache, zeroed."""
+        import torch
+        return tuple(torch.zeros((n_pages, n_kv_heads, page, head_dim), dtype=torch.bfloat16, device=device)
+                     for _ in range(2))
+
+    _done = staticmethod(KV4Cache._done)
+    check = KV4Cache.check
+
+    def plan(self, lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left, stride: int = 0):
+        """Pages and slots of ``n_new`` further tokens of each sequence (``la_kv4_plan``)."""
+        rc = self._kv16.plan(self._handle, lens, n_new, free_pages, n_free, table, slots, new_lens, pages_left, stride)
+        if rc:
+            self._done(rc, "la_kv4_plan")
+
+    def release(self, done, lens, table, free_pages, n_free):
+        """Give back the pages of the sequences with ``done`` != 0 (``la_kv4_release``)."""
+        rc = self._kv16.release(self._handle, done, lens, table, free_pages, n_free)
+        if rc:
+            self._done(rc, "la_kv4_release")
+
+    def append(self, k, v, slots, rows=None, positions=None, rope=None, k_out=None, q=None, q_out=None):
+        """Tokens' K and V (bf16 or fp32) into their slots (< 0 or ``slots``
+        None: not kept), K turned to its position where there is a ``rope``;
+        the turned rows also into ``k_out``, and those of ``q`` into ``q_out``
+        (bf16).  ``rows``: the row of k, v and q each entry takes
+        (``la_kv16_append``)."""
+        rc = self._kv16.append(self._handle, k, v, slots, rows, positions, rope.address if rope is not None else None,
+                               k_out, q, q_out)
+        if rc:
+            self._done(rc, "la_kv16_append")
+
+    def attention_bytes(self, batch: int, n_heads: int, W: int, N: int, G: int, prefixes: int = 0, prefix_pages: int = 0,
+                        max_len: int = 0, max_prefix_len: int = 0) -> int:
+        """Bytes of workspace ``attention`` needs for these shapes."""
+        return la_kv16_attention_bytes(self.desc, la_kv16_attn(
+            batch=batch, n_heads=n_heads, W=W, N=N, G=G, max_len=max_len, n_prefix=prefixes, prefix_pages=prefix_pages,
+            max_prefix_len=max_prefix_len))
+
+    def attention(self, q, k_step, v_step, lens, table, W: int, N: int, G: int, out, workspace, prefix_lens=None,
+                  prefix_table=None, prefix_first=None, max_len: int = 0, max_prefix_len: int = 0):
+        """Masked attention of a step's rows over the cache (``la_kv16_attention``).
+        ``q``: bf16 ``[batch * T, n_heads * head_dim]``, ``k_step`` and
+        ``v_step`` likewise for the KV heads (views into a fused projection
+        do), ``out``: contiguous ``[batch * T, n_heads * head_dim]``.
+        Sequences ``prefix_first[p]`` to ``prefix_first[p + 1] - 1`` begin with
+        the ``prefix_lens[p]`` tokens in the pages of ``prefix_table[p]``."""
+        rc = self._kv16.attention(self._handle, q, k_step, v_step, lens, table, W, N, G, out, workspace, max_len,
+                                  prefix_lens, prefix_table, prefix_first, max_prefix_len)
+        if rc:
+            self._done(rc, "la_kv16_attention")

@@ -3,9 +3,10 @@
 Each csrc/*.cu is compiled in parallel into _build/, then linked into
 lossless_lookahead_decoding_gb300/liblookahead.so against the shared CUDA
 runtime.  Rebuilds only what changed (object newer than its source and every
-header).  csrc/kv4_torch.cpp becomes _kv4.so, the Python module behind
-KV4Cache, compiled by the host compiler against torch's headers; without a
-CUDA build of torch, which KV4Cache needs, it is left out.
+header).  csrc/kv4_torch.cpp and kv16_torch.cpp become _kv4.so and _kv16.so,
+the Python modules behind KV4Cache and KV16Cache, compiled by the host
+compiler against torch's headers; without a CUDA build of torch, which the
+classes need, they are left out.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblookahead.so")
 BINDING = os.path.join(HERE, "_kv4.so")
+BINDING16 = os.path.join(HERE, "_kv16.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -64,12 +66,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return r.stderr
 
-    # the binding's object: as the others, with the host compiler
-    bsrc, bobj = os.path.join(CSRC, "kv4_torch.cpp"), os.path.join(BUILD, "kv4_torch.o")
+    # the bindings' objects: as the others, with the host compiler
     torch = torch_dir()
-    binding = torch and (force or not os.path.exists(bobj) or os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_t))
+    binding_hdr_t = max(hdr_t, os.path.getmtime(os.path.join(CSRC, "torch_args.h")))
+    bindings = []  # source, object, module, whether to compile
+    for name, so in (("kv4_torch", BINDING), ("kv16_torch", BINDING16)) if torch else ():
+        bsrc, bobj = os.path.join(CSRC, name + ".cpp"), os.path.join(BUILD, name + ".o")
+        stale = force or not os.path.exists(bobj) or os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), binding_hdr_t)
+        bindings.append((bsrc, bobj, so, stale))
 
-    def cc_binding():
+    def cc_binding(bsrc, bobj):
         t = os.path.join(torch, "include")
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-c", bsrc, "-o", bobj, "-I", t,
                "-I", os.path.join(t, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
@@ -78,8 +84,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode:
             raise RuntimeError(f"g++ failed for {bsrc}:\n{r.stderr}")
 
-    with cf.ThreadPoolExecutor(max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
-        other = ex.submit(cc_binding) if binding else None
+    with cf.ThreadPoolExecutor(max(1, min(len(jobs) + 2, os.cpu_count() or 1))) as ex:
+        others = [ex.submit(cc_binding, bsrc, bobj) for bsrc, bobj, _, stale in bindings if stale]
         logs = list(ex.map(cc, jobs))
     if verbose:
         for log in logs:
@@ -89,14 +95,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".{os.getpid()}.tmp"
         subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if other:
+    for other in others:
         other.result()
-    if torch and (binding or not os.path.exists(BINDING)):
+    for _, bobj, so, stale in bindings:
+        if not stale and os.path.exists(so):
+            continue
         lib = os.path.join(torch, "lib")
-        tmp = BINDING + f".{os.getpid()}.tmp"
+        tmp = so + f".{os.getpid()}.tmp"
         subprocess.check_call(["g++", "-shared", "-o", tmp, bobj, "-L", HERE, "-llookahead", "-Wl,-rpath,$ORIGIN",
                                "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
-        os.replace(tmp, BINDING)
+        os.replace(tmp, so)
     return LIB
 
 

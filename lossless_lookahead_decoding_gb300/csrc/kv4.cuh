@@ -92,6 +92,23 @@ struct Kv4Attn {
     float sl2;               // log2(e) / sqrt(D)
 };
 
+// Host helpers of both caches' entry points.
+inline int log2_of(int x)
+{
+    int l = 0;
+    while ((1 << l) < x) l++;
+    return l;
+}
+
+inline bool aligned(const void* p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }
+
+// every address one of an int (a misaligned access would end the context)
+template <typename... P>
+bool ints_aligned(const P*... p)
+{
+    return (aligned(p, 4) && ...);
+}
+
 // kv4_cache.cu
 int launch_kv4_plan(cudaStream_t s, const la_kv4_desc& c, const int* lens, const int* n_new, int B, const int* free_pages,
                     const int* n_free, int* table, int* slots, int n_slots, int stride, int* new_lens, int* left);

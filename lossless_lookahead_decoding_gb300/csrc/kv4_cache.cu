@@ -610,13 +610,6 @@ __global__ void __launch_bounds__(256) k_kv4_read(ReadArgs a)
     }
 }
 
-int log2_of(int x)
-{
-    int l = 0;
-    while ((1 << l) < x) l++;
-    return l;
-}
-
 // More shared memory than 48 KB for the large-batch plan, once per device.
 std::mutex g_plan_mu;
 bool g_plan_ready[256];
@@ -711,15 +704,6 @@ bool desc_ok(const la_kv4_desc* c)
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
     if (c->n_pages < 1 || (long long)c->n_pages * c->page >= (1LL << 31)) return false;
     return c->max_pages >= 1 && (long long)c->max_pages * c->page <= (1LL << 30);  // (lengths in tiles stay within an int)
-}
-
-bool aligned(const void* p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }
-
-// every address one of an int (a misaligned access would end the context)
-template <typename... P>
-bool ints_aligned(const P*... p)
-{
-    return (aligned(p, 4) && ...);
 }
 
 bool pool_ok(const la_kv4_desc* c) { return desc_ok(c) && c->pages && aligned(c->pages, 16) && aligned(c->status, 4); }
