@@ -16,66 +16,11 @@ namespace la {
 bool kv16_rows_init();
 int kv16_rows_teams();
 cudaError_t launch_kv16_rows(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D);
+bool kv16_wide_init();
+int kv16_wide_teams();
+int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D, int rows_all);
 
 namespace {
-// One warp per row and query head; a lane holds D / 32 channels.
-template <int D>
-__global__ void __launch_bounds__(256) k_kv16_simple(const __grid_constant__ Kv16Attn a)
-{
-    constexpr int C = D / 32;
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item >= (long long)a.B * a.T * a.H) return;
-    const int h = (int)(item % a.H), row = (int)(item / a.H), b = row / a.T, i = row - b * a.T, g = h / (a.H / a.Hkv);
-    bool skip = false;
-    int pre = -1, plen = 0;
-    for (int p = lane; p < a.nP; p += 32) {
-        const int lo = a.pfirst[p], hi = a.pfirst[p + 1];
-        if (lo < 0 || hi > a.B || lo > hi) skip = true;
-        if (lo <= b && b < hi) pre = p;
-    }
-    skip = __any_sync(0xffffffffu, skip);
-    pre = __reduce_max_sync(0xffffffffu, pre);
-    if (pre >= 0) plen = a.plens[pre];
-    const int len = a.lens[b];
-    if (plen > a.max_plen || len > a.max_len) skip = true;
-    if (skip && lane == 0) kv4_raise(a.status, LA_ERR_ARG);
-    if (skip || len < 0) return;
-    float q[C], o[C] = {}, m = kNoRef, l = 0.f;
-    for (int c = 0; c < C; c++) q[c] = __bfloat162float(a.q[(size_t)row * a.q_ld + (size_t)h * D + c * 32 + lane]) * a.sl2;
-    auto key = [&](const __nv_bfloat16* k, const __nv_bfloat16* v) {
-        float s = 0.f;
-        for (int c = 0; c < C; c++) s += q[c] * __bfloat162float(k[c * 32 + lane]);
-        s = warp_sum(s);
-        const float top = fmaxf(m, s), f = exp2f(m - top), p = exp2f(s - top);
-        m = top;
-        l = l * f + p;
-        for (int c = 0; c < C; c++) o[c] = o[c] * f + p * __bfloat162float(v[c * 32 + lane]);
-    };
-    auto cached = [&](const int* table, int n) {
-        for (int t = 0; t < n; t++) {
-            const int page = table[t >> a.page_log2];
-            if ((unsigned)page >= (unsigned)a.n_pages) {
-                if (lane == 0) kv4_raise(a.status, LA_ERR_ARG);
-                continue;
-            }
-            const size_t at = ((((size_t)page * a.Hkv + g) << a.page_log2) + (t & ((1 << a.page_log2) - 1))) * D;
-            key(a.kp + at, a.vp + at);
-        }
-    };
-    if (plen > 0) cached(a.ptable + (size_t)pre * a.pp, plen);
-    cached(a.table + (size_t)b * a.max_pages, len);
-    for (int j = 0; j < a.T; j++)
-        if (kv4_sees(i, j, a.W, a.n1)) {
-            const size_t r = (size_t)b * a.T + j, at = (size_t)g * D;
-            key(a.ks + r * a.k_ld + at, a.vs + r * a.v_ld + at);
-        }
-    for (int c = 0; c < C; c++) a.out[((size_t)row * a.H + h) * D + c * 32 + lane] = __float2bfloat16_rn(o[c] / l);
-}
-
-
 // ------------------------------------------------------------------- merge ---
 
 constexpr int kMergeRows = 8, kMergeThreads = 512;
@@ -203,7 +148,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv16_merge(const __grid_const
 struct Plan {
     Kv16Attn k;
     Kv16Merge w;
-    bool rows, merge;
+    bool rows, wide, merge;
     size_t bytes;
 };
 
@@ -230,21 +175,55 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
         at += (bytes + 255) / 256 * 256;
         return x;
     };
+    p.w.rows_all = k.B * k.R;
+    const size_t all = (size_t)k.Hkv * p.w.rows_all * (D + 2) * 4;  // results of whole items
+    // A prefix by itself, for all of its sequences at once, where reading it for each would cost
+    // more than the further launches and parts (these bytes come from L2 at 8 TB/s: 2 us), and
+    // where a sequence has too few rows to fill a tile.
+    const long long again = (long long)k.B * k.Hkv * k.max_plen * D * 4;
+    const bool apart = k.B > 1 && k.R <= 64 && again > (16 << 20);
+    k.concat = !apart;
     p.rows = k.R <= 16;
+    p.wide = !p.rows || apart;
+    p.merge = apart;
+    auto notes = [&](Kv16Sched& s, size_t part) {
+        s.shares = (Kv16Shares*)room(sizeof(Kv16Shares)), s.base = (long long*)room(8 * (size_t)(s.n_pre + s.n_seq));
+        s.slots = (float*)room((size_t)s.nteams * 2 * part);
+    };
+    if (p.wide) {
+        Kv16Sched& s = p.w.pre;
+        s.n_pre = apart ? k.nP : 0, s.n_seq = p.rows ? 0 : k.B;
+        s.row_tile = kWideRows, s.blk_log2 = 3, s.wide = 128, s.extra = 4;
+        s.nteams = kv16_wide_teams(), s.min_run = 6, s.slack = 12;
+        s.finish = !apart, s.first = 1;
+        const long long items = (long long)k.B * k.Hkv * ((k.R + kWideRows - 1) / kWideRows);
+        const int most = (blocks(k.max_len) + blocks(k.max_plen) + blocks(k.T) + 7) / 8 * (k.R > 128 ? 2 : 1);
+        if (!apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.slack = 1 << 30;
+        else {
+            p.merge = true;
+            notes(s, wide_part(D) * 4);
+        }
+        if (apart) {
+            s.whole_pre = (float*)room(all);
+            if (!p.rows) s.whole = (float*)room(all);
+        }
+        if (!p.rows) p.w.seq = s;
+        if (!apart) p.w.pre.n_pre = 0;
+    }
     if (p.rows) {
         Kv16Sched& s = p.w.seq;
         s.n_seq = k.B, s.row_tile = 16, s.wide = 1 << 30, s.extra = 2;
         const long long items = (long long)k.B * k.Hkv;
         const int most = blocks(k.max_len) + blocks(k.max_plen) + 1;  // blocks of an item, at most
         s.nteams = kv16_rows_teams(), s.min_run = 16, s.slack = 16;
-        s.finish = s.first = 1;
-        p.merge = !(items <= s.nteams && most <= s.slack);
-        if (!p.merge) s.nteams = (int)items, s.slack = 1 << 30;
+        s.finish = !apart, s.first = !apart;
+        if (!apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.slack = 1 << 30;
         else {
-            s.shares = (Kv16Shares*)room(sizeof(Kv16Shares)), s.base = (long long*)room(8 * (size_t)k.B);
-            s.slots = (float*)room((size_t)s.nteams * 2 * rows_part(D, k.R) * 4);
+            p.merge = true;
+            notes(s, rows_part(D, k.R) * 4);
         }
-        p.w.seq_rows = 1, p.w.rows_all = k.B * k.R;
+        if (apart) s.whole = (float*)room(all);
+        p.w.seq_rows = 1;
     }
     p.bytes = at;
     return p;
@@ -254,7 +233,7 @@ bool init()
 {
     static std::once_flag once;
     static bool ok;
-    std::call_once(once, [] { ok = kv16_rows_init(); });
+    std::call_once(once, [] { ok = kv16_rows_init() && kv16_wide_init(); });
     return ok;
 }
 
@@ -274,14 +253,12 @@ int launch_kv16_attn(cudaStream_t s, const la_kv16_desc& c, const la_kv16_attn& 
     k.kp = (const __nv_bfloat16*)c.k_pages, k.vp = (const __nv_bfloat16*)c.v_pages;
     k.q_ld = a.q_ld, k.k_ld = a.k_ld, k.v_ld = a.v_ld;
     const int D = c.head_dim;
-    cudaError_t e;
-    if (p.rows) {
-        e = launch_kv16_rows(s, k, p.w.seq, D);
-    } else {
-        const long long items = (long long)k.B * k.T * k.H;
-        const dim3 grid((unsigned)((items + 7) / 8));
-        e = D == 128 ? launch_pdl(k_kv16_simple<128>, grid, dim3(256), 0, s, k) : launch_pdl(k_kv16_simple<64>, grid, dim3(256), 0, s, k);
+    if (p.wide) {
+        const int rc = launch_kv16_wide(s, k, p.w.pre, D, p.w.rows_all);
+        if (rc != LA_OK) return rc;
     }
+    cudaError_t e = cudaSuccess;
+    if (p.rows) e = launch_kv16_rows(s, k, p.w.seq, D);
     if (e == cudaSuccess && p.merge) {
         const dim3 grid((p.w.rows_all + kMergeRows - 1) / kMergeRows, k.Hkv), block(kMergeThreads);
         e = D == 128 ? launch_pdl(k_kv16_merge<128>, grid, block, 0, s, k, p.w) : launch_pdl(k_kv16_merge<64>, grid, block, 0, s, k, p.w);

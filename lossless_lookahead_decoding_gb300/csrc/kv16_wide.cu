@@ -1,0 +1,593 @@
+// kv16_wide.cu -- the step's masked attention over the paged bf16 cache for
+// many rows per KV head, on tcgen05: lookahead steps, prompt blocks, and the
+// rows of all sequences that share a prefix.
+//
+// An item is up to 256 rows of a KV head.  Its keys come in tiles of 128: 8
+// blocks of 16, each from a page of the prefix or of the sequence or from the
+// step's rows, each two boxes (64 channels x 16 keys) of a tensor map.  Two
+// streams of 128 rows work at once, so that one's products run while the other
+// weighs: with more than 128 rows each has its own rows and both use every
+// tile (a tile is read once for 256 rows: 128 rows a tile would need all that an
+// SM can read from L2); with fewer, both have the same rows and take every
+// second tile, and join their results at the end.  Per stream and tile
+//   S = Q K^T          Q and K in shared memory, S in tensor memory
+//   P = exp2(S f - M)  in bf16, in the place of S
+//   O += P V           P from tensor memory, V in shared memory
+// with S, M, the sums and O in fp32.  The reference M is the largest score of a
+// row's first tile and moves only when a row's P of a tile sum to more than
+// 2^15; the weights stay in registers until that is known.
+//
+// Keys that are not there: their scores count as -inf, and their values, of
+// which a product would take 0 x NaN, are cleared in shared memory, as are the
+// step rows' that are not finite; these are added to the rows that see them at
+// the end.
+//
+// One CTA per SM: warps 0-3 and 4-7 the streams' softmax (a row per thread), 8
+// issues the products, 9 the copies, 10-11 clear values.
+#include <cudaTypedefs.h>
+
+#include "kv16_sched.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kInfos = 8;
+
+// What is known of a tile; eight in turn.
+struct alignas(16) TileInfo {
+    uint32_t code[2];  // a byte for each block: keys, or 128 + number of the step's block; 0: none
+    int blocks, part;  // blocks; are scores to be left out
+};
+
+template <int D>
+struct WideSmem {
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kOperand = kAtoms * 128 * 128;  // [atom][128 rows][128 bytes]
+    static constexpr int kStages = D == 128 ? 5 : 9;     // K and V by turns: odd, so that each use is known by the fill
+    static constexpr int kQ = 0, kRing = 2 * kOperand;
+    static constexpr int kVis = kRing + kStages * kOperand;  // [step row][4]: step rows it sees
+    static constexpr int kBar = kVis + 128 * 16;
+    static constexpr int kBars = 2 * kStages + 16;
+    static constexpr int kInfo = (kBar + kBars * 8 + 15) / 16 * 16;
+    static constexpr int kOdd = kInfo + kInfos * (int)sizeof(TileInfo);  // [run][warp][4]: step rows whose values are not finite
+    static constexpr int kMisc = kOdd + 8 * 2 * 16;
+    static constexpr int kBytes = kMisc + 16;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ int piece_at(int i, int row)
+{
+    return (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
+}
+
+// Adds what is not finite among the values of the step rows (bits of odd and see
+// both set) to 32 channels from col.
+__device__ __noinline__ void add_odd_to(const Kv16Attn& a, const uint32_t* odd, const uint32_t* see, int b, int col, float* o)
+{
+    for (int key = 0; key < a.T; key++) {
+        if (!((((odd[key >> 5] | odd[4 + (key >> 5)]) & see[key >> 5]) >> (key & 31)) & 1)) continue;
+        const __nv_bfloat16* v = a.vs + (size_t)(b * (long long)a.T + key) * a.v_ld + col;
+        for (int i = 0; i < 32; i++) {
+            const float x = __bfloat162float(v[i]);
+            if (!(fabsf(x) < INFINITY)) o[i] += x;
+        }
+    }
+}
+
+struct Maps {
+    CUtensorMap kp, vp, ks, vs;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv16_wide(const __grid_constant__ Kv16Attn a, const __grid_constant__ Kv16Sched s, const __grid_constant__ Maps maps, int rows_all)
+{
+    using L = WideSmem<D>;
+    constexpr int kSt = L::kStages;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bar = (uint64_t*)(sm + L::kBar);
+    uint64_t *b_full = bar, *b_empty = bar + kSt, *b_vready = bar + 2 * kSt, *b_s = b_vready + 8, *b_p = b_s + 2, *b_q = b_p + 2,
+             *b_o = b_q + 1, *b_end = b_o + 1;
+    TileInfo* info = (TileInfo*)(sm + L::kInfo);
+    uint32_t *vis = (uint32_t*)(sm + L::kVis), *odds = (uint32_t*)(sm + L::kOdd);
+    uint32_t* tmem_slot = (uint32_t*)(sm + L::kMisc);
+    volatile int* abort_flag = (volatile int*)(sm + L::kMisc + 4);
+    // (before the queries come)
+    Scan* sc = (Scan*)(sm + L::kQ);
+    Start* start = (Start*)(sc + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.group;
+
+    if (warp == 8) tmem_alloc(tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSt; i++) mbar_init(b_full + i, 1), mbar_init(b_empty + i, 1);
+        for (int i = 0; i < 8; i++) mbar_init(b_vready + i, 2);
+        for (int i = 0; i < 2; i++) mbar_init(b_s + i, 1), mbar_init(b_p + i, 4);
+        mbar_init(b_q, 8);
+        mbar_init(b_o, 1);
+        mbar_init(b_end, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (threadIdx.x >= 32 && threadIdx.x < 36) {
+        const CUtensorMap* m[4] = {&maps.kp, &maps.vp, &maps.ks, &maps.vs};
+        prefetch_map(m[threadIdx.x - 32]);
+    }
+    if (s.n_seq)
+        for (int i = threadIdx.x - 64; i >= 0 && i < a.T; i += kThreads) {
+            // the step rows that step row i sees (the mask), as bits
+            uint32_t m[4];
+            const int nl = a.W * a.n1;
+            int lo, hi;  // besides row 0: lo .. hi, and column c of the levels up to lv
+            int lv = 0, c = 0;
+            if (i <= nl) lv = i ? (i - 1) / a.W : 0, c = i ? (i - 1) % a.W : 0, lo = 1, hi = i ? 1 + c : 0;
+            else lo = i - (i - 1 - nl) % a.n1, hi = i;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                const int x = max(lo - 32 * w, 0), y = min(hi - 32 * w, 31);
+                m[w] = x <= y ? (~0u << x) & (~0u >> (31 - y)) : 0u;
+            }
+            m[0] |= 1u;
+            for (int v = 1; v <= lv; v++) {
+                const int j = 1 + v * a.W + c;
+#pragma unroll
+                for (int w = 0; w < 4; w++) m[w] |= j >> 5 == w ? 1u << (j & 31) : 0u;
+            }
+            *(uint4*)(vis + 4 * i) = make_uint4(m[0], m[1], m[2], m[3]);
+        }
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    find_starts(a, s, blockIdx.x, 1, start, sc);
+    tc_fence_after();
+    const Kv16Shares sh = sc->shares;
+    const Start st = *start;
+    const uint32_t tmem = *tmem_slot;
+    // (the swizzle and the products' descriptors count from multiples of 1024)
+    const bool placed = (smem_u32(sm) & 1023) == 0, work = st.count > 0 && placed;
+    if (!placed && threadIdx.x == 0) kv4_raise(a.status, LA_ERR_CUDA);
+    __syncthreads();
+
+    // A wait that gives up ends every later one at once, but no role leaves its
+    // loops: the named barriers keep their counts.
+    bool ok = true;
+    auto wait = [&](uint64_t* b, int parity) {
+        if (!ok || try_wait_long(b, parity & 1)) return;
+        const unsigned long long t0 = globaltimer();
+        while (!try_wait_long(b, parity & 1)) {
+            if (*abort_flag || globaltimer() - t0 > kWaitNs) {
+                ok = false;
+                *abort_flag = 1;
+                kv4_raise(a.status, LA_ERR_TIMEOUT);
+                return;
+            }
+        }
+    };
+    constexpr uint32_t kColO = 256;  // tensor memory: S [2][128] (P in their place), O [2][128]
+    int n = 0;     // tiles so far
+    int segs = 0;  // runs with tiles so far
+    Run run;
+    if (work) run.begin(a, s, st, sh);
+    if (work && warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int q = warp & 3, str = warp >> 2, row = q * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16), ts = trow + str * 128, to = trow + kColO + str * 128;
+        int done = 0;  // this stream's tiles so far
+        do {
+            const int nt = run.t1 - run.t0;
+            if (nt <= 0) continue;
+            const Entry& x = run.x;
+            const int g = run.item / x.mt, r0 = (run.item - g * x.mt) * kWideRows, nrows = min(kWideRows, x.rows - r0);
+            const bool pair = nrows > 128;
+            const int tiles = pair ? nt : (nt + 1 - str) >> 1;
+            const int mine = pair ? str * 128 : 0;  // of the item's rows, the stream's first
+            const int gr = x.row0 + r0 + mine + row;
+            const bool live_row = mine + row < nrows, any = mine + q * 32 < nrows;
+            // ---- queries.  Neighbouring threads take neighbouring 16-byte pieces of a row.
+            if (tiles > 0) {
+                constexpr int kPieces = D / 8, kPass = 128 / kPieces;
+                const int t = threadIdx.x & 127, pc = t % kPieces, rr = t / kPieces;
+                const int first = x.row0 + r0 + mine + rr;
+                int si = first / group, sj = first - si * group;
+                const int di = kPass / group, dj = kPass - di * group;
+                uint8_t* dst = sm + L::kQ + str * L::kOperand;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 128 / kPass; i0 += 8) {
+                    uint4 u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        if (mine + rr + (i0 + i) * kPass < nrows)
+                            u[i] = *(const uint4*)(a.q + (size_t)si * a.q_ld + (size_t)(g * group + sj) * D + 8 * pc);
+                        si += di, sj += dj;
+                        if (sj >= group) sj -= group, si++;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++) *(uint4*)(dst + piece_at(pc, rr + (i0 + i) * kPass)) = u[i];
+                }
+                fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_q);
+            const int step_row = x.b < 0 ? 0 : ((gr - x.row0) / group < a.T ? (gr - x.row0) / group : a.T - 1);
+            const uint32_t* see = vis + 4 * step_row;
+            float m = kNoRef, l = 0.f;
+            for (int i = 0; i < tiles; i++, done++) {
+                wait(b_s + str, done);
+                tc_fence_after();
+                if (any) {
+                    const TileInfo ti = info[(n + (pair ? i : 2 * i + str)) & (kInfos - 1)];
+                    const int n32 = (ti.blocks + 1) >> 1;
+                    auto counts = [&](int c) -> uint32_t {  // which of the scores 32 c .. count
+                        const uint32_t code = ti.code[c >> 1] >> (16 * (c & 1));
+                        auto half = [&](uint32_t k) -> uint32_t {
+                            if (k & 128) return see[(k & 127) >> 1] >> (16 * (k & 1)) & 0xffffu;
+                            return (1u << k) - 1u;
+                        };
+                        return half(code & 255) | half(code >> 8 & 255) << 16;
+                    };
+                    uint32_t p[64];
+                    float sum;
+                    bool look = i == 0;
+                    while (true) {
+                        if (look) {
+                            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < n32; c++) {
+                                float y[32];
+                                tmem_ld32(ts + c * 32, y);
+                                const uint32_t k = ti.part ? counts(c) : ~0u;
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    t0 = fmaxf(t0, (k >> j) & 1 ? y[j] : -INFINITY);
+                                    t1 = fmaxf(t1, (k >> j) & 2 ? y[j + 1] : -INFINITY);
+                                }
+                            }
+                            const float top = fmaxf(m, fmaxf(t0, t1) * a.sl2), c = ex2(m - top);
+                            m = top;
+                            l *= c;
+                            if (i > 0) {
+                                // (this tile's scores came behind the last one's products)
+#pragma unroll 1
+                                for (int j = 0; j < D; j += 8) {
+                                    uint32_t o[8];
+                                    tmem_ld8(to + j, o);
+#pragma unroll
+                                    for (int k = 0; k < 8; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
+                                    tmem_st8(to + j, o);
+                                }
+                            }
+                        }
+                        uint64_t s2 = 0;  // two sums
+                        const uint64_t f2 = la::pair(a.sl2, a.sl2), c2 = la::pair(-m, -m);
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            if (c >= n32) break;
+                            float y[32];
+                            tmem_ld32(ts + c * 32, y);
+                            if (ti.part) {
+                                const uint32_t k = counts(c);
+#pragma unroll
+                                for (int j = 0; j < 32; j++)
+                                    if (!((k >> j) & 1)) y[j] = -INFINITY;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                float e0, e1;
+                                unpair(fma2(la::pair(y[j], y[j + 1]), f2, c2), e0, e1);
+                                e0 = ex2(e0), e1 = ex2(e1);
+                                s2 = add2(s2, la::pair(e0, e1));
+                                p[c * 16 + j / 2] = pack_bf16(e0, e1);
+                            }
+                        }
+                        float s0, s1;
+                        unpair(s2, s0, s1);
+                        sum = s0 + s1;
+                        if (look || !__any_sync(0xffffffffu, sum > 32768.f)) break;
+                        look = true;
+                    }
+                    l += sum;
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        if (c < n32) tmem_st16(ts + c * 16, p + c * 16);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p + str);
+            }
+            // ---- the run's result
+            wait(b_o, segs);
+            tc_fence_after();
+            const bool all = run.all();
+            const uint32_t* odd = odds + (segs & 7) * 8;
+            const bool fix = x.b >= 0 && (odd[0] | odd[1] | odd[2] | odd[3] | odd[4] | odd[5] | odd[6] | odd[7]) != 0;
+            float w0 = 1.f, w1 = 0.f;  // of this stream's outputs, and of the other's
+            int c0 = 0, c1 = D;
+            if (!pair) {
+                // both streams' rows are the same: half of the channels each
+                float2* ml = (float2*)(sm + L::kQ);  // (the queries are done with)
+                ml[str * 128 + row] = make_float2(m, l);
+                named_sync(1, 256);
+                const float2 other = ml[(str ^ 1) * 128 + row];
+                const float top = fmaxf(m, other.x);
+                w0 = ex2(m - top), w1 = ex2(other.x - top);
+                l = l * w0 + other.y * w1, m = top;
+                c0 = str * (D / 2), c1 = c0 + D / 2;
+            }
+            if (any) {
+                const bool out = all && s.finish;
+                const float inv = 1.f / l;
+                float* col = nullptr;
+                size_t pitch = 128;
+                if (all) col = (x.b < 0 ? s.whole_pre : s.whole) + (size_t)g * (D + 2) * rows_all + gr, pitch = rows_all;
+                else col = s.slots + ((size_t)blockIdx.x * 2 + run.slot()) * wide_part(D) + (mine ? 128 * (D + 2) : 0) + row;
+                __nv_bfloat16* orow = a.out + ((size_t)(gr / group) * a.H + (size_t)g * group + gr % group) * D;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    tmem_ld32(to + c, o);
+                    if (!pair) {
+                        float u[32];
+                        // (a stream without tiles has weight 0, and whatever is in its outputs' place)
+                        tmem_ld32(trow + kColO + (str ^ 1) * 128 + c, u);
+                        const bool h0 = tiles > 0, h1 = nt > 1 || str == 1;
+#pragma unroll
+                        for (int j = 0; j < 32; j++) o[j] = (h0 ? o[j] * w0 : 0.f) + (h1 ? u[j] * w1 : 0.f);
+                    }
+                    if (fix && live_row) {
+                        float t[32];  // (in memory for the call; o stays in registers)
+#pragma unroll
+                        for (int j = 0; j < 32; j++) t[j] = o[j];
+                        add_odd_to(a, odd, see, x.b, g * D + c, t);
+#pragma unroll
+                        for (int j = 0; j < 32; j++) o[j] = t[j];
+                    }
+                    if (!live_row) continue;
+                    if (out) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *(uint4*)(orow + c + j) = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
+                                                                 pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j++) col[(size_t)(c + j) * pitch] = o[j];  // a line per warp
+                    }
+                }
+                if (!out && live_row && (pair || str == 0)) col[(size_t)D * pitch] = m, col[(size_t)(D + 1) * pitch] = l;
+            }
+            tc_fence_before();
+            if (!pair) named_sync(1, 256);  // the other stream's outputs are read, and the queries' place is free
+            n += nt;
+            segs++;
+        } while (run.next(a, s));
+    } else if (work && warp == 8) {
+        // ---------------------------------------------------------------- MMA
+        constexpr uint32_t id_s = idesc_bf16(128, 0, false), id_o = idesc_bf16(128, D, true);
+        const uint32_t base = smem_u32(sm);
+        const uint64_t dk = desc_sw128_kmajor(base), dv = desc_sw128_mnmajor(base, 128 * 128);
+        const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+        const bool chosen = elect_one();
+        int weighed0 = 0, weighed1 = 0;
+        do {
+            const int nt = run.t1 - run.t0;
+            if (nt <= 0) continue;
+            const int g = run.item / run.x.mt, r0 = (run.item - g * run.x.mt) * kWideRows;
+            const bool pair = min(kWideRows, run.x.rows - r0) > 128;
+            const int jobs = pair ? 2 * nt : nt;  // a tile for a stream: the streams by turns
+            auto scores = [&](int j, int str) {
+                const int tile = n + (pair ? j >> 1 : j), fill = 2 * tile, stage = fill % kSt;
+                wait(b_full + stage, fill / kSt);
+                if (j < 2) wait(b_q, segs);
+                tc_fence_after();
+                const int blocks = info[tile & (kInfos - 1)].blocks;
+                if (chosen && ok) {
+                    const uint32_t id = id_s | (uint32_t)(2 * blocks) << 17, ka = k_lo + ((L::kRing + stage * L::kOperand) >> 4),
+                                   qa = k_lo + ((L::kQ + str * L::kOperand) >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                        mma_ss(tmem + str * 128, qa + at, ka + at, k_hi, id, k > 0);
+                    }
+                    mma_commit(b_s + str);
+                    if (!pair || str) mma_commit(b_empty + stage);
+                }
+                __syncwarp();
+            };
+            scores(0, 0);
+            if (jobs > 1) scores(1, 1);
+#pragma unroll 1
+            for (int j = 0; j < jobs; j++) {
+                const int str = j & 1, tile = n + (pair ? j >> 1 : j), fill = 2 * tile + 1, stage = fill % kSt;
+                wait(b_p + str, str ? weighed1 : weighed0);
+                if (str) weighed1++;
+                else weighed0++;
+                wait(b_vready + (tile & 7), tile >> 3);
+                const int blocks = info[tile & (kInfos - 1)].blocks;
+                tc_fence_after();
+                if (chosen && ok) {
+                    const uint32_t va = v_lo + ((L::kRing + stage * L::kOperand) >> 4), d = tmem + kColO + str * 128, pa = tmem + str * 128;
+                    auto step16 = [&](int k) { mma_ts(d, pa + k * 8, va + ((k * 16 * 128) >> 4), v_hi, id_o, j > 1 || k > 0); };
+                    if (blocks == 8) {
+#pragma unroll
+                        for (int k = 0; k < 8; k++) step16(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < blocks; k++) step16(k);
+                    }
+                    if (!pair || str) mma_commit(b_empty + stage);
+                }
+                __syncwarp();
+                if (j + 2 < jobs) scores(j + 2, str);
+            }
+            if (chosen && ok) mma_commit(b_o);
+            __syncwarp();
+            n += nt;
+            segs++;
+        } while (run.next(a, s));
+        if (!ok && chosen) {
+            // let the products that were issued finish before the memory goes
+            mma_commit(b_end);
+            mbar_drain(b_end, 0);
+        }
+        __syncwarp();
+    } else if (work && warp == 9) {
+        // -------------------------------------------------------------- copies
+        const uint64_t pol = policy_evict_normal();
+        constexpr int kAtoms = L::kAtoms;
+        const int blk = lane / kAtoms, atom = lane % kAtoms;
+        do {
+            if (run.t1 <= run.t0) continue;
+            const Entry& x = run.x;
+            const int g = run.item / x.mt, nc = x.nb_cached();
+            // block kb's page (its table entry is looked up a tile ahead)
+            auto page_of = [&](int kb) {
+                if (blk >= 8 || kb >= nc) return 0;
+                const bool own = kb >= x.nb_pre;
+                const int at = (own ? kb - x.nb_pre : kb) * 16 >> a.page_log2;
+                return own ? a.table[(size_t)x.b * a.max_pages + at] : a.ptable[(size_t)x.p * a.pp + at];
+            };
+            int next = page_of(run.t0 * 8 + blk);
+            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+                const int kb = tile * 8 + blk, page = next, blocks = min(8, x.nb - tile * 8);
+                if (tile + 1 < run.t1) next = page_of(kb + 8);
+                const bool mine = blk < blocks, cached = mine && kb < nc, own = kb >= x.nb_pre;
+                const bool bad = cached && (unsigned)page >= (unsigned)a.n_pages;
+                const int tok = (own ? kb - x.nb_pre : kb) * 16, live = cached ? min(16, (own ? x.len : x.plen) - tok) : min(16, a.T - (kb - nc) * 16);
+                const uint32_t code = !mine || bad ? 0u : cached ? (uint32_t)live : 128u + (kb - nc);
+                const uint32_t mask = atom == 0 && blk < 8 ? code << (8 * (blk & 3)) : 0u;
+                const uint32_t lo = __reduce_or_sync(0xffffffffu, blk < 4 ? mask : 0u), hi = __reduce_or_sync(0xffffffffu, blk < 4 ? 0u : mask);
+                const bool part = __any_sync(0xffffffffu, blk < 8 && code != 16);
+                const int boxes = __popc(__ballot_sync(0xffffffffu, mine && !bad));
+                const int cx = (cached ? 0 : g * D) + atom * 64;
+                const int cy = cached ? (int)((((long long)page * a.Hkv + g) << a.page_log2) + (tok & ((1 << a.page_log2) - 1)))
+                                      : x.b * a.T + (kb - nc) * 16;
+                if (bad) kv4_raise(a.status, LA_ERR_ARG);
+#pragma unroll
+                for (int v = 0; v < 2; v++) {
+                    const int fill = 2 * n + v, stage = fill % kSt;
+                    if (fill >= kSt) wait(b_empty + stage, fill / kSt - 1);
+                    if (!__all_sync(0xffffffffu, ok)) continue;
+                    if (lane == 0) {
+                        if (v == 0) {
+                            TileInfo* ti = info + (n & (kInfos - 1));
+                            ti->code[0] = lo, ti->code[1] = hi, ti->blocks = blocks, ti->part = part;
+                        }
+                        mbar_expect_tx(b_full + stage, boxes * 2048);
+                    }
+                    __syncwarp();
+                    if (mine && !bad)
+                        tma_load_2d(cached ? (v ? &maps.vp : &maps.kp) : (v ? &maps.vs : &maps.ks), b_full + stage,
+                                    sm + L::kRing + stage * L::kOperand + atom * (128 * 128) + blk * 2048, cx, cy, pol);
+                    __syncwarp();
+                }
+            }
+        } while (run.next(a, s));
+        // no copy may still be on its way when the CTA ends
+        for (int i = 1; i <= kSt && i <= 2 * n; i++) mbar_drain(b_full + (2 * n - i) % kSt, ((2 * n - i) / kSt) & 1);
+    } else if (work) {
+        // ------------------------------------------------------- values cleared
+        const int me = warp - 10;
+        do {
+            if (run.t1 <= run.t0) continue;
+            uint32_t* odd = odds + (segs & 7) * 8 + me * 4;
+            if (lane < 4) odd[lane] = 0;
+            __syncwarp();
+            for (int tile = run.t0; tile < run.t1; tile++, n++) {
+                const int fill = 2 * n + 1, stage = fill % kSt;
+                wait(b_full + stage, fill / kSt);
+                const TileInfo ti = info[n & (kInfos - 1)];
+                if (ti.part && ok) {
+                    uint8_t* v = sm + L::kRing + stage * L::kOperand;
+                    for (int blk = me; blk < ti.blocks; blk += 2) {
+                        const uint32_t code = ti.code[blk >> 2] >> (8 * (blk & 3)) & 255;
+                        const bool step = code & 128;
+                        const int j0 = (code & 127) * 16, live = step ? min(16, a.T - j0) : (int)code;
+                        if (live == 16 && (!step || a.T == 1)) continue;
+#pragma unroll
+                        for (int i = 0; i < 4 * L::kAtoms; i++) {
+                            const int piece = lane + 32 * i, r = (piece >> 3) & 15;
+                            uint4* at = (uint4*)(v + (piece >> 7) * (128 * 128) + blk * 2048 + (piece & 127) * 16);
+                            if (r >= live) *at = make_uint4(0, 0, 0, 0);
+                            else if (step && a.T > 1) {
+                                const uint4 u = *at;
+                                uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                                bool found = false;
+#pragma unroll
+                                for (int k = 0; k < 4; k++) {
+                                    const bool b0 = (w[k] & 0x7f80u) == 0x7f80u, b1 = (w[k] & 0x7f800000u) == 0x7f800000u;
+                                    if (b0) w[k] &= 0xffff0000u;
+                                    if (b1) w[k] &= 0x0000ffffu;
+                                    found |= b0 || b1;
+                                }
+                                if (found) {
+                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                    atomicOr(&odd[(j0 + r) >> 5], 1u << ((j0 + r) & 31));
+                                }
+                            }
+                        }
+                    }
+                    fence_proxy_async();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_vready + (n & 7));
+            }
+            segs++;
+        } while (run.next(a, s));
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? (PFN_cuTensorMapEncodeTiled_v12000)p : nullptr;
+    }();
+    return fn;
+}
+
+// A map over rows `ld` elements apart, boxes of 64 channels x 16 rows, 128-byte
+// swizzle; rows past the last read as zeros.
+bool encode(CUtensorMap* m, const void* base, long long rows, int cols, size_t ld)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int kv16_wide_teams() { return kSMs; }
+
+bool kv16_wide_init()
+{
+    return encode_fn() && cudaFuncSetAttribute(k_kv16_wide<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem<128>::kBytes) == cudaSuccess &&
+           cudaFuncSetAttribute(k_kv16_wide<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem<64>::kBytes) == cudaSuccess;
+}
+
+int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D, int rows_all)
+{
+    Maps m;
+    const long long rows = (long long)a.n_pages * a.Hkv << a.page_log2, steps = (long long)a.B * a.T;
+    if (rows >= 1LL << 31) return LA_ERR_ARG;  // (more than the card holds)
+    if (!encode(&m.kp, a.kp, rows, D, D) || !encode(&m.vp, a.vp, rows, D, D) || !encode(&m.ks, a.ks, steps, a.Hkv * D, a.k_ld) ||
+        !encode(&m.vs, a.vs, steps, a.Hkv * D, a.v_ld))
+        return LA_ERR_CUDA;
+    const dim3 grid(w.nteams), block(kThreads);
+    const cudaError_t e = D == 128 ? launch_pdl(k_kv16_wide<128>, grid, block, WideSmem<128>::kBytes, s, a, w, m, rows_all)
+                                   : launch_pdl(k_kv16_wide<64>, grid, block, WideSmem<64>::kBytes, s, a, w, m, rows_all);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+}  // namespace la
