@@ -23,10 +23,13 @@ struct Kv16Attn {
     float sl2;                // log2(e) / sqrt(D)
 };
 
-// Of a schedule, once it is known (on the device, for the merge).
-struct Kv16Shares {
-    long long q;              // team t begins at unit q t + min(t, r)
-    int r, nteams, whole, pad;  // whole: a unit is a whole item; nteams 0: nothing to do
+// An item whose parts are to be joined, left by the team that begins it.
+struct alignas(16) Kv16Item {
+    int t0, n;        // the teams that have a part, one after the other (n 0: none)
+    int row, rows;    // its first row (among all sequences' rows of its KV head), and how many
+    int g;            // KV head
+    int pre_row;      // first row of the sequence's prefix (-1: none)
+    int pad[2];
 };
 
 // How one kernel's teams share its entries (prefixes, then sequences), and
@@ -37,11 +40,14 @@ struct Kv16Sched {
     int blk_log2;             // blocks of 16 keys in a tile
     int wide;                 // with more rows than these an entry's tiles count twice
     int extra;                // units an item counts for beyond its tiles
-    int nteams, min_run, slack;
+    int nteams, per_cta;      // teams; of a CTA
+    int min_run, slack;
+    int direct;               // team t has item t: all items are sequences', and there is a team for each
     int finish;               // whole items go to the output (else to `whole`)
     int first;                // the call's first kernel
-    Kv16Shares* shares;
-    long long* base;          // [entries]: units before each
+    int beside;               // the other kernel's items run at the same time: the SMs are shared by their work
+    Kv16Item* items;          // finish: [nteams]; else [KV heads][rows]: of prefixes, then of sequences
+    int* bad;                 // prefix_first is out of order: nothing is done
     float* slots;             // [nteams][2]: parts of split items
     float *whole, *whole_pre; // by row: results of sequences' and of prefixes' whole items
 };

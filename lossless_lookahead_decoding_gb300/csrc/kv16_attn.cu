@@ -23,7 +23,16 @@ int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int 
 namespace {
 // ------------------------------------------------------------------- merge ---
 
-constexpr int kMergeRows = 8, kMergeThreads = 512;
+constexpr int kMergeRows = 8, kMaxGroups = 4;
+
+struct MergeArgs {
+    Kv16Attn a;
+    const Kv16Item* items;
+    const int* bad;
+    const float *slots_pre, *slots_seq, *whole_pre, *whole_seq;
+    int rows_pre_tile;        // rows of a prefix's item
+    int by_rows;              // sequences' parts are rows (k_kv16_rows), else columns
+};
 
 struct Sum {
     float top, l, o[4];
@@ -37,36 +46,12 @@ struct Sum {
     }
 };
 
-// Row r of entry x and KV head g, of which every `step`-th part from `first`
-// is added to y; false: nothing is to be done for this row (the item's team
-// has written its output, or nobody works on it).
+// Of the parts of teams t0 .. t0 + n - 1, every `step`-th from `first` is added
+// to y: row r of their item, channels ch .. ch + 3.
 template <int D>
-__device__ __forceinline__ bool add_parts(const Kv16Attn& a, const Kv16Sched& s, const float* whole, bool by_rows, int e, const Entry& x,
-                                          int g, int r, int rows_all, int ch, int first, int step, Sum& y)
+__device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots, bool by_rows, int t0, int n, int r, int ch, int first,
+                                          int step, Sum& y)
 {
-    const Kv16Shares h = *s.shares;
-    if (h.nteams == 0 || x.nu == 0) return false;
-    const int mt = r / s.row_tile, rr = r - mt * s.row_tile, nu = h.whole ? 1 : x.nu, gr = x.row0 + r;
-    const long long u0 = s.base[e] + ((long long)g * x.mt + mt) * nu;
-    const int t0 = team_of(h, u0), n = team_of(h, u0 + nu - 1) - t0 + 1;
-    if (n == 1) {
-        if (s.finish) return false;
-        if (first) return true;
-        float v[4];
-        if (by_rows) {
-            const size_t at = (size_t)g * rows_all + gr;
-            const float4 o = *(const float4*)(whole + at * D + ch);
-            const float2 ml = *(const float2*)(whole + (size_t)a.Hkv * rows_all * D + 2 * at);
-            v[0] = o.x, v[1] = o.y, v[2] = o.z, v[3] = o.w;
-            y.add(ml.x, ml.y, v);
-        } else {
-            const float* col = whole + (size_t)g * (D + 2) * rows_all + gr;
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = col[(size_t)(ch + i) * rows_all];
-            y.add(col[(size_t)D * rows_all], col[(size_t)(D + 1) * rows_all], v);
-        }
-        return true;
-    }
     constexpr int kBatch = 4;
 #pragma unroll 1
     for (int k0 = first; k0 < n; k0 += kBatch * step) {
@@ -76,79 +61,132 @@ __device__ __forceinline__ bool add_parts(const Kv16Attn& a, const Kv16Sched& s,
             m[j] = kNoRef, l[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; i++) v[j][i] = 0.f;
-            const int k = k0 + j * step, t = t0 + k;
+            const int k = k0 + j * step;
             if (k >= n) continue;
-            const int f = (int)max(0LL, units_at(h, t) - u0), b = (int)min((long long)nu, units_at(h, t + 1) - u0);
-            if (tile_at(s, x, b) <= tile_at(s, x, f)) continue;  // no keys, no part
-            const size_t slot = (size_t)t * 2 + (f == 0);
+            const size_t slot = (size_t)(t0 + k) * 2 + (k == 0);
             if (by_rows) {
-                const float* part = s.slots + slot * rows_part(D, a.R);
-                const float4 o = *(const float4*)(part + (size_t)rr * D + ch);
-                const float2 ml = *(const float2*)(part + (size_t)a.R * D + 2 * rr);
+                const float* part = slots + slot * rows_part(D, a.R);
+                const float4 o = *(const float4*)(part + (size_t)r * D + ch);
+                const float2 ml = *(const float2*)(part + (size_t)a.R * D + 2 * r);
                 m[j] = ml.x, l[j] = ml.y, v[j][0] = o.x, v[j][1] = o.y, v[j][2] = o.z, v[j][3] = o.w;
             } else {
-                const float* col = s.slots + slot * wide_part(D) + (rr >> 7) * (128 * (D + 2)) + (rr & 127);
+                const float* col = slots + slot * wide_part(D) + (r >> 7) * (128 * (D + 2)) + (r & 127);
                 m[j] = col[D * 128], l[j] = col[(D + 1) * 128];
 #pragma unroll
                 for (int i = 0; i < 4; i++) v[j][i] = col[(ch + i) * 128];
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; j++) y.add(m[j], l[j], v[j]);
-    }
-    return true;
-}
-
-// A CTA: 8 rows of a KV head; a warp: 16 of their channels and every kGroups-th
-// part (8 rows x 4 lanes of 4 channels: whole sectors of either kind of part).
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) k_kv16_merge(const __grid_constant__ Kv16Attn a, const __grid_constant__ Kv16Merge w)
-{
-    constexpr int kSlices = D / 16, kGroups = kMergeThreads / 32 / kSlices;
-    __shared__ float sums[kGroups - 1][6][kSlices * 32];
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
-    const int gr = blockIdx.x * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, g = blockIdx.y;
-    Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
-    bool live = false;
-    if (gr < w.rows_all) {
-        const int b = gr / a.R, es = w.seq.n_pre + b;
-        const Entry x = entry_of(a, w.seq, es);
-        live = x.nu > 0 && add_parts<D>(a, w.seq, w.seq.whole, w.seq_rows, es, x, g, gr - x.row0, w.rows_all, ch, part, kGroups, y);
-        if (live && w.pre.n_pre && x.p >= 0) {
-            const Entry p = entry_of(a, w.pre, x.p);
-            if (p.nu > 0) add_parts<D>(a, w.pre, w.pre.whole_pre, false, x.p, p, g, gr - p.row0, w.rows_all, ch, part, kGroups, y);
+        for (int j = 0; j < kBatch; j++) {
+            // (a part without keys has no outputs, whatever is in their place)
+            if (m[j] == kNoRef && l[j] == 0.f)
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[j][i] = 0.f;
+            y.add(m[j], l[j], v[j]);
         }
     }
-    if (!__syncthreads_or(live)) return;
+}
+
+// The groups of warps that took different parts meet; the result goes out.
+template <int D>
+__device__ __forceinline__ void finish_rows(const Kv16Attn& a, Sum& y, bool live, int part, int groups, int at, int g, int gr, int ch)
+{
+    constexpr int kWide = D / 16 * 32;
+    __shared__ float sums[kMaxGroups - 1][6][kWide];
     if (part) {
-        float* to = &sums[part - 1][0][slice * 32 + lane];
-        to[0] = y.top, to[kSlices * 32] = y.l;
+        float* to = &sums[part - 1][0][at];
+        to[0] = y.top, to[kWide] = y.l;
 #pragma unroll
-        for (int i = 0; i < 4; i++) to[(2 + i) * kSlices * 32] = y.o[i];
+        for (int i = 0; i < 4; i++) to[(2 + i) * kWide] = y.o[i];
     }
-    __syncthreads();
+    if (groups > 1) __syncthreads();
     if (part || !live) return;
-#pragma unroll
-    for (int k = 0; k < kGroups - 1; k++) {
-        const float* from = &sums[k][0][slice * 32 + lane];
+#pragma unroll 1
+    for (int k = 0; k < groups - 1; k++) {
+        const float* from = &sums[k][0][at];
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = from[(2 + i) * kSlices * 32];
-        y.add(from[0], from[kSlices * 32], v);
+        for (int i = 0; i < 4; i++) v[i] = from[(2 + i) * kWide];
+        y.add(from[0], from[kWide], v);
     }
     const float inv = 1.f / y.l;
     __nv_bfloat16* dst = a.out + ((size_t)(gr / a.group) * a.H + (size_t)g * a.group + gr % a.group) * D + ch;
     *(uint2*)dst = make_uint2(pack_bf16(y.o[0] * inv, y.o[1] * inv), pack_bf16(y.o[2] * inv, y.o[3] * inv));
 }
 
+// Joins the parts of items that several teams hold.  A CTA: 8 rows of the item
+// that team blockIdx.x begins; a warp: 16 of their channels and every groups-th
+// part (8 rows x 4 lanes of 4 channels: whole sectors of either kind of part).
+template <int D>
+__global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_merge(const __grid_constant__ MergeArgs w)
+{
+    constexpr int kSlices = D / 16;
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
+    const int r = blockIdx.y * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, groups = blockDim.x / (kSlices * 32);
+    const Kv16Item it = w.items[blockIdx.x];
+    if (it.n == 0 || (int)blockIdx.y * kMergeRows >= it.rows) return;
+    const bool live = r < it.rows;
+    Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    if (live) add_parts<D>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r, ch, part, groups, y);
+    finish_rows<D>(w.a, y, live, part, groups, slice * 32 + lane, it.g, it.row + r, ch);
+}
+
+// Joins every row's own keys and its prefix's.  A CTA: 8 rows of a KV head.
+template <int D>
+__global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_constant__ MergeArgs w)
+{
+    constexpr int kSlices = D / 16;
+    pdl_wait();
+    pdl_trigger();
+    const Kv16Attn& a = w.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
+    const int gr = blockIdx.x * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, g = blockIdx.y, rows_all = a.B * a.R;
+    const int groups = blockDim.x / (kSlices * 32);
+    Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    bool live = gr < rows_all && !*w.bad;
+    if (live) {
+        const int row0 = gr / a.R * a.R;
+        const Kv16Item it = w.items[(size_t)(a.Hkv + g) * rows_all + row0];
+        live = it.n > 0;
+        auto add_whole = [&](const float* whole, bool by_rows) {
+            float v[4];
+            if (by_rows) {
+                const size_t at = (size_t)g * rows_all + gr;
+                const float4 o = *(const float4*)(whole + at * D + ch);
+                const float2 ml = *(const float2*)(whole + (size_t)a.Hkv * rows_all * D + 2 * at);
+                v[0] = o.x, v[1] = o.y, v[2] = o.z, v[3] = o.w;
+                y.add(ml.x, ml.y, v);
+            } else {
+                const float* col = whole + (size_t)g * (D + 2) * rows_all + gr;
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] = col[(size_t)(ch + i) * rows_all];
+                y.add(col[(size_t)D * rows_all], col[(size_t)(D + 1) * rows_all], v);
+            }
+        };
+        if (live) {
+            if (it.n > 1) add_parts<D>(a, w.slots_seq, w.by_rows, it.t0, it.n, gr - row0, ch, part, groups, y);
+            else if (part == 0) add_whole(w.whole_seq, w.by_rows);
+            if (it.pre_row >= 0) {
+                const int first = it.pre_row + (gr - it.pre_row) / w.rows_pre_tile * w.rows_pre_tile;
+                const Kv16Item p = w.items[(size_t)g * rows_all + first];
+                if (p.n > 1) add_parts<D>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
+                else if (part == groups - 1) add_whole(w.whole_pre, false);
+            }
+        }
+    }
+    finish_rows<D>(a, y, live, part, groups, slice * 32 + lane, g, gr, ch);
+}
+
 // -------------------------------------------------------------------- plan ---
 
 struct Plan {
     Kv16Attn k;
-    Kv16Merge w;
-    bool rows, wide, merge;
+    Kv16Sched wide, rows;
+    MergeArgs m;
+    bool use_wide, use_rows, apart, merge;
+    int teams, row_tile, groups;  // of the merge
     size_t bytes;
 };
 
@@ -166,8 +204,7 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     k.nP = a.n_prefix, k.pp = a.prefix_pages;
     k.max_plen = a.n_prefix ? bound(a.max_prefix_len, a.prefix_pages * c.page) : 0;
     k.sl2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
-    k.concat = 1;
-    const int D = c.head_dim;
+    const int D = c.head_dim, rows_all = k.B * k.R;
     auto blocks = [](int n) { return (n + 15) / 16; };
     size_t at = 0;
     auto room = [&](size_t bytes) {
@@ -175,58 +212,67 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
         at += (bytes + 255) / 256 * 256;
         return x;
     };
-    p.w.rows_all = k.B * k.R;
-    const size_t all = (size_t)k.Hkv * p.w.rows_all * (D + 2) * 4;  // results of whole items
     // A prefix by itself, for all of its sequences at once, where reading it for each would cost
     // more than the further launches and parts (these bytes come from L2 at 8 TB/s: 2 us), and
     // where a sequence has too few rows to fill a tile.
     const long long again = (long long)k.B * k.Hkv * k.max_plen * D * 4;
-    const bool apart = k.B > 1 && k.R <= 64 && again > (16 << 20);
-    k.concat = !apart;
-    p.rows = k.R <= 16;
-    p.wide = !p.rows || apart;
-    p.merge = apart;
-    auto notes = [&](Kv16Sched& s, size_t part) {
-        s.shares = (Kv16Shares*)room(sizeof(Kv16Shares)), s.base = (long long*)room(8 * (size_t)(s.n_pre + s.n_seq));
-        s.slots = (float*)room((size_t)s.nteams * 2 * part);
-    };
-    if (p.wide) {
-        Kv16Sched& s = p.w.pre;
-        s.n_pre = apart ? k.nP : 0, s.n_seq = p.rows ? 0 : k.B;
+    p.apart = k.B > 1 && k.R <= 64 && again > (16 << 20);
+    k.concat = !p.apart;
+    p.use_rows = k.R <= 16;
+    p.use_wide = !p.use_rows || p.apart;
+    // ---- who begins where
+    const int most = blocks(k.max_len) + (p.apart ? 0 : blocks(k.max_plen)) + blocks(k.T);  // blocks of a sequence, at most
+    if (p.use_wide) {
+        Kv16Sched& s = p.wide;
+        s.n_pre = p.apart ? k.nP : 0, s.n_seq = p.use_rows ? 0 : k.B;
         s.row_tile = kWideRows, s.blk_log2 = 3, s.wide = 128, s.extra = 4;
-        s.nteams = kv16_wide_teams(), s.min_run = 6, s.slack = 12;
-        s.finish = !apart, s.first = 1;
+        s.nteams = kv16_wide_teams(), s.per_cta = 1, s.min_run = 6, s.slack = 12;
         const long long items = (long long)k.B * k.Hkv * ((k.R + kWideRows - 1) / kWideRows);
-        const int most = (blocks(k.max_len) + blocks(k.max_plen) + blocks(k.T) + 7) / 8 * (k.R > 128 ? 2 : 1);
-        if (!apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.slack = 1 << 30;
-        else {
-            p.merge = true;
-            notes(s, wide_part(D) * 4);
-        }
-        if (apart) {
-            s.whole_pre = (float*)room(all);
-            if (!p.rows) s.whole = (float*)room(all);
-        }
-        if (!p.rows) p.w.seq = s;
-        if (!apart) p.w.pre.n_pre = 0;
+        if (!p.apart && items <= s.nteams && (most + 7) / 8 * (k.R > 128 ? 2 : 1) <= s.slack) s.nteams = (int)items, s.direct = 1;
     }
-    if (p.rows) {
-        Kv16Sched& s = p.w.seq;
+    if (p.use_rows) {
+        Kv16Sched& s = p.rows;
         s.n_seq = k.B, s.row_tile = 16, s.wide = 1 << 30, s.extra = 2;
         const long long items = (long long)k.B * k.Hkv;
-        const int most = blocks(k.max_len) + blocks(k.max_plen) + 1;  // blocks of an item, at most
-        s.nteams = kv16_rows_teams(), s.min_run = 16, s.slack = 16;
-        s.finish = !apart, s.first = !apart;
-        if (!apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.slack = 1 << 30;
-        else {
-            p.merge = true;
-            notes(s, rows_part(D, k.R) * 4);
-        }
-        if (apart) s.whole = (float*)room(all);
-        p.w.seq_rows = 1;
+        s.nteams = kv16_rows_teams(), s.per_cta = kv16_rows_teams() / kSMs, s.min_run = 16, s.slack = 16;
+        if (!p.apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.direct = 1;
     }
+    // ---- where their results go
+    Kv16Sched& last = p.use_rows ? p.rows : p.wide;
+    (p.use_wide ? p.wide : p.rows).first = 1;
+    const size_t all = (size_t)k.Hkv * rows_all * (D + 2) * 4;  // results of whole items
+    if (p.apart) {
+        p.m.bad = (int*)room(4);
+        p.m.items = (Kv16Item*)room(2 * (size_t)k.Hkv * rows_all * sizeof(Kv16Item));
+        p.m.whole_pre = (float*)room(all), p.m.whole_seq = (float*)room(all);
+        p.wide.beside = p.rows.beside = p.use_rows;
+    } else {
+        if (!last.direct) p.m.items = (Kv16Item*)room(last.nteams * sizeof(Kv16Item));
+        last.finish = 1;
+    }
+    if (p.use_wide && !p.wide.direct) p.wide.slots = (float*)room((size_t)p.wide.nteams * 2 * wide_part(D) * 4);
+    if (p.use_rows && !p.rows.direct) p.rows.slots = (float*)room((size_t)p.rows.nteams * 2 * rows_part(D, k.R) * 4);
+    for (Kv16Sched* s : {&p.wide, &p.rows}) {
+        s->items = (Kv16Item*)p.m.items, s->bad = (int*)p.m.bad;
+        s->whole = (float*)p.m.whole_seq, s->whole_pre = (float*)p.m.whole_pre;
+    }
+    p.m.slots_pre = p.wide.slots, p.m.slots_seq = last.slots;
+    p.m.rows_pre_tile = kWideRows, p.m.by_rows = p.use_rows;
+    p.merge = !last.direct;
+    p.teams = last.nteams, p.row_tile = std::min(last.row_tile, k.R);
+    // as many groups of warps as an item may have fours of parts
+    const long long parts = (p.use_wide ? p.wide.nteams : p.rows.nteams) / std::max(1LL, (long long)k.Hkv * (p.apart ? (rows_all + 255) / 256 : k.B));
+    p.groups = parts >= 12 ? 4 : parts >= 6 ? 2 : 1;
     p.bytes = at;
     return p;
+}
+
+template <int D>
+cudaError_t launch_merge(cudaStream_t s, const Plan& p)
+{
+    const dim3 block(D * 2 * p.groups);
+    if (p.apart) return launch_pdl(k_kv16_join<D>, dim3((p.k.B * p.k.R + kMergeRows - 1) / kMergeRows, p.k.Hkv), block, 0, s, p.m);
+    return launch_pdl(k_kv16_merge<D>, dim3(p.teams, (p.row_tile + kMergeRows - 1) / kMergeRows), block, 0, s, p.m);
 }
 
 bool init()
@@ -252,17 +298,14 @@ int launch_kv16_attn(cudaStream_t s, const la_kv16_desc& c, const la_kv16_attn& 
     k.plens = a.prefix_lens, k.ptable = a.prefix_table, k.pfirst = a.prefix_first;
     k.kp = (const __nv_bfloat16*)c.k_pages, k.vp = (const __nv_bfloat16*)c.v_pages;
     k.q_ld = a.q_ld, k.k_ld = a.k_ld, k.v_ld = a.v_ld;
+    p.m.a = k;
     const int D = c.head_dim;
-    if (p.wide) {
-        const int rc = launch_kv16_wide(s, k, p.w.pre, D, p.w.rows_all);
+    if (p.use_wide) {
+        const int rc = launch_kv16_wide(s, k, p.wide, D, k.B * k.R);
         if (rc != LA_OK) return rc;
     }
-    cudaError_t e = cudaSuccess;
-    if (p.rows) e = launch_kv16_rows(s, k, p.w.seq, D);
-    if (e == cudaSuccess && p.merge) {
-        const dim3 grid((p.w.rows_all + kMergeRows - 1) / kMergeRows, k.Hkv), block(kMergeThreads);
-        e = D == 128 ? launch_pdl(k_kv16_merge<128>, grid, block, 0, s, k, p.w) : launch_pdl(k_kv16_merge<64>, grid, block, 0, s, k, p.w);
-    }
+    cudaError_t e = p.use_rows ? launch_kv16_rows(s, k, p.rows, D) : cudaSuccess;
+    if (e == cudaSuccess && p.merge) e = D == 128 ? launch_merge<128>(s, p) : launch_merge<64>(s, p);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

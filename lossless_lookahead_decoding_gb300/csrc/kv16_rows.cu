@@ -31,7 +31,7 @@ struct RowsSmem {
     static constexpr int kRing = kWarps * kStages * 2 * kSide;
     static constexpr int kInfo = kRing;                    // of each stage: keys | step << 8
     static constexpr int kMisc = kInfo + kWarps * kStages * 4;
-    static constexpr int kBytes = (kMisc + 7) / 8 * 8 + (int)sizeof(Scan) + kWarps * (int)sizeof(Start);
+    static constexpr int kBytes = (kMisc + 7) / 8 * 8 + (int)sizeof(Scan) + kWarps * (int)sizeof(Start) + (int)sizeof(PreShared);
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -78,12 +78,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
     extern __shared__ __align__(16) uint8_t sm[];
     Scan* sc = (Scan*)(sm + (L::kMisc + 7) / 8 * 8);
     Start* starts = (Start*)(sc + 1);
+    PreShared* ps = (PreShared*)(starts + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     // As the call's second kernel it needs nothing of the first, whose CTAs have all seen the calls before it end.
     if (s.first) pdl_wait();
     pdl_trigger();
-    find_starts(a, s, blockIdx.x * kWarps, kWarps, starts, sc);
-    const Kv16Shares sh = sc->shares;
+    const Prefixes pre = find_starts<D>(a, s, starts, sc, ps);
+    const Shares sh = sc->shares;
+    const int team = blockIdx.x * kWarps + warp;
+    if (s.finish && s.items && lane == 0 && team < s.nteams) s.items[team].n = 0;
     const Start st = starts[warp];
     if (st.count > 0) {
         const uint32_t ring = smem_u32(sm) + warp * (L::kStages * 2 * L::kSide);
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
 
         // ---- feeding
         Run f;
-        f.begin(a, s, st, sh);
+        f.begin(a, s, pre, st, sh);
         bool feeding = true;
         int fk = f.t0, stage_in = 0, window = -1, page_of = 0;
         auto start_feed = [&]() {
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
         auto feed = [&]() {
             while (feeding && fk >= f.t1) {
                 const int e = f.e;
-                feeding = f.next(a, s);
+                feeding = f.next(a, s, pre);
                 if (!feeding) break;
                 if (f.e != e) window = -1;
                 start_feed();
@@ -174,9 +177,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
         const uint32_t k_at = krow * (D * 2), v_at = L::kSide + vrow * (D * 2);
         int stage = 0;
         Run c;
-        c.begin(a, s, st, sh);
+        c.begin(a, s, pre, st, sh);
         do {
-            if (c.t1 <= c.t0) continue;
+            if (c.t1 <= c.t0) {
+                // (units, but no keys)
+                if (c.x.nu && lane == 0) c.note(a, s, pre, sh, team);
+                if (c.x.nu && lane < a.R)
+                    *(float2*)(s.slots + ((size_t)team * 2 + c.slot()) * rows_part(D, a.R) + (size_t)a.R * D + 2 * lane) = make_float2(kNoRef, 0.f);
+                continue;
+            }
             const int g = c.item;
             uint32_t q[kSteps][4];
             {
@@ -313,6 +322,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
             la += __shfl_xor_sync(0xffffffffu, la, 1), lb += __shfl_xor_sync(0xffffffffu, lb, 1);
             la += __shfl_xor_sync(0xffffffffu, la, 2), lb += __shfl_xor_sync(0xffffffffu, lb, 2);
             const bool all = c.all();
+            if (lane == 0) c.note(a, s, pre, sh, team);
 #pragma unroll
             for (int half = 0; half < 2; half++) {
                 const int r = half ? rb : ra;
@@ -329,14 +339,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                     // by row: [rows][D], then [rows][M, sum]
                     const size_t rows = all ? (size_t)a.B * a.R * a.Hkv : a.R;
                     const size_t at = all ? (size_t)g * a.B * a.R + c.x.row0 + r : r;
-                    float* part = all ? s.whole : s.slots + ((size_t)(blockIdx.x * kWarps + warp) * 2 + c.slot()) * rows_part(D, a.R);
+                    float* part = all ? s.whole : s.slots + ((size_t)team * 2 + c.slot()) * rows_part(D, a.R);
                     float* dst = part + at * D + 2 * tig;
 #pragma unroll
                     for (int i = 0; i < D / 8; i++) *(float2*)(dst + 8 * i) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
                     if (tig == 0) *(float2*)(part + rows * D + 2 * at) = make_float2(m, l);
                 }
             }
-        } while (c.next(a, s));
+        } while (c.next(a, s, pre));
         cp_wait<0>();
     }
     // (its end says that the first kernel's work is done, too)

@@ -28,38 +28,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 __device__ __forceinline__ int blocks_of(int n) { return (n + 15) >> 4; }
 
+// The prefixes' bounds and lengths, copied to shared memory where they fit.
+struct Prefixes {
+    const int *first, *lens;
+};
+
 // The prefix of sequence b, or -1.
-__device__ __forceinline__ int prefix_of(const Kv16Attn& a, int b)
+__device__ __forceinline__ int prefix_of(const Kv16Attn& a, const Prefixes& pre, int b)
 {
-    int lo = -1, hi = a.nP;  // pfirst[lo] <= b < pfirst[hi], taking the ends as -inf and inf
+    int lo = -1, hi = a.nP;  // first[lo] <= b < first[hi], taking the ends as -inf and inf
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.pfirst[mid] <= b) lo = mid;
+        if (pre.first[mid] <= b) lo = mid;
         else hi = mid;
     }
-    return lo >= 0 && b < a.pfirst[lo + 1] ? lo : -1;
+    return lo >= 0 && b < pre.first[lo + 1] ? lo : -1;
 }
 
 struct Entry {
     int rows, row0;    // rows of a KV head (0: nothing to do), the first of them among all sequences'
-    int b, p;          // sequence (-1: a prefix's entry); prefix whose tokens come first (-1: none)
+    int b, p;          // sequence (-1: a prefix's entry); prefix (-1: none)
     int plen, len;     // tokens
     int nb_pre, nb;    // blocks: the prefix's, all
     int wide, tiles, mt, nu;  // does a tile count twice; tiles; row tiles; an item's units
     __device__ __forceinline__ int nb_cached() const { return nb_pre + blocks_of(len); }
 };
 
-__device__ __forceinline__ Entry entry_of(const Kv16Attn& a, const Kv16Sched& s, int e)
+// An entry; n: the sequence's own tokens (not looked at for a prefix's entry).
+__device__ __forceinline__ Entry entry_with(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, int e, int n)
 {
     Entry x;
     x.plen = x.len = x.rows = x.row0 = x.nb = 0;
     if (e < s.n_pre) {
-        const int lo = a.pfirst[e], n = a.plens[e];
+        const int lo = pre.first[e], m = pre.lens[e];
         x.b = -1, x.p = e;
-        if (n > 0 && n <= a.max_plen) x.plen = n, x.rows = (a.pfirst[e + 1] - lo) * a.R, x.row0 = lo * a.R;
+        if (m > 0 && m <= a.max_plen) x.plen = m, x.rows = (pre.first[e + 1] - lo) * a.R, x.row0 = lo * a.R;
     } else {
-        const int b = e - s.n_pre, n = a.lens[b], p = a.nP ? prefix_of(a, b) : -1, pn = p >= 0 ? a.plens[p] : 0;
-        x.b = b, x.p = p, x.row0 = b * a.R;
+        const int b = e - s.n_pre, p = a.nP ? prefix_of(a, pre, b) : -1, pn = p >= 0 ? pre.lens[p] : 0;
+        x.b = b, x.p = pn > 0 ? p : -1, x.row0 = b * a.R;
         if (n >= 0 && n <= a.max_len && pn <= a.max_plen) {
             x.len = n, x.rows = a.R, x.nb = blocks_of(a.T);
             if (a.concat && pn > 0) x.plen = pn;
@@ -74,10 +80,13 @@ __device__ __forceinline__ Entry entry_of(const Kv16Attn& a, const Kv16Sched& s,
     return x;
 }
 
+__device__ __forceinline__ Entry entry_of(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, int e)
+{
+    return entry_with(a, s, pre, e, e < s.n_pre ? 0 : a.lens[e - s.n_pre]);
+}
+
 // The first tile at or behind unit u of an item.
 __device__ __forceinline__ int tile_at(const Kv16Sched& s, const Entry& x, int u) { return max(u - s.extra + x.wide, 0) >> x.wide; }
-
-__device__ __forceinline__ long long units_at(const Kv16Shares& h, int t) { return h.q * t + min(t, h.r); }
 
 __device__ __noinline__ long long div_long(long long a, long long b) { return a / b; }
 
@@ -87,98 +96,173 @@ __device__ __forceinline__ long long div_units(long long a, long long b)
     return (a | b) < (1LL << 32) ? (long long)((uint32_t)a / (uint32_t)b) : div_long(a, b);
 }
 
-// The team that holds a unit.
-__device__ __forceinline__ int team_of(const Kv16Shares& h, long long u)
-{
-    const long long wide = (h.q + 1) * h.r;
-    return (int)(u < wide ? div_units(u, h.q + 1) : h.r + div_units(u - wide, h.q));
-}
+// The teams' runs: team t begins at unit q t + min(t, r).
+struct Shares {
+    long long q;
+    int r, nteams, whole;  // whole: a unit is a whole item
+    __device__ __forceinline__ long long at(int t) const { return q * t + min(t, r); }
+    __device__ __forceinline__ int team_of(long long u) const  // that holds unit u
+    {
+        const long long wide = (q + 1) * r;
+        return (int)(u < wide ? div_units(u, q + 1) : r + div_units(u - wide, q));
+    }
+};
 
 struct Start {
     int e, pad;
     long long off, count;  // offset in the units of entry e's items; units of the team
 };
 
-struct Scan {
-    long long units[33], items[33];
-    int top[32];
-    Kv16Shares shares;
+struct PreShared {
+    static constexpr int kMost = 32;
+    int first[kMost + 1], lens[kMost];
 };
 
-// Where each of the CTA's teams t0 .. t0 + n - 1 begins.  CTA 0 leaves the
-// schedule for the merge and raises what is wrong with the sequences.
-__device__ void find_starts(const Kv16Attn& a, const Kv16Sched& s, int t0, int n, Start* starts, Scan* sc)
+struct Scan {
+    long long units[32], cost[32];
+    int items[32], top[32];
+    Shares shares;
+};
+
+// Costs of a unit of k_kv16_wide and of k_kv16_rows in SM time (a tile for a
+// stream beside a kernel that saturates HBM 2.3 us; a block's bytes at the card's
+// rate by 152).
+__device__ __forceinline__ int unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2 : 1) : 25; }
+
+// Where each of the CTA's teams begins; the shares go to sc.  CTA 0 of the
+// call's first kernel raises what is wrong with the sequences.
+template <int D>
+__device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* starts, Scan* sc, PreShared* ps)
 {
+    const int t0 = blockIdx.x * s.per_cta, n = s.per_cta;
     const int entries = s.n_pre + s.n_seq, per = ceil_div(entries, (int)blockDim.x), e0 = threadIdx.x * per, e1 = min(e0 + per, entries);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    bool bad = false;
+    // ---- all loads at once
+    const int len0 = !s.direct && e0 < e1 && e0 >= s.n_pre ? a.lens[e0 - s.n_pre] : 0;
+    const bool fits = a.nP <= PreShared::kMost;
+    bool bad = false, wrong = false;
     for (int p = threadIdx.x; p < a.nP; p += blockDim.x) {
-        const int lo = a.pfirst[p], hi = a.pfirst[p + 1];
+        const int lo = a.pfirst[p], hi = a.pfirst[p + 1], m = a.plens[p];
         bad |= lo < 0 || hi > a.B || lo > hi;
-    }
-    bad = __syncthreads_or(bad);
-    if (blockIdx.x == 0 && s.first) {
-        bool wrong = bad;
-        for (int b = threadIdx.x; b < a.B; b += blockDim.x) wrong |= a.lens[b] > a.max_len;
-        for (int p = threadIdx.x; p < a.nP; p += blockDim.x) wrong |= a.plens[p] > a.max_plen;
-        if (wrong) kv4_raise(a.status, LA_ERR_ARG);
-    }
-    long long units = 0, items = 0;
-    int top = 0;
-    if (!bad)
-        for (int e = e0; e < e1; e++) {
-            const Entry x = entry_of(a, s, e);
-            const int k = a.Hkv * x.mt;
-            units += (long long)k * x.nu, items += k, top = max(top, x.nu);
+        wrong |= m > a.max_plen;
+        if (fits) {
+            ps->first[p] = lo, ps->lens[p] = m;
+            if (p == a.nP - 1) ps->first[p + 1] = hi;
         }
+    }
+    if (blockIdx.x == 0 && s.first) {
+        for (int b = threadIdx.x; b < a.B; b += blockDim.x) wrong |= a.lens[b] > a.max_len;
+        if (wrong || bad) kv4_raise(a.status, LA_ERR_ARG);
+    }
+    const Prefixes pre = fits ? Prefixes{ps->first, ps->lens} : Prefixes{a.pfirst, a.plens};
     if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
-    long long xu = units, xi = items;
+    bad = __syncthreads_or(bad);
+    if (s.bad && s.first && blockIdx.x == 0 && threadIdx.x == 0) *s.bad = bad;
+    if (s.direct) {
+        const int mt = (a.R + s.row_tile - 1) / s.row_tile, each = a.Hkv * mt;
+        if (threadIdx.x == 0) sc->shares = Shares{1, 0, s.nteams, 1};
+        if ((int)threadIdx.x < n && t0 + (int)threadIdx.x < s.nteams && !bad) {
+            const int t = t0 + threadIdx.x;
+            starts[threadIdx.x] = Start{t / each, 0, t % each, 1};
+        }
+        __syncthreads();
+        return pre;
+    }
+    long long units = 0, cost = 0;
+    int items = 0, top = 0;
+    Entry x0;
+    x0.mt = x0.nu = 0;
+    if (!bad) {
+        for (int e = e0; e < e1; e++) {
+            const Entry x = e == e0 ? entry_with(a, s, pre, e, len0) : entry_of(a, s, pre, e);
+            const int k = a.Hkv * x.mt;
+            if (e == e0) x0 = x;
+            if (x.nu) units += (long long)k * x.nu, items = min(items + k, 1 << 20), top = max(top, x.nu);
+            else if (!s.finish && x.b >= 0 && blockIdx.x == 0)
+                // no rows, which the merge is to know
+                for (int g = 0; g < a.Hkv; g++) s.items[(size_t)(a.Hkv + g) * a.B * a.R + x.row0].n = 0;
+        }
+        if (s.beside) {
+            // the other kernel's work
+            if (s.n_pre)
+                for (int b = threadIdx.x; b < a.B; b += blockDim.x) cost += (long long)a.Hkv * (blocks_of(min(max(a.lens[b], 0), a.max_len)) + 3);
+            else
+                for (int p = threadIdx.x; p < a.nP; p += blockDim.x) {
+                    const int rows = (pre.first[p + 1] - pre.first[p]) * a.R, m = min(max(pre.lens[p], 0), a.max_plen);
+                    cost += (long long)a.Hkv * ((rows + 255) / 256) * (4 + ((blocks_of(m) + 7) / 8 << (rows > 128)));
+                }
+        }
+    }
+    long long xu = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long yu = __shfl_up_sync(0xffffffffu, xu, o), yi = __shfl_up_sync(0xffffffffu, xi, o);
-        if (lane >= o) xu += yu, xi += yi;
+        const long long yu = __shfl_up_sync(0xffffffffu, xu, o);
+        if (lane >= o) xu += yu;
+    }
+    if (s.beside) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 31) sc->units[warp] = xu, sc->items[warp] = xi, sc->top[warp] = top;
+    const int w_items = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 31) sc->units[warp] = xu, sc->items[warp] = w_items, sc->top[warp] = top, sc->cost[warp] = cost;
     __syncthreads();
-    long long bu = xu - units, bi = xi - items, all_u = 0, all_i = 0;
+    long long before = xu - units, all_u = 0, all_c = 0;
+    int all_i = 0;
     for (int w = 0; w < nw; w++) {
-        const long long u = sc->units[w], i = sc->items[w];
-        if (w < warp) bu += u, bi += i;
-        all_u += u, all_i += i, top = max(top, sc->top[w]);
+        const long long u = sc->units[w];
+        if (w < warp) before += u;
+        all_u += u, all_c += sc->cost[w], all_i = min(all_i + sc->items[w], 1 << 20), top = max(top, sc->top[w]);
     }
-    Kv16Shares h;
-    h.whole = all_i <= s.nteams && top - s.slack <= div_units(all_u, s.nteams), h.pad = 0;
+    int room = s.nteams;
+    if (s.beside) {
+        // Both kernels count alike: the wide one takes a share of the SMs by its work (and a quarter more: its
+        // last item is the call's end), the rows' one the others; not where it would need most of them.
+        const long long mine = all_u * unit_cost(s.n_pre == 0, D), other = all_c * unit_cost(s.n_pre != 0, D);
+        const long long wide = s.n_pre ? mine : other, sum = max(mine + other, 1LL);
+        const int sms = (int)div_long(wide * kSMs * 5 / 4, sum) + 1;
+        if (sms <= kSMs * 3 / 4) room = (s.n_pre ? sms : kSMs - sms) * s.per_cta;
+    }
+    Shares h;
+    h.whole = all_i <= room && top - s.slack <= div_units(all_u, room);
+    int bi = 0;
+    if (h.whole) {
+        // the same for whole items (few: there is a team for each)
+        int xi = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, xi, o);
+            if (lane >= o) xi += y;
+        }
+        bi = xi - items;
+        for (int w = 0; w < warp; w++) bi += sc->items[w];
+    }
     const long long all = h.whole ? all_i : all_u;
-    h.nteams = h.whole ? (int)all_i : (int)min((long long)s.nteams, max(1LL, div_units(all, s.min_run)));
+    h.nteams = h.whole ? all_i : (int)min((long long)room, max(1LL, div_units(all, s.min_run)));
     if (all == 0) h.nteams = 0;
     h.q = h.nteams ? div_units(all, h.nteams) : 0;
     h.r = (int)(all - h.q * h.nteams);
-    const bool notes = blockIdx.x == 0;
-    if (threadIdx.x == 0) {
-        sc->shares = h;
-        if (notes && s.shares) *s.shares = h;
-    }
-    if (h.nteams && (notes || units)) {
-        long long at = h.whole ? bi : bu;
+    if (threadIdx.x == 0) sc->shares = h;
+    if (h.nteams && units) {
+        long long at = h.whole ? bi : before;
         const long long end = at + (h.whole ? items : units);
         int i = 0;
         // the teams that begin within this thread's entries
-        while (i < n && (t0 + i >= h.nteams || units_at(h, t0 + i) < at)) i++;
-        if (notes ? s.base != nullptr || i < n : i < n && units_at(h, t0 + i) < end)
+        while (i < n && (t0 + i >= h.nteams || h.at(t0 + i) < at)) i++;
+        if (i < n && h.at(t0 + i) < end)
             for (int e = e0; e < e1; e++) {
-                const Entry x = entry_of(a, s, e);
-                const long long c = (long long)a.Hkv * x.mt * (h.whole ? 1 : x.nu);
-                if (notes && s.base) s.base[e] = at;
+                const Entry x = e == e0 ? x0 : entry_of(a, s, pre, e);
+                const long long c = (long long)a.Hkv * x.mt * (h.whole ? x.nu > 0 : x.nu);
                 for (; i < n && t0 + i < h.nteams; i++) {
-                    const long long u0 = units_at(h, t0 + i);
+                    const long long u0 = h.at(t0 + i);
                     if (u0 >= at + c) break;
-                    starts[i] = Start{e, 0, u0 - at, units_at(h, t0 + i + 1) - u0};
+                    starts[i] = Start{e, 0, u0 - at, h.at(t0 + i + 1) - u0};
                 }
                 at += c;
             }
     }
     __syncthreads();
+    return pre;
 }
 
 // The run of one item's units that a team works on: tiles t0 .. t1 - 1 of KV
@@ -195,23 +279,24 @@ struct Run {
         left -= u1 - u0;
         t0 = whole ? 0 : tile_at(s, x, u0);
         t1 = whole ? x.tiles : tile_at(s, x, u1);
+        if (x.nu == 0) t0 = t1 = 0;  // (a direct team's sequence may be none)
     }
-    __device__ __forceinline__ void begin(const Kv16Attn& a, const Kv16Sched& s, const Start& st, const Kv16Shares& h)
+    __device__ __forceinline__ void begin(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, const Start& st, const Shares& h)
     {
         left = st.count, whole = h.whole, e = st.e;
-        x = entry_of(a, s, e);
+        x = entry_of(a, s, pre, e);
         const int n = whole ? 1 : x.nu;
         item = (int)div_units(st.off, n);
         cut(s, (int)(st.off - (long long)item * n));
     }
-    __device__ __forceinline__ bool next(const Kv16Attn& a, const Kv16Sched& s)
+    __device__ __forceinline__ bool next(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre)
     {
         if (left <= 0) return false;
         if (++item == a.Hkv * x.mt) {
             item = 0;
             do {
                 if (++e >= s.n_pre + s.n_seq) return false;  // only if the lengths change under the call
-                x = entry_of(a, s, e);
+                x = entry_of(a, s, pre, e);
             } while (x.nu == 0);
         }
         cut(s, 0);
@@ -221,6 +306,18 @@ struct Run {
     __device__ __forceinline__ bool all() const { return u0 == 0 && u1 == nu; }
     // which of the team's two parts it is: 1 begins an item, 0 goes on with one
     __device__ __forceinline__ int slot() const { return u0 == 0; }
+    // leaves word of where the item's parts are, if it begins here (one thread)
+    __device__ __forceinline__ void note(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, const Shares& h, int team) const
+    {
+        if (u0 != 0 || (s.finish && all())) return;
+        const int g = item / x.mt, r0 = (item - g * x.mt) * s.row_tile;
+        Kv16Item it;
+        it.t0 = team, it.n = all() ? 1 : h.team_of(h.at(team + 1) + (nu - u1) - 1) - team + 1;
+        it.row = x.row0 + r0, it.rows = min(s.row_tile, x.rows - r0), it.g = g;
+        it.pre_row = x.b >= 0 && x.p >= 0 && !a.concat ? pre.first[x.p] * a.R : -1;
+        if (s.finish) s.items[team] = it;
+        else s.items[(size_t)((x.b >= 0) * a.Hkv + g) * a.B * a.R + it.row] = it;
+    }
 };
 
 // Floats of a part and of the results of whole items.  A thread per row writes
@@ -231,12 +328,5 @@ __host__ __device__ constexpr size_t wide_part(int D) { return (size_t)2 * 128 *
 __host__ __device__ constexpr size_t rows_part(int D, int R) { return ((size_t)R * (D + 2) + 3) / 4 * 4; }  // (16-byte aligned)
 
 }  // namespace
-
-// Joins the parts of every row (kv16_attn.cu).
-struct Kv16Merge {
-    Kv16Sched pre, seq;       // n_pre of `pre` 0: no prefixes of their own
-    int seq_rows;             // sequences' parts are rows (k_kv16_rows), else columns
-    int rows_all;             // rows of a KV head of all sequences
-};
 
 }  // namespace la

@@ -23,7 +23,7 @@
 // the end.
 //
 // One CTA per SM: warps 0-3 and 4-7 the streams' softmax (a row per thread), 8
-// issues the products, 9 the copies, 10-11 clear values.
+// issues the products, 9 the copies, 10 clears values.
 #include <cudaTypedefs.h>
 
 #include "kv16_sched.cuh"
@@ -31,13 +31,22 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 352;
 constexpr int kInfos = 8;
+constexpr uint32_t kColO = 256;  // tensor memory: S [2][128] (P in their place), O [2][128]
 
 // What is known of a tile; eight in turn.
 struct alignas(16) TileInfo {
     uint32_t code[2];  // a byte for each block: keys, or 128 + number of the step's block; 0: none
     int blocks, part;  // blocks; are scores to be left out
+};
+
+template <int S>
+struct Bars {
+    uint64_t full[S], empty[S];  // of the ring's stages
+    uint64_t vready[8];          // of the tile's values: cleared where they have to be
+    uint64_t s[2], p[2][2], h[2];  // of a stream's tile: scores; [half][stream] weights; the first half's products
+    uint64_t q, o, end;          // of a run: queries; the last products
 };
 
 template <int D>
@@ -48,11 +57,11 @@ struct WideSmem {
     static constexpr int kQ = 0, kRing = 2 * kOperand;
     static constexpr int kVis = kRing + kStages * kOperand;  // [step row][4]: step rows it sees
     static constexpr int kBar = kVis + 128 * 16;
-    static constexpr int kBars = 2 * kStages + 16;
-    static constexpr int kInfo = (kBar + kBars * 8 + 15) / 16 * 16;
-    static constexpr int kOdd = kInfo + kInfos * (int)sizeof(TileInfo);  // [run][warp][4]: step rows whose values are not finite
-    static constexpr int kMisc = kOdd + 8 * 2 * 16;
-    static constexpr int kBytes = kMisc + 16;
+    static constexpr int kInfo = (kBar + (int)sizeof(Bars<kStages>) + 15) / 16 * 16;
+    static constexpr int kOdd = kInfo + kInfos * (int)sizeof(TileInfo);  // [run][4]: step rows whose values are not finite
+    static constexpr int kMisc = kOdd + 8 * 16;
+    static constexpr int kPre = kMisc + 16;
+    static constexpr int kBytes = kPre + (int)sizeof(PreShared);
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -66,13 +75,162 @@ __device__ __forceinline__ int piece_at(int i, int row)
 __device__ __noinline__ void add_odd_to(const Kv16Attn& a, const uint32_t* odd, const uint32_t* see, int b, int col, float* o)
 {
     for (int key = 0; key < a.T; key++) {
-        if (!((((odd[key >> 5] | odd[4 + (key >> 5)]) & see[key >> 5]) >> (key & 31)) & 1)) continue;
+        if (!(((odd[key >> 5] & see[key >> 5]) >> (key & 31)) & 1)) continue;
         const __nv_bfloat16* v = a.vs + (size_t)(b * (long long)a.T + key) * a.v_ld + col;
         for (int i = 0; i < 32; i++) {
             const float x = __bfloat162float(v[i]);
             if (!(fabsf(x) < INFINITY)) o[i] += x;
         }
     }
+}
+
+// Which of a tile's scores 32 c .. 32 c + 31 count for a row that sees the step rows `see`.
+__device__ __forceinline__ uint32_t counted(const TileInfo& ti, int c, const uint32_t* see)
+{
+    const uint32_t code = ti.code[c >> 1] >> (16 * (c & 1));
+    auto half = [&](uint32_t k) -> uint32_t {
+        if (k & 128) return see[(k & 127) >> 1] >> (16 * (k & 1)) & 0xffffu;
+        return (1u << k) - 1u;
+    };
+    return half(code & 255) | half(code >> 8 & 255) << 16;
+}
+
+// 64 scores x of a row as weights p = exp2(x f - m), in bf16; returns their sum.
+__device__ __forceinline__ float weigh64(const uint32_t (&x)[64], float f, float m, uint32_t (&p)[32])
+{
+    const uint64_t f2 = la::pair(f, f), c2 = la::pair(-m, -m);
+    uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+    for (int j = 0; j < 64; j += 4) {
+        float e0, e1, e2, e3;
+        unpair(fma2(la::pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, c2), e0, e1);
+        unpair(fma2(la::pair(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), f2, c2), e2, e3);
+        e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+        s0 = add2(s0, la::pair(e0, e1)), s1 = add2(s1, la::pair(e2, e3));
+        p[j / 2] = pack_bf16(e0, e1), p[j / 2 + 1] = pack_bf16(e2, e3);
+    }
+    float t0, t1, t2, t3;
+    unpair(s0, t0, t1), unpair(s1, t2, t3);
+    return (t0 + t1) + (t2 + t3);
+}
+
+// A wait that gives up ends every later one at once, but no role leaves its
+// loops: the named barriers keep their counts.
+struct Wait {
+    volatile int* abort_flag;
+    int* status;
+    bool ok;
+    __device__ __forceinline__ void operator()(uint64_t* b, int parity)
+    {
+        if (!ok || try_wait_long(b, parity & 1)) return;
+        const unsigned long long t0 = globaltimer();
+        while (!try_wait_long(b, parity & 1)) {
+            if (*abort_flag || globaltimer() - t0 > kWaitNs) {
+                ok = false;
+                *abort_flag = 1;
+                kv4_raise(status, LA_ERR_TIMEOUT);
+                return;
+            }
+        }
+    }
+};
+
+// A stream's tiles of a run, `step` apart from tile n (`done` before them): the
+// scores become weights where they are.  Returns the row's reference and sum.  A
+// function, so that what its caller keeps over it leaves the registers once and
+// not in every tile (spilt around the loop's body, a tile took 2.2 us, not 1.7).
+template <int D>
+__device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, int n, int step, int tiles, int done, bool any, const uint32_t* see,
+                                           float f, int* status)
+{
+    using L = WideSmem<D>;
+    Bars<L::kStages>& bar = *(Bars<L::kStages>*)(sm + L::kBar);
+    uint64_t *b_s = bar.s, *b_p = bar.p[0], *b_h = bar.h;
+    const TileInfo* info = (const TileInfo*)(sm + L::kInfo);
+    Wait wait{(volatile int*)(sm + L::kMisc + 4), status, true};
+    const uint32_t ts = trow + str * 128, to = trow + kColO + str * 128;
+    const int lane = threadIdx.x & 31;
+    float m = kNoRef, l = 0.f;
+    bool first = true;
+    for (int i = 0; i < tiles; i++, done++) {
+        wait(b_s + str, done);
+        tc_fence_after();
+        if (any) {
+            const TileInfo ti = info[(n + i * step) & (kInfos - 1)];
+            const int n32 = (ti.blocks + 1) >> 1;
+            // Half a tile at a time.  Its weights go to the columns of scores that are taken once the reference is
+            // known to do for all of them.
+#pragma unroll 1
+            for (int h = 0; h < 2; h++) {
+                if (2 * h < n32) {
+                    uint32_t p[32];
+                    float sum;
+                    while (true) {
+                        uint32_t x[64];
+                        tmem_ld64_raw(ts + h * 64, x);
+                        if (ti.part) {
+                            const uint32_t k0 = counted(ti, 2 * h, see), k1 = counted(ti, 2 * h + 1, see);
+#pragma unroll
+                            for (int j = 0; j < 32; j++) {
+                                if (!((k0 >> j) & 1)) x[j] = 0xff800000u;  // -inf
+                                if (!((k1 >> j) & 1)) x[32 + j] = 0xff800000u;
+                            }
+                        }
+                        if (first) {
+                            // (of the run's first scores that there are)
+                            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < 64; j += 2) t0 = fmaxf(t0, __uint_as_float(x[j])), t1 = fmaxf(t1, __uint_as_float(x[j + 1]));
+                            m = fmaxf(m, fmaxf(t0, t1) * f);
+                            first = false;
+                        }
+                        sum = weigh64(x, f, m, p);
+                        if (!__any_sync(0xffffffffu, sum > 32768.f)) break;
+                        // (rare) the reference moves up to the largest of the scores from here on, and the outputs down
+                        // with it, once the products before are in them
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 2 * h; c < n32; c++) {
+                            const uint32_t k = ti.part ? counted(ti, c, see) : ~0u;
+#pragma unroll 1
+                            for (int j = 0; j < 32; j += 8) {
+                                uint32_t y[8];
+                                tmem_ld8(ts + c * 32 + j, y);
+#pragma unroll
+                                for (int e = 0; e < 8; e++)
+                                    if ((k >> (j + e)) & 1) top = fmaxf(top, __uint_as_float(y[e]));
+                            }
+                        }
+                        top = fmaxf(m, top * f);
+                        const float by = ex2(m - top);
+                        m = top, l *= by;
+                        if (h) wait(b_h + str, done), tc_fence_after();
+                        if (h || i > 0) {
+#pragma unroll 1
+                            for (int j = 0; j < D; j += 8) {
+                                uint32_t o[8];
+                                tmem_ld8(to + j, o);
+#pragma unroll
+                                for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                                tmem_st8(to + j, o);
+                            }
+                        }
+                    }
+                    l += sum;
+                    tmem_st16(ts + h * 32, p);
+                    tmem_st16(ts + h * 32 + 16, p + 16);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p + 2 * h + str);
+            }
+        } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_p + str), mbar_arrive(b_p + 2 + str);
+        }
+    }
+    return make_float2(m, l);
 }
 
 struct Maps {
@@ -86,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using L = WideSmem<D>;
     constexpr int kSt = L::kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
-    uint64_t* bar = (uint64_t*)(sm + L::kBar);
-    uint64_t *b_full = bar, *b_empty = bar + kSt, *b_vready = bar + 2 * kSt, *b_s = b_vready + 8, *b_p = b_s + 2, *b_q = b_p + 2,
-             *b_o = b_q + 1, *b_end = b_o + 1;
+    Bars<kSt>& bar = *(Bars<kSt>*)(sm + L::kBar);
+    uint64_t *b_full = bar.full, *b_empty = bar.empty, *b_vready = bar.vready, *b_s = bar.s, *b_p = bar.p[0], *b_h = bar.h, *b_q = &bar.q,
+             *b_o = &bar.o, *b_end = &bar.end;
     TileInfo* info = (TileInfo*)(sm + L::kInfo);
     uint32_t *vis = (uint32_t*)(sm + L::kVis), *odds = (uint32_t*)(sm + L::kOdd);
     uint32_t* tmem_slot = (uint32_t*)(sm + L::kMisc);
@@ -101,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_alloc(tmem_slot, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSt; i++) mbar_init(b_full + i, 1), mbar_init(b_empty + i, 1);
-        for (int i = 0; i < 8; i++) mbar_init(b_vready + i, 2);
-        for (int i = 0; i < 2; i++) mbar_init(b_s + i, 1), mbar_init(b_p + i, 4);
+        for (int i = 0; i < 8; i++) mbar_init(b_vready + i, 1);
+        for (int i = 0; i < 4; i++) mbar_init(b_p + i, 4);  // [half][stream]
+        for (int i = 0; i < 2; i++) mbar_init(b_s + i, 1), mbar_init(b_h + i, 1);
         mbar_init(b_q, 8);
         mbar_init(b_o, 1);
         mbar_init(b_end, 1);
@@ -138,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
     tc_fence_before();
-    find_starts(a, s, blockIdx.x, 1, start, sc);
+    const Prefixes pre = find_starts<D>(a, s, start, sc, (PreShared*)(sm + L::kPre));
     tc_fence_after();
-    const Kv16Shares sh = sc->shares;
+    const Shares sh = sc->shares;
     const Start st = *start;
     const uint32_t tmem = *tmem_slot;
     // (the swizzle and the products' descriptors count from multiples of 1024)
@@ -148,34 +307,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!placed && threadIdx.x == 0) kv4_raise(a.status, LA_ERR_CUDA);
     __syncthreads();
 
-    // A wait that gives up ends every later one at once, but no role leaves its
-    // loops: the named barriers keep their counts.
-    bool ok = true;
-    auto wait = [&](uint64_t* b, int parity) {
-        if (!ok || try_wait_long(b, parity & 1)) return;
-        const unsigned long long t0 = globaltimer();
-        while (!try_wait_long(b, parity & 1)) {
-            if (*abort_flag || globaltimer() - t0 > kWaitNs) {
-                ok = false;
-                *abort_flag = 1;
-                kv4_raise(a.status, LA_ERR_TIMEOUT);
-                return;
-            }
-        }
-    };
-    constexpr uint32_t kColO = 256;  // tensor memory: S [2][128] (P in their place), O [2][128]
+    Wait wait{abort_flag, a.status, true};
+    const bool& ok = wait.ok;
     int n = 0;     // tiles so far
     int segs = 0;  // runs with tiles so far
     Run run;
-    if (work) run.begin(a, s, st, sh);
+    if (work) run.begin(a, s, pre, st, sh);
+    if (!work && threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
     if (work && warp < 8) {
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, str = warp >> 2, row = q * 32 + lane;
-        const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16), ts = trow + str * 128, to = trow + kColO + str * 128;
+        const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16), to = trow + kColO + str * 128;
         int done = 0;  // this stream's tiles so far
+        if (threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
         do {
             const int nt = run.t1 - run.t0;
-            if (nt <= 0) continue;
+            if (run.x.nu && threadIdx.x == 0) run.note(a, s, pre, sh, blockIdx.x);
+            if (nt <= 0) {
+                // (units, but no keys)
+                if (run.x.nu && str == 0)
+                    for (int i = 0; i < 2; i++) {
+                        float* col = s.slots + ((size_t)blockIdx.x * 2 + run.slot()) * wide_part(D) + i * 128 * (D + 2) + row;
+                        col[D * 128] = kNoRef, col[(D + 1) * 128] = 0.f;
+                    }
+                continue;
+            }
             const Entry& x = run.x;
             const int g = run.item / x.mt, r0 = (run.item - g * x.mt) * kWideRows, nrows = min(kWideRows, x.rows - r0);
             const bool pair = nrows > 128;
@@ -211,97 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(b_q);
             const int step_row = x.b < 0 ? 0 : ((gr - x.row0) / group < a.T ? (gr - x.row0) / group : a.T - 1);
             const uint32_t* see = vis + 4 * step_row;
-            float m = kNoRef, l = 0.f;
-            for (int i = 0; i < tiles; i++, done++) {
-                wait(b_s + str, done);
-                tc_fence_after();
-                if (any) {
-                    const TileInfo ti = info[(n + (pair ? i : 2 * i + str)) & (kInfos - 1)];
-                    const int n32 = (ti.blocks + 1) >> 1;
-                    auto counts = [&](int c) -> uint32_t {  // which of the scores 32 c .. count
-                        const uint32_t code = ti.code[c >> 1] >> (16 * (c & 1));
-                        auto half = [&](uint32_t k) -> uint32_t {
-                            if (k & 128) return see[(k & 127) >> 1] >> (16 * (k & 1)) & 0xffffu;
-                            return (1u << k) - 1u;
-                        };
-                        return half(code & 255) | half(code >> 8 & 255) << 16;
-                    };
-                    uint32_t p[64];
-                    float sum;
-                    bool look = i == 0;
-                    while (true) {
-                        if (look) {
-                            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll 1
-                            for (int c = 0; c < n32; c++) {
-                                float y[32];
-                                tmem_ld32(ts + c * 32, y);
-                                const uint32_t k = ti.part ? counts(c) : ~0u;
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    t0 = fmaxf(t0, (k >> j) & 1 ? y[j] : -INFINITY);
-                                    t1 = fmaxf(t1, (k >> j) & 2 ? y[j + 1] : -INFINITY);
-                                }
-                            }
-                            const float top = fmaxf(m, fmaxf(t0, t1) * a.sl2), c = ex2(m - top);
-                            m = top;
-                            l *= c;
-                            if (i > 0) {
-                                // (this tile's scores came behind the last one's products)
-#pragma unroll 1
-                                for (int j = 0; j < D; j += 8) {
-                                    uint32_t o[8];
-                                    tmem_ld8(to + j, o);
-#pragma unroll
-                                    for (int k = 0; k < 8; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
-                                    tmem_st8(to + j, o);
-                                }
-                            }
-                        }
-                        uint64_t s2 = 0;  // two sums
-                        const uint64_t f2 = la::pair(a.sl2, a.sl2), c2 = la::pair(-m, -m);
-#pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            if (c >= n32) break;
-                            float y[32];
-                            tmem_ld32(ts + c * 32, y);
-                            if (ti.part) {
-                                const uint32_t k = counts(c);
-#pragma unroll
-                                for (int j = 0; j < 32; j++)
-                                    if (!((k >> j) & 1)) y[j] = -INFINITY;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float e0, e1;
-                                unpair(fma2(la::pair(y[j], y[j + 1]), f2, c2), e0, e1);
-                                e0 = ex2(e0), e1 = ex2(e1);
-                                s2 = add2(s2, la::pair(e0, e1));
-                                p[c * 16 + j / 2] = pack_bf16(e0, e1);
-                            }
-                        }
-                        float s0, s1;
-                        unpair(s2, s0, s1);
-                        sum = s0 + s1;
-                        if (look || !__any_sync(0xffffffffu, sum > 32768.f)) break;
-                        look = true;
-                    }
-                    l += sum;
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        if (c < n32) tmem_st16(ts + c * 16, p + c * 16);
-                    tmem_st_wait();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p + str);
-            }
+            const float2 y = weigh_tiles<D>(sm, trow, str, n + (pair ? 0 : str), pair ? 1 : 2, tiles, done, any, see, a.sl2, a.status);
+            float m = y.x, l = y.y;
+            done += tiles;
             // ---- the run's result
             wait(b_o, segs);
             tc_fence_after();
             const bool all = run.all();
-            const uint32_t* odd = odds + (segs & 7) * 8;
-            const bool fix = x.b >= 0 && (odd[0] | odd[1] | odd[2] | odd[3] | odd[4] | odd[5] | odd[6] | odd[7]) != 0;
+            const uint32_t* odd = odds + (segs & 7) * 4;
+            const bool fix = x.b >= 0 && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
             float w0 = 1.f, w1 = 0.f;  // of this stream's outputs, and of the other's
             int c0 = 0, c1 = D;
             if (!pair) {
@@ -361,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!pair) named_sync(1, 256);  // the other stream's outputs are read, and the queries' place is free
             n += nt;
             segs++;
-        } while (run.next(a, s));
+        } while (run.next(a, s, pre));
     } else if (work && warp == 8) {
-        // ---------------------------------------------------------------- MMA
+        // ----------------------------------------------------------- products
         constexpr uint32_t id_s = idesc_bf16(128, 0, false), id_o = idesc_bf16(128, D, true);
         const uint32_t base = smem_u32(sm);
         const uint64_t dk = desc_sw128_kmajor(base), dv = desc_sw128_mnmajor(base, 128 * 128);
@@ -376,11 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int g = run.item / run.x.mt, r0 = (run.item - g * run.x.mt) * kWideRows;
             const bool pair = min(kWideRows, run.x.rows - r0) > 128;
             const int jobs = pair ? 2 * nt : nt;  // a tile for a stream: the streams by turns
-            auto scores = [&](int j, int str) {
-                const int tile = n + (pair ? j >> 1 : j), fill = 2 * tile, stage = fill % kSt;
-                wait(b_full + stage, fill / kSt);
-                if (j < 2) wait(b_q, segs);
-                tc_fence_after();
+            auto tile_of = [&](int j) { return n + (pair ? j >> 1 : j); };
+            auto keys = [&](int j) {
+                const int fill = 2 * tile_of(j);
+                wait(b_full + fill % kSt, fill / kSt);
+            };
+            auto scores = [&](int j) {
+                const int str = j & 1, tile = tile_of(j), stage = 2 * tile % kSt;
                 const int blocks = info[tile & (kInfos - 1)].blocks;
                 if (chosen && ok) {
                     const uint32_t id = id_s | (uint32_t)(2 * blocks) << 17, ka = k_lo + ((L::kRing + stage * L::kOperand) >> 4),
@@ -395,37 +471,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            scores(0, 0);
-            if (jobs > 1) scores(1, 1);
+            wait(b_q, segs);
+            keys(0);
+            tc_fence_after();
+            scores(0);
+            if (jobs > 1) keys(1), tc_fence_after(), scores(1);
 #pragma unroll 1
             for (int j = 0; j < jobs; j++) {
-                const int str = j & 1, tile = n + (pair ? j >> 1 : j), fill = 2 * tile + 1, stage = fill % kSt;
-                wait(b_p + str, str ? weighed1 : weighed0);
-                if (str) weighed1++;
-                else weighed0++;
+                const int str = j & 1, tile = tile_of(j), stage = (2 * tile + 1) % kSt;
                 wait(b_vready + (tile & 7), tile >> 3);
-                const int blocks = info[tile & (kInfos - 1)].blocks;
-                tc_fence_after();
-                if (chosen && ok) {
-                    const uint32_t va = v_lo + ((L::kRing + stage * L::kOperand) >> 4), d = tmem + kColO + str * 128, pa = tmem + str * 128;
+                const int blocks = info[tile & (kInfos - 1)].blocks, done = str ? weighed1 : weighed0;
+                const uint32_t va = v_lo + ((L::kRing + stage * L::kOperand) >> 4), d = tmem + kColO + str * 128, pa = tmem + str * 128;
+                auto half = [&](int h) {
                     auto step16 = [&](int k) { mma_ts(d, pa + k * 8, va + ((k * 16 * 128) >> 4), v_hi, id_o, j > 1 || k > 0); };
-                    if (blocks == 8) {
+                    if (blocks >= 4 * h + 4) {
 #pragma unroll
-                        for (int k = 0; k < 8; k++) step16(k);
+                        for (int k = 0; k < 4; k++) step16(4 * h + k);
                     } else {
 #pragma unroll 1
-                        for (int k = 0; k < blocks; k++) step16(k);
+                        for (int k = 4 * h; k < blocks; k++) step16(k);
                     }
+                };
+                wait(b_p + str, done);
+                tc_fence_after();
+                if (chosen && ok) {
+                    half(0);
+                    mma_commit(b_h + str);
+                }
+                __syncwarp();
+                if (j + 2 < jobs) keys(j + 2);  // (waited for here: nothing is to come between the weights and the next scores)
+                wait(b_p + 2 + str, done);
+                if (str) weighed1++;
+                else weighed0++;
+                tc_fence_after();
+                if (chosen && ok) {
+                    half(1);
                     if (!pair || str) mma_commit(b_empty + stage);
                 }
                 __syncwarp();
-                if (j + 2 < jobs) scores(j + 2, str);
+                // (in the place of this tile's weights, behind their products)
+                if (j + 2 < jobs) scores(j + 2);
             }
             if (chosen && ok) mma_commit(b_o);
             __syncwarp();
             n += nt;
             segs++;
-        } while (run.next(a, s));
+        } while (run.next(a, s, pre));
         if (!ok && chosen) {
             // let the products that were issued finish before the memory goes
             mma_commit(b_end);
@@ -483,15 +574,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-        } while (run.next(a, s));
+        } while (run.next(a, s, pre));
         // no copy may still be on its way when the CTA ends
         for (int i = 1; i <= kSt && i <= 2 * n; i++) mbar_drain(b_full + (2 * n - i) % kSt, ((2 * n - i) / kSt) & 1);
     } else if (work) {
         // ------------------------------------------------------- values cleared
-        const int me = warp - 10;
         do {
             if (run.t1 <= run.t0) continue;
-            uint32_t* odd = odds + (segs & 7) * 8 + me * 4;
+            uint32_t* odd = odds + (segs & 7) * 4;
             if (lane < 4) odd[lane] = 0;
             __syncwarp();
             for (int tile = run.t0; tile < run.t1; tile++, n++) {
@@ -500,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const TileInfo ti = info[n & (kInfos - 1)];
                 if (ti.part && ok) {
                     uint8_t* v = sm + L::kRing + stage * L::kOperand;
-                    for (int blk = me; blk < ti.blocks; blk += 2) {
+                    for (int blk = 0; blk < ti.blocks; blk++) {
                         const uint32_t code = ti.code[blk >> 2] >> (8 * (blk & 3)) & 255;
                         const bool step = code & 128;
                         const int j0 = (code & 127) * 16, live = step ? min(16, a.T - j0) : (int)code;
@@ -534,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(b_vready + (n & 7));
             }
             segs++;
-        } while (run.next(a, s));
+        } while (run.next(a, s, pre));
     }
     tc_fence_before();
     __syncthreads();
