@@ -67,6 +67,9 @@ __device__ __forceinline__ void cp_wait()
 }
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
+// of a bf16 pair (weights are summed as rounded: what one loses is then lost above and below)
+__device__ __forceinline__ float sum_of(uint32_t u) { return __uint_as_float(u << 16) + __uint_as_float(u & 0xffff0000u); }
+
 __device__ __forceinline__ bool odd(float x) { return !(fabsf(x) < INFINITY); }
 
 template <int D>
@@ -282,13 +285,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                     }
                     const float e0 = ex2(fmaf(x[0][0], a.sl2, -ma)), e1 = ex2(fmaf(x[0][1], a.sl2, -ma)),
                                 e2 = ex2(fmaf(x[1][0], a.sl2, -ma)), e3 = ex2(fmaf(x[1][1], a.sl2, -ma));
-                    sa = (e0 + e1) + (e2 + e3);
                     p[0] = pack_bf16(e0, e1), p[2] = pack_bf16(e2, e3);
+                    sa = sum_of(p[0]) + sum_of(p[2]);
                     if (two) {
                         const float g0 = ex2(fmaf(x[0][2], a.sl2, -mb)), g1 = ex2(fmaf(x[0][3], a.sl2, -mb)),
                                     g2 = ex2(fmaf(x[1][2], a.sl2, -mb)), g3 = ex2(fmaf(x[1][3], a.sl2, -mb));
-                        sb = (g0 + g1) + (g2 + g3);
                         p[1] = pack_bf16(g0, g1), p[3] = pack_bf16(g2, g3);
+                        sb = sum_of(p[1]) + sum_of(p[3]);
                     }
                     if (look || !__any_sync(0xffffffffu, sa > 32768.f || sb > 32768.f)) break;
                     look = true;

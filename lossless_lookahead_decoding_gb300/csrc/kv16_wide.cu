@@ -44,8 +44,7 @@ struct alignas(16) TileInfo {
 template <int S>
 struct Bars {
     uint64_t full[S], empty[S];  // of the ring's stages
-    uint64_t vready[8];          // of the tile's values: cleared where they have to be
-    uint64_t s[2], p[2][2], h[2];  // of a stream's tile: scores; [half][stream] weights; the first half's products
+    uint64_t s[2], p[2];         // of a stream's tile: scores; weights, its values cleared and the next one's keys
     uint64_t q, o, end;          // of a run: queries; the last products
 };
 
@@ -95,19 +94,20 @@ __device__ __forceinline__ uint32_t counted(const TileInfo& ti, int c, const uin
     return half(code & 255) | half(code >> 8 & 255) << 16;
 }
 
-// 64 scores x of a row as weights p = exp2(x f - m), in bf16; returns their sum.
+// 64 scores x of a row as weights p = exp2(x f - m), in bf16; returns their sum
+// (of the rounded ones: what a weight loses is then lost above and below).
 __device__ __forceinline__ float weigh64(const uint32_t (&x)[64], float f, float m, uint32_t (&p)[32])
 {
     const uint64_t f2 = la::pair(f, f), c2 = la::pair(-m, -m);
     uint64_t s0 = 0, s1 = 0;
+    auto values = [](uint32_t u) { return la::pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); };
 #pragma unroll
     for (int j = 0; j < 64; j += 4) {
         float e0, e1, e2, e3;
         unpair(fma2(la::pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, c2), e0, e1);
         unpair(fma2(la::pair(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), f2, c2), e2, e3);
-        e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-        s0 = add2(s0, la::pair(e0, e1)), s1 = add2(s1, la::pair(e2, e3));
-        p[j / 2] = pack_bf16(e0, e1), p[j / 2 + 1] = pack_bf16(e2, e3);
+        p[j / 2] = pack_bf16(ex2(e0), ex2(e1)), p[j / 2 + 1] = pack_bf16(ex2(e2), ex2(e3));
+        s0 = add2(s0, values(p[j / 2])), s1 = add2(s1, values(p[j / 2 + 1]));
     }
     float t0, t1, t2, t3;
     unpair(s0, t0, t1), unpair(s1, t2, t3);
@@ -122,7 +122,7 @@ struct Wait {
     bool ok;
     __device__ __forceinline__ void operator()(uint64_t* b, int parity)
     {
-        if (!ok || try_wait_long(b, parity & 1)) return;
+        if (!ok || mbar_try_wait(b, parity & 1)) return;
         const unsigned long long t0 = globaltimer();
         while (!try_wait_long(b, parity & 1)) {
             if (*abort_flag || globaltimer() - t0 > kWaitNs) {
@@ -145,7 +145,7 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
 {
     using L = WideSmem<D>;
     Bars<L::kStages>& bar = *(Bars<L::kStages>*)(sm + L::kBar);
-    uint64_t *b_s = bar.s, *b_p = bar.p[0], *b_h = bar.h;
+    uint64_t *b_s = bar.s, *b_p = bar.p;
     const TileInfo* info = (const TileInfo*)(sm + L::kInfo);
     Wait wait{(volatile int*)(sm + L::kMisc + 4), status, true};
     const uint32_t ts = trow + str * 128, to = trow + kColO + str * 128;
@@ -186,8 +186,8 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                         }
                         sum = weigh64(x, f, m, p);
                         if (!__any_sync(0xffffffffu, sum > 32768.f)) break;
-                        // (rare) the reference moves up to the largest of the scores from here on, and the outputs down
-                        // with it, once the products before are in them
+                        // (rare) the reference moves up to the largest of the scores from here on, and the weights before
+                        // and the outputs down with it (this tile's scores came behind the last one's products)
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int c = 2 * h; c < n32; c++) {
@@ -201,19 +201,30 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                                     if ((k >> (j + e)) & 1) top = fmaxf(top, __uint_as_float(y[e]));
                             }
                         }
-                        top = fmaxf(m, top * f);
-                        const float by = ex2(m - top);
-                        m = top, l *= by;
-                        if (h) wait(b_h + str, done), tc_fence_after();
-                        if (h || i > 0) {
+                        top *= f;
+                        // (by a whole number: weights in bf16 are moved by a power of two, exactly)
+                        const float up = top > m + 8.f ? ceilf(top - m) : 0.f;
+                        const float by = up <= 126.f ? __uint_as_float((uint32_t)(127 - (int)up) << 23) : 0.f;
+                        m = up <= 126.f ? m + up : top, l *= by;
+                        const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
 #pragma unroll 1
-                            for (int j = 0; j < D; j += 8) {
-                                uint32_t o[8];
-                                tmem_ld8(to + j, o);
+                        for (int j = 0; j < h * 32; j += 8) {
+                            uint32_t y[8];
+                            tmem_ld8(ts + j, y);
 #pragma unroll
-                                for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-                                tmem_st8(to + j, o);
+                            for (int e = 0; e < 8; e++) {
+                                const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&y[e]), by2);
+                                y[e] = *reinterpret_cast<const uint32_t*>(&z);
                             }
+                            tmem_st8(ts + j, y);
+                        }
+#pragma unroll 1
+                        for (int j = 0; i > 0 && j < D; j += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(to + j, o);
+#pragma unroll
+                            for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                            tmem_st8(to + j, o);
                         }
                     }
                     l += sum;
@@ -221,14 +232,11 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                     tmem_st16(ts + h * 32 + 16, p + 16);
                     tmem_st_wait();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p + 2 * h + str);
             }
-        } else {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_p + str), mbar_arrive(b_p + 2 + str);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + str);
     }
     return make_float2(m, l);
 }
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kSt = L::kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
     Bars<kSt>& bar = *(Bars<kSt>*)(sm + L::kBar);
-    uint64_t *b_full = bar.full, *b_empty = bar.empty, *b_vready = bar.vready, *b_s = bar.s, *b_p = bar.p[0], *b_h = bar.h, *b_q = &bar.q,
+    uint64_t *b_full = bar.full, *b_empty = bar.empty, *b_s = bar.s, *b_p = bar.p, *b_q = &bar.q,
              *b_o = &bar.o, *b_end = &bar.end;
     TileInfo* info = (TileInfo*)(sm + L::kInfo);
     uint32_t *vis = (uint32_t*)(sm + L::kVis), *odds = (uint32_t*)(sm + L::kOdd);
@@ -259,9 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_alloc(tmem_slot, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSt; i++) mbar_init(b_full + i, 1), mbar_init(b_empty + i, 1);
-        for (int i = 0; i < 8; i++) mbar_init(b_vready + i, 1);
-        for (int i = 0; i < 4; i++) mbar_init(b_p + i, 4);  // [half][stream]
-        for (int i = 0; i < 2; i++) mbar_init(b_s + i, 1), mbar_init(b_h + i, 1);
+        for (int i = 0; i < 2; i++) mbar_init(b_s + i, 1), mbar_init(b_p + i, 5);
         mbar_init(b_q, 8);
         mbar_init(b_o, 1);
         mbar_init(b_end, 1);
@@ -451,69 +457,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool pair = min(kWideRows, run.x.rows - r0) > 128;
             const int jobs = pair ? 2 * nt : nt;  // a tile for a stream: the streams by turns
             auto tile_of = [&](int j) { return n + (pair ? j >> 1 : j); };
-            auto keys = [&](int j) {
-                const int fill = 2 * tile_of(j);
-                wait(b_full + fill % kSt, fill / kSt);
-            };
-            auto scores = [&](int j) {
-                const int str = j & 1, tile = tile_of(j), stage = 2 * tile % kSt;
-                const int blocks = info[tile & (kInfos - 1)].blocks;
-                if (chosen && ok) {
-                    const uint32_t id = id_s | (uint32_t)(2 * blocks) << 17, ka = k_lo + ((L::kRing + stage * L::kOperand) >> 4),
-                                   qa = k_lo + ((L::kQ + str * L::kOperand) >> 4);
+            auto scores = [&](int j, int stage, int blocks) {
+                const int str = j & 1;
+                const bool go = chosen && ok;
+                const uint32_t id = id_s | (uint32_t)(2 * blocks) << 17, ka = k_lo + ((L::kRing + stage * L::kOperand) >> 4),
+                               qa = k_lo + ((L::kQ + str * L::kOperand) >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++) {
-                        const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-                        mma_ss(tmem + str * 128, qa + at, ka + at, k_hi, id, k > 0);
-                    }
-                    mma_commit(b_s + str);
-                    if (!pair || str) mma_commit(b_empty + stage);
+                for (int k = 0; k < D / 16; k++) {
+                    const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                    mma_ss_if(go, tmem + str * 128, qa + at, ka + at, k_hi, id, k > 0);
                 }
-                __syncwarp();
+                commit_if(go, b_s + str);
+                commit_if(go && (!pair || str), b_empty + stage);
             };
+            auto blocks_of_tile = [&](int tile) { return info[tile & (kInfos - 1)].blocks; };
             wait(b_q, segs);
-            keys(0);
-            tc_fence_after();
-            scores(0);
-            if (jobs > 1) keys(1), tc_fence_after(), scores(1);
+            for (int j = 0; j < min(jobs, 2); j++) {
+                const int tile = tile_of(j), fill = 2 * tile;
+                wait(b_full + fill % kSt, fill / kSt);
+                tc_fence_after();
+                scores(j, fill % kSt, blocks_of_tile(tile));
+            }
 #pragma unroll 1
             for (int j = 0; j < jobs; j++) {
-                const int str = j & 1, tile = tile_of(j), stage = (2 * tile + 1) % kSt;
-                wait(b_vready + (tile & 7), tile >> 3);
-                const int blocks = info[tile & (kInfos - 1)].blocks, done = str ? weighed1 : weighed0;
+                const int str = j & 1, tile = tile_of(j), stage = (2 * tile + 1) % kSt, stage_k = 2 * tile_of(j + 2) % kSt;
                 const uint32_t va = v_lo + ((L::kRing + stage * L::kOperand) >> 4), d = tmem + kColO + str * 128, pa = tmem + str * 128;
-                auto half = [&](int h) {
-                    auto step16 = [&](int k) { mma_ts(d, pa + k * 8, va + ((k * 16 * 128) >> 4), v_hi, id_o, j > 1 || k > 0); };
-                    if (blocks >= 4 * h + 4) {
-#pragma unroll
-                        for (int k = 0; k < 4; k++) step16(4 * h + k);
-                    } else {
-#pragma unroll 1
-                        for (int k = 4 * h; k < blocks; k++) step16(k);
-                    }
-                };
-                wait(b_p + str, done);
-                tc_fence_after();
-                if (chosen && ok) {
-                    half(0);
-                    mma_commit(b_h + str);
-                }
-                __syncwarp();
-                if (j + 2 < jobs) keys(j + 2);  // (waited for here: nothing is to come between the weights and the next scores)
-                wait(b_p + 2 + str, done);
+                wait(b_p + str, str ? weighed1 : weighed0);
                 if (str) weighed1++;
                 else weighed0++;
+                const int blocks = blocks_of_tile(tile);
+                int next = blocks_of_tile(tile_of(j + 2));
                 tc_fence_after();
-                if (chosen && ok) {
-                    half(1);
-                    if (!pair || str) mma_commit(b_empty + stage);
+                const bool go = chosen && ok;
+                auto step16 = [&](int k) { mma_ts_if(go, d, pa + k * 8, va + ((k * 16 * 128) >> 4), v_hi, id_o, j > 1 || k > 0); };
+                if (blocks == 8) {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) step16(k);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < blocks; k++) step16(k);
                 }
-                __syncwarp();
+                commit_if(go && (!pair || str), b_empty + stage);
                 // (in the place of this tile's weights, behind their products)
-                if (j + 2 < jobs) scores(j + 2);
+                if (j + 2 < jobs) {
+                    if (!pair) wait(b_full + stage_k, 2 * tile_of(j + 2) / kSt), next = blocks_of_tile(tile_of(j + 2)), tc_fence_after();
+                    scores(j + 2, stage_k, next);
+                }
             }
-            if (chosen && ok) mma_commit(b_o);
-            __syncwarp();
+            commit_if(chosen && ok, b_o);
             n += nt;
             segs++;
         } while (run.next(a, s, pre));
@@ -579,13 +570,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 1; i <= kSt && i <= 2 * n; i++) mbar_drain(b_full + (2 * n - i) % kSt, ((2 * n - i) / kSt) & 1);
     } else if (work) {
         // ------------------------------------------------------- values cleared
+        // (and one word to the products for all that is to be there beside the weights)
+        int said0 = 0, said1 = 0;
         do {
-            if (run.t1 <= run.t0) continue;
+            const int nt = run.t1 - run.t0;
+            if (nt <= 0) continue;
+            const int g = run.item / run.x.mt, r0 = (run.item - g * run.x.mt) * kWideRows;
+            const bool pair = min(kWideRows, run.x.rows - r0) > 128;
             uint32_t* odd = odds + (segs & 7) * 4;
             if (lane < 4) odd[lane] = 0;
             __syncwarp();
-            for (int tile = run.t0; tile < run.t1; tile++, n++) {
-                const int fill = 2 * n + 1, stage = fill % kSt;
+            for (int i = 0; i < nt; i++, n++) {
+                const int fill = 2 * n + 1, stage = fill % kSt, after = fill + 1;
                 wait(b_full + stage, fill / kSt);
                 const TileInfo ti = info[n & (kInfos - 1)];
                 if (ti.part && ok) {
@@ -596,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int j0 = (code & 127) * 16, live = step ? min(16, a.T - j0) : (int)code;
                         if (live == 16 && (!step || a.T == 1)) continue;
 #pragma unroll
-                        for (int i = 0; i < 4 * L::kAtoms; i++) {
-                            const int piece = lane + 32 * i, r = (piece >> 3) & 15;
+                        for (int k = 0; k < 4 * L::kAtoms; k++) {
+                            const int piece = lane + 32 * k, r = (piece >> 3) & 15;
                             uint4* at = (uint4*)(v + (piece >> 7) * (128 * 128) + blk * 2048 + (piece & 127) * 16);
                             if (r >= live) *at = make_uint4(0, 0, 0, 0);
                             else if (step && a.T > 1) {
@@ -605,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t w[4] = {u.x, u.y, u.z, u.w};
                                 bool found = false;
 #pragma unroll
-                                for (int k = 0; k < 4; k++) {
-                                    const bool b0 = (w[k] & 0x7f80u) == 0x7f80u, b1 = (w[k] & 0x7f800000u) == 0x7f800000u;
-                                    if (b0) w[k] &= 0xffff0000u;
-                                    if (b1) w[k] &= 0x0000ffffu;
+                                for (int c = 0; c < 4; c++) {
+                                    const bool b0 = (w[c] & 0x7f80u) == 0x7f80u, b1 = (w[c] & 0x7f800000u) == 0x7f800000u;
+                                    if (b0) w[c] &= 0xffff0000u;
+                                    if (b1) w[c] &= 0x0000ffffu;
                                     found |= b0 || b1;
                                 }
                                 if (found) {
@@ -620,8 +616,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async();
                 }
+                // (where both streams use a tile, the next one's keys were asked for two tiles ago; else they may still
+                // be on their way, and the products with these values go first)
+                if (pair && i + 1 < nt) wait(b_full + after % kSt, after / kSt);
+                // (not into the phase of the tile before)
+                if (pair || !(i & 1)) {
+                    if (said0) wait(b_p, said0 - 1);
+                    said0++;
+                }
+                if (pair || (i & 1)) {
+                    if (said1) wait(b_p + 1, said1 - 1);
+                    said1++;
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_vready + (n & 7));
+                if (lane == 0) {
+                    if (pair || !(i & 1)) mbar_arrive(b_p);
+                    if (pair || (i & 1)) mbar_arrive(b_p + 1);
+                }
             }
             segs++;
         } while (run.next(a, s, pre));

@@ -319,6 +319,30 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
+// mma_ss, mma_ts and mma_commit where `go`, by predicates: the warp stays together.
+__device__ __forceinline__ void mma_ss_if(bool go, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 x, {%1, %3};\n"
+        " mov.b64 y, {%2, %3};\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)go));
+}
+__device__ __forceinline__ void mma_ts_if(bool go, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 y, {%2, %3};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)go));
+}
+__device__ __forceinline__ void commit_if(bool go, uint64_t* bar)
+{
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"((uint32_t)go)
+        : "memory");
+}
+
 // 64 consecutive columns of this thread's TMEM lane, as they are.
 __device__ __forceinline__ void tmem_ld64_raw(uint32_t taddr, uint32_t (&r)[64])
 {
