@@ -47,7 +47,7 @@ struct Kv16Sched {
     int first;                // the call's first kernel
     int beside;               // the other kernel's items run at the same time: the SMs are shared by their work
     Kv16Item* items;          // finish: [nteams]; else [KV heads][rows]: of prefixes, then of sequences
-    int* bad;                 // prefix_first is out of order: nothing is done
+    int* bad;                 // prefix_first is out of order, or there is too much to do: nothing is done
     float* slots;             // [nteams][2]: parts of split items
     float *whole, *whole_pre; // by row: results of sequences' and of prefixes' whole items
 };

@@ -23,7 +23,7 @@ int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int 
 namespace {
 // ------------------------------------------------------------------- merge ---
 
-constexpr int kMergeRows = 8, kMaxGroups = 4;
+constexpr int kMergeRows = 8, kMaxGroups = 2;
 
 struct MergeArgs {
     Kv16Attn a;
@@ -32,6 +32,9 @@ struct MergeArgs {
     const float *slots_pre, *slots_seq, *whole_pre, *whole_seq;
     int rows_pre_tile;        // rows of a prefix's item
     int by_rows;              // sequences' parts are rows (k_kv16_rows), else columns
+    int kernels;              // that said whether all is well
+    int teams, teams_pre;     // that may have parts (nothing else is read, whatever a workspace holds)
+    int chunks;               // 16s of rows of an item
 };
 
 struct Sum {
@@ -114,9 +117,10 @@ __device__ __forceinline__ void finish_rows(const Kv16Attn& a, Sum& y, bool live
     *(uint2*)dst = make_uint2(pack_bf16(y.o[0] * inv, y.o[1] * inv), pack_bf16(y.o[2] * inv, y.o[3] * inv));
 }
 
-// Joins the parts of items that several teams hold.  A CTA: 8 rows of the item
-// that team blockIdx.x begins; a warp: 16 of their channels and every groups-th
+// Joins the parts of items that several teams hold.  A CTA at a time: 16 rows of
+// the item that a team begins; a warp: 16 of their channels and every groups-th
 // part (8 rows x 4 lanes of 4 channels: whole sectors of either kind of part).
+// CTAs go through teams and rows by turns, the next item's record on its way.
 template <int D>
 __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_merge(const __grid_constant__ MergeArgs w)
 {
@@ -124,13 +128,28 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_merge(const __grid_
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
-    const int r = blockIdx.y * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, groups = blockDim.x / (kSlices * 32);
-    const Kv16Item it = w.items[blockIdx.x];
-    if (it.n == 0 || (int)blockIdx.y * kMergeRows >= it.rows) return;
-    const bool live = r < it.rows;
-    Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
-    if (live) add_parts<D>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r, ch, part, groups, y);
-    finish_rows<D>(w.a, y, live, part, groups, slice * 32 + lane, it.g, it.row + r, ch);
+    const int ch = slice * 16 + (lane >> 3) * 4, groups = blockDim.x / (kSlices * 32), all = w.teams * w.chunks;
+    auto record = [&](int i) { return i < all ? w.items[i / w.chunks] : Kv16Item{}; };
+    Kv16Item next = record(blockIdx.x);
+#pragma unroll 1
+    for (int i = blockIdx.x; i < all; i += gridDim.x) {
+        const Kv16Item it = next;
+        next = record(i + gridDim.x);
+        const int r0 = i % w.chunks * (2 * kMergeRows) + (lane & 7);
+        if (it.n <= 0 || it.t0 < 0 || it.n > w.teams - it.t0 || r0 - (lane & 7) >= it.rows) continue;
+        Sum y[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            y[k] = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
+            if (r0 + k * kMergeRows < it.rows) add_parts<D>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r0 + k * kMergeRows, ch, part, groups, y[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int r = r0 + k * kMergeRows;
+            finish_rows<D>(w.a, y[k], r < it.rows, part, groups, slice * 32 + lane, it.g, it.row + r, ch);
+            if (groups > 1) __syncthreads();
+        }
+    }
 }
 
 // Joins every row's own keys and its prefix's.  A CTA: 8 rows of a KV head.
@@ -139,17 +158,18 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_c
 {
     constexpr int kSlices = D / 16;
     pdl_wait();
+    fence_acquire();  // (of both kernels before it)
     pdl_trigger();
     const Kv16Attn& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
     const int gr = blockIdx.x * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, g = blockIdx.y, rows_all = a.B * a.R;
     const int groups = blockDim.x / (kSlices * 32);
     Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
-    bool live = gr < rows_all && !*w.bad;
+    bool live = gr < rows_all && !w.bad[0] && !w.bad[w.kernels - 1];
     if (live) {
         const int row0 = gr / a.R * a.R;
         const Kv16Item it = w.items[(size_t)(a.Hkv + g) * rows_all + row0];
-        live = it.n > 0;
+        live = it.n > 0 && it.t0 >= 0 && it.n <= w.teams - it.t0;
         auto add_whole = [&](const float* whole, bool by_rows) {
             float v[4];
             if (by_rows) {
@@ -171,7 +191,7 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_c
             if (it.pre_row >= 0) {
                 const int first = it.pre_row + (gr - it.pre_row) / w.rows_pre_tile * w.rows_pre_tile;
                 const Kv16Item p = w.items[(size_t)g * rows_all + first];
-                if (p.n > 1) add_parts<D>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
+                if (p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) add_parts<D>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
                 else if (part == groups - 1) add_whole(w.whole_pre, false);
             }
         }
@@ -186,7 +206,7 @@ struct Plan {
     Kv16Sched wide, rows;
     MergeArgs m;
     bool use_wide, use_rows, apart, merge;
-    int teams, row_tile, groups;  // of the merge
+    int groups;  // of the merge
     size_t bytes;
 };
 
@@ -234,7 +254,7 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
         Kv16Sched& s = p.rows;
         s.n_seq = k.B, s.row_tile = 16, s.wide = 1 << 30, s.extra = 2;
         const long long items = (long long)k.B * k.Hkv;
-        s.nteams = kv16_rows_teams(), s.per_cta = kv16_rows_teams() / kSMs, s.min_run = 16, s.slack = 16;
+        s.nteams = kv16_rows_teams(), s.per_cta = kv16_rows_teams() / kSMs, s.min_run = 8, s.slack = 16;
         if (!p.apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.direct = 1;
     }
     // ---- where their results go
@@ -242,7 +262,7 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     (p.use_wide ? p.wide : p.rows).first = 1;
     const size_t all = (size_t)k.Hkv * rows_all * (D + 2) * 4;  // results of whole items
     if (p.apart) {
-        p.m.bad = (int*)room(4);
+        p.m.bad = (int*)room(8);
         p.m.items = (Kv16Item*)room(2 * (size_t)k.Hkv * rows_all * sizeof(Kv16Item));
         p.m.whole_pre = (float*)room(all), p.m.whole_seq = (float*)room(all);
         p.wide.beside = p.rows.beside = p.use_rows;
@@ -253,16 +273,18 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     if (p.use_wide && !p.wide.direct) p.wide.slots = (float*)room((size_t)p.wide.nteams * 2 * wide_part(D) * 4);
     if (p.use_rows && !p.rows.direct) p.rows.slots = (float*)room((size_t)p.rows.nteams * 2 * rows_part(D, k.R) * 4);
     for (Kv16Sched* s : {&p.wide, &p.rows}) {
-        s->items = (Kv16Item*)p.m.items, s->bad = (int*)p.m.bad;
+        s->items = (Kv16Item*)p.m.items;
+        if (p.apart) s->bad = (int*)p.m.bad + (s->first ? 0 : 1);
         s->whole = (float*)p.m.whole_seq, s->whole_pre = (float*)p.m.whole_pre;
     }
     p.m.slots_pre = p.wide.slots, p.m.slots_seq = last.slots;
     p.m.rows_pre_tile = kWideRows, p.m.by_rows = p.use_rows;
     p.merge = !last.direct;
-    p.teams = last.nteams, p.row_tile = std::min(last.row_tile, k.R);
+    p.m.kernels = p.use_rows && p.use_wide ? 2 : 1;
+    p.m.teams = last.nteams, p.m.teams_pre = p.wide.nteams, p.m.chunks = (std::min(last.row_tile, k.R) + 2 * kMergeRows - 1) / (2 * kMergeRows);
     // as many groups of warps as an item may have fours of parts
     const long long parts = (p.use_wide ? p.wide.nteams : p.rows.nteams) / std::max(1LL, (long long)k.Hkv * (p.apart ? (rows_all + 255) / 256 : k.B));
-    p.groups = parts >= 12 ? 4 : parts >= 6 ? 2 : 1;
+    p.groups = parts >= 6 ? 2 : 1;
     p.bytes = at;
     return p;
 }
@@ -272,7 +294,7 @@ cudaError_t launch_merge(cudaStream_t s, const Plan& p)
 {
     const dim3 block(D * 2 * p.groups);
     if (p.apart) return launch_pdl(k_kv16_join<D>, dim3((p.k.B * p.k.R + kMergeRows - 1) / kMergeRows, p.k.Hkv), block, 0, s, p.m);
-    return launch_pdl(k_kv16_merge<D>, dim3(p.teams, (p.row_tile + kMergeRows - 1) / kMergeRows), block, 0, s, p.m);
+    return launch_pdl(k_kv16_merge<D>, dim3(std::min(p.m.teams * p.m.chunks, kSMs * 1024 / (int)block.x)), block, 0, s, p.m);
 }
 
 bool init()

@@ -83,14 +83,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
     Start* starts = (Start*)(sc + 1);
     PreShared* ps = (PreShared*)(starts + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    // As the call's second kernel it needs nothing of the first, whose CTAs have all seen the calls before it end.
+    // As the call's second kernel it needs nothing of the first, whose CTAs have all seen the calls before it
+    // end: what these wrote is in L2, and the fence drops what L1 held of it before.
     if (s.first) pdl_wait();
+    else fence_acquire();
     pdl_trigger();
     const Prefixes pre = find_starts<D>(a, s, starts, sc, ps);
     const Shares sh = sc->shares;
-    const int team = blockIdx.x * kWarps + warp;
-    if (s.finish && s.items && lane == 0 && team < s.nteams) s.items[team].n = 0;
     const Start st = starts[warp];
+    const int team = st.team;
+    if (s.finish && s.items && lane == 0) {
+        const int id = blockIdx.x * kWarps + warp;  // (every entry is written by one warp)
+        if (id >= sh.nteams && id < s.nteams) s.items[id].n = 0;
+        if (st.count > 0) s.items[team].n = 0;
+    }
     if (st.count > 0) {
         const uint32_t ring = smem_u32(sm) + warp * (L::kStages * 2 * L::kSide);
         int* info = (int*)(sm + L::kInfo) + warp * L::kStages;
@@ -98,7 +104,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
         // ---- feeding
         Run f;
         f.begin(a, s, pre, st, sh);
+        Run c = f;
         bool feeding = true;
+        const int pc = lane % kPieces, r0 = lane / kPieces;
         int fk = f.t0, stage_in = 0, window = -1, page_of = 0;
         auto start_feed = [&]() {
             fk = f.t0;
@@ -148,15 +156,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                     k_row = a.k_ld, v_row = a.v_ld;
                     if (lane == 0) info[stage_in] = live | 256;
                 }
-                const uint32_t dst = ring + stage_in * (2 * L::kSide);
-                const int pc = lane % kPieces, r0 = lane / kPieces;
+                const uint32_t dst = ring + stage_in * (2 * L::kSide) + r0 * (D * 2);
+                const char *k8 = (const char*)(k + r0 * k_row + pc * 8), *v8 = (const char*)(v + r0 * v_row + pc * 8);
+                const size_t k_step = k_row * (2 * kRowsPass), v_step = v_row * (2 * kRowsPass);
 #pragma unroll
                 for (int i = 0; i < 16 / kRowsPass; i++) {
-                    const int row = r0 + i * kRowsPass;
-                    const bool there = row < live;
-                    const uint32_t at = dst + row * (D * 2) + ((pc ^ (row & 7)) << 4);
-                    cp16(at, k + (there ? row * k_row : 0) + pc * 8, there);
-                    cp16(at + L::kSide, v + (there ? row * v_row : 0) + pc * 8, there);
+                    const bool there = r0 + i * kRowsPass < live;
+                    const uint32_t at = dst + i * (kRowsPass * D * 2) + ((pc ^ ((r0 + i * kRowsPass) & 7)) << 4);
+                    cp16(at, there ? k8 + i * k_step : (const char*)a.kp, there);
+                    cp16(at + L::kSide, there ? v8 + i * v_step : (const char*)a.kp, there);
                 }
                 fk++;
             }
@@ -179,8 +187,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
         const int vrow = (lane & 7) + (lane & 8), vpc = lane >> 4;
         const uint32_t k_at = krow * (D * 2), v_at = L::kSide + vrow * (D * 2);
         int stage = 0;
-        Run c;
-        c.begin(a, s, pre, st, sh);
         do {
             if (c.t1 <= c.t0) {
                 // (units, but no keys)

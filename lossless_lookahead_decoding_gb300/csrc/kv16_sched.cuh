@@ -26,6 +26,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void fence_acquire() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 __device__ __forceinline__ int blocks_of(int n) { return (n + 15) >> 4; }
 
 // The prefixes' bounds and lengths, copied to shared memory where they fit.
@@ -88,29 +90,20 @@ __device__ __forceinline__ Entry entry_of(const Kv16Attn& a, const Kv16Sched& s,
 // The first tile at or behind unit u of an item.
 __device__ __forceinline__ int tile_at(const Kv16Sched& s, const Entry& x, int u) { return max(u - s.extra + x.wide, 0) >> x.wide; }
 
-__device__ __noinline__ long long div_long(long long a, long long b) { return a / b; }
-
-__device__ __forceinline__ long long div_units(long long a, long long b)
-{
-    // (a 64-bit division takes half a microsecond)
-    return (a | b) < (1LL << 32) ? (long long)((uint32_t)a / (uint32_t)b) : div_long(a, b);
-}
-
-// The teams' runs: team t begins at unit q t + min(t, r).
+// The teams' runs: team t begins at unit q t + min(t, r).  (All units fit 31 bits,
+// or nothing is done: 64-bit sums and divisions took most of a small call's time.)
 struct Shares {
-    long long q;
-    int r, nteams, whole;  // whole: a unit is a whole item
-    __device__ __forceinline__ long long at(int t) const { return q * t + min(t, r); }
-    __device__ __forceinline__ int team_of(long long u) const  // that holds unit u
+    int q, r, nteams, whole;  // whole: a unit is a whole item
+    __device__ __forceinline__ int at(int t) const { return q * t + min(t, r); }
+    __device__ __forceinline__ int team_of(int u) const  // that holds unit u
     {
-        const long long wide = (q + 1) * r;
-        return (int)(u < wide ? div_units(u, q + 1) : r + div_units(u - wide, q));
+        const int wide = (q + 1) * r;
+        return u < wide ? (int)((unsigned)u / (unsigned)(q + 1)) : r + (int)((unsigned)(u - wide) / (unsigned)q);
     }
 };
 
 struct Start {
-    int e, pad;
-    long long off, count;  // offset in the units of entry e's items; units of the team
+    int e, off, count, team;  // entry, offset in the units of its items; units of the team
 };
 
 struct PreShared {
@@ -119,23 +112,22 @@ struct PreShared {
 };
 
 struct Scan {
-    long long units[32], cost[32];
-    int items[32], top[32];
+    int units[32], big[32], cost[32], items[32], top[32];
     Shares shares;
 };
 
 // Costs of a unit of k_kv16_wide and of k_kv16_rows in SM time (a tile for a
 // stream beside a kernel that saturates HBM 2.3 us; a block's bytes at the card's
 // rate by 152).
-__device__ __forceinline__ int unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2 : 1) : 25; }
+__device__ __forceinline__ float unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2.f : 1.f) : 25.f; }
 
 // Where each of the CTA's teams begins; the shares go to sc.  CTA 0 of the
 // call's first kernel raises what is wrong with the sequences.
 template <int D>
 __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* starts, Scan* sc, PreShared* ps)
 {
-    const int t0 = blockIdx.x * s.per_cta, n = s.per_cta;
-    const int entries = s.n_pre + s.n_seq, per = ceil_div(entries, (int)blockDim.x), e0 = threadIdx.x * per, e1 = min(e0 + per, entries);
+    const int n = s.per_cta, entries = s.n_pre + s.n_seq;
+    const int per = entries <= (int)blockDim.x ? 1 : ceil_div(entries, (int)blockDim.x), e0 = threadIdx.x * per, e1 = min(e0 + per, entries);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     // ---- all loads at once
     const int len0 = !s.direct && e0 < e1 && e0 >= s.n_pre ? a.lens[e0 - s.n_pre] : 0;
@@ -157,74 +149,74 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
     const Prefixes pre = fits ? Prefixes{ps->first, ps->lens} : Prefixes{a.pfirst, a.plens};
     if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
     bad = __syncthreads_or(bad);
-    if (s.bad && s.first && blockIdx.x == 0 && threadIdx.x == 0) *s.bad = bad;
     if (s.direct) {
-        const int mt = (a.R + s.row_tile - 1) / s.row_tile, each = a.Hkv * mt;
+        const int mt = (a.R + s.row_tile - 1) / s.row_tile, each = a.Hkv * mt, t = blockIdx.x * n + threadIdx.x;
         if (threadIdx.x == 0) sc->shares = Shares{1, 0, s.nteams, 1};
-        if ((int)threadIdx.x < n && t0 + (int)threadIdx.x < s.nteams && !bad) {
-            const int t = t0 + threadIdx.x;
-            starts[threadIdx.x] = Start{t / each, 0, t % each, 1};
+        if ((int)threadIdx.x < n && t < s.nteams && !bad) {
+            const int e = (unsigned)t / (unsigned)each;
+            starts[threadIdx.x] = Start{e, t - e * each, 1, t};
         }
         __syncthreads();
         return pre;
     }
-    long long units = 0, cost = 0;
-    int items = 0, top = 0;
+    long long sum = 0;
+    int items = 0, top = 0, cost = 0;
     Entry x0;
     x0.mt = x0.nu = 0;
     if (!bad) {
         for (int e = e0; e < e1; e++) {
-            const Entry x = e == e0 ? entry_with(a, s, pre, e, len0) : entry_of(a, s, pre, e);
+            const Entry x = entry_with(a, s, pre, e, e == e0 || e < s.n_pre ? len0 : a.lens[e - s.n_pre]);
             const int k = a.Hkv * x.mt;
             if (e == e0) x0 = x;
-            if (x.nu) units += (long long)k * x.nu, items = min(items + k, 1 << 20), top = max(top, x.nu);
+            if (x.nu) sum += (long long)k * x.nu, items = min(items + k, 1 << 20), top = max(top, x.nu);
             else if (!s.finish && x.b >= 0 && blockIdx.x == 0)
                 // no rows, which the merge is to know
                 for (int g = 0; g < a.Hkv; g++) s.items[(size_t)(a.Hkv + g) * a.B * a.R + x.row0].n = 0;
         }
         if (s.beside) {
-            // the other kernel's work
+            // the other kernel's work, by KV heads
             if (s.n_pre)
-                for (int b = threadIdx.x; b < a.B; b += blockDim.x) cost += (long long)a.Hkv * (blocks_of(min(max(a.lens[b], 0), a.max_len)) + 3);
+                for (int b = threadIdx.x; b < a.B; b += blockDim.x) cost += blocks_of(min(max(a.lens[b], 0), a.max_len)) + 3;
             else
                 for (int p = threadIdx.x; p < a.nP; p += blockDim.x) {
                     const int rows = (pre.first[p + 1] - pre.first[p]) * a.R, m = min(max(pre.lens[p], 0), a.max_plen);
-                    cost += (long long)a.Hkv * ((rows + 255) / 256) * (4 + ((blocks_of(m) + 7) / 8 << (rows > 128)));
+                    cost += (rows + 255) / 256 * (4 + ((blocks_of(m) + 7) / 8 << (rows > 128)));
                 }
         }
     }
-    long long xu = units;
+    const int units = (int)min(sum, 1LL << 30);
+    int xu = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long yu = __shfl_up_sync(0xffffffffu, xu, o);
-        if (lane >= o) xu += yu;
+        const int y = __shfl_up_sync(0xffffffffu, xu, o);
+        if (lane >= o) xu += y;
     }
-    if (s.beside) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+    {
+        const int w_big = __reduce_add_sync(0xffffffffu, (int)min(sum >> 16, 1LL << 20)), w_cost = __reduce_add_sync(0xffffffffu, cost),
+                  w_items = __reduce_add_sync(0xffffffffu, items), w_top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 31) sc->units[warp] = xu, sc->big[warp] = w_big, sc->items[warp] = w_items, sc->top[warp] = w_top, sc->cost[warp] = w_cost;
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    const int w_items = __reduce_add_sync(0xffffffffu, items);
-    if (lane == 31) sc->units[warp] = xu, sc->items[warp] = w_items, sc->top[warp] = top, sc->cost[warp] = cost;
     __syncthreads();
-    long long before = xu - units, all_u = 0, all_c = 0;
-    int all_i = 0;
-    for (int w = 0; w < nw; w++) {
-        const long long u = sc->units[w];
-        if (w < warp) before += u;
-        all_u += u, all_c += sc->cost[w], all_i = min(all_i + sc->items[w], 1 << 20), top = max(top, sc->top[w]);
-    }
-    int room = s.nteams;
+    const bool in = lane < nw;
+    const int u = in ? sc->units[lane] : 0, it = in ? sc->items[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? u : 0) + xu - units, all_u = __reduce_add_sync(0xffffffffu, u);
+    const int all_i = __reduce_add_sync(0xffffffffu, it);
+    top = __reduce_max_sync(0xffffffffu, in ? sc->top[lane] : 0);
+    const bool huge = __reduce_add_sync(0xffffffffu, in ? sc->big[lane] : 0) >= 0x7000;
+    if (huge && blockIdx.x == 0 && threadIdx.x == 0) kv4_raise(a.status, LA_ERR_ARG);
+    if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) *s.bad = bad || huge;
+    int ctas = gridDim.x;
     if (s.beside) {
         // Both kernels count alike: the wide one takes a share of the SMs by its work (and a quarter more: its
         // last item is the call's end), the rows' one the others; not where it would need most of them.
-        const long long mine = all_u * unit_cost(s.n_pre == 0, D), other = all_c * unit_cost(s.n_pre != 0, D);
-        const long long wide = s.n_pre ? mine : other, sum = max(mine + other, 1LL);
-        const int sms = (int)div_long(wide * kSMs * 5 / 4, sum) + 1;
-        if (sms <= kSMs * 3 / 4) room = (s.n_pre ? sms : kSMs - sms) * s.per_cta;
+        const float mine = (float)all_u * unit_cost(s.n_pre == 0, D),
+                    other = (float)__reduce_add_sync(0xffffffffu, in ? sc->cost[lane] : 0) * (float)a.Hkv * unit_cost(s.n_pre != 0, D);
+        const int sms = (int)((s.n_pre ? mine : other) * (kSMs * 1.25f) / fmaxf(mine + other, 1.f)) + 1;
+        if (sms <= kSMs * 3 / 4) ctas = s.n_pre ? sms : kSMs - sms;
     }
+    const int room = min(s.nteams, ctas * n);
     Shares h;
-    h.whole = all_i <= room && top - s.slack <= div_units(all_u, room);
+    h.whole = all_i <= room && top - s.slack <= (int)((unsigned)all_u / (unsigned)room);
     int bi = 0;
     if (h.whole) {
         // the same for whole items (few: there is a team for each)
@@ -234,29 +226,29 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
             const int y = __shfl_up_sync(0xffffffffu, xi, o);
             if (lane >= o) xi += y;
         }
-        bi = xi - items;
-        for (int w = 0; w < warp; w++) bi += sc->items[w];
+        bi = xi - items + __reduce_add_sync(0xffffffffu, lane < warp ? it : 0);
     }
-    const long long all = h.whole ? all_i : all_u;
-    h.nteams = h.whole ? all_i : (int)min((long long)room, max(1LL, div_units(all, s.min_run)));
-    if (all == 0) h.nteams = 0;
-    h.q = h.nteams ? div_units(all, h.nteams) : 0;
-    h.r = (int)(all - h.q * h.nteams);
+    const int all = huge ? 0 : h.whole ? all_i : all_u;
+    h.nteams = all == 0 ? 0 : h.whole ? all_i : min(room, max(1, (int)((unsigned)all / (unsigned)s.min_run)));
+    h.q = h.nteams ? (int)((unsigned)all / (unsigned)h.nteams) : 0;
+    h.r = all - h.q * h.nteams;
     if (threadIdx.x == 0) sc->shares = h;
     if (h.nteams && units) {
-        long long at = h.whole ? bi : before;
-        const long long end = at + (h.whole ? items : units);
+        int at = h.whole ? bi : before;
+        const int end = at + (h.whole ? items : units);
+        // the CTAs' teams by turns: few teams are spread over the SMs
         int i = 0;
+        auto team = [&](int j) { return j * ctas + (int)blockIdx.x; };
         // the teams that begin within this thread's entries
-        while (i < n && (t0 + i >= h.nteams || h.at(t0 + i) < at)) i++;
-        if (i < n && h.at(t0 + i) < end)
+        while (i < n && (int)blockIdx.x < ctas && team(i) < h.nteams && h.at(team(i)) < at) i++;
+        if (i < n && (int)blockIdx.x < ctas && team(i) < h.nteams && h.at(team(i)) < end)
             for (int e = e0; e < e1; e++) {
                 const Entry x = e == e0 ? x0 : entry_of(a, s, pre, e);
-                const long long c = (long long)a.Hkv * x.mt * (h.whole ? x.nu > 0 : x.nu);
-                for (; i < n && t0 + i < h.nteams; i++) {
-                    const long long u0 = h.at(t0 + i);
+                const int c = a.Hkv * x.mt * (h.whole ? x.nu > 0 : x.nu);
+                for (; i < n && team(i) < h.nteams; i++) {
+                    const int u0 = h.at(team(i));
                     if (u0 >= at + c) break;
-                    starts[i] = Start{e, 0, u0 - at, h.at(t0 + i + 1) - u0};
+                    starts[i] = Start{e, u0 - at, h.at(team(i) + 1) - u0, team(i)};
                 }
                 at += c;
             }
@@ -270,12 +262,12 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
 struct Run {
     Entry x;
     int e, item, whole, u0, u1, nu, t0, t1;
-    long long left;
+    int left;
     __device__ __forceinline__ void cut(const Kv16Sched& s, int from)
     {
         nu = whole ? 1 : x.nu;
         u0 = from;
-        u1 = (int)min((long long)nu, u0 + left);
+        u1 = min(nu, u0 + left);
         left -= u1 - u0;
         t0 = whole ? 0 : tile_at(s, x, u0);
         t1 = whole ? x.tiles : tile_at(s, x, u1);
@@ -286,8 +278,8 @@ struct Run {
         left = st.count, whole = h.whole, e = st.e;
         x = entry_of(a, s, pre, e);
         const int n = whole ? 1 : x.nu;
-        item = (int)div_units(st.off, n);
-        cut(s, (int)(st.off - (long long)item * n));
+        item = (unsigned)st.off / (unsigned)max(n, 1);
+        cut(s, st.off - item * n);
     }
     __device__ __forceinline__ bool next(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre)
     {

@@ -319,13 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int segs = 0;  // runs with tiles so far
     Run run;
     if (work) run.begin(a, s, pre, st, sh);
-    if (!work && threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
+    if (threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
     if (work && warp < 8) {
         // ------------------------------------------------------------ softmax
         const int q = warp & 3, str = warp >> 2, row = q * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16), to = trow + kColO + str * 128;
         int done = 0;  // this stream's tiles so far
-        if (threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
         do {
             const int nt = run.t1 - run.t0;
             if (run.x.nu && threadIdx.x == 0) run.note(a, s, pre, sh, blockIdx.x);
