@@ -27,7 +27,7 @@ constexpr int kWarps = 8;
 template <int D>
 struct RowsSmem {
     static constexpr int kSide = 16 * D * 2;               // a block's keys, or its values
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int kRing = kWarps * kStages * 2 * kSide;
     static constexpr int kInfo = kRing;                    // of each stage: keys | step << 8
     static constexpr int kMisc = kInfo + kWarps * kStages * 4;

@@ -119,7 +119,7 @@ struct Scan {
 // Costs of a unit of k_kv16_wide and of k_kv16_rows in SM time (a tile for a
 // stream beside a kernel that saturates HBM 2.3 us; a block's bytes at the card's
 // rate by 152).
-__device__ __forceinline__ float unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2.f : 1.f) : 25.f; }
+__device__ __forceinline__ float unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2.f : 1.f) : 30.f; }
 
 // Where each of the CTA's teams begins; the shares go to sc.  CTA 0 of the
 // call's first kernel raises what is wrong with the sequences.

@@ -581,6 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             for (int i = 0; i < nt; i++, n++) {
                 const int fill = 2 * n + 1, stage = fill % kSt, after = fill + 1;
+                // (the keys, too, although nothing here needs them: loads end in any order, and a stage whose last fill
+                // was not waited for could be two phases behind, which its parity does not tell from here)
+                wait(b_full + (fill - 1) % kSt, (fill - 1) / kSt);
                 wait(b_full + stage, fill / kSt);
                 const TileInfo ti = info[n & (kInfos - 1)];
                 if (ti.part && ok) {

@@ -472,6 +472,25 @@ def test_attention_equal_calls_give_equal_bits_in_graphs_and_streams():
         c["cache"].check()
 
 
+@pytest.mark.parametrize("heads,kv_heads,D,W,N,G", [(32, 32, 128, 0, 2, 0), (16, 16, 64, 0, 2, 0), (8, 8, 128, 3, 3, 3)])
+def test_attention_many_times_under_load(heads, kv_heads, D, W, N, G):
+    """A batch whose prefix and sequences contend for memory, so that loads end in other orders: equal bits every time."""
+    import torch
+    g = np.random.default_rng(12)
+    c = _case(g.integers(1, 256, 100).tolist(), [(1000, 60), (777, 40)], heads, kv_heads, D, 64, W, N, G, seed=12)
+    first = _call(c).clone()
+    c["cache"].check()
+    _compare(c, first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            _call(c)
+    for _ in range(10):
+        graph.replay()
+        assert torch.equal(c["out"], first)
+    c["cache"].check()
+
+
 def test_attention_pages_past_32_bits():
     """Pages whose elements lie past 2^32 from the arrays' start."""
     import torch
