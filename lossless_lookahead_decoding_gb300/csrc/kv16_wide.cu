@@ -23,7 +23,7 @@
 // the end.
 //
 // One CTA per SM: warps 0-3 and 4-7 the streams' softmax (a row per thread), 8
-// issues the products, 9 the copies, 10 clears values.
+// issues the products, 9 and 11 the copies of keys and of values, 10 clears values.
 #include <cudaTypedefs.h>
 
 #include "kv16_sched.cuh"
@@ -31,11 +31,12 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kInfos = 8;
 constexpr uint32_t kColO = 256;  // tensor memory: S [2][128] (P in their place), O [2][128]
 
-// What is known of a tile; eight in turn.
+// What is known of a tile; eight in turn, of its keys and of its values (which may
+// be there first).
 struct alignas(16) TileInfo {
     uint32_t code[2];  // a byte for each block: keys, or 128 + number of the step's block; 0: none
     int blocks, part;  // blocks; are scores to be left out
@@ -57,7 +58,7 @@ struct WideSmem {
     static constexpr int kVis = kRing + kStages * kOperand;  // [step row][4]: step rows it sees
     static constexpr int kBar = kVis + 128 * 16;
     static constexpr int kInfo = (kBar + (int)sizeof(Bars<kStages>) + 15) / 16 * 16;
-    static constexpr int kOdd = kInfo + kInfos * (int)sizeof(TileInfo);  // [run][4]: step rows whose values are not finite
+    static constexpr int kOdd = kInfo + 2 * kInfos * (int)sizeof(TileInfo);  // [run][4]: step rows whose values are not finite
     static constexpr int kMisc = kOdd + 8 * 16;
     static constexpr int kPre = kMisc + 16;
     static constexpr int kBytes = kPre + (int)sizeof(PreShared);
@@ -241,8 +242,9 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
     return make_float2(m, l);
 }
 
+// Tensor maps of keys and values: blocks of 16 rows of the step and of pages, and whole pages.
 struct Maps {
-    CUtensorMap kp, vp, ks, vs;
+    CUtensorMap step[2], block[2], page[2];
 };
 
 template <int D>
@@ -274,10 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (threadIdx.x >= 32 && threadIdx.x < 36) {
-        const CUtensorMap* m[4] = {&maps.kp, &maps.vp, &maps.ks, &maps.vs};
-        prefetch_map(m[threadIdx.x - 32]);
-    }
+    if (threadIdx.x >= 32 && threadIdx.x < 38) prefetch_map(&maps.step[0] + (threadIdx.x - 32));
     if (s.n_seq)
         for (int i = threadIdx.x - 64; i >= 0 && i < a.T; i += kThreads) {
             // the step rows that step row i sees (the mask), as bits
@@ -513,11 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_drain(b_end, 0);
         }
         __syncwarp();
-    } else if (work && warp == 9) {
+    } else if (work && (warp == 9 || warp == 11)) {
         // -------------------------------------------------------------- copies
+        // A lane for each block and half of the channels; where a page's blocks are in the tile side by side, the
+        // first block's lane brings all of them (a warp of lanes with a box of 16 rows each brings 40 GB/s, two
+        // warps 56, one with boxes of 64 rows 68).
         const uint64_t pol = policy_evict_normal();
         constexpr int kAtoms = L::kAtoms;
-        const int blk = lane / kAtoms, atom = lane % kAtoms;
+        const int v = warp == 11, blk = lane / kAtoms, atom = lane % kAtoms, per_page = 1 << (a.page_log2 - 4);
         do {
             if (run.t1 <= run.t0) continue;
             const Entry& x = run.x;
@@ -535,38 +537,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tile + 1 < run.t1) next = page_of(kb + 8);
                 const bool mine = blk < blocks, cached = mine && kb < nc, own = kb >= x.nb_pre;
                 const bool bad = cached && (unsigned)page >= (unsigned)a.n_pages;
-                const int tok = (own ? kb - x.nb_pre : kb) * 16, live = cached ? min(16, (own ? x.len : x.plen) - tok) : min(16, a.T - (kb - nc) * 16);
-                const uint32_t code = !mine || bad ? 0u : cached ? (uint32_t)live : 128u + (kb - nc);
-                const uint32_t mask = atom == 0 && blk < 8 ? code << (8 * (blk & 3)) : 0u;
-                const uint32_t lo = __reduce_or_sync(0xffffffffu, blk < 4 ? mask : 0u), hi = __reduce_or_sync(0xffffffffu, blk < 4 ? 0u : mask);
-                const bool part = __any_sync(0xffffffffu, blk < 8 && code != 16);
+                const int sb = own ? kb - x.nb_pre : kb, segment = own ? nc - x.nb_pre : x.nb_pre;  // of the segment's blocks
+                const int tok = sb * 16, live = cached ? min(16, (own ? x.len : x.plen) - tok) : min(16, a.T - (kb - nc) * 16);
+                const int in_page = sb & (per_page - 1), p0 = blk - in_page;  // the page's first block, in the tile
+                const bool whole = per_page > 1 && cached && p0 >= 0 && p0 + per_page <= 8 && sb - in_page + per_page <= segment;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, mine && !bad));
                 const int cx = (cached ? 0 : g * D) + atom * 64;
                 const int cy = cached ? (int)((((long long)page * a.Hkv + g) << a.page_log2) + (tok & ((1 << a.page_log2) - 1)))
                                       : x.b * a.T + (kb - nc) * 16;
-                if (bad) kv4_raise(a.status, LA_ERR_ARG);
-#pragma unroll
-                for (int v = 0; v < 2; v++) {
-                    const int fill = 2 * n + v, stage = fill % kSt;
-                    if (fill >= kSt) wait(b_empty + stage, fill / kSt - 1);
-                    if (!__all_sync(0xffffffffu, ok)) continue;
-                    if (lane == 0) {
-                        if (v == 0) {
-                            TileInfo* ti = info + (n & (kInfos - 1));
-                            ti->code[0] = lo, ti->code[1] = hi, ti->blocks = blocks, ti->part = part;
-                        }
-                        mbar_expect_tx(b_full + stage, boxes * 2048);
-                    }
-                    __syncwarp();
-                    if (mine && !bad)
-                        tma_load_2d(cached ? (v ? &maps.vp : &maps.kp) : (v ? &maps.vs : &maps.ks), b_full + stage,
-                                    sm + L::kRing + stage * L::kOperand + atom * (128 * 128) + blk * 2048, cx, cy, pol);
-                    __syncwarp();
+                const int fill = 2 * n + v, stage = fill % kSt;
+                if (fill >= kSt) wait(b_empty + stage, fill / kSt - 1);
+                const bool go = __all_sync(0xffffffffu, ok);
+                const uint32_t code = !mine || bad ? 0u : cached ? (uint32_t)live : 128u + (kb - nc);
+                const uint32_t mask = atom == 0 && blk < 8 ? code << (8 * (blk & 3)) : 0u;
+                const uint32_t lo = __reduce_or_sync(0xffffffffu, blk < 4 ? mask : 0u), hi = __reduce_or_sync(0xffffffffu, blk < 4 ? 0u : mask);
+                const bool part = __any_sync(0xffffffffu, blk < 8 && code != 16);
+                if (lane == 0 && go) {
+                    TileInfo* ti = info + v * kInfos + (n & (kInfos - 1));
+                    ti->code[0] = lo, ti->code[1] = hi, ti->blocks = blocks, ti->part = part;
                 }
+                if (bad) kv4_raise(a.status, LA_ERR_ARG);
+                if (!go) continue;
+                if (lane == 0) mbar_expect_tx(b_full + stage, boxes * 2048);
+                __syncwarp();
+                if (mine && !bad && (!whole || in_page == 0))
+                    tma_load_2d((cached ? whole ? maps.page : maps.block : maps.step) + v, b_full + stage,
+                                sm + L::kRing + stage * L::kOperand + atom * (128 * 128) + blk * 2048, cx, cy, pol);
+                __syncwarp();
             }
         } while (run.next(a, s, pre));
         // no copy may still be on its way when the CTA ends
-        for (int i = 1; i <= kSt && i <= 2 * n; i++) mbar_drain(b_full + (2 * n - i) % kSt, ((2 * n - i) / kSt) & 1);
+        // (a stage's last fill: before it the parity would be another's)
+        for (int fill = 2 * (n - 1) + v; fill >= 0 && fill >= 2 * n - kSt; fill -= 2) mbar_drain(b_full + fill % kSt, (fill / kSt) & 1);
     } else if (work) {
         // ------------------------------------------------------- values cleared
         // (and one word to the products for all that is to be there beside the weights)
@@ -581,11 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             for (int i = 0; i < nt; i++, n++) {
                 const int fill = 2 * n + 1, stage = fill % kSt, after = fill + 1;
-                // (the keys, too, although nothing here needs them: loads end in any order, and a stage whose last fill
-                // was not waited for could be two phases behind, which its parity does not tell from here)
-                wait(b_full + (fill - 1) % kSt, (fill - 1) / kSt);
+                // A wait's parity tells a phase from the one before it, not from the one before that.  The stage's last
+                // fill were the keys of two tiles ago (or earlier ones): loads end in any order, so their scores' weights
+                // are waited for first.  (Nor may this tile's word go into the phase of the stream's tile before.)
+                const bool for0 = pair || !(i & 1), for1 = pair || (i & 1);
+                if (for0 && said0) wait(b_p, said0 - 1);
+                if (for1 && said1) wait(b_p + 1, said1 - 1);
                 wait(b_full + stage, fill / kSt);
-                const TileInfo ti = info[n & (kInfos - 1)];
+                const TileInfo ti = info[kInfos + (n & (kInfos - 1))];
                 if (ti.part && ok) {
                     uint8_t* v = sm + L::kRing + stage * L::kOperand;
                     for (int blk = 0; blk < ti.blocks; blk++) {
@@ -621,19 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (where both streams use a tile, the next one's keys were asked for two tiles ago; else they may still
                 // be on their way, and the products with these values go first)
                 if (pair && i + 1 < nt) wait(b_full + after % kSt, after / kSt);
-                // (not into the phase of the tile before)
-                if (pair || !(i & 1)) {
-                    if (said0) wait(b_p, said0 - 1);
-                    said0++;
-                }
-                if (pair || (i & 1)) {
-                    if (said1) wait(b_p + 1, said1 - 1);
-                    said1++;
-                }
+                if (for0) said0++;
+                if (for1) said1++;
                 __syncwarp();
                 if (lane == 0) {
-                    if (pair || !(i & 1)) mbar_arrive(b_p);
-                    if (pair || (i & 1)) mbar_arrive(b_p + 1);
+                    if (for0) mbar_arrive(b_p);
+                    if (for1) mbar_arrive(b_p + 1);
                 }
             }
             segs++;
@@ -659,12 +657,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// A map over rows `ld` elements apart, boxes of 64 channels x 16 rows, 128-byte
+// A map over rows `ld` elements apart, boxes of 64 channels x `high` rows, 128-byte
 // swizzle; rows past the last read as zeros.
-bool encode(CUtensorMap* m, const void* base, long long rows, int cols, size_t ld)
+bool encode(CUtensorMap* m, const void* base, long long rows, int cols, size_t ld, int high)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {64, (cuuint32_t)high}, es[2] = {1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -684,9 +682,11 @@ int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int 
     Maps m;
     const long long rows = (long long)a.n_pages * a.Hkv << a.page_log2, steps = (long long)a.B * a.T;
     if (rows >= 1LL << 31) return LA_ERR_ARG;  // (more than the card holds)
-    if (!encode(&m.kp, a.kp, rows, D, D) || !encode(&m.vp, a.vp, rows, D, D) || !encode(&m.ks, a.ks, steps, a.Hkv * D, a.k_ld) ||
-        !encode(&m.vs, a.vs, steps, a.Hkv * D, a.v_ld))
-        return LA_ERR_CUDA;
+    const void *pages[2] = {a.kp, a.vp}, *step[2] = {a.ks, a.vs};
+    for (int v = 0; v < 2; v++)
+        if (!encode(&m.step[v], step[v], steps, a.Hkv * D, v ? a.v_ld : a.k_ld, 16) || !encode(&m.block[v], pages[v], rows, D, D, 16) ||
+            !encode(&m.page[v], pages[v], rows, D, D, 1 << a.page_log2))
+            return LA_ERR_CUDA;
     const dim3 grid(w.nteams), block(kThreads);
     const cudaError_t e = D == 128 ? launch_pdl(k_kv16_wide<128>, grid, block, WideSmem<128>::kBytes, s, a, w, m, rows_all)
                                    : launch_pdl(k_kv16_wide<64>, grid, block, WideSmem<64>::kBytes, s, a, w, m, rows_all);
