@@ -50,43 +50,50 @@ struct Sum {
 };
 
 // Of the parts of teams t0 .. t0 + n - 1, every `step`-th from `first` is added
-// to y: row r of their item, channels ch .. ch + 3.
-template <int D>
-__device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots, bool by_rows, int t0, int n, int r, int ch, int first,
-                                          int step, Sum& y)
+// to y[i]: row r + i * kMergeRows of their item, while it is below rows; channels
+// ch .. ch + 3.  kBatch parts are on their way at once.
+template <int D, int kRowsEach, int kBatch>
+__device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots, bool by_rows, int t0, int n, int r, int rows, int ch, int first,
+                                          int step, Sum (&y)[kRowsEach])
 {
-    constexpr int kBatch = 4;
 #pragma unroll 1
     for (int k0 = first; k0 < n; k0 += kBatch * step) {
-        float m[kBatch], l[kBatch], v[kBatch][4];
+        float m[kBatch][kRowsEach], l[kBatch][kRowsEach], v[kBatch][kRowsEach][4];
 #pragma unroll
         for (int j = 0; j < kBatch; j++) {
-            m[j] = kNoRef, l[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] = 0.f;
             const int k = k0 + j * step;
-            if (k >= n) continue;
             const size_t slot = (size_t)(t0 + k) * 2 + (k == 0);
-            if (by_rows) {
-                const float* part = slots + slot * rows_part(D, a.R);
-                const float4 o = *(const float4*)(part + (size_t)r * D + ch);
-                const float2 ml = *(const float2*)(part + (size_t)a.R * D + 2 * r);
-                m[j] = ml.x, l[j] = ml.y, v[j][0] = o.x, v[j][1] = o.y, v[j][2] = o.z, v[j][3] = o.w;
-            } else {
-                const float* col = slots + slot * wide_part(D) + (r >> 7) * (128 * (D + 2)) + (r & 127);
-                m[j] = col[D * 128], l[j] = col[(D + 1) * 128];
 #pragma unroll
-                for (int i = 0; i < 4; i++) v[j][i] = col[(ch + i) * 128];
+            for (int e = 0; e < kRowsEach; e++) {
+                const int row = r + e * kMergeRows;
+                m[j][e] = kNoRef, l[j][e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[j][e][i] = 0.f;
+                if (k < n && row < rows) {
+                    if (by_rows) {
+                        const float* part = slots + slot * rows_part(D, a.R);
+                        const float4 o = *(const float4*)(part + (size_t)row * D + ch);
+                        const float2 ml = *(const float2*)(part + (size_t)a.R * D + 2 * row);
+                        m[j][e] = ml.x, l[j][e] = ml.y, v[j][e][0] = o.x, v[j][e][1] = o.y, v[j][e][2] = o.z, v[j][e][3] = o.w;
+                    } else {
+                        const float* col = slots + slot * wide_part(D) + (row >> 7) * (128 * (D + 2)) + (row & 127);
+                        m[j][e] = col[D * 128], l[j][e] = col[(D + 1) * 128];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) v[j][e][i] = col[(ch + i) * 128];
+                    }
+                }
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; j++) {
-            // (a part without keys has no outputs, whatever is in their place)
-            if (m[j] == kNoRef && l[j] == 0.f)
+        for (int j = 0; j < kBatch; j++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) v[j][i] = 0.f;
-            y.add(m[j], l[j], v[j]);
-        }
+            for (int e = 0; e < kRowsEach; e++) {
+                // (a part without keys has no outputs, whatever is in their place)
+                const bool none = m[j][e] == kNoRef && l[j][e] == 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[j][e][i] = none ? 0.f : v[j][e][i];
+                y[e].add(m[j][e], l[j][e], v[j][e]);
+            }
     }
 }
 
@@ -137,12 +144,8 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_merge(const __grid_
         next = record(i + gridDim.x);
         const int r0 = i % w.chunks * (2 * kMergeRows) + (lane & 7);
         if (it.n <= 0 || it.t0 < 0 || it.n > w.teams - it.t0 || r0 - (lane & 7) >= it.rows) continue;
-        Sum y[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            y[k] = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
-            if (r0 + k * kMergeRows < it.rows) add_parts<D>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r0 + k * kMergeRows, ch, part, groups, y[k]);
-        }
+        Sum y[2] = {{kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}, {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}};
+        add_parts<D, 2, 2>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r0, it.rows, ch, part, groups, y);
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             const int r = r0 + k * kMergeRows;
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
     const int gr = blockIdx.x * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, g = blockIdx.y, rows_all = a.B * a.R;
     const int groups = blockDim.x / (kSlices * 32);
-    Sum y = {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    Sum ys[1] = {{kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}}, &y = ys[0];
     bool live = gr < rows_all && !w.bad[0] && !w.bad[w.kernels - 1];
     if (live) {
         const int row0 = gr / a.R * a.R;
@@ -186,12 +189,13 @@ __global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_c
             }
         };
         if (live) {
-            if (it.n > 1) add_parts<D>(a, w.slots_seq, w.by_rows, it.t0, it.n, gr - row0, ch, part, groups, y);
+            if (it.n > 1) add_parts<D, 1, 4>(a, w.slots_seq, w.by_rows, it.t0, it.n, gr - row0, a.R, ch, part, groups, ys);
             else if (part == 0) add_whole(w.whole_seq, w.by_rows);
             if (it.pre_row >= 0) {
                 const int first = it.pre_row + (gr - it.pre_row) / w.rows_pre_tile * w.rows_pre_tile;
                 const Kv16Item p = w.items[(size_t)g * rows_all + first];
-                if (p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) add_parts<D>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
+                if (p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) 
+                    add_parts<D, 1, 4>(a, w.slots_pre, false, p.t0, p.n, gr - first, w.rows_pre_tile, ch, part, groups, ys);
                 else if (part == groups - 1) add_whole(w.whole_pre, false);
             }
         }

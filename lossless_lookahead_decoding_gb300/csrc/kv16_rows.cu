@@ -55,9 +55,9 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
                  : "memory");
 }
 // 16 bytes, or zeros (then nothing is read)
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there, uint64_t pol)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0), "l"(pol) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
         Run c = f;
         bool feeding = true;
         const int pc = lane % kPieces, r0 = lane / kPieces;
+        // what is read once goes from L2 first: tables, parts and code stay
+        const uint64_t once = policy_evict_first(), shared = policy_evict_normal();
         int fk = f.t0, stage_in = 0, window = -1, page_of = 0;
         auto start_feed = [&]() {
             fk = f.t0;
@@ -130,10 +132,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                 const int nc = f.x.nb_cached(), g = f.item;
                 const __nv_bfloat16 *k, *v;
                 int live;
+                uint64_t pol = once;
                 size_t k_row = D, v_row = D;
                 if (fk < nc) {
                     // the pages of 32 table entries at a time, one a lane
                     const bool own = fk >= f.x.nb_pre;
+                    pol = own ? once : shared;
                     const int tok = (own ? fk - f.x.nb_pre : fk) * 16, n = own ? f.x.len : f.x.plen, at = tok >> a.page_log2;
                     const int w = (at >> 5) * 2 + own;
                     if (w != window) {
@@ -163,8 +167,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                 for (int i = 0; i < 16 / kRowsPass; i++) {
                     const bool there = r0 + i * kRowsPass < live;
                     const uint32_t at = dst + i * (kRowsPass * D * 2) + ((pc ^ ((r0 + i * kRowsPass) & 7)) << 4);
-                    cp16(at, there ? k8 + i * k_step : (const char*)a.kp, there);
-                    cp16(at + L::kSide, there ? v8 + i * v_step : (const char*)a.kp, there);
+                    cp16(at, there ? k8 + i * k_step : (const char*)a.kp, there, pol);
+                    cp16(at + L::kSide, there ? v8 + i * v_step : (const char*)a.kp, there, pol);
                 }
                 fk++;
             }

@@ -517,13 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A lane for each block and half of the channels; where a page's blocks are in the tile side by side, the
         // first block's lane brings all of them (a warp of lanes with a box of 16 rows each brings 40 GB/s, two
         // warps 56, one with boxes of 64 rows 68).
-        const uint64_t pol = policy_evict_normal();
+        // what is read once goes from L2 first: tables, parts and code stay
+        const uint64_t once = policy_evict_first(), shared = policy_evict_normal();
         constexpr int kAtoms = L::kAtoms;
         const int v = warp == 11, blk = lane / kAtoms, atom = lane % kAtoms, per_page = 1 << (a.page_log2 - 4);
         do {
             if (run.t1 <= run.t0) continue;
             const Entry& x = run.x;
             const int g = run.item / x.mt, nc = x.nb_cached();
+            const uint64_t pol_pre = x.b < 0 && x.mt == 1 ? once : shared, pol_own = x.mt == 1 ? once : shared;
             // block kb's page (its table entry is looked up a tile ahead)
             auto page_of = [&](int kb) {
                 if (blk >= 8 || kb >= nc) return 0;
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (mine && !bad && (!whole || in_page == 0))
                     tma_load_2d((cached ? whole ? maps.page : maps.block : maps.step) + v, b_full + stage,
-                                sm + L::kRing + stage * L::kOperand + atom * (128 * 128) + blk * 2048, cx, cy, pol);
+                                sm + L::kRing + stage * L::kOperand + atom * (128 * 128) + blk * 2048, cx, cy, own ? pol_own : pol_pre);
                 __syncwarp();
             }
         } while (run.next(a, s, pre));
