@@ -586,11 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < nt; i++, n++) {
                 const int fill = 2 * n + 1, stage = fill % kSt, after = fill + 1;
                 // A wait's parity tells a phase from the one before it, not from the one before that.  The stage's last
-                // fill were the keys of two tiles ago (or earlier ones): loads end in any order, so their scores' weights
-                // are waited for first.  (Nor may this tile's word go into the phase of the stream's tile before.)
+                // fill were the keys of two tiles ago (or earlier ones): loads end in any order, so these have to be
+                // known to be there, by a wait for them (below) or for their scores' weights.
                 const bool for0 = pair || !(i & 1), for1 = pair || (i & 1);
-                if (for0 && said0) wait(b_p, said0 - 1);
-                if (for1 && said1) wait(b_p + 1, said1 - 1);
+                auto last_words = [&](bool w0, bool w1) {
+                    if (w0 && said0) wait(b_p, said0 - 1);
+                    if (w1 && said1) wait(b_p + 1, said1 - 1);
+                };
+                if (i == 0) last_words(true, true);
+                else if (!pair) last_words(for0, for1);
                 wait(b_full + stage, fill / kSt);
                 const TileInfo ti = info[kInfos + (n & (kInfos - 1))];
                 if (ti.part && ok) {
@@ -599,14 +603,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t code = ti.code[blk >> 2] >> (8 * (blk & 3)) & 255;
                         const bool step = code & 128;
                         const int j0 = (code & 127) * 16, live = step ? min(16, a.T - j0) : (int)code;
-                        if (live == 16 && (!step || a.T == 1)) continue;
+                        const bool look = step && a.T > 1;
+                        if (live == 16 && !look) continue;
+                        // (a lane's pieces are in rows lane / 8, + 4, ..., of each half of the channels)
+                        uint4* at = (uint4*)(v + blk * 2048) + lane;
+                        constexpr int kPieces = 4 * L::kAtoms, kAtomStep = 128 * 128 / 16;
+                        uint32_t top = 0;  // the largest exponent
+                        if (look) {
+                            uint4 u[kPieces];
 #pragma unroll
-                        for (int k = 0; k < 4 * L::kAtoms; k++) {
-                            const int piece = lane + 32 * k, r = (piece >> 3) & 15;
-                            uint4* at = (uint4*)(v + (piece >> 7) * (128 * 128) + blk * 2048 + (piece & 127) * 16);
-                            if (r >= live) *at = make_uint4(0, 0, 0, 0);
-                            else if (step && a.T > 1) {
-                                const uint4 u = *at;
+                            for (int k = 0; k < kPieces; k++) u[k] = at[(k >> 2) * kAtomStep + (k & 3) * 32];
+#pragma unroll
+                            for (int k = 0; k < kPieces; k++) {
+                                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                                for (int c = 0; c < 4; c++) top = max(top, max(w[c] & 0x7f80u, (w[c] >> 16) & 0x7f80u));
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, top == 0x7f80u)) {
+                            // (rare)
+#pragma unroll 1
+                            for (int k = 0; k < kPieces; k++) {
+                                uint4* p = at + (k >> 2) * kAtomStep + (k & 3) * 32;
+                                const uint4 u = *p;
                                 uint32_t w[4] = {u.x, u.y, u.z, u.w};
                                 bool found = false;
 #pragma unroll
@@ -616,18 +635,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (b1) w[c] &= 0x0000ffffu;
                                     found |= b0 || b1;
                                 }
-                                if (found) {
-                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                                    atomicOr(&odd[(j0 + r) >> 5], 1u << ((j0 + r) & 31));
-                                }
+                                const int row = j0 + (lane >> 3) + (k & 3) * 4;
+                                if (found) *p = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (found && row < a.T) atomicOr(&odd[row >> 5], 1u << (row & 31));
                             }
                         }
+                        if (live < 16)
+#pragma unroll
+                            for (int k = 0; k < kPieces; k++)
+                                if ((lane >> 3) + (k & 3) * 4 >= live) at[(k >> 2) * kAtomStep + (k & 3) * 32] = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async();
                 }
                 // (where both streams use a tile, the next one's keys were asked for two tiles ago; else they may still
                 // be on their way, and the products with these values go first)
                 if (pair && i + 1 < nt) wait(b_full + after % kSt, after / kSt);
+                last_words(for0, for1);  // (not into the phase of the stream's tile before)
                 if (for0) said0++;
                 if (for1) said1++;
                 __syncwarp();
