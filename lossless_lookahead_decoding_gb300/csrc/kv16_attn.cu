@@ -23,8 +23,6 @@ int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int 
 namespace {
 // ------------------------------------------------------------------- merge ---
 
-constexpr int kMergeRows = 8, kMaxGroups = 2;
-
 struct MergeArgs {
     Kv16Attn a;
     const Kv16Item* items;
@@ -34,173 +32,172 @@ struct MergeArgs {
     int by_rows;              // sequences' parts are rows (k_kv16_rows), else columns
     int kernels;              // that said whether all is well
     int teams, teams_pre;     // that may have parts (nothing else is read, whatever a workspace holds)
-    int chunks;               // 16s of rows of an item
+    int chunks;               // groups of rows of an item
 };
 
+template <int C>
 struct Sum {
-    float top, l, o[4];
-    __device__ __forceinline__ void add(float m, float sum, const float (&v)[4])
+    float top = kNoRef, l = 0.f, o[C] = {};
+    __device__ __forceinline__ void add(float m, float sum, const float (&v)[C])
     {
         const float t = fmaxf(top, m), f = ex2(top - t), h = ex2(m - t);
         top = t;
         l = l * f + sum * h;
 #pragma unroll
-        for (int i = 0; i < 4; i++) o[i] = o[i] * f + v[i] * h;
+        for (int i = 0; i < C; i++) o[i] = o[i] * f + v[i] * h;
     }
 };
 
+// Row r's M, sum and C channels from ch, of a part or of whole items' results:
+// columns `pitch` apart, or rows (of which there are `rows`).
+template <int D, int C>
+__device__ __forceinline__ void load_cols(const float* col, size_t pitch, int ch, float& m, float& l, float (&v)[C])
+{
+    m = col[D * pitch], l = col[(D + 1) * pitch];
+#pragma unroll
+    for (int i = 0; i < C; i++) v[i] = col[(ch + i) * pitch];
+}
+template <int D, int C>
+__device__ __forceinline__ void load_rows(const float* part, size_t r, size_t rows, int ch, float& m, float& l, float (&v)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C; i += 4) *(float4*)(v + i) = *(const float4*)(part + r * D + ch + i);
+    const float2 ml = *(const float2*)(part + rows * D + 2 * r);
+    m = ml.x, l = ml.y;
+}
+
 // Of the parts of teams t0 .. t0 + n - 1, every `step`-th from `first` is added
-// to y[i]: row r + i * kMergeRows of their item, while it is below rows; channels
-// ch .. ch + 3.  kBatch parts are on their way at once.
-template <int D, int kRowsEach, int kBatch>
-__device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots, bool by_rows, int t0, int n, int r, int rows, int ch, int first,
-                                          int step, Sum (&y)[kRowsEach])
+// to y: row r of their item, channels ch .. ch + C - 1.  kBatch parts are on
+// their way at once.
+template <int D, int C, int kBatch>
+__device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots, bool by_rows, int t0, int n, int r, int ch, int first, int step, Sum<C>& y)
 {
 #pragma unroll 1
     for (int k0 = first; k0 < n; k0 += kBatch * step) {
-        float m[kBatch][kRowsEach], l[kBatch][kRowsEach], v[kBatch][kRowsEach][4];
+        float m[kBatch], l[kBatch], v[kBatch][C];
 #pragma unroll
         for (int j = 0; j < kBatch; j++) {
             const int k = k0 + j * step;
             const size_t slot = (size_t)(t0 + k) * 2 + (k == 0);
+            m[j] = kNoRef, l[j] = 0.f;
 #pragma unroll
-            for (int e = 0; e < kRowsEach; e++) {
-                const int row = r + e * kMergeRows;
-                m[j][e] = kNoRef, l[j][e] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[j][e][i] = 0.f;
-                if (k < n && row < rows) {
-                    if (by_rows) {
-                        const float* part = slots + slot * rows_part(D, a.R);
-                        const float4 o = *(const float4*)(part + (size_t)row * D + ch);
-                        const float2 ml = *(const float2*)(part + (size_t)a.R * D + 2 * row);
-                        m[j][e] = ml.x, l[j][e] = ml.y, v[j][e][0] = o.x, v[j][e][1] = o.y, v[j][e][2] = o.z, v[j][e][3] = o.w;
-                    } else {
-                        const float* col = slots + slot * wide_part(D) + (row >> 7) * (128 * (D + 2)) + (row & 127);
-                        m[j][e] = col[D * 128], l[j][e] = col[(D + 1) * 128];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) v[j][e][i] = col[(ch + i) * 128];
-                    }
-                }
+            for (int i = 0; i < C; i++) v[j][i] = 0.f;
+            if (k < n) {
+                if (by_rows) load_rows<D, C>(slots + slot * rows_part(D, a.R), r, a.R, ch, m[j], l[j], v[j]);
+                else load_cols<D, C>(slots + slot * wide_part(D) + (r >> 7) * (128 * (D + 2)) + (r & 127), 128, ch, m[j], l[j], v[j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; j++)
+        for (int j = 0; j < kBatch; j++) {
+            // (a part without keys has no outputs, whatever is in their place)
+            const bool none = m[j] == kNoRef && l[j] == 0.f;
 #pragma unroll
-            for (int e = 0; e < kRowsEach; e++) {
-                // (a part without keys has no outputs, whatever is in their place)
-                const bool none = m[j][e] == kNoRef && l[j][e] == 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[j][e][i] = none ? 0.f : v[j][e][i];
-                y[e].add(m[j][e], l[j][e], v[j][e]);
-            }
+            for (int i = 0; i < C; i++) v[j][i] = none ? 0.f : v[j][i];
+            y.add(m[j], l[j], v[j]);
+        }
     }
 }
 
-// The groups of warps that took different parts meet; the result goes out.
-template <int D>
-__device__ __forceinline__ void finish_rows(const Kv16Attn& a, Sum& y, bool live, int part, int groups, int at, int g, int gr, int ch)
+template <int D, int C>
+__device__ __forceinline__ void put_row(const Kv16Attn& a, const Sum<C>& y, int g, int gr, int ch)
 {
-    constexpr int kWide = D / 16 * 32;
-    __shared__ float sums[kMaxGroups - 1][6][kWide];
+    const float inv = 1.f / y.l;
+    uint32_t z[C / 2];
+#pragma unroll
+    for (int i = 0; i < C; i += 2) z[i / 2] = pack_bf16(y.o[i] * inv, y.o[i + 1] * inv);
+    __nv_bfloat16* dst = a.out + ((size_t)(gr / a.group) * a.H + (size_t)g * a.group + gr % a.group) * D + ch;
+    if (C == 8) *(uint4*)dst = make_uint4(z[0], z[1], z[C / 2 - 2], z[C / 2 - 1]);
+    else *(uint2*)dst = make_uint2(z[0], z[1]);
+}
+
+// Joins the parts of items that several teams hold.  CTAs go through teams and
+// groups of rows by turns, the next item's record on its way.  kRowParts: 8 rows
+// x all channels, a warp 8 rows x 4 lanes of 4 channels (whole sectors of rows);
+// else 32 rows x 64 channels, a warp 32 rows x 8 channels (lines of columns).
+constexpr int kMergeThreads = 256;
+template <int D, bool kRowParts>
+__global__ void __launch_bounds__(kMergeThreads) k_kv16_merge(const __grid_constant__ MergeArgs w)
+{
+    constexpr int C = kRowParts ? 4 : 8, kHigh = kRowParts ? 8 : 32, kSlices = kRowParts ? 1 : D / 64;
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, each = w.chunks * kSlices, all = w.teams * each;
+    auto record = [&](int i) { return i < all ? w.items[i / each] : Kv16Item{}; };
+    Kv16Item next = record(blockIdx.x);
+#pragma unroll 1
+    for (int i = blockIdx.x; i < all; i += gridDim.x) {
+        const Kv16Item it = next;
+        next = record(i + gridDim.x);
+        const int part = i % each, r0 = part / kSlices * kHigh;
+        if (it.n <= 0 || it.t0 < 0 || it.n > w.teams - it.t0 || r0 >= it.rows) continue;
+        const int r = r0 + (kRowParts ? lane & 7 : lane), ch = kRowParts ? warp * 16 + (lane >> 3) * 4 : part % kSlices * 64 + warp * 8;
+        if (r >= it.rows || ch >= D) continue;
+        Sum<C> y;
+        add_parts<D, C, kRowParts ? 4 : 2>(w.a, w.slots_seq, kRowParts, it.t0, it.n, r, ch, 0, 1, y);
+        put_row<D, C>(w.a, y, it.g, it.row + r, ch);
+    }
+}
+
+// Joins every row's own keys and its prefix's.  A CTA: 32 rows of a KV head x 64
+// channels; a warp 8 of them and every groups-th part.
+constexpr int kMaxGroups = 4;
+template <int D>
+__global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_constant__ MergeArgs w)
+{
+    __shared__ float sums[kMaxGroups - 1][10][256];
+    pdl_wait();
+    fence_acquire();  // (of both kernels before it)
+    pdl_trigger();
+    const Kv16Attn& a = w.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp >> 3, groups = blockDim.x >> 8, at = threadIdx.x & 255;
+    const int gr = blockIdx.x * 32 + lane, ch = blockIdx.z * 64 + (warp & 7) * 8, g = blockIdx.y, rows_all = a.B * a.R;
+    Sum<8> y;
+    bool live = gr < rows_all;
+    if (live) {
+        const int row0 = gr / a.R * a.R;
+        const Kv16Item it = w.items[(size_t)(a.Hkv + g) * rows_all + row0];
+        live = !w.bad[0] && !w.bad[w.kernels - 1] && it.n > 0 && it.t0 >= 0 && it.n <= w.teams - it.t0;
+        if (live) {
+            float m, l, v[8];
+            const bool shared = it.pre_row >= 0 && it.pre_row <= gr;
+            Kv16Item p = {};
+            int first = 0;
+            if (shared) {
+                first = it.pre_row + (gr - it.pre_row) / w.rows_pre_tile * w.rows_pre_tile;
+                p = w.items[(size_t)g * rows_all + first];
+            }
+            if (it.n > 1) {
+                add_parts<D, 8, 2>(a, w.slots_seq, w.by_rows, it.t0, it.n, gr - row0, ch, part, groups, y);
+            } else if (part == 0) {
+                if (w.by_rows) load_rows<D, 8>(w.whole_seq, (size_t)g * rows_all + gr, (size_t)a.Hkv * rows_all, ch, m, l, v);
+                else load_cols<D, 8>(w.whole_seq + (size_t)g * (D + 2) * rows_all + gr, rows_all, ch, m, l, v);
+                y.add(m, l, v);
+            }
+            if (shared && p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) {
+                add_parts<D, 8, 3>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
+            } else if (shared && part == groups - 1) {
+                load_cols<D, 8>(w.whole_pre + (size_t)g * (D + 2) * rows_all + gr, rows_all, ch, m, l, v);
+                y.add(m, l, v);
+            }
+        }
+    }
     if (part) {
         float* to = &sums[part - 1][0][at];
-        to[0] = y.top, to[kWide] = y.l;
+        to[0] = y.top, to[256] = y.l;
 #pragma unroll
-        for (int i = 0; i < 4; i++) to[(2 + i) * kWide] = y.o[i];
+        for (int i = 0; i < 8; i++) to[(2 + i) * 256] = y.o[i];
     }
     if (groups > 1) __syncthreads();
     if (part || !live) return;
 #pragma unroll 1
     for (int k = 0; k < groups - 1; k++) {
         const float* from = &sums[k][0][at];
-        float v[4];
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = from[(2 + i) * kWide];
-        y.add(from[0], from[kWide], v);
+        for (int i = 0; i < 8; i++) v[i] = from[(2 + i) * 256];
+        y.add(from[0], from[256], v);
     }
-    const float inv = 1.f / y.l;
-    __nv_bfloat16* dst = a.out + ((size_t)(gr / a.group) * a.H + (size_t)g * a.group + gr % a.group) * D + ch;
-    *(uint2*)dst = make_uint2(pack_bf16(y.o[0] * inv, y.o[1] * inv), pack_bf16(y.o[2] * inv, y.o[3] * inv));
-}
-
-// Joins the parts of items that several teams hold.  A CTA at a time: 16 rows of
-// the item that a team begins; a warp: 16 of their channels and every groups-th
-// part (8 rows x 4 lanes of 4 channels: whole sectors of either kind of part).
-// CTAs go through teams and rows by turns, the next item's record on its way.
-template <int D>
-__global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_merge(const __grid_constant__ MergeArgs w)
-{
-    constexpr int kSlices = D / 16;
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
-    const int ch = slice * 16 + (lane >> 3) * 4, groups = blockDim.x / (kSlices * 32), all = w.teams * w.chunks;
-    auto record = [&](int i) { return i < all ? w.items[i / w.chunks] : Kv16Item{}; };
-    Kv16Item next = record(blockIdx.x);
-#pragma unroll 1
-    for (int i = blockIdx.x; i < all; i += gridDim.x) {
-        const Kv16Item it = next;
-        next = record(i + gridDim.x);
-        const int r0 = i % w.chunks * (2 * kMergeRows) + (lane & 7);
-        if (it.n <= 0 || it.t0 < 0 || it.n > w.teams - it.t0 || r0 - (lane & 7) >= it.rows) continue;
-        Sum y[2] = {{kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}, {kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}};
-        add_parts<D, 2, 2>(w.a, w.slots_seq, w.by_rows, it.t0, it.n, r0, it.rows, ch, part, groups, y);
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int r = r0 + k * kMergeRows;
-            finish_rows<D>(w.a, y[k], r < it.rows, part, groups, slice * 32 + lane, it.g, it.row + r, ch);
-            if (groups > 1) __syncthreads();
-        }
-    }
-}
-
-// Joins every row's own keys and its prefix's.  A CTA: 8 rows of a KV head.
-template <int D>
-__global__ void __launch_bounds__(D * 2 * kMaxGroups) k_kv16_join(const __grid_constant__ MergeArgs w)
-{
-    constexpr int kSlices = D / 16;
-    pdl_wait();
-    fence_acquire();  // (of both kernels before it)
-    pdl_trigger();
-    const Kv16Attn& a = w.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % kSlices, part = warp / kSlices;
-    const int gr = blockIdx.x * kMergeRows + (lane & 7), ch = slice * 16 + (lane >> 3) * 4, g = blockIdx.y, rows_all = a.B * a.R;
-    const int groups = blockDim.x / (kSlices * 32);
-    Sum ys[1] = {{kNoRef, 0.f, {0.f, 0.f, 0.f, 0.f}}}, &y = ys[0];
-    bool live = gr < rows_all && !w.bad[0] && !w.bad[w.kernels - 1];
-    if (live) {
-        const int row0 = gr / a.R * a.R;
-        const Kv16Item it = w.items[(size_t)(a.Hkv + g) * rows_all + row0];
-        live = it.n > 0 && it.t0 >= 0 && it.n <= w.teams - it.t0;
-        auto add_whole = [&](const float* whole, bool by_rows) {
-            float v[4];
-            if (by_rows) {
-                const size_t at = (size_t)g * rows_all + gr;
-                const float4 o = *(const float4*)(whole + at * D + ch);
-                const float2 ml = *(const float2*)(whole + (size_t)a.Hkv * rows_all * D + 2 * at);
-                v[0] = o.x, v[1] = o.y, v[2] = o.z, v[3] = o.w;
-                y.add(ml.x, ml.y, v);
-            } else {
-                const float* col = whole + (size_t)g * (D + 2) * rows_all + gr;
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[i] = col[(size_t)(ch + i) * rows_all];
-                y.add(col[(size_t)D * rows_all], col[(size_t)(D + 1) * rows_all], v);
-            }
-        };
-        if (live) {
-            if (it.n > 1) add_parts<D, 1, 4>(a, w.slots_seq, w.by_rows, it.t0, it.n, gr - row0, a.R, ch, part, groups, ys);
-            else if (part == 0) add_whole(w.whole_seq, w.by_rows);
-            if (it.pre_row >= 0) {
-                const int first = it.pre_row + (gr - it.pre_row) / w.rows_pre_tile * w.rows_pre_tile;
-                const Kv16Item p = w.items[(size_t)g * rows_all + first];
-                if (p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) 
-                    add_parts<D, 1, 4>(a, w.slots_pre, false, p.t0, p.n, gr - first, w.rows_pre_tile, ch, part, groups, ys);
-                else if (part == groups - 1) add_whole(w.whole_pre, false);
-            }
-        }
-    }
-    finish_rows<D>(a, y, live, part, groups, slice * 32 + lane, g, gr, ch);
+    put_row<D, 8>(a, y, g, gr, ch);
 }
 
 // -------------------------------------------------------------------- plan ---
@@ -285,10 +282,10 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     p.m.rows_pre_tile = kWideRows, p.m.by_rows = p.use_rows;
     p.merge = !last.direct;
     p.m.kernels = p.use_rows && p.use_wide ? 2 : 1;
-    p.m.teams = last.nteams, p.m.teams_pre = p.wide.nteams, p.m.chunks = (std::min(last.row_tile, k.R) + 2 * kMergeRows - 1) / (2 * kMergeRows);
+    p.m.teams = last.nteams, p.m.teams_pre = p.wide.nteams, p.m.chunks = (std::min(last.row_tile, k.R) + (p.use_rows ? 7 : 31)) / (p.use_rows ? 8 : 32);
     // as many groups of warps as an item may have fours of parts
     const long long parts = (p.use_wide ? p.wide.nteams : p.rows.nteams) / std::max(1LL, (long long)k.Hkv * (p.apart ? (rows_all + 255) / 256 : k.B));
-    p.groups = parts >= 6 ? 2 : 1;
+    p.groups = parts >= 9 ? 4 : parts >= 4 ? 2 : 1;
     p.bytes = at;
     return p;
 }
@@ -296,9 +293,11 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
 template <int D>
 cudaError_t launch_merge(cudaStream_t s, const Plan& p)
 {
-    const dim3 block(D * 2 * p.groups);
-    if (p.apart) return launch_pdl(k_kv16_join<D>, dim3((p.k.B * p.k.R + kMergeRows - 1) / kMergeRows, p.k.Hkv), block, 0, s, p.m);
-    return launch_pdl(k_kv16_merge<D>, dim3(std::min(p.m.teams * p.m.chunks, kSMs * 1024 / (int)block.x)), block, 0, s, p.m);
+    if (p.apart) return launch_pdl(k_kv16_join<D>, dim3((p.k.B * p.k.R + 31) / 32, p.k.Hkv, D / 64), dim3(256 * p.groups), 0, s, p.m);
+    const long long all = (long long)p.m.teams * p.m.chunks * (p.use_rows ? 1 : D / 64);
+    const dim3 grid((unsigned)std::min(all, (long long)kSMs * 6));
+    return p.use_rows ? launch_pdl(k_kv16_merge<D, true>, grid, dim3(kMergeThreads), 0, s, p.m)
+                      : launch_pdl(k_kv16_merge<D, false>, grid, dim3(kMergeThreads), 0, s, p.m);
 }
 
 bool init()
