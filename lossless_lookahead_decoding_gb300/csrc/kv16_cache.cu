@@ -100,31 +100,40 @@ __global__ void __launch_bounds__(kThreads) k_kv16_append(const __grid_constant_
         cs[t][i] = make_float2(c, s);
     }
     __syncthreads();
-    const int share = min(a.share, a.heads - h0), nq = a.q_out ? a.H : 0;
-    for (int j = threadIdx.x; j < tokens * a.share * kUnits; j += kThreads) {
-        const int item = j / kUnits, u = j % kUnits;
-        const int t = __umulhi((uint32_t)item, a.inv_share), hh = item - t * a.share;
-        const int row = s_row[t], slot = s_slot[t];
-        if (hh >= share || row < 0) continue;
-        int h = h0 + hh;
-        const int what = h < nq ? 0 : h < nq + a.Hkv ? 1 : 2;
-        h -= what == 0 ? 0 : what == 1 ? nq : nq + a.Hkv;
-        if (slot < 0 && (what == 2 || (what == 1 && !a.k_out))) continue;
-        // the unit's two pieces: partners half a rotation apart, or next to each other
-        const bool turns = what < 2 && 16 * u < a.rot, apart = 16 * u < a.rot && !a.neighbours;
-        const int p0 = apart ? u : 2 * u, p1 = apart ? u + a.rot / 16 : 2 * u + 1;
-        const uint8_t* src = what == 0 ? a.q + row * a.q_ld : what == 1 ? a.k + row * a.k_ld : a.v + row * a.v_ld;
-        src += (size_t)h * D * E;
+    const int share = min(a.share, a.heads - h0), nq = a.q_out ? a.H : 0, all = tokens * a.share * kUnits;
+    // A unit's two pieces: partners half a rotation apart, or next to each other.
+    struct Unit {
+        int t, h, what, p0, p1, slot;  // token, head, 0 query, 1 key, 2 value; pieces; slot
+        bool live, turns, apart;
         Piece<F32> x0, x1;
-        x0.load(src + p0 * 8 * E);
-        x1.load(src + p1 * 8 * E);
+    };
+    auto fetch = [&](int j, Unit& n) {
+        const int item = j / kUnits, u = j % kUnits, t = __umulhi((uint32_t)item, a.inv_share), hh = item - t * a.share;
+        n.live = false;
+        if (j >= all || hh >= share) return;
+        const int row = s_row[t], h = h0 + hh;
+        n.t = t, n.slot = s_slot[t];
+        n.what = h < nq ? 0 : h < nq + a.Hkv ? 1 : 2;
+        n.h = h - (n.what == 0 ? 0 : n.what == 1 ? nq : nq + a.Hkv);
+        n.live = row >= 0 && !(n.slot < 0 && (n.what == 2 || (n.what == 1 && !a.k_out)));
+        if (!n.live) return;
+        n.turns = n.what < 2 && 16 * u < a.rot, n.apart = 16 * u < a.rot && !a.neighbours;
+        n.p0 = n.apart ? u : 2 * u, n.p1 = n.apart ? u + a.rot / 16 : 2 * u + 1;
+        const uint8_t* src = n.what == 0 ? a.q + row * a.q_ld : n.what == 1 ? a.k + row * a.k_ld : a.v + row * a.v_ld;
+        src += (size_t)n.h * D * E;
+        n.x0.load(src + n.p0 * 8 * E);
+        n.x1.load(src + n.p1 * 8 * E);
+    };
+    auto put = [&](int j, const Unit& n) {
+        if (!n.live) return;
+        const int u = j % kUnits;
         uint4 y0, y1;
-        if (turns || F32) {
+        if (n.turns || F32) {
             float a0[8], a1[8];
-            x0.get(a0), x1.get(a1);
-            if (turns) {
-                const float2* w = cs[t] + 8 * u;
-                if (apart) {
+            n.x0.get(a0), n.x1.get(a1);
+            if (n.turns) {
+                const float2* w = cs[n.t] + 8 * u;
+                if (n.apart) {
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         const float2 r = w[i];
@@ -147,22 +156,33 @@ __global__ void __launch_bounds__(kThreads) k_kv16_append(const __grid_constant_
             }
             y0 = pack8(a0), y1 = pack8(a1);
         } else {
-            y0 = x0.w[0], y1 = x1.w[0];
+            y0 = n.x0.w[0], y1 = n.x1.w[0];
         }
-        if (what == 0) {
-            uint4* o = (uint4*)((uint8_t*)a.q_out + (long long)(i0 + t) * a.qo_ld) + (size_t)h * (D / 8);
-            o[p0] = y0, o[p1] = y1;
-            continue;
+        const int i = i0 + n.t;
+        if (n.what == 0) {
+            uint4* o = (uint4*)((uint8_t*)a.q_out + (long long)i * a.qo_ld) + (size_t)n.h * (D / 8);
+            o[n.p0] = y0, o[n.p1] = y1;
+            return;
         }
-        if (what == 1 && a.k_out) {
-            uint4* o = (uint4*)((uint8_t*)a.k_out + (long long)(i0 + t) * a.ko_ld) + (size_t)h * (D / 8);
-            o[p0] = y0, o[p1] = y1;
+        if (n.what == 1 && a.k_out) {
+            uint4* o = (uint4*)((uint8_t*)a.k_out + (long long)i * a.ko_ld) + (size_t)n.h * (D / 8);
+            o[n.p0] = y0, o[n.p1] = y1;
         }
-        if (slot >= 0) {
-            const size_t at = ((((size_t)(slot >> a.page_log2) * a.Hkv + h) << a.page_log2) + (slot & ((1 << a.page_log2) - 1))) * D;
-            uint4* o = (uint4*)((what == 1 ? a.kp : a.vp) + at);
-            o[p0] = y0, o[p1] = y1;
+        if (n.slot >= 0) {
+            const size_t at = ((((size_t)(n.slot >> a.page_log2) * a.Hkv + n.h) << a.page_log2) + (n.slot & ((1 << a.page_log2) - 1))) * D;
+            uint4* o = (uint4*)((n.what == 1 ? a.kp : a.vp) + at);
+            o[n.p0] = y0, o[n.p1] = y1;
         }
+    };
+    // kAhead units of a thread on their way at once.  (In place: a unit writes only what it has read itself.)
+    constexpr int kAhead = F32 ? 1 : 2;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < all; j += kAhead * kThreads) {
+        Unit n[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) fetch(j + k * kThreads, n[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) put(j + k * kThreads, n[k]);
     }
 }
 
