@@ -116,10 +116,20 @@ struct Scan {
     Shares shares;
 };
 
-// Costs of a unit of k_kv16_wide and of k_kv16_rows in SM time (a tile for a
-// stream beside a kernel that saturates HBM 2.3 us; a block's bytes at the card's
-// rate by 152).
-__device__ __forceinline__ float unit_cost(bool rows, int D) { return rows ? (D == 128 ? 2.f : 1.f) : 30.f; }
+// Of two kernels that run at the same time, the SMs of the wide one: with uw units
+// (a tile for a stream: 32 KB of a pair's tile, 0.9 us) and ur blocks (8 KB at D =
+// 128, 0.13 us at what one SM can read) both end together.  Where HBM and not the
+// SMs sets the pace, a wide unit waits for its tiles and takes 1.7 us.  (128 single
+// tokens behind 1000: 65 us; at 1.0 and 2.4 us a unit 78 and 67; one kernel after
+// the other 89.  32 behind 32 K: see k_kv16_wide.)
+__device__ __forceinline__ int wide_sms(float uw, float ur, int D)
+{
+    const float half = D == 128 ? 1.f : 0.6f, tw = 0.95f * half, tr = 0.126f * half;
+    const float hbm = (uw * 32.f + ur * 8.f) * (D / 128.f) / 6600.f;
+    const bool waits = hbm > (uw * tw + ur * tr) / kSMs;
+    const float w = uw * (waits ? 1.73f * half : tw), r = ur * tr;
+    return min(max((int)(w * kSMs / fmaxf(w + r, 1e-3f)) + 1, 4), kSMs - 8);
+}
 
 // Where each of the CTA's teams begins; the shares go to sc.  CTA 0 of the
 // call's first kernel raises what is wrong with the sequences.
@@ -207,12 +217,10 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
     if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) *s.bad = bad || huge;
     int ctas = gridDim.x;
     if (s.beside) {
-        // Both kernels count alike: the wide one takes a share of the SMs by its work (and a quarter more: its
-        // last item is the call's end), the rows' one the others; not where it would need most of them.
-        const float mine = (float)all_u * unit_cost(s.n_pre == 0, D),
-                    other = (float)__reduce_add_sync(0xffffffffu, in ? sc->cost[lane] : 0) * (float)a.Hkv * unit_cost(s.n_pre != 0, D);
-        const int sms = (int)((s.n_pre ? mine : other) * (kSMs * 1.25f) / fmaxf(mine + other, 1.f)) + 1;
-        if (sms <= kSMs * 3 / 4) ctas = s.n_pre ? sms : kSMs - sms;
+        // (both kernels count alike)
+        const float mine = (float)all_u, other = (float)__reduce_add_sync(0xffffffffu, in ? sc->cost[lane] : 0) * (float)a.Hkv;
+        const int sms = s.n_pre ? wide_sms(mine, other, D) : wide_sms(other, mine, D);
+        ctas = s.n_pre ? sms : kSMs - sms;
     }
     const int room = min(s.nteams, ctas * n);
     Shares h;
