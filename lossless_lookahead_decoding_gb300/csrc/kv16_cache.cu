@@ -35,7 +35,7 @@ struct AppendArgs {
     int heads;             // queries', keys' and values' heads that the call moves
     int share;             // heads of a CTA
     int tokens;            // tokens of a CTA
-    uint32_t inv_share;    // ceil(2^32 / share)
+    uint32_t inv_share;    // ceil(2^32 / share) modulo 2^32: 0 for a single head
     int rot, neighbours;   // rot 0: nothing turns
     Turns t;
 };
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) k_kv16_append(const __grid_constant_
         Piece<F32> x0, x1;
     };
     auto fetch = [&](int j, Unit& n) {
-        const int item = j / kUnits, u = j % kUnits, t = __umulhi((uint32_t)item, a.inv_share), hh = item - t * a.share;
+        const int item = j / kUnits, u = j % kUnits, t = a.inv_share ? __umulhi((uint32_t)item, a.inv_share) : item, hh = item - t * a.share;
         n.live = false;
         if (j >= all || hh >= share) return;
         const int row = s_row[t], h = h0 + hh;
@@ -229,7 +229,7 @@ int launch_append(cudaStream_t s, const la_kv16_desc& c, const la_kv16_rows& r)
         a.share = a.heads;
     }
     while (a.share > 1024) a.share = (a.share + 1) / 2;
-    a.inv_share = a.share == 1 ? 0xffffffffu : (uint32_t)(((1ull << 32) + a.share - 1) / a.share);
+    a.inv_share = (uint32_t)(((1ull << 32) + a.share - 1) / a.share);
     auto kern = c.head_dim == 128 ? (f32 ? k_kv16_append<128, true> : k_kv16_append<128, false>)
                                   : (f32 ? k_kv16_append<64, true> : k_kv16_append<64, false>);
     const dim3 grid((unsigned)((r.n + a.tokens - 1) / a.tokens), (unsigned)((a.heads + a.share - 1) / a.share));

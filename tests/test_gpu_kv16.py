@@ -109,6 +109,22 @@ def test_append_turns_and_keeps(n, heads, kv_heads, D, page, rope, dtype):
     assert (kp.transpose(1, 2)[left] == 7).all() and (vp.transpose(1, 2)[left] == -7).all()
 
 
+@pytest.mark.parametrize("n", [1, 1216, 1217, 2500])
+@pytest.mark.parametrize("what", ["k", "q"])
+def test_append_turns_a_single_head(what, n):
+    """A call that moves one head, of few tokens and of many."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    D, g = 64, np.random.default_rng(n)
+    c = LA.KV16Cache(*LA.KV16Cache.empty_pages(2, 1, D, 16), max_pages=2)
+    x, pos, out = _bf(g.standard_normal((n, D))), g.integers(0, 4096, n), torch.zeros((n, D), dtype=torch.bfloat16, device="cuda")
+    to = dict(k_out=out) if what == "k" else dict(q=x, q_out=out)
+    c.append(x, None, None, positions=_i32(pos), rope=LA.Rope(D), **to)
+    c.check()
+    y, err = _turned(_np(x)[:, None], pos, dict(rot=D), D)
+    _near(out, y[:, 0], err[:, 0])
+
+
 def test_append_given_frequencies_and_far_positions():
     """Angles of far positions lose nothing: the last position of 31 bits, negative ones, frequencies of one's own."""
     import torch
