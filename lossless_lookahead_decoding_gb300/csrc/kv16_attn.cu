@@ -300,12 +300,17 @@ cudaError_t launch_merge(cudaStream_t s, const Plan& p)
                       : launch_pdl(k_kv16_merge<D, false>, grid, dim3(kMergeThreads), 0, s, p.m);
 }
 
-bool init()
+std::mutex g_mu;
+unsigned char g_ready[256];
+
+// The kernels' shared-memory limits, once per device.
+bool attn_ready()
 {
-    static std::once_flag once;
-    static bool ok;
-    std::call_once(once, [] { ok = kv16_rows_init() && kv16_wide_init(); });
-    return ok;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return false;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_ready[dev]) g_ready[dev] = kv16_rows_init() && kv16_wide_init();
+    return g_ready[dev] != 0;
 }
 
 }  // namespace
@@ -314,7 +319,7 @@ size_t kv16_attn_bytes(const la_kv16_desc& c, const la_kv16_attn& a) { return pl
 
 int launch_kv16_attn(cudaStream_t s, const la_kv16_desc& c, const la_kv16_attn& a)
 {
-    if (!init()) return LA_ERR_CUDA;
+    if (!attn_ready()) return LA_ERR_CUDA;
     Plan p = plan_of(c, a, (uint8_t*)a.workspace);
     Kv16Attn& k = p.k;
     k.q = (const __nv_bfloat16*)a.q, k.ks = (const __nv_bfloat16*)a.k_step, k.vs = (const __nv_bfloat16*)a.v_step;

@@ -194,7 +194,7 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
                 }
         }
     }
-    const int units = (int)min(sum, 1LL << 30);
+    const int units = (int)min(sum, 0x7fff0000LL);  // (there, or nothing is done: see `huge`)
     int xu = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -385,6 +385,81 @@ def test_attention_nan_and_infinity_stay_with_their_rows():
         _compare(c, got, want)
 
 
+MANY = [  # prefixes worth reading by themselves, many entries, many prefixes: lens, prefixes, heads, kv heads, D, page, (W, N, G)
+    ([7, -1, 130, 0, 64, 33, 2, 1, 90, 5], [(3000, 6), (0, 1), (2111, 3)], 4, 2, 128, 64, (3, 3, 3)),       # 26 rows a sequence
+    ([3, 40, 0, -2, 17, 200, 8, 1] * 2, [(2500, 16)], 8, 1, 128, 32, (1, 5, 0)),                           # 40 rows, all with one
+    ([20, 0, 61, 7, 5, 128, 300, 9, -1], [(6000, 2), (5000, 3), (-1, 1)], 8, 2, 64, 128, (2, 5, 1)),         # 52; a length below 0
+    ([int(n) for n in np.random.default_rng(1).integers(-1, 40, 420)], [(170, 201), (40, 199), (3, 1)], 1, 1, 64, 16, (0, 2, 0)),
+    ([int(n) for n in np.random.default_rng(2).integers(-1, 40, 400)], [(100, 30), (170, 333)], 2, 1, 64, 16, (2, 5, 0)),   # 18 rows
+    ([int(n) for n in np.random.default_rng(3).integers(-1, 90, 400)], [], 2, 2, 64, 32, (0, 2, 0)),
+    ([5, 0, 31, -1, 77, 16, 2, 50] * 5, [(20 * i, 1) for i in range(36)], 2, 1, 64, 16, (0, 2, 0)),          # 36 prefixes, read per sequence
+    ([5, 0, 31, -1, 77, 16, 2, 50] * 5, [(13 * i, 1) for i in range(36)], 40, 1, 64, 16, (0, 2, 0)),         # and by many rows
+    ([9, 1, 60] * 17, [(30 + 20 * i, 1) for i in range(42)], 4, 2, 128, 32, (0, 2, 0)),                      # 42 by themselves
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_attention_many(i):
+    lens, prefixes, H, Hkv, D, page, (W, N, G) = MANY[i]
+    c = _case(lens, [(max(n, 0), k) for n, k in prefixes], H, Hkv, D, page, W, N, G, seed=40 + i)
+    c["d"]["plens"].copy_(_i32([n for n, _ in prefixes]))
+    got = _call(c)
+    c["cache"].check()
+    _compare(c, got)
+
+
+def test_attention_bad_values_beside_shared_prefixes():
+    """Prefixes read by themselves: bad pages, lengths over their bounds, prefix_first out of order."""
+    import lossless_lookahead_decoding_gb300 as LA
+
+    def refused(c):
+        with pytest.raises(LA.LAError) as e:
+            c["cache"].check()
+        return e.value.code == LA.LA_ERR_ARG
+
+    for rows in ((0, 2, 0), (3, 3, 2)):
+        new = lambda: _case([30, 40, 50, 6, 77, 8], [(4000, 3), (3000, 2)], 4, 2, 128, 64, *rows, seed=17)
+        c = new()
+        for t, p, j in (("table", 0, 0), ("ptable", 0, 3), ("ptable", 1, 46), ("table", 4, 1)):
+            for bad in (-1, 10 ** 6):
+                c[t][p, j] = bad
+        for t in ("table", "ptable"):
+            c["d"][t].copy_(_i32(c[t]))
+        got = _call(c)
+        assert refused(c)
+        _compare(c, got)
+        c = new()
+        got = _call(c, max_len=60, max_prefix_len=3999)
+        for b in (0, 1, 2, 4):
+            c["lens"][b] = -1
+        assert refused(c)
+        _compare(c, got)
+        for first in ([0, 4, 3], [-1, 2, 3], [0, 4, 7], [2 ** 31 - 1, 0, -2 ** 31]):
+            c = new()
+            c["d"]["first"].copy_(_i32(first))
+            assert (_call(c) == 123).all() and refused(c)
+
+
+def test_attention_buffers_at_odd_16_byte_places():
+    """q, k_step, v_step, out and the workspace at 16 bytes past other boundaries; what lies beside them stays."""
+    import torch
+    for shape in (([30, 400, 5], [(200, 2)], 4, 2, 128, 32, 0, 2, 0), ([30, 400, 5], [(200, 2)], 4, 2, 64, 32, 5, 4, 5),
+                  ([30, 40, 5, 9], [(5000, 4)], 4, 2, 128, 32, 2, 3, 2)):
+        c = _case(*shape, seed=18)
+        want = _call(c).clone()
+
+        def moved(x, fill):
+            room = torch.full((x.numel() * x.element_size() + 48,), fill, dtype=torch.uint8, device="cuda")
+            return room, room[16:-32].view(x.dtype).view(x.shape)
+
+        for name in ("q", "k", "v"):
+            c[name] = moved(c[name].contiguous(), 255)[1].copy_(c[name])
+        (oroom, c["out"]), (wroom, c["ws"]) = moved(c["out"], 77), moved(c["ws"], 78)
+        assert torch.equal(_call(c), want)
+        assert (oroom[:16] == 77).all() and (oroom[-32:] == 77).all() and (wroom[:16] == 78).all() and (wroom[-32:] == 78).all()
+        c["cache"].check()
+
+
 def test_attention_prefixes_in_gaps():
     """Sequences before the first prefix and behind the last have none."""
     c = _case([12, 40, 9, 77, 30, 5], [(150, 2), (33, 1)], 4, 2, 64, 16, 1, 3, 1, seed=6)
