@@ -116,7 +116,8 @@ __device__ __forceinline__ float weigh64(const uint32_t (&x)[64], float f, float
 }
 
 // A wait that gives up ends every later one at once, but no role leaves its
-// loops: the named barriers keep their counts.
+// loops: the named barriers keep their counts.  From then on the role tells the
+// others nothing, so that none goes on with what is not there: their own waits end.
 struct Wait {
     volatile int* abort_flag;
     int* status;
@@ -237,7 +238,7 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_p + str);
+        if (lane == 0 && wait.ok) mbar_arrive(b_p + str);
     }
     return make_float2(m, l);
 }
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_q);
+            if (lane == 0 && ok) mbar_arrive(b_q);
             const int step_row = x.b < 0 ? 0 : ((gr - x.row0) / group < a.T ? (gr - x.row0) / group : a.T - 1);
             const uint32_t* see = vis + 4 * step_row;
             const float2 y = weigh_tiles<D>(sm, trow, str, n + (pair ? 0 : str), pair ? 1 : 2, tiles, done, any, see, a.sl2, a.status);
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (for0) said0++;
                 if (for1) said1++;
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0 && ok) {
                     if (for0) mbar_arrive(b_p);
                     if (for1) mbar_arrive(b_p + 1);
                 }
