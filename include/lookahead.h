@@ -663,13 +663,15 @@ LA_API size_t la_kv16_attention_bytes(const la_kv16_desc* c, const la_kv16_attn*
  * la_attention for a batch over the paged bf16 cache: row i of sequence b
  * attends to its prefix's tokens, to the lens[b] tokens of its own and to the
  * step rows the 2D-window + verification mask lets it see (never none: each
- * row sees row 0), scaled by 1 / sqrt(head_dim).  A prefix is read once for
- * all of its sequences, not once for each.  Positions past a length are never
+ * row sees row 0), scaled by 1 / sqrt(head_dim).  A prefix is read from memory
+ * once, and multiplied with all of its sequences' rows at once where that pays
+ * (up to 64 rows a sequence and KV head).  Positions past a length are never
  * used, whatever bytes they hold, and a NaN or infinity in a step row reaches
  * only rows that see it.  out overlaps no other buffer.  A length above its
  * bound (of a prefix: for all of its sequences) leaves a sequence's rows alone,
  * a page index outside the pool counts as no keys, prefix_first out of order
- * leaves every row alone (each LA_ERR_ARG in *status).  Asynchronous on
+ * or more than 2^34 keys in all (over sequences, KV heads and groups of 256
+ * rows) leave every row alone (each LA_ERR_ARG in *status).  Asynchronous on
  * `stream`; equal calls give equal bits.  Two calls that may run at the same
  * time (two streams, two captured graphs) need a workspace each. */
 LA_API int la_kv16_attention(const la_kv16_desc* c, const la_kv16_attn* a, void* stream);

@@ -113,7 +113,9 @@ __device__ __forceinline__ void put_row(const Kv16Attn& a, const Sum<C>& y, int 
 // Joins the parts of items that several teams hold.  CTAs go through teams and
 // groups of rows by turns, the next item's record on its way.  kRowParts: 8 rows
 // x all channels, a warp 8 rows x 4 lanes of 4 channels (whole sectors of rows);
-// else 32 rows x 64 channels, a warp 32 rows x 8 channels (lines of columns).
+// else 32 rows x 64 channels, a warp 32 rows x 8 channels (lines of columns).  Bound
+// by two dependent trips, record and parts: 35 MB of parts take 10 us behind the
+// kernel that wrote them, none 5 us.
 constexpr int kMergeThreads = 256;
 template <int D, bool kRowParts>
 __global__ void __launch_bounds__(kMergeThreads) k_kv16_merge(const __grid_constant__ MergeArgs w)
@@ -139,7 +141,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv16_merge(const __grid_const
 }
 
 // Joins every row's own keys and its prefix's.  A CTA: 32 rows of a KV head x 64
-// channels; a warp 8 of them and every groups-th part.
+// channels; a warp 8 of them and every groups-th part.  (128 sequences, 32 heads:
+// 14 MB from L2, 7.6 us by itself.)
 constexpr int kMaxGroups = 4;
 template <int D>
 __global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_constant__ MergeArgs w)
@@ -235,7 +238,10 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     };
     // A prefix by itself, for all of its sequences at once, where reading it for each would cost
     // more than the further launches and parts (these bytes come from L2 at 8 TB/s: 2 us), and
-    // where a sequence has too few rows to fill a tile.
+    // where a sequence has too few rows to fill a tile: with 100 rows of each of 6 prompts behind
+    // 1024 tokens 56 against 44 us, with 121 rows of 4 steps 33 against 20, with 456 of 8 160
+    // against 130; but 128 single tokens of 32 heads behind 1000 tokens 65 against 234, 32 of 64
+    // heads behind 32 767 55 against 397, 48 behind up to 4000 54 against 73.
     const long long again = (long long)k.B * k.Hkv * k.max_plen * D * 4;
     p.apart = k.B > 1 && k.R <= 64 && again > (16 << 20);
     k.concat = !p.apart;

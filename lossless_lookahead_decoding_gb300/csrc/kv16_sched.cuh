@@ -118,11 +118,12 @@ struct Scan {
 };
 
 // Of two kernels that run at the same time, the SMs of the wide one: with uw units
-// (a tile for a stream: 32 KB of a pair's tile, 0.9 us) and ur blocks (8 KB at D =
-// 128, 0.13 us at what one SM can read) both end together.  Where HBM and not the
-// SMs sets the pace, a wide unit waits for its tiles and takes 1.7 us.  (128 single
-// tokens behind 1000: 65 us; at 1.0 and 2.4 us a unit 78 and 67; one kernel after
-// the other 89.  32 behind 32 K: see k_kv16_wide.)
+// (a tile for a stream: 32 KB of a pair's tile, 0.95 us) and ur blocks (8 KB at D =
+// 128, 0.126 us at what one SM can read) both end together.  Where HBM and not the
+// SMs sets the pace, a wide unit waits for its tiles and takes 1.73 us.  (128 single
+// tokens behind 1000, us in all, at 1.0, 1.4, 1.73 and 2.4 us a unit: 77, 67, 65, 64;
+// 48 behind prefixes of up to 4000: 61, 56, 54, 56; one kernel after the other, the
+// former: 89.)
 __device__ __forceinline__ int wide_sms(float uw, float ur, int D)
 {
     const float half = D == 128 ? 1.f : 0.6f, tw = 0.95f * half, tr = 0.126f * half;

@@ -13,9 +13,11 @@
 //   S = Q K^T          Q and K in shared memory, S in tensor memory
 //   P = exp2(S f - M)  in bf16, in the place of S
 //   O += P V           P from tensor memory, V in shared memory
-// with S, M, the sums and O in fp32.  The reference M is the largest score of a
-// row's first tile and moves only when a row's P of a tile sum to more than
-// 2^15; the weights stay in registers until that is known.
+// with S, M, the sums and O in fp32, half a tile at a time.  The reference M is
+// the largest score of a row's first half tile and moves, by a power of two, only
+// when a row's P of a half tile sum to more than 2^15: weights of up to 2^15 lose
+// no more in bf16 than smaller ones, and O is read back once in many thousand
+// tiles.  The half's weights stay in registers until that is known.
 //
 // Keys that are not there: their scores count as -inf, and their values, of
 // which a product would take 0 x NaN, are cleared in shared memory, as are the
@@ -24,6 +26,19 @@
 //
 // One CTA per SM: warps 0-3 and 4-7 the streams' softmax (a row per thread), 8
 // issues the products, 9 and 11 the copies of keys and of values, 10 clears values.
+//
+// What bounds it.  A tile of 256 rows takes 1.7 us: 1.1 us of a stream's softmax
+// and the two products after it (0.27 us each, with the hand-overs 0.6 us), which
+// the other stream's softmax only hides in part: tensor pipe 54 %, issue slots
+// 41 %, special functions 26 %.  8 steps of 57 rows x 8 heads, 8 KV heads, over
+// 8.3 to 9.5 K keys (133 GFLOP): 130 us, 1.02 PFLOP/s.  Measured for that call and not taken:
+// 16 softmax warps (147 against 122 us for the kernel: twice the loads from tensor
+// memory), streams strictly by turns (150), loads from tensor memory ahead of their
+// use (165), sums of unrounded weights (126 against 120), sums by a product (152),
+// the next scores made half by half behind the weights' own half (168 against 130),
+// values' products by halves (161), more registers for the softmax by setmaxnreg
+// (spills).  With up to 128 rows a tile takes what an SM can read: 64 KB in 1.2 us
+// where pages are 16 tokens.
 #include <cudaTypedefs.h>
 
 #include "kv16_sched.cuh"
@@ -141,6 +156,7 @@ struct Wait {
 // scores become weights where they are.  Returns the row's reference and sum.  A
 // function, so that what its caller keeps over it leaves the registers once and
 // not in every tile (spilt around the loop's body, a tile took 2.2 us, not 1.7).
+// 64 scores at a time: by 32 the call above took 147 us, by 16 177.
 template <int D>
 __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, int n, int step, int tiles, int done, bool any, const uint32_t* see,
                                            float f, int* status)
@@ -149,7 +165,8 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
     Bars<L::kStages>& bar = *(Bars<L::kStages>*)(sm + L::kBar);
     uint64_t *b_s = bar.s, *b_p = bar.p;
     const TileInfo* info = (const TileInfo*)(sm + L::kInfo);
-    Wait wait{(volatile int*)(sm + L::kMisc + 4), status, true};
+    volatile int* abort_flag = (volatile int*)(sm + L::kMisc + 4);
+    Wait wait{abort_flag, status, *abort_flag == 0};
     const uint32_t ts = trow + str * 128, to = trow + kColO + str * 128;
     const int lane = threadIdx.x & 31;
     float m = kNoRef, l = 0.f;
@@ -374,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t* see = vis + 4 * step_row;
             const float2 y = weigh_tiles<D>(sm, trow, str, n + (pair ? 0 : str), pair ? 1 : 2, tiles, done, any, see, a.sl2, a.status);
             float m = y.x, l = y.y;
+            wait.ok = wait.ok && *abort_flag == 0;
             done += tiles;
             // ---- the run's result
             wait(b_o, segs);
