@@ -19,8 +19,6 @@
 // heads over 31 to 256 keys behind 1000 shared ones (303 MB read here, 18 in
 // k_kv16_wide beside it): 65 us in all, 59 alone on its share of the SMs, 5.2 TB/s.
 // Two stages of 8 KB a team: with three that call took 78 us, not 71.
-#include <cuda_fp16.h>
-
 #include "kv16_sched.cuh"
 
 namespace la {

@@ -440,6 +440,25 @@ def test_attention_bad_values_beside_shared_prefixes():
             assert (_call(c) == 123).all() and refused(c)
 
 
+def test_attention_more_keys_than_a_schedule_holds():
+    """64 sequences x 64 heads over 7.9 M keys each (one page named again and again) are refused on the device."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    B, H, D, page, mp = 64, 64, 64, 128, 61440
+    c = LA.KV16Cache(*LA.KV16Cache.empty_pages(1, H, D, page), max_pages=mp)
+    x = torch.zeros((B, H * D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 123.0)
+    table = torch.zeros((B, mp), dtype=torch.int32, device="cuda")
+    ws = torch.empty(c.attention_bytes(B, H, 0, 2, 0), dtype=torch.uint8, device="cuda")
+    c.attention(x, x, x, _i32([page * mp] * B), table, 0, 2, 0, out=out, workspace=ws)
+    with pytest.raises(LA.LAError) as e:
+        c.check()
+    assert e.value.code == LA.LA_ERR_ARG and (out == 123).all()
+    c.attention(x, x, x, _i32([300] * B), table, 0, 2, 0, out=out, workspace=ws)
+    c.check()
+    assert (out == 0).all()
+
+
 def test_attention_buffers_at_odd_16_byte_places():
     """q, k_step, v_step, out and the workspace at 16 bytes past other boundaries; what lies beside them stays."""
     import torch
