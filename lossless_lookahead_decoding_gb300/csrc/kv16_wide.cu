@@ -31,7 +31,7 @@
 // and the two products after it (0.27 us each, with the hand-overs 0.6 us), which
 // the other stream's softmax only hides in part: tensor pipe 54 %, issue slots
 // 41 %, special functions 26 %.  8 steps of 57 rows x 8 heads, 8 KV heads, over
-// 8.3 to 9.5 K keys (133 GFLOP): 130 us, 1.02 PFLOP/s.  Measured for that call and not taken:
+// 8.3 to 9.5 K keys (133 GFLOP): 129 us, 1.03 PFLOP/s.  Measured for that call and not taken:
 // 16 softmax warps (147 against 122 us for the kernel: twice the loads from tensor
 // memory), streams strictly by turns (150), loads from tensor memory ahead of their
 // use (165), sums of unrounded weights (126 against 120), sums by a product (152),
@@ -128,6 +128,12 @@ __device__ __forceinline__ float weigh64(const uint32_t (&x)[64], float f, float
     float t0, t1, t2, t3;
     unpair(s0, t0, t1), unpair(s1, t2, t3);
     return (t0 + t1) + (t2 + t3);
+}
+
+// 16 bytes, or zeros (then nothing is read)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // A wait that gives up ends every later one at once, but no role leaves its
@@ -361,28 +367,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int mine = pair ? str * 128 : 0;  // of the item's rows, the stream's first
             const int gr = x.row0 + r0 + mine + row;
             const bool live_row = mine + row < nrows, any = mine + q * 32 < nrows;
-            // ---- queries.  Neighbouring threads take neighbouring 16-byte pieces of a row.
+            // ---- queries.  Neighbouring threads take neighbouring 16-byte pieces of a row, all on their way at once.  (In a
+            // short loop: unrolled it cost the tiles' loops 10 %, the roles' code shares the instruction caches.  Asking
+            // for the next run's while this one's result is written won nothing.)
             if (tiles > 0) {
                 constexpr int kPieces = D / 8, kPass = 128 / kPieces;
                 const int t = threadIdx.x & 127, pc = t % kPieces, rr = t / kPieces;
                 const int first = x.row0 + r0 + mine + rr;
                 int si = first / group, sj = first - si * group;
                 const int di = kPass / group, dj = kPass - di * group;
-                uint8_t* dst = sm + L::kQ + str * L::kOperand;
+                const uint32_t dst = smem_u32(sm) + L::kQ + str * L::kOperand;
 #pragma unroll 1
-                for (int i0 = 0; i0 < 128 / kPass; i0 += 8) {
-                    uint4 u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        u[i] = make_uint4(0, 0, 0, 0);
-                        if (mine + rr + (i0 + i) * kPass < nrows)
-                            u[i] = *(const uint4*)(a.q + (size_t)si * a.q_ld + (size_t)(g * group + sj) * D + 8 * pc);
-                        si += di, sj += dj;
-                        if (sj >= group) sj -= group, si++;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i++) *(uint4*)(dst + piece_at(pc, rr + (i0 + i) * kPass)) = u[i];
+                for (int i = 0; i < 128 / kPass; i++) {
+                    const bool there = mine + rr + i * kPass < nrows;
+                    const size_t at = there ? (size_t)si * a.q_ld + (size_t)(g * group + sj) * D + 8 * pc : 0;
+                    cp16(dst + piece_at(pc, rr + i * kPass), a.q + at, there);
+                    si += di, sj += dj;
+                    if (sj >= group) sj -= group, si++;
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async();
             }
             __syncwarp();
