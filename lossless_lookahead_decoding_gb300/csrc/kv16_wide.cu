@@ -214,6 +214,7 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                         // (rare) the reference moves up to the largest of the scores from here on, and the weights before
                         // and the outputs down with it (this tile's scores came behind the last one's products)
                         float top = -INFINITY;
+                        tmem_st_wait();  // (the first half's weights)
 #pragma unroll 1
                         for (int c = 2 * h; c < n32; c++) {
                             const uint32_t k = ti.part ? counted(ti, c, see) : ~0u;
@@ -255,9 +256,9 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                     l += sum;
                     tmem_st16(ts + h * 32, p);
                     tmem_st16(ts + h * 32 + 16, p + 16);
-                    tmem_st_wait();
                 }
             }
+            tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
