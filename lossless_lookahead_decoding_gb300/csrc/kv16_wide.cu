@@ -190,7 +190,7 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                 if (2 * h < n32) {
                     uint32_t p[32];
                     float sum;
-                    while (true) {
+                    for (bool moved = false;; moved = true) {
                         uint32_t x[64];
                         tmem_ld64_raw(ts + h * 64, x);
                         if (ti.part) {
@@ -210,7 +210,9 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                             first = false;
                         }
                         sum = weigh64(x, f, m, p);
-                        if (!__any_sync(0xffffffffu, sum > 32768.f)) break;
+                        // (one move does, and ends: behind it the largest score counts at most 2^8, but for what m is off by
+                        // itself, half a unit in its last place, which another move would not change)
+                        if (moved || !__any_sync(0xffffffffu, sum > 32768.f)) break;
                         // (rare) the reference moves up to the largest of the scores from here on, and the weights before
                         // and the outputs down with it (this tile's scores came behind the last one's products)
                         float top = -INFINITY;

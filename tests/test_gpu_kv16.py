@@ -682,3 +682,48 @@ def test_prompt_then_steps():
     done = _i32([0, 1, 1])
     cache.release(done, lens, table, free, n_free)
     assert lens.tolist() == [71, 0, 0] and int(n_free) == n_pages - 5
+
+
+# ------------------------------------------------- scores far from 0, nearly equal
+
+def _level(c, exp, sign=1, seed=0):
+    """Scores sign 2^exp (C + 0 or 1) of each KV head, C a whole number of 20 bits: exact in fp32, in whatever order
+    they are summed, so that the 64-bit reference has the same."""
+    import torch
+    g = np.random.default_rng(seed)
+    Hkv, D = c["cache"].n_kv_heads, c["D"]
+    c["q"].copy_(torch.full_like(c["q"], sign * 2.0 ** exp))
+    base = g.integers(128, 256, (Hkv, 3)) * 2.0 ** np.array([0, 6, 12])
+
+    def keys(shape):                                 # [..., Hkv, D]
+        k = np.zeros((*shape, Hkv, D))
+        k[..., :3], k[..., 3] = base, g.integers(0, 2, (*shape, Hkv))
+        return _bf(k)
+
+    kp = c["cache"].k_pages                          # [n_pages, Hkv, page, D]; unwritten slots stay NaN
+    n_pages, _, page, _ = kp.shape
+    kp.copy_(torch.where(torch.isnan(kp), kp, keys((n_pages, page)).transpose(1, 2)))
+    c["k"].copy_(keys((len(c["k"]),)).flatten(1))
+
+
+LEVELS = [  # lens, prefixes, heads, kv heads, D, page, (W, N, G)
+    ([300, 40, 0], [(600, 2)], 8, 8, 128, 32, (0, 2, 0)),              # a row a sequence and KV head
+    ([300, 40, 0], [(600, 2)], 8, 4, 64, 16, (1, 4, 1)),               # 14
+    ([300, 40], [(600, 2)], 12, 6, 128, 16, (2, 4, 2)),                # 26: both streams have the same rows
+    ([300, 40], [(700, 2)], 24, 6, 64, 64, (7, 5, 7)),                 # 228: a stream has its own
+    ([30, 140, 7, 61] * 3, [(4000, 7), (3500, 5)], 12, 6, 128, 64, (0, 2, 0)),   # prefixes by themselves
+    ([30, 140, 7, 61] * 3, [(4000, 7), (3500, 5)], 12, 6, 64, 128, (3, 3, 3)),
+]
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exp", [0, 7, 11])
+@pytest.mark.parametrize("i", range(len(LEVELS)))
+def test_attention_nearly_equal_scores_far_from_zero(i, exp, sign):
+    """Scores of up to 2^28 (as powers of two of a weight) whose reference is off by several powers of two itself."""
+    lens, prefixes, H, Hkv, D, page, (W, N, G) = LEVELS[i]
+    c = _case(lens, prefixes, H, Hkv, D, page, W, N, G, seed=60 + i)
+    _level(c, exp, sign, seed=i)
+    got = _call(c)
+    c["cache"].check()
+    _compare(c, got)
