@@ -3,9 +3,11 @@
 // their parts.
 //
 // A row's keys are its prefix's tokens, its sequence's own and the step's rows
-// that it sees: o = sum p_j v_j / sum p_j, p_j = exp2(s_j f - m) with f =
-// log2(e) / sqrt(D) and m the running largest of s_j f.  Any two parts of the
-// keys join by o = sum o_k 2^(m_k - m), l = sum l_k 2^(m_k - m).
+// that it sees: o = sum p_j v_j / sum p_j, p_j = exp2((s_j - m) f) with f =
+// log2(e) / sqrt(D) and m one of the s_j, about the largest.  Any two parts of the
+// keys join by o = sum o_k exp2((m_k - m) f), l = sum l_k exp2((m_k - m) f).
+// (Scores are subtracted before they are scaled: m f in fp32 is off by up to 2^-24 of
+// itself, at 2^31 more than exp2 can hold.)
 #include <algorithm>
 #include <mutex>
 
@@ -38,9 +40,9 @@ struct MergeArgs {
 template <int C>
 struct Sum {
     float top = kNoRef, l = 0.f, o[C] = {};
-    __device__ __forceinline__ void add(float m, float sum, const float (&v)[C])
+    __device__ __forceinline__ void add(float sl2, float m, float sum, const float (&v)[C])
     {
-        const float t = fmaxf(top, m), f = ex2(top - t), h = ex2(m - t);
+        const float t = fmaxf(top, m), f = ex2((top - t) * sl2), h = ex2((m - t) * sl2);
         top = t;
         l = l * f + sum * h;
 #pragma unroll
@@ -93,7 +95,7 @@ __device__ __forceinline__ void add_parts(const Kv16Attn& a, const float* slots,
             const bool none = m[j] == kNoRef && l[j] == 0.f;
 #pragma unroll
             for (int i = 0; i < C; i++) v[j][i] = none ? 0.f : v[j][i];
-            y.add(m[j], l[j], v[j]);
+            y.add(a.sl2, m[j], l[j], v[j]);
         }
     }
 }
@@ -174,13 +176,13 @@ __global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_con
             } else if (part == 0) {
                 if (w.by_rows) load_rows<D, 8>(w.whole_seq, (size_t)g * rows_all + gr, (size_t)a.Hkv * rows_all, ch, m, l, v);
                 else load_cols<D, 8>(w.whole_seq + (size_t)g * (D + 2) * rows_all + gr, rows_all, ch, m, l, v);
-                y.add(m, l, v);
+                y.add(a.sl2, m, l, v);
             }
             if (shared && p.n > 1 && p.t0 >= 0 && p.n <= w.teams_pre - p.t0) {
                 add_parts<D, 8, 3>(a, w.slots_pre, false, p.t0, p.n, gr - first, ch, part, groups, y);
             } else if (shared && part == groups - 1) {
                 load_cols<D, 8>(w.whole_pre + (size_t)g * (D + 2) * rows_all + gr, rows_all, ch, m, l, v);
-                y.add(m, l, v);
+                y.add(a.sl2, m, l, v);
             }
         }
     }
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_con
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = from[(2 + i) * 256];
-        y.add(from[0], from[256], v);
+        y.add(a.sl2, from[0], from[256], v);
     }
     put_row<D, 8>(a, y, g, gr, ch);
 }

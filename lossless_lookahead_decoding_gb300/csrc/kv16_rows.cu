@@ -10,9 +10,10 @@
 // swizzle that keeps ldmatrix free of bank conflicts.  Feeding runs ahead of
 // the products by the ring's stages, over the ends of items.
 //
-// P = exp2(S f - M) in bf16, S, M, the sums and O in fp32.  The reference M is
-// the row's largest score of the run's first block and moves only when a row's
-// P of a block sum to more than 2^15: a vote per block, no reduction.
+// P = exp2((S - M) f) in bf16, S, M, the sums and O in fp32.  The reference M is
+// the row's largest score of the run's first block and moves, to the largest so
+// far, only when a row's P of a block sum to more than 2^15: a vote per block, no
+// reduction.
 //
 // HBM bound: 4 D bytes a key and KV head, 32 products a block.  One CTA of 8 teams
 // a SM (243 registers: queries and outputs stay in them).  128 single tokens of 32
@@ -289,19 +290,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_kv16_rows(const __grid_const
                         float yb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
                         ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, 1)), yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, 1));
                         ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, 2)), yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, 2));
-                        const float na = fmaxf(ma, ya * a.sl2), nb = fmaxf(mb, yb * a.sl2);
-                        const float fa = ex2(ma - na), fb = ex2(mb - nb);
+                        const float na = fmaxf(ma, ya), nb = fmaxf(mb, yb);
+                        const float fa = ex2((ma - na) * a.sl2), fb = ex2((mb - nb) * a.sl2);
                         ma = na, mb = nb, la *= fa, lb *= fb;
 #pragma unroll
                         for (int i = 0; i < D / 8; i++) o[i][0] *= fa, o[i][1] *= fa, o[i][2] *= fb, o[i][3] *= fb;
                     }
-                    const float e0 = ex2(fmaf(x[0][0], a.sl2, -ma)), e1 = ex2(fmaf(x[0][1], a.sl2, -ma)),
-                                e2 = ex2(fmaf(x[1][0], a.sl2, -ma)), e3 = ex2(fmaf(x[1][1], a.sl2, -ma));
+                    const float e0 = ex2((x[0][0] - ma) * a.sl2), e1 = ex2((x[0][1] - ma) * a.sl2),
+                                e2 = ex2((x[1][0] - ma) * a.sl2), e3 = ex2((x[1][1] - ma) * a.sl2);
                     p[0] = pack_bf16(e0, e1), p[2] = pack_bf16(e2, e3);
                     sa = sum_of(p[0]) + sum_of(p[2]);
                     if (two) {
-                        const float g0 = ex2(fmaf(x[0][2], a.sl2, -mb)), g1 = ex2(fmaf(x[0][3], a.sl2, -mb)),
-                                    g2 = ex2(fmaf(x[1][2], a.sl2, -mb)), g3 = ex2(fmaf(x[1][3], a.sl2, -mb));
+                        const float g0 = ex2((x[0][2] - mb) * a.sl2), g1 = ex2((x[0][3] - mb) * a.sl2),
+                                    g2 = ex2((x[1][2] - mb) * a.sl2), g3 = ex2((x[1][3] - mb) * a.sl2);
                         p[1] = pack_bf16(g0, g1), p[3] = pack_bf16(g2, g3);
                         sb = sum_of(p[1]) + sum_of(p[3]);
                     }

@@ -11,6 +11,8 @@
 // which then leave no parts (240 items of 10 or 11 tiles on 152 teams, one or two
 // each: 42.2 us, cut into equal runs 44.3).
 #pragma once
+#include <cfloat>
+
 #include "kv16.cuh"
 
 namespace la {
@@ -19,7 +21,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kSMs = 152;
-constexpr float kNoRef = -3e38f;  // below every score: exp2(-inf - kNoRef) = 0
+constexpr float kNoRef = -FLT_MAX;  // below every score: exp2((-inf - kNoRef) f) = 0
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {

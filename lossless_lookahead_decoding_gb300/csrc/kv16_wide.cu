@@ -11,13 +11,16 @@
 // SM can read from L2); with fewer, both have the same rows and take every
 // second tile, and join their results at the end.  Per stream and tile
 //   S = Q K^T          Q and K in shared memory, S in tensor memory
-//   P = exp2(S f - M)  in bf16, in the place of S
+//   P = exp2((S - M) f)  in bf16, in the place of S
 //   O += P V           P from tensor memory, V in shared memory
 // with S, M, the sums and O in fp32, half a tile at a time.  The reference M is
-// the largest score of a row's first half tile and moves, by a power of two, only
-// when a row's P of a half tile sum to more than 2^15: weights of up to 2^15 lose
-// no more in bf16 than smaller ones, and O is read back once in many thousand
-// tiles.  The half's weights stay in registers until that is known.
+// the largest score of a row's first half tile and moves, to the largest since,
+// only when a row's P of a half tile sum to more than a bound: weights above 1
+// lose no more in bf16 than smaller ones, and O is read back once in many thousand
+// tiles.  The half's weights stay in registers until that is known.  The bound is
+// 2^15 for a tile's first half and 2^30 for its second (O has room for 2^17 tiles
+// of values up to 2^70): a move in the second rounds the first one's weights, in
+// their place already, once more, when they are less than 2^-15 of the sum.
 //
 // Keys that are not there: their scores count as -inf, and their values, of
 // which a product would take 0 x NaN, are cleared in shared memory, as are the
@@ -158,6 +161,30 @@ struct Wait {
     }
 };
 
+// A reference m, as f times a score, does for |m| < 512: it is off by no more than
+// 2^-16 then.  Where it is further from 0 (what it is off by grows with it, at 2^31
+// past what exp2 can hold) m is kFar, with which any score's weight is past every
+// bound, and the score itself is taken away from the others before they are scaled.
+// (So it is before a run's first score that counts.)  x - m for every score would be
+// one instruction more for two of them: 145 us, not 130, for the call above.
+constexpr float kFar = kNoRef;
+__device__ __forceinline__ float near_of(float score, float f) { return fabsf(score * f) < 512.f ? score * f : kFar; }
+
+// Takes `far` away from 64 scores, where they are.
+__device__ __noinline__ void take_away(uint32_t ts, float far)
+{
+#pragma unroll 1
+    for (int j = 0; j < 64; j += 8) {
+        uint32_t y[8];
+        tmem_ld8(ts + j, y);
+#pragma unroll
+        for (int e = 0; e < 8; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) - far);
+        tmem_st8(ts + j, y);
+    }
+    tmem_st_wait();
+}
+
+
 // A stream's tiles of a run, `step` apart from tile n (`done` before them): the
 // scores become weights where they are.  Returns the row's reference and sum.  A
 // function, so that what its caller keeps over it leaves the registers once and
@@ -175,7 +202,8 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
     Wait wait{abort_flag, status, *abort_flag == 0};
     const uint32_t ts = trow + str * 128, to = trow + kColO + str * 128;
     const int lane = threadIdx.x & 31;
-    float m = kNoRef, l = 0.f;
+    volatile float ref = kNoRef;  // the reference as a score (in memory: it is looked at once in a while, and in a register the call takes 139 us)
+    float m = kFar, l = 0.f;
     bool first = true;
     for (int i = 0; i < tiles; i++, done++) {
         wait(b_s + str, done);
@@ -190,7 +218,8 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                 if (2 * h < n32) {
                     uint32_t p[32];
                     float sum;
-                    for (bool moved = false;; moved = true) {
+                    bool moved = false;
+                    while (true) {
                         uint32_t x[64];
                         tmem_ld64_raw(ts + h * 64, x);
                         if (ti.part) {
@@ -206,15 +235,15 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                             float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                             for (int j = 0; j < 64; j += 2) t0 = fmaxf(t0, __uint_as_float(x[j])), t1 = fmaxf(t1, __uint_as_float(x[j + 1]));
-                            m = fmaxf(m, fmaxf(t0, t1) * f);
+                            t0 = fmaxf(kNoRef, fmaxf(t0, t1)), m = near_of(t0, f), ref = t0;
                             first = false;
                         }
                         sum = weigh64(x, f, m, p);
-                        // (one move does, and ends: behind it the largest score counts at most 2^8, but for what m is off by
-                        // itself, half a unit in its last place, which another move would not change)
-                        if (moved || !__any_sync(0xffffffffu, sum > 32768.f)) break;
-                        // (rare) the reference moves up to the largest of the scores from here on, and the weights before
-                        // and the outputs down with it (this tile's scores came behind the last one's products)
+                        if (moved || !__any_sync(0xffffffffu, sum > (h ? 0x1p30f : 0x1p15f))) break;
+                        moved = true;
+                        // (rare) a row's reference moves up to the largest of its scores from here on, where that one counts more
+                        // than 2^9 (2^24), and the weights before and the outputs down with it (this tile's scores came behind
+                        // the last one's products)
                         float top = -INFINITY;
                         tmem_st_wait();  // (the first half's weights)
 #pragma unroll 1
@@ -229,11 +258,12 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                                     if ((k >> (j + e)) & 1) top = fmaxf(top, __uint_as_float(y[e]));
                             }
                         }
-                        top *= f;
-                        // (by a whole number: weights in bf16 are moved by a power of two, exactly)
-                        const float up = top > m + 8.f ? ceilf(top - m) : 0.f;
-                        const float by = up <= 126.f ? __uint_as_float((uint32_t)(127 - (int)up) << 23) : 0.f;
-                        m = up <= 126.f ? m + up : top, l *= by;
+                        float far = ref;
+                        const float power = m == kFar ? (top - far) * f : fmaf(top, f, -m);
+                        const bool up = power > (h ? 24.f : 9.f);
+                        const float by = up ? ex2(-power) : 1.f;
+                        if (up) ref = far = top, m = near_of(top, f);
+                        l *= by;
                         const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
 #pragma unroll 1
                         for (int j = 0; j < h * 32; j += 8) {
@@ -254,7 +284,10 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
                             for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
                             tmem_st8(to + j, o);
                         }
+                        take_away(ts + h * 64, m == kFar ? far : 0.f);
+                        m = m == kFar ? 0.f : m;
                     }
+                    if (moved) m = near_of(ref, f);
                     l += sum;
                     tmem_st16(ts + h * 32, p);
                     tmem_st16(ts + h * 32 + 16, p + 16);
@@ -266,7 +299,7 @@ __device__ __noinline__ float2 weigh_tiles(uint8_t* sm, uint32_t trow, int str, 
         __syncwarp();
         if (lane == 0 && wait.ok) mbar_arrive(b_p + str);
     }
-    return make_float2(m, l);
+    return make_float2(ref, l);
 }
 
 // Tensor maps of keys and values: blocks of 16 rows of the step and of pages, and whole pages.
@@ -414,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_sync(1, 256);
                 const float2 other = ml[(str ^ 1) * 128 + row];
                 const float top = fmaxf(m, other.x);
-                w0 = ex2(m - top), w1 = ex2(other.x - top);
+                w0 = ex2((m - top) * a.sl2), w1 = ex2((other.x - top) * a.sl2);
                 l = l * w0 + other.y * w1, m = top;
                 c0 = str * (D / 2), c1 = c0 + D / 2;
             }

@@ -727,3 +727,47 @@ def test_attention_nearly_equal_scores_far_from_zero(i, exp, sign):
     got = _call(c)
     c["cache"].check()
     _compare(c, got)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exp", [14, 20, 45, 100])
+@pytest.mark.parametrize("i", range(len(LEVELS)))
+def test_attention_finite_scores_of_any_size(i, exp, sign):
+    """Scores of 2^31 to 2^118: what fp32 makes of their product with log2(e) / sqrt(D) is off by more than exp2 can hold."""
+    test_attention_nearly_equal_scores_far_from_zero(i, exp, sign)
+
+
+@pytest.mark.parametrize("bits", [0.3, 0.6, 2.0, 40.0, -0.6])
+@pytest.mark.parametrize("i", range(len(LEVELS)))
+def test_attention_scores_that_rise_along_the_keys(i, bits):
+    """Every key weighs 2^bits times the one before it, so that references move in either half of a tile, in many of
+    them, and parts differ by hundreds of powers of two."""
+    import math
+    lens, prefixes, H, Hkv, D, page, (W, N, G) = LEVELS[i]
+    c = _case(lens, prefixes, H, Hkv, D, page, W, N, G, seed=70 + i, level=0.5)
+    step = np.float32(bits * math.log(2) * math.sqrt(D))
+
+    def put(row, at, t):                                # position t as 256 a + b, each exact in bf16 but for the step
+        kp[int(row[at // page]), :, at % page, 0] = float(step * 256 * (t // 256))
+        kp[int(row[at // page]), :, at % page, 1] = float(step * (t % 256))
+
+    kp = c["cache"].k_pages.cpu()
+    for p, (_, _, n) in enumerate(c["spans"]):
+        for t in range(n):
+            put(c["ptable"][p], t, t)
+    for b, n in enumerate(lens):
+        before = sum(m for lo, hi, m in c["spans"] if lo <= b < hi)
+        for t in range(n):
+            put(c["table"][b], t, before + t)
+    c["cache"].k_pages.copy_(kp)
+    q = c["q"].reshape(-1, H, D).clone()
+    q[..., :2] = 1
+    c["q"] = q.flatten(1)
+    got = _call(c)
+    c["cache"].check()
+    # A score far from 0 is known to 2^-23 of itself for each of its D / 16 + 1 sums in fp32, its weight to as much, in
+    # nats: sum p e (v - o) is at most e (|v| + |o|) more.
+    far = abs(bits) * math.log(2) * (max(lens) + max(m for _, _, m in c["spans"])) + 10
+    e = (D // 16 + 1) * 2.0 ** -23 * far
+    o, spread = _want(c)
+    _compare(c, got, (o, spread + 2.0 ** 7 * e * (4 + o.abs())))
