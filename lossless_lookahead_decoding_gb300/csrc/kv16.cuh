@@ -32,20 +32,23 @@ struct alignas(16) Kv16Item {
     int pad[2];
 };
 
-// How one kernel's teams share its entries (prefixes, then sequences), and
+// What the two kinds of teams work in: rows of an item; blocks of 16 keys in a tile;
+// with more rows than these (0: never) an entry's tiles count twice; units an item
+// counts for beyond its tiles; units worth a team; units that whole items are worth.
+struct WideKind {
+    static constexpr int row_tile = 256, blk_log2 = 3, twice = 128, extra = 4, min_run = 6, slack = 12;
+};
+struct RowsKind {
+    static constexpr int row_tile = 16, blk_log2 = 0, twice = 0, extra = 2, min_run = 8, slack = 16;  // (one item holds all rows)
+};
+
+// How one kind of teams share its entries (prefixes, then sequences), and
 // where what they do not finish goes.
 struct Kv16Sched {
     int n_pre, n_seq;         // entries
-    int row_tile;             // rows of an item
-    int blk_log2;             // blocks of 16 keys in a tile
-    int wide;                 // with more rows than these an entry's tiles count twice
-    int extra;                // units an item counts for beyond its tiles
     int nteams, per_cta;      // teams; of a CTA
-    int min_run, slack;
     int direct;               // team t has item t: all items are sequences', and there is a team for each
     int finish;               // whole items go to the output (else to `whole`)
-    int first;                // the call's first kernel
-    int beside;               // the other kernel's items run at the same time: the SMs are shared by their work
     Kv16Item* items;          // finish: [nteams]; else [KV heads][rows]: of prefixes, then of sequences
     int* bad;                 // prefix_first is out of order, or there is too much to do: nothing is done
     float* slots;             // [nteams][2]: parts of split items

@@ -20,7 +20,8 @@ int kv16_rows_teams();
 cudaError_t launch_kv16_rows(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D);
 bool kv16_wide_init();
 int kv16_wide_teams();
-int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D, int rows_all);
+int kv16_beside_teams();
+int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, const Kv16Sched* beside, int D, int rows_all);
 
 namespace {
 // ------------------------------------------------------------------- merge ---
@@ -32,7 +33,6 @@ struct MergeArgs {
     const float *slots_pre, *slots_seq, *whole_pre, *whole_seq;
     int rows_pre_tile;        // rows of a prefix's item
     int by_rows;              // sequences' parts are rows (k_kv16_rows), else columns
-    int kernels;              // that said whether all is well
     int teams, teams_pre;     // that may have parts (nothing else is read, whatever a workspace holds)
     int chunks;               // groups of rows of an item
 };
@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_con
 {
     __shared__ float sums[kMaxGroups - 1][10][256];
     pdl_wait();
-    fence_acquire();  // (of both kernels before it)
     pdl_trigger();
     const Kv16Attn& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp >> 3, groups = blockDim.x >> 8, at = threadIdx.x & 255;
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(256 * kMaxGroups) k_kv16_join(const __grid_con
     if (live) {
         const int row0 = gr / a.R * a.R;
         const Kv16Item it = w.items[(size_t)(a.Hkv + g) * rows_all + row0];
-        live = !w.bad[0] && !w.bad[w.kernels - 1] && it.n > 0 && it.t0 >= 0 && it.n <= w.teams - it.t0;
+        live = !*w.bad && it.n > 0 && it.t0 >= 0 && it.n <= w.teams - it.t0;
         if (live) {
             float m, l, v[8];
             const bool shared = it.pre_row >= 0 && it.pre_row <= gr;
@@ -254,27 +253,24 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     if (p.use_wide) {
         Kv16Sched& s = p.wide;
         s.n_pre = p.apart ? k.nP : 0, s.n_seq = p.use_rows ? 0 : k.B;
-        s.row_tile = kWideRows, s.blk_log2 = 3, s.wide = 128, s.extra = 4;
-        s.nteams = kv16_wide_teams(), s.per_cta = 1, s.min_run = 6, s.slack = 12;
+        s.nteams = kv16_wide_teams(), s.per_cta = 1;
         const long long items = (long long)k.B * k.Hkv * ((k.R + kWideRows - 1) / kWideRows);
-        if (!p.apart && items <= s.nteams && (most + 7) / 8 * (k.R > 128 ? 2 : 1) <= s.slack) s.nteams = (int)items, s.direct = 1;
+        if (!p.apart && items <= s.nteams && (most + 7) / 8 * (k.R > WideKind::twice ? 2 : 1) <= WideKind::slack) s.nteams = (int)items, s.direct = 1;
     }
     if (p.use_rows) {
         Kv16Sched& s = p.rows;
-        s.n_seq = k.B, s.row_tile = 16, s.wide = 1 << 30, s.extra = 2;
+        s.n_seq = k.B;
         const long long items = (long long)k.B * k.Hkv;
-        s.nteams = kv16_rows_teams(), s.per_cta = kv16_rows_teams() / kSMs, s.min_run = 8, s.slack = 16;
-        if (!p.apart && items <= s.nteams && most <= s.slack) s.nteams = (int)items, s.direct = 1;
+        s.nteams = p.apart ? kv16_beside_teams() : kv16_rows_teams(), s.per_cta = s.nteams / kSMs;
+        if (!p.apart && items <= s.nteams && most <= RowsKind::slack) s.nteams = (int)items, s.direct = 1;
     }
     // ---- where their results go
     Kv16Sched& last = p.use_rows ? p.rows : p.wide;
-    (p.use_wide ? p.wide : p.rows).first = 1;
     const size_t all = (size_t)k.Hkv * rows_all * (D + 2) * 4;  // results of whole items
     if (p.apart) {
-        p.m.bad = (int*)room(8);
+        p.m.bad = (int*)room(4);
         p.m.items = (Kv16Item*)room(2 * (size_t)k.Hkv * rows_all * sizeof(Kv16Item));
         p.m.whole_pre = (float*)room(all), p.m.whole_seq = (float*)room(all);
-        p.wide.beside = p.rows.beside = p.use_rows;
     } else {
         if (!last.direct) p.m.items = (Kv16Item*)room(last.nteams * sizeof(Kv16Item));
         last.finish = 1;
@@ -283,14 +279,13 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
     if (p.use_rows && !p.rows.direct) p.rows.slots = (float*)room((size_t)p.rows.nteams * 2 * rows_part(D, k.R) * 4);
     for (Kv16Sched* s : {&p.wide, &p.rows}) {
         s->items = (Kv16Item*)p.m.items;
-        if (p.apart) s->bad = (int*)p.m.bad + (s->first ? 0 : 1);
+        if (p.apart) s->bad = (int*)p.m.bad;
         s->whole = (float*)p.m.whole_seq, s->whole_pre = (float*)p.m.whole_pre;
     }
     p.m.slots_pre = p.wide.slots, p.m.slots_seq = last.slots;
     p.m.rows_pre_tile = kWideRows, p.m.by_rows = p.use_rows;
     p.merge = !last.direct;
-    p.m.kernels = p.use_rows && p.use_wide ? 2 : 1;
-    p.m.teams = last.nteams, p.m.teams_pre = p.wide.nteams, p.m.chunks = (std::min(last.row_tile, k.R) + (p.use_rows ? 7 : 31)) / (p.use_rows ? 8 : 32);
+    p.m.teams = last.nteams, p.m.teams_pre = p.wide.nteams, p.m.chunks = (std::min(p.use_rows ? RowsKind::row_tile : WideKind::row_tile, k.R) + (p.use_rows ? 7 : 31)) / (p.use_rows ? 8 : 32);
     // as many groups of warps as an item may have fours of parts
     const long long parts = (p.use_wide ? p.wide.nteams : p.rows.nteams) / std::max(1LL, (long long)k.Hkv * (p.apart ? (rows_all + 255) / 256 : k.B));
     p.groups = parts >= 9 ? 4 : parts >= 4 ? 2 : 1;
@@ -339,10 +334,10 @@ int launch_kv16_attn(cudaStream_t s, const la_kv16_desc& c, const la_kv16_attn& 
     p.m.a = k;
     const int D = c.head_dim;
     if (p.use_wide) {
-        const int rc = launch_kv16_wide(s, k, p.wide, D, k.B * k.R);
+        const int rc = launch_kv16_wide(s, k, p.wide, p.use_rows ? &p.rows : nullptr, D, k.B * k.R);
         if (rc != LA_OK) return rc;
     }
-    cudaError_t e = p.use_rows ? launch_kv16_rows(s, k, p.rows, D) : cudaSuccess;
+    cudaError_t e = p.use_rows && !p.use_wide ? launch_kv16_rows(s, k, p.rows, D) : cudaSuccess;
     if (e == cudaSuccess && p.merge) e = D == 128 ? launch_merge<128>(s, p) : launch_merge<64>(s, p);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }

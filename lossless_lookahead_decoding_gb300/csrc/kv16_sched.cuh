@@ -29,8 +29,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void fence_acquire() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
-
 __device__ __forceinline__ int blocks_of(int n) { return (n + 15) >> 4; }
 
 // The prefixes' bounds and lengths, copied to shared memory where they fit.
@@ -59,7 +57,11 @@ struct Entry {
     __device__ __forceinline__ int nb_cached() const { return nb_pre + blocks_of(len); }
 };
 
+template <class K>
+__device__ __forceinline__ int tiles_of(int blocks) { return (blocks + (1 << K::blk_log2) - 1) >> K::blk_log2; }
+
 // An entry; n: the sequence's own tokens (not looked at for a prefix's entry).
+template <class K>
 __device__ __forceinline__ Entry entry_with(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, int e, int n)
 {
     Entry x;
@@ -78,20 +80,22 @@ __device__ __forceinline__ Entry entry_with(const Kv16Attn& a, const Kv16Sched& 
     }
     x.nb_pre = blocks_of(x.plen);
     x.nb += x.nb_pre + blocks_of(x.len);
-    x.wide = x.rows > s.wide;
-    x.tiles = (x.nb + (1 << s.blk_log2) - 1) >> s.blk_log2;
-    x.mt = (x.rows + s.row_tile - 1) / s.row_tile;
-    x.nu = x.rows ? s.extra + (x.tiles << x.wide) : 0;
+    x.wide = K::twice && x.rows > K::twice;
+    x.tiles = tiles_of<K>(x.nb);
+    x.mt = K::twice ? (x.rows + K::row_tile - 1) / K::row_tile : x.rows > 0;
+    x.nu = x.rows ? K::extra + (x.tiles << x.wide) : 0;
     return x;
 }
 
+template <class K>
 __device__ __forceinline__ Entry entry_of(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, int e)
 {
-    return entry_with(a, s, pre, e, e < s.n_pre ? 0 : a.lens[e - s.n_pre]);
+    return entry_with<K>(a, s, pre, e, e < s.n_pre ? 0 : a.lens[e - s.n_pre]);
 }
 
 // The first tile at or behind unit u of an item.
-__device__ __forceinline__ int tile_at(const Kv16Sched& s, const Entry& x, int u) { return max(u - s.extra + x.wide, 0) >> x.wide; }
+template <class K>
+__device__ __forceinline__ int tile_at(const Entry& x, int u) { return max(u - K::extra + x.wide, 0) >> x.wide; }
 
 // The teams' runs: team t begins at unit q t + min(t, r).  (All units fit 31 bits,
 // or nothing is done: 64-bit sums and divisions took most of a small call's time.)
@@ -115,13 +119,13 @@ struct PreShared {
 };
 
 struct Scan {
-    int units[32], big[32], cost[32], items[32], top[32];
+    int units[32], big[32], items[32], top[32];
     Shares shares;
 };
 
-// Of two kernels that run at the same time, the SMs of the wide one: with uw units
-// (a tile for a stream: 32 KB of a pair's tile, 0.95 us) and ur blocks (8 KB at D =
-// 128, 0.126 us at what one SM can read) both end together.  Where HBM and not the
+// Where some CTAs take prefixes and the others sequences, how many take prefixes: with
+// uw units (a tile for a stream: 32 KB of a pair's tile, 0.95 us) and ur blocks (8 KB at
+// D = 128, 0.126 us at what one SM can read) both end together.  Where HBM and not the
 // SMs sets the pace, a wide unit waits for its tiles and takes 1.73 us.  (128 single
 // tokens behind 1000, us in all, at 1.0, 1.4, 1.73 and 2.4 us a unit: 77, 67, 65, 64;
 // 48 behind prefixes of up to 4000: 61, 56, 54, 56; one kernel after the other, the
@@ -135,16 +139,17 @@ __device__ __forceinline__ int wide_sms(float uw, float ur, int D)
     return min(max((int)(w * kSMs / fmaxf(w + r, 1e-3f)) + 1, 4), kSMs - 8);
 }
 
-// Where each of the CTA's teams begins; the shares go to sc.  CTA 0 of the
-// call's first kernel raises what is wrong with the sequences.
-template <int D>
-__device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* starts, Scan* sc, PreShared* ps)
+// What a thread's entries come to.
+struct Sums {
+    int e0, e1, units, items, before;  // before: units of the warp's threads up to this one
+    Entry x0;
+};
+
+// The sequences and prefixes as they are, the same for all schedules: word of what is
+// wrong with them (by CTA 0), prefixes to shared memory where they fit.  True: nothing
+// is to be done.
+__device__ __forceinline__ bool look_over(const Kv16Attn& a, PreShared* ps, Prefixes& pre)
 {
-    const int n = s.per_cta, entries = s.n_pre + s.n_seq;
-    const int per = entries <= (int)blockDim.x ? 1 : ceil_div(entries, (int)blockDim.x), e0 = threadIdx.x * per, e1 = min(e0 + per, entries);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    // ---- all loads at once
-    const int len0 = !s.direct && e0 < e1 && e0 >= s.n_pre ? a.lens[e0 - s.n_pre] : 0;
     const bool fits = a.nP <= PreShared::kMost;
     bool bad = false, wrong = false;
     for (int p = threadIdx.x; p < a.nP; p += blockDim.x) {
@@ -156,107 +161,116 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
             if (p == a.nP - 1) ps->first[p + 1] = hi;
         }
     }
-    if (blockIdx.x == 0 && s.first) {
+    if (blockIdx.x == 0) {
         for (int b = threadIdx.x; b < a.B; b += blockDim.x) wrong |= a.lens[b] > a.max_len;
         if (wrong || bad) kv4_raise(a.status, LA_ERR_ARG);
     }
-    const Prefixes pre = fits ? Prefixes{ps->first, ps->lens} : Prefixes{a.pfirst, a.plens};
-    if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
-    bad = __syncthreads_or(bad);
-    if (s.direct) {
-        const int mt = (a.R + s.row_tile - 1) / s.row_tile, each = a.Hkv * mt, t = blockIdx.x * n + threadIdx.x;
-        if (threadIdx.x == 0) sc->shares = Shares{1, 0, s.nteams, 1};
-        if ((int)threadIdx.x < n && t < s.nteams && !bad) {
-            const int e = (unsigned)t / (unsigned)each;
-            starts[threadIdx.x] = Start{e, t - e * each, 1, t};
-        }
-        __syncthreads();
-        return pre;
-    }
+    pre = fits ? Prefixes{ps->first, ps->lens} : Prefixes{a.pfirst, a.plens};
+    return __syncthreads_or(bad);
+}
+
+__device__ __forceinline__ void first_entry(const Kv16Sched& s, int& e0, int& e1)
+{
+    const int entries = s.n_pre + s.n_seq, per = entries <= (int)blockDim.x ? 1 : ceil_div(entries, (int)blockDim.x);
+    e0 = threadIdx.x * per, e1 = min(e0 + per, entries);
+}
+
+// Adds up the entries of each thread, and those of a warp in sc (len0: the length of the thread's first one).
+template <class K>
+__device__ __forceinline__ Sums add_up(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, Scan* sc, bool bad, int len0)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums y;
+    first_entry(s, y.e0, y.e1);
+    y.x0.mt = y.x0.nu = 0;
     long long sum = 0;
-    int items = 0, top = 0, cost = 0;
-    Entry x0;
-    x0.mt = x0.nu = 0;
+    int items = 0, top = 0;
     if (!bad) {
-        for (int e = e0; e < e1; e++) {
-            const Entry x = entry_with(a, s, pre, e, e == e0 || e < s.n_pre ? len0 : a.lens[e - s.n_pre]);
+        for (int e = y.e0; e < y.e1; e++) {
+            const Entry x = entry_with<K>(a, s, pre, e, e == y.e0 || e < s.n_pre ? len0 : a.lens[e - s.n_pre]);
             const int k = a.Hkv * x.mt;
-            if (e == e0) x0 = x;
+            if (e == y.e0) y.x0 = x;
             if (x.nu) sum += (long long)k * x.nu, items = min(items + k, 1 << 20), top = max(top, x.nu);
             else if (!s.finish && x.b >= 0 && blockIdx.x == 0)
                 // no rows, which the merge is to know
                 for (int g = 0; g < a.Hkv; g++) s.items[(size_t)(a.Hkv + g) * a.B * a.R + x.row0].n = 0;
         }
-        if (s.beside) {
-            // the other kernel's work, by KV heads
-            if (s.n_pre)
-                for (int b = threadIdx.x; b < a.B; b += blockDim.x) cost += blocks_of(min(max(a.lens[b], 0), a.max_len)) + 3;
-            else
-                for (int p = threadIdx.x; p < a.nP; p += blockDim.x) {
-                    const int rows = (pre.first[p + 1] - pre.first[p]) * a.R, m = min(max(pre.lens[p], 0), a.max_plen);
-                    cost += (rows + 255) / 256 * (4 + ((blocks_of(m) + 7) / 8 << (rows > 128)));
-                }
-        }
     }
-    const int units = (int)min(sum, 0x7fff0000LL);  // (there, or nothing is done: see `huge`)
-    int xu = units;
+    y.units = (int)min(sum, 0x7fff0000LL);  // (there, or nothing is done: see `huge`)
+    y.items = items;
+    int xu = y.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, xu, o);
-        if (lane >= o) xu += y;
+        const int z = __shfl_up_sync(0xffffffffu, xu, o);
+        if (lane >= o) xu += z;
     }
-    {
-        const int w_big = __reduce_add_sync(0xffffffffu, (int)min(sum >> 16, 1LL << 20)), w_cost = __reduce_add_sync(0xffffffffu, cost),
-                  w_items = __reduce_add_sync(0xffffffffu, items), w_top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 31) sc->units[warp] = xu, sc->big[warp] = w_big, sc->items[warp] = w_items, sc->top[warp] = w_top, sc->cost[warp] = w_cost;
-    }
-    __syncthreads();
-    const bool in = lane < nw;
-    const int u = in ? sc->units[lane] : 0, it = in ? sc->items[lane] : 0;
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? u : 0) + xu - units, all_u = __reduce_add_sync(0xffffffffu, u);
-    const int all_i = __reduce_add_sync(0xffffffffu, it);
-    top = __reduce_max_sync(0xffffffffu, in ? sc->top[lane] : 0);
+    y.before = xu - y.units;
+    const int w_big = __reduce_add_sync(0xffffffffu, (int)min(sum >> 16, 1LL << 20)), w_items = __reduce_add_sync(0xffffffffu, items),
+              w_top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 31) sc->units[warp] = xu, sc->big[warp] = w_big, sc->items[warp] = w_items, sc->top[warp] = w_top;
+    return y;
+}
+
+// All entries' units, or -1 if they do not fit.  (Behind a barrier after add_up.)
+__device__ __forceinline__ int all_units(const Scan* sc)
+{
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < (int)blockDim.x >> 5;
     const bool huge = __reduce_add_sync(0xffffffffu, in ? sc->big[lane] : 0) >= 0x7000;
-    if (huge && blockIdx.x == 0 && threadIdx.x == 0) kv4_raise(a.status, LA_ERR_ARG);
-    if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) *s.bad = bad || huge;
-    int ctas = gridDim.x;
-    if (s.beside) {
-        // (both kernels count alike)
-        const float mine = (float)all_u, other = (float)__reduce_add_sync(0xffffffffu, in ? sc->cost[lane] : 0) * (float)a.Hkv;
-        const int sms = s.n_pre ? wide_sms(mine, other, D) : wide_sms(other, mine, D);
-        ctas = s.n_pre ? sms : kSMs - sms;
-    }
+    const int all = __reduce_add_sync(0xffffffffu, in ? sc->units[lane] : 0);
+    return huge ? -1 : all;
+}
+
+// Word of whether all is well, by one thread of the call.
+__device__ __forceinline__ void say_bad(const Kv16Attn& a, const Kv16Sched& s, bool bad, bool huge)
+{
+    if (blockIdx.x != 0 || threadIdx.x != 0) return;
+    if (huge) kv4_raise(a.status, LA_ERR_ARG);
+    if (s.bad) *s.bad = bad || huge;
+}
+
+// Where each of the teams of CTA `cta` of `ctas` begins; the shares go to sc.
+template <class K>
+__device__ __forceinline__ void share_out(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, const Sums& y, int all_u, Start* starts, Scan* sc,
+                                          int cta, int ctas)
+{
+    const int n = s.per_cta, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool in = lane < (int)blockDim.x >> 5;
+    const int it = in ? sc->items[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sc->units[lane] : 0) + y.before;
+    const int all_i = __reduce_add_sync(0xffffffffu, it), top = __reduce_max_sync(0xffffffffu, in ? sc->top[lane] : 0);
+    const bool huge = all_u < 0;
     const int room = min(s.nteams, ctas * n);
     Shares h;
     // Whole items leave no parts: worth `slack` units of the longest team's work.
-    h.whole = all_i <= 4 * room && ceil_div(all_i, room) * top - s.slack <= (int)((unsigned)all_u / (unsigned)room);
+    h.whole = !huge && all_i <= 4 * room && ceil_div(all_i, room) * top - K::slack <= (int)((unsigned)all_u / (unsigned)room);
     int bi = 0;
     if (h.whole) {
         // the same for whole items
-        int xi = items;
+        int xi = y.items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, xi, o);
-            if (lane >= o) xi += y;
+            const int z = __shfl_up_sync(0xffffffffu, xi, o);
+            if (lane >= o) xi += z;
         }
-        bi = xi - items + __reduce_add_sync(0xffffffffu, lane < warp ? it : 0);
+        bi = xi - y.items + __reduce_add_sync(0xffffffffu, lane < warp ? it : 0);
     }
     const int all = huge ? 0 : h.whole ? all_i : all_u;
-    h.nteams = all == 0 ? 0 : h.whole ? min(all_i, room) : min(room, max(1, (int)((unsigned)all / (unsigned)s.min_run)));
+    h.nteams = all == 0 ? 0 : h.whole ? min(all_i, room) : min(room, max(1, (int)((unsigned)all / (unsigned)K::min_run)));
     h.q = h.nteams ? (int)((unsigned)all / (unsigned)h.nteams) : 0;
     h.r = all - h.q * h.nteams;
     if (threadIdx.x == 0) sc->shares = h;
-    if (h.nteams && units) {
+    if (h.nteams && y.units) {
         int at = h.whole ? bi : before;
-        const int end = at + (h.whole ? items : units);
+        const int end = at + (h.whole ? y.items : y.units);
         // the CTAs' teams by turns: few teams are spread over the SMs
         int i = 0;
-        auto team = [&](int j) { return j * ctas + (int)blockIdx.x; };
+        auto team = [&](int j) { return j * ctas + cta; };
         // the teams that begin within this thread's entries
-        while (i < n && (int)blockIdx.x < ctas && team(i) < h.nteams && h.at(team(i)) < at) i++;
-        if (i < n && (int)blockIdx.x < ctas && team(i) < h.nteams && h.at(team(i)) < end)
-            for (int e = e0; e < e1; e++) {
-                const Entry x = e == e0 ? x0 : entry_of(a, s, pre, e);
+        while (i < n && team(i) < h.nteams && h.at(team(i)) < at) i++;
+        if (i < n && team(i) < h.nteams && h.at(team(i)) < end)
+            for (int e = y.e0; e < y.e1; e++) {
+                const Entry x = e == y.e0 ? y.x0 : entry_of<K>(a, s, pre, e);
                 const int c = a.Hkv * x.mt * (h.whole ? x.nu > 0 : x.nu);
                 for (; i < n && team(i) < h.nteams; i++) {
                     const int u0 = h.at(team(i));
@@ -267,32 +281,87 @@ __device__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* st
             }
     }
     __syncthreads();
+}
+
+// The length of the thread's first entry, asked for before anything else.
+__device__ __forceinline__ int first_len(const Kv16Attn& a, const Kv16Sched& s)
+{
+    int e0, e1;
+    first_entry(s, e0, e1);
+    return !s.direct && e0 < e1 && e0 >= s.n_pre ? a.lens[e0 - s.n_pre] : 0;
+}
+
+// Where each of the CTA's teams begins, for a kernel of one schedule.
+template <class K>
+__device__ __forceinline__ Prefixes find_starts(const Kv16Attn& a, const Kv16Sched& s, Start* starts, Scan* sc, PreShared* ps)
+{
+    const int len0 = first_len(a, s), n = s.per_cta;
+    Prefixes pre;
+    if ((int)threadIdx.x < n) starts[threadIdx.x].count = 0;
+    const bool bad = look_over(a, ps, pre);
+    if (s.direct) {
+        const int mt = (a.R + K::row_tile - 1) / K::row_tile, each = a.Hkv * mt, t = blockIdx.x * n + threadIdx.x;
+        if (threadIdx.x == 0) sc->shares = Shares{1, 0, s.nteams, 1};
+        if ((int)threadIdx.x < n && t < s.nteams && !bad) {
+            const int e = (unsigned)t / (unsigned)each;
+            starts[threadIdx.x] = Start{e, t - e * each, 1, t};
+        }
+        __syncthreads();
+        return pre;
+    }
+    const Sums y = add_up<K>(a, s, pre, sc, bad, len0);
+    __syncthreads();
+    const int all_u = all_units(sc);
+    say_bad(a, s, bad, all_u < 0);
+    share_out<K>(a, s, pre, y, all_u, starts, sc, blockIdx.x, gridDim.x);
     return pre;
+}
+
+// For a kernel some of whose CTAs take the prefixes (schedule sp) and the others the
+// sequences (ss): how many take prefixes, the same in every CTA.  starts: room for
+// either's teams; sc: two.
+template <int D>
+__device__ __forceinline__ int find_starts_beside(const Kv16Attn& a, const Kv16Sched& sp, const Kv16Sched& ss, Start* starts, Scan* sc, PreShared* ps,
+                                                  Prefixes& pre)
+{
+    const int len0 = first_len(a, ss);
+    if ((int)threadIdx.x < max(sp.per_cta, ss.per_cta)) starts[threadIdx.x].count = 0;
+    const bool bad = look_over(a, ps, pre);
+    const Sums yp = add_up<WideKind>(a, sp, pre, sc, bad, 0), ys = add_up<RowsKind>(a, ss, pre, sc + 1, bad, len0);
+    __syncthreads();
+    const int up = all_units(sc), us = all_units(sc + 1);
+    say_bad(a, sp, bad, up < 0 || us < 0);
+    // (units that do not fit are not worked on)
+    const int ctas = wide_sms((float)max(up, 0), (float)max(us, 0), D);
+    if ((int)blockIdx.x < ctas) share_out<WideKind>(a, sp, pre, yp, up, starts, sc, blockIdx.x, ctas);
+    else share_out<RowsKind>(a, ss, pre, ys, us, starts, sc + 1, blockIdx.x - ctas, gridDim.x - ctas);
+    return ctas;
 }
 
 // The run of one item's units that a team works on: tiles t0 .. t1 - 1 of KV
 // head g's rows from r0 of entry e.
+template <class K>
 struct Run {
     Entry x;
     int e, item, whole, u0, u1, nu, t0, t1;
     int left;
-    __device__ __forceinline__ void cut(const Kv16Sched& s, int from)
+    __device__ __forceinline__ void cut(int from)
     {
         nu = whole ? 1 : x.nu;
         u0 = from;
         u1 = min(nu, u0 + left);
         left -= u1 - u0;
-        t0 = whole ? 0 : tile_at(s, x, u0);
-        t1 = whole ? x.tiles : tile_at(s, x, u1);
+        t0 = whole ? 0 : tile_at<K>(x, u0);
+        t1 = whole ? x.tiles : tile_at<K>(x, u1);
         if (x.nu == 0) t0 = t1 = 0;  // (a direct team's sequence may be none)
     }
     __device__ __forceinline__ void begin(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, const Start& st, const Shares& h)
     {
         left = st.count, whole = h.whole, e = st.e;
-        x = entry_of(a, s, pre, e);
+        x = entry_of<K>(a, s, pre, e);
         const int n = whole ? 1 : x.nu;
         item = (unsigned)st.off / (unsigned)max(n, 1);
-        cut(s, st.off - item * n);
+        cut(st.off - item * n);
     }
     __device__ __forceinline__ bool next(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre)
     {
@@ -301,10 +370,10 @@ struct Run {
             item = 0;
             do {
                 if (++e >= s.n_pre + s.n_seq) return false;  // only if the lengths change under the call
-                x = entry_of(a, s, pre, e);
+                x = entry_of<K>(a, s, pre, e);
             } while (x.nu == 0);
         }
-        cut(s, 0);
+        cut(0);
         return true;
     }
     // all of the item's units: no other team has a part of it
@@ -315,10 +384,10 @@ struct Run {
     __device__ __forceinline__ void note(const Kv16Attn& a, const Kv16Sched& s, const Prefixes& pre, const Shares& h, int team) const
     {
         if (u0 != 0 || (s.finish && all())) return;
-        const int g = item / x.mt, r0 = (item - g * x.mt) * s.row_tile;
+        const int g = item / x.mt, r0 = (item - g * x.mt) * K::row_tile;
         Kv16Item it;
         it.t0 = team, it.n = all() ? 1 : h.team_of(h.at(team + 1) + (nu - u1) - 1) - team + 1;
-        it.row = x.row0 + r0, it.rows = min(s.row_tile, x.rows - r0), it.g = g;
+        it.row = x.row0 + r0, it.rows = min(K::row_tile, x.rows - r0), it.g = g;
         it.pre_row = x.b >= 0 && x.p >= 0 && !a.concat ? pre.first[x.p] * a.R : -1;
         if (s.finish) s.items[team] = it;
         else s.items[(size_t)((x.b >= 0) * a.Hkv + g) * a.B * a.R + it.row] = it;
@@ -328,7 +397,7 @@ struct Run {
 // Floats of a part and of the results of whole items.  A thread per row writes
 // columns ([D + 2][rows]: outputs, M, sum), so that a warp's stores are lines;
 // fragments of 8 rows x 4 lanes write rows ([rows][D], then [rows][M, sum]).
-constexpr int kWideRows = 256;   // rows of an item of k_kv16_wide, in two tiles
+constexpr int kWideRows = WideKind::row_tile;  // in two tiles
 __host__ __device__ constexpr size_t wide_part(int D) { return (size_t)2 * 128 * (D + 2); }
 __host__ __device__ constexpr size_t rows_part(int D, int R) { return ((size_t)R * (D + 2) + 3) / 4 * 4; }  // (16-byte aligned)
 

@@ -44,7 +44,7 @@
 // where pages are 16 tokens.
 #include <cudaTypedefs.h>
 
-#include "kv16_sched.cuh"
+#include "kv16_rows.cuh"
 
 namespace la {
 namespace {
@@ -307,13 +307,18 @@ struct Maps {
     CUtensorMap step[2], block[2], page[2];
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_kv16_wide(const __grid_constant__ Kv16Attn a, const __grid_constant__ Kv16Sched s, const __grid_constant__ Maps maps, int rows_all)
+// What a CTA does.  kBeside: other CTAs of the kernel do other things, and it is known
+// (given) where this one begins.
+struct Given {
+    Prefixes pre;
+    Shares shares;
+    Start start;
+};
+template <int D, bool kBeside>
+__device__ __forceinline__ void wide_cta(const Kv16Attn& a, const Kv16Sched& s, const Maps& maps, int rows_all, uint8_t* sm, const Given& given)
 {
     using L = WideSmem<D>;
     constexpr int kSt = L::kStages;
-    extern __shared__ __align__(1024) uint8_t sm[];
     Bars<kSt>& bar = *(Bars<kSt>*)(sm + L::kBar);
     uint64_t *b_full = bar.full, *b_empty = bar.empty, *b_s = bar.s, *b_p = bar.p, *b_q = &bar.q,
              *b_o = &bar.o, *b_end = &bar.end;
@@ -359,13 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             *(uint4*)(vis + 4 * i) = make_uint4(m[0], m[1], m[2], m[3]);
         }
-    pdl_wait();
-    pdl_trigger();
+    if (!kBeside) {
+        pdl_wait();
+        pdl_trigger();
+    }
     tc_fence_before();
-    const Prefixes pre = find_starts<D>(a, s, start, sc, (PreShared*)(sm + L::kPre));
+    const Prefixes pre = kBeside ? given.pre : find_starts<WideKind>(a, s, start, sc, (PreShared*)(sm + L::kPre));
+    if (kBeside) __syncthreads();
     tc_fence_after();
-    const Shares sh = sc->shares;
-    const Start st = *start;
+    const Shares sh = kBeside ? given.shares : sc->shares;
+    const Start st = kBeside ? given.start : *start;
     const uint32_t tmem = *tmem_slot;
     // (the swizzle and the products' descriptors count from multiples of 1024)
     const bool placed = (smem_u32(sm) & 1023) == 0, work = st.count > 0 && placed;
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool& ok = wait.ok;
     int n = 0;     // tiles so far
     int segs = 0;  // runs with tiles so far
-    Run run;
+    Run<WideKind> run;
     if (work) run.begin(a, s, pre, st, sh);
     if (threadIdx.x == 0 && s.finish && s.items) s.items[blockIdx.x].n = 0;
     if (work && warp < 8) {
@@ -728,6 +736,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv16_wide(const __grid_constant__ Kv16Attn a, const __grid_constant__ Kv16Sched s, const __grid_constant__ Maps maps, int rows_all)
+{
+    extern __shared__ __align__(1024) uint8_t sm[];
+    wide_cta<D, false>(a, s, maps, rows_all, sm, {});
+}
+
+// Prefixes by themselves, and their sequences of at most 16 rows a KV head beside them
+// on CTAs of their own (as a second kernel these would have to wait for the first one's
+// end before they may read what earlier calls wrote).
+constexpr int kRowWarps = kThreads / 32;
+template <int D>
+struct BesideSmem {
+    using Rows = RowsSmem<D, kRowWarps>;
+    // where the schedules are found: behind the rings of rows_team (in wide_cta's stages, until tiles come)
+    static constexpr int kScan = Rows::kScan, kStarts = kScan + 2 * (int)sizeof(Scan), kEnd = (kStarts + kRowWarps * (int)sizeof(Start) + 15) / 16 * 16;
+    static constexpr int kPre = WideSmem<D>::kPre > kEnd ? WideSmem<D>::kPre : kEnd;
+    static constexpr int kBytes = kPre + (int)sizeof(PreShared);
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_kv16_beside(const __grid_constant__ Kv16Attn a, const __grid_constant__ Kv16Sched sp,
+                                                             const __grid_constant__ Kv16Sched ss, const __grid_constant__ Maps maps, int rows_all)
+{
+    using L = BesideSmem<D>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    pdl_wait();
+    pdl_trigger();
+    Scan* sc = (Scan*)(sm + L::kScan);
+    Start* starts = (Start*)(sm + L::kStarts);
+    Prefixes pre;
+    const int ctas = find_starts_beside<D>(a, sp, ss, starts, sc, (PreShared*)(sm + L::kPre), pre);
+    if ((int)blockIdx.x < ctas) wide_cta<D, true>(a, sp, maps, rows_all, sm, Given{pre, sc[0].shares, *starts});
+    else rows_team<D, kRowWarps>(a, ss, sm, pre, sc[1].shares, starts[threadIdx.x >> 5]);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -753,14 +799,17 @@ bool encode(CUtensorMap* m, const void* base, long long rows, int cols, size_t l
 }  // namespace
 
 int kv16_wide_teams() { return kSMs; }
+int kv16_beside_teams() { return kSMs * kRowWarps; }
 
 bool kv16_wide_init()
 {
-    return encode_fn() && cudaFuncSetAttribute(k_kv16_wide<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem<128>::kBytes) == cudaSuccess &&
-           cudaFuncSetAttribute(k_kv16_wide<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem<64>::kBytes) == cudaSuccess;
+    auto room = [](auto* kernel, int bytes) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess; };
+    return encode_fn() && room(k_kv16_wide<128>, WideSmem<128>::kBytes) && room(k_kv16_wide<64>, WideSmem<64>::kBytes) &&
+           room(k_kv16_beside<128>, BesideSmem<128>::kBytes) && room(k_kv16_beside<64>, BesideSmem<64>::kBytes);
 }
 
-int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int D, int rows_all)
+// beside: the sequences' schedule, where the same kernel takes them.
+int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, const Kv16Sched* beside, int D, int rows_all)
 {
     Maps m;
     const long long rows = (long long)a.n_pages * a.Hkv << a.page_log2, steps = (long long)a.B * a.T;
@@ -771,8 +820,13 @@ int launch_kv16_wide(cudaStream_t s, const Kv16Attn& a, const Kv16Sched& w, int 
             !encode(&m.page[v], pages[v], rows, D, D, 1 << a.page_log2))
             return LA_ERR_CUDA;
     const dim3 grid(w.nteams), block(kThreads);
-    const cudaError_t e = D == 128 ? launch_pdl(k_kv16_wide<128>, grid, block, WideSmem<128>::kBytes, s, a, w, m, rows_all)
-                                   : launch_pdl(k_kv16_wide<64>, grid, block, WideSmem<64>::kBytes, s, a, w, m, rows_all);
+    cudaError_t e;
+    if (beside)
+        e = D == 128 ? launch_pdl(k_kv16_beside<128>, grid, block, BesideSmem<128>::kBytes, s, a, w, *beside, m, rows_all)
+                     : launch_pdl(k_kv16_beside<64>, grid, block, BesideSmem<64>::kBytes, s, a, w, *beside, m, rows_all);
+    else
+        e = D == 128 ? launch_pdl(k_kv16_wide<128>, grid, block, WideSmem<128>::kBytes, s, a, w, m, rows_all)
+                     : launch_pdl(k_kv16_wide<64>, grid, block, WideSmem<64>::kBytes, s, a, w, m, rows_all);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

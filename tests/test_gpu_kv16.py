@@ -771,3 +771,50 @@ def test_attention_scores_that_rise_along_the_keys(i, bits):
     e = (D // 16 + 1) * 2.0 ** -23 * far
     o, spread = _want(c)
     _compare(c, got, (o, spread + 2.0 ** 7 * e * (4 + o.abs())))
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,W,N,G", [(16, 16, 128, 0, 2, 0), (16, 8, 64, 1, 4, 1), (8, 8, 128, 2, 4, 2)])
+def test_attention_sees_what_the_calls_before_it_wrote(heads, kv_heads, D, W, N, G):
+    """Lengths, prefixes and rows written on the same stream right before each call, without a wait in between: as if
+    everything were waited for, in a graph too."""
+    import torch
+    g = np.random.default_rng(21)
+    B = 24
+    c = _case([200] * B, [(4000, 14), (3000, 10)], heads, kv_heads, D, 64, W, N, G, seed=21)
+    d, each = c["d"], []
+    for _ in range(12):
+        cut = int(g.integers(1, B))
+        each.append((_i32(g.integers(-1, 201, B)), _i32(g.integers(1, 3001, 2)), _i32([0, cut, B]),
+                     _bf(g.standard_normal(tuple(c["q"].shape))), torch.full_like(c["out"], 123.0)))
+
+    def write(x):
+        for to, what in zip((d["lens"], d["plens"], d["first"], c["q"]), x):
+            to.copy_(what)
+        c["out"].fill_(123)
+
+    def run(wait):
+        for x in each:
+            write(x)
+            if wait:
+                torch.cuda.synchronize()
+            _call(c)
+            if wait:
+                torch.cuda.synchronize()
+            x[4].copy_(c["out"])
+
+    run(True)
+    want = [x[4].clone() for x in each]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(False)
+    for again in (lambda: run(False), graph.replay):
+        for _ in range(5):
+            for x in each:
+                x[4].fill_(7)
+            again()
+            for x, y in zip(each, want):
+                assert torch.equal(x[4], y)
+    c["cache"].check()
+    c["lens"], c["spans"] = each[0][0].tolist(), [(0, int(each[0][2][1]), int(each[0][1][0])), (int(each[0][2][1]), B, int(each[0][1][1]))]
+    write(each[0])
+    _compare(c, _call(c))
