@@ -818,3 +818,29 @@ def test_attention_sees_what_the_calls_before_it_wrote(heads, kv_heads, D, W, N,
     c["lens"], c["spans"] = each[0][0].tolist(), [(0, int(each[0][2][1]), int(each[0][1][0])), (int(each[0][2][1]), B, int(each[0][1][1]))]
     write(each[0])
     _compare(c, _call(c))
+
+
+def test_attention_more_keys_than_a_count_holds_behind_a_prefix():
+    """64 sequences of 2^30 tokens each (one page named again and again) behind a prefix read by itself: their blocks
+    pass 2^31, and every row is left alone; the same buffers then do for lengths that fit."""
+    import torch
+    import lossless_lookahead_decoding_gb300 as LA
+    B, D, page, mp = 64, 64, 128, 1 << 23
+    c = LA.KV16Cache(*LA.KV16Cache.empty_pages(2, 1, D, page), max_pages=mp)
+    c.v_pages.fill_(3)
+    x = torch.zeros((B, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 123.0)
+    table, ptable = torch.zeros((B, mp), dtype=torch.int32, device="cuda"), torch.ones((1, 24), dtype=torch.int32, device="cuda")
+    ws = torch.empty(c.attention_bytes(B, 1, 0, 2, 0, prefixes=1, prefix_pages=24), dtype=torch.uint8, device="cuda")
+
+    def call(n):
+        c.attention(x, x, x + 3, _i32([n] * B), table, 0, 2, 0, out=out, workspace=ws, prefix_lens=_i32([3000]), prefix_table=ptable,
+                    prefix_first=_i32([0, B]))
+
+    call(page * mp)
+    with pytest.raises(LA.LAError) as e:
+        c.check()
+    assert e.value.code == LA.LA_ERR_ARG and (out == 123).all()
+    call(300)
+    c.check()
+    assert (out == 3).all()
