@@ -170,6 +170,21 @@ def test_attention_bytes_grow_with_the_rows():
             assert LA.la_kv16_attention(_desc(), _attn(**bad)) == LA.LA_ERR_ARG, bad
 
 
+def test_attention_needs_a_workspace_where_items_are_split():
+    """None for few short sequences, which a team each holds; some for longer ones, more for more rows to join; and what
+    is less, missing or misaligned is refused."""
+    import lossless_lookahead_decoding_gb300 as LA
+    E, bytes_of = LA.LA_ERR_ARG, lambda **kw: LA.la_kv16_attention_bytes(_desc(), _attn(**kw))
+    assert bytes_of(n_prefix=0, max_len=64) == 0 and bytes_of(n_prefix=0, max_len=64, W=7, N=5, G=7) == 0
+    # results of 200 sequences' rows, of the prefix's and of their own keys, are to be joined
+    assert bytes_of(batch=200) >= bytes_of() + 2 * 200 * 64 * 128 * 4
+    for rows in (dict(), dict(W=0, N=17, G=1), dict(W=7, N=5, G=7)):
+        need = bytes_of(**rows)
+        assert need > 0
+        for bad in (dict(workspace=None), dict(workspace=FAKE + 8), dict(ws_bytes=need - 1), dict(ws_bytes=0)):
+            assert LA.la_kv16_attention(_desc(), _attn(**rows, **bad)) == E, (rows, bad)
+
+
 def test_python_refusals_need_no_gpu():
     import torch
     import lossless_lookahead_decoding_gb300 as LA
