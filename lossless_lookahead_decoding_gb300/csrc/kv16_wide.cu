@@ -614,6 +614,9 @@ __device__ __forceinline__ void wide_cta(const Kv16Attn& a, const Kv16Sched& s, 
                 const int cy = cached ? (int)((((long long)page * a.Hkv + g) << a.page_log2) + (tok & ((1 << a.page_log2) - 1)))
                                       : x.b * a.T + (kb - nc) * 16;
                 const int fill = 2 * n + v, stage = fill % kSt;
+                // (The parity could be that of the phase two before, were fill - 2 kSt not known to be done with.  Stages are
+                // done with in the order of the products, that of their fills but for neighbours (K0 K1 V0 K2 V1 ... where
+                // the streams take alternate tiles), and this warp has waited for fill - 2 - kSt, at least 3 fills later.)
                 if (fill >= kSt) wait(b_empty + stage, fill / kSt - 1);
                 const bool go = __all_sync(0xffffffffu, ok);
                 const uint32_t code = !mine || bad ? 0u : cached ? (uint32_t)live : 128u + (kb - nc);
