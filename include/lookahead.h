@@ -599,7 +599,9 @@ typedef struct la_rope {
 /* No counterpart on the pages: position rotation of a caller's own layer loop.
  * HOST only.  freq: HOST double[rot_dim / 2], radians per position, or NULL:
  * theta^(-2 i / rot_dim).  The angle of a position is formed as an exact
- * multiple of turn, modulo a circle, so far positions lose nothing.
+ * multiple of turn, modulo a circle: at position t it is off by what a double
+ * holds of a frequency f, about 2^-52 t f radians (2^-21 at the last position
+ * and f = 1), and by 2^-24 of half a circle.
  * LA_ERR_ARG for rot_dim not a multiple of 16 in 16..128, theta not above 0,
  * frequencies not finite or above 2^20. */
 LA_API int la_rope_init(la_rope* r, int rot_dim, int neighbours, double theta, const double* freq);
@@ -672,8 +674,10 @@ LA_API size_t la_kv16_attention_bytes(const la_kv16_desc* c, const la_kv16_attn*
  * a page index outside the pool counts as no keys, prefix_first out of order
  * or more than 2^34 keys in all (over sequences, KV heads and groups of 256
  * rows) leave every row alone (each LA_ERR_ARG in *status).  Asynchronous on
- * `stream`; equal calls give equal bits.  Two calls that may run at the same
- * time (two streams, two captured graphs) need a workspace each. */
+ * `stream`; equal calls give equal bits, but how a row's sum is cut depends on
+ * the call's shapes and lengths, so the same row in another batch or step may
+ * differ in roundings.  Two calls that may run at the same time (two streams,
+ * two captured graphs) need a workspace each. */
 LA_API int la_kv16_attention(const la_kv16_desc* c, const la_kv16_attn* a, void* stream);
 
 #ifdef __cplusplus

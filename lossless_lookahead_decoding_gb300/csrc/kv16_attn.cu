@@ -238,14 +238,20 @@ Plan plan_of(const la_kv16_desc& c, const la_kv16_attn& a, uint8_t* ws)
         return x;
     };
     // A prefix by itself, for all of its sequences at once, where reading it for each would cost
-    // more than the further launches and parts (these bytes come from L2 at 8 TB/s: 2 us), and
-    // where a sequence has too few rows to fill a tile: with 100 rows of each of 6 prompts behind
-    // 1024 tokens 56 against 44 us, with 121 rows of 4 steps 33 against 20, with 456 of 8 160
-    // against 130; but 128 single tokens of 32 heads behind 1000 tokens 65 against 234, 32 of 64
-    // heads behind 32 767 55 against 397, 48 behind up to 4000 54 against 73.
+    // more than the further launch and parts (these bytes come from L2 at 8 TB/s: 2 us), and
+    // where a sequence has too few rows to fill a tile.  Both ways, in us, 8 KV heads over 50 to
+    // 600 tokens at D 128: 32 sequences behind 4000, with 8, 17, 32, 64 and 80 rows each, 28, 40,
+    // 46, 59, 70 by itself and 68, 67, 67, 70, 74 with each; behind 1000 24, 33, 36, 41, 45 and 32,
+    // 36, 36, 37, 39; 2 behind 4000, 8 and 64 rows, 20, 19 and 26, 20, behind 1000 (8 MB) 20, 18
+    // and 18, 18.  With 100 rows of each of 6 prompts behind 1024 56 against 44, with 456 of 8
+    // steps 160 against 130.  (The table's width stands for the prefixes' lengths, which are on
+    // the device, and any number of prefixes for one.)
     const long long again = (long long)k.B * k.Hkv * k.max_plen * D * 4;
     p.apart = k.B > 1 && k.R <= 64 && again > (16 << 20);
     k.concat = !p.apart;
+    // k_kv16_rows holds up to 16 rows.  The other kernel for these, 8 KV heads at D 128, 8 rows: 200
+    // sequences of 20 to 300 tokens 81 us and here 33, 32 of 500 to 4000 54 and 56, 4 of 4000 20 and
+    // 28 (more parts to join here); at 16 rows 81, 54, 20 and 40, 61, 32.
     p.use_rows = k.R <= 16;
     p.use_wide = !p.use_rows || p.apart;
     // ---- who begins where

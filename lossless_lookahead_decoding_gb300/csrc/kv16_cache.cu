@@ -7,7 +7,7 @@
 // the exact angle of u_i modulo a circle, one 64-bit product whatever t is,
 // where t f_i in fp32 would be off by 2^-24 t radians (0.06 at a million).
 // Its upper 32 bits, in half circles, go to sincospi in fp32: an angle within
-// 2^-24 pi of the true one.  y = x cos - x' sin and x' cos + x sin in fp32,
+// 2^-24 pi of t times u_i's frequency, which is f_i to a double's precision.  y = x cos - x' sin and x' cos + x sin in fp32,
 // one rounding to bf16.
 #include <math.h>
 

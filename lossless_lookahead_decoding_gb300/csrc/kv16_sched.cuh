@@ -127,9 +127,11 @@ struct Scan {
 // uw units (a tile for a stream: 32 KB of a pair's tile, 0.95 us) and ur blocks (8 KB at
 // D = 128, 0.126 us at what one SM can read) both end together.  Where HBM and not the
 // SMs sets the pace, a wide unit waits for its tiles and takes 1.73 us.  (128 single
-// tokens behind 1000, us in all, at 1.0, 1.4, 1.73 and 2.4 us a unit: 77, 67, 65, 64;
-// 48 behind prefixes of up to 4000: 61, 56, 54, 56; one kernel after the other, the
-// former: 89.)
+// tokens behind 1000 and 48 behind prefixes of up to 4000, us in all, at 1.0, 1.4, 1.73
+// and 2.4 us a unit: 74.8, 64.0, 65.5, 67.5 and 64.4, 57.1, 54.5, 55.8; at 0.09, 0.126
+// and 0.18 us a block: 67.6, 65.5, 64.1 and 55.6, 54.5, 75.4.  At D = 64 the former is
+// 42.5 with 0.45 or 0.6 of these times, 51.9 with 0.8 or all.)  One kind after the other
+// took 89 us for the former.
 __device__ __forceinline__ int wide_sms(float uw, float ur, int D)
 {
     const float half = D == 128 ? 1.f : 0.6f, tw = 0.95f * half, tr = 0.126f * half;

@@ -34,7 +34,7 @@
 // and the two products after it (0.27 us each, with the hand-overs 0.6 us), which
 // the other stream's softmax only hides in part: tensor pipe 54 %, issue slots
 // 41 %, special functions 26 %.  8 steps of 57 rows x 8 heads, 8 KV heads, over
-// 8.3 to 9.5 K keys (133 GFLOP): 129 us, 1.03 PFLOP/s.  Measured for that call and not taken:
+// 8.3 to 9.5 K keys (133 GFLOP): 128 us, 1.04 PFLOP/s.  Measured for that call and not taken:
 // 16 softmax warps (147 against 122 us for the kernel: twice the loads from tensor
 // memory), streams strictly by turns (150), loads from tensor memory ahead of their
 // use (165), sums of unrounded weights (126 against 120), sums by a product (152),
